@@ -34,6 +34,11 @@ EXPORTS = ("moe_router_logits", "moe_route", "moe_permute", "moe_expert_ffn", "m
            "moe_decode_stack_plan_bytes", "moe_decode_stack_prepare",
            "moe_decode_stack_prepare_routed", "moe_decode_stack")
 
+# names of every entry point declared in include/moe_kv.h
+KV_EXPORTS = ("moe_kv_workspace_bytes", "moe_kv_append", "moe_attn_decode", "moe_attn_chunk", "moe_kv_grow",
+              "moe_kv_fork", "moe_kv_free", "moe_kv_compact", "moe_kv_copy_pages")
+MOE_KV_BF16, MOE_KV_F16 = 1, 2
+
 
 class MoeError(RuntimeError):
     def __init__(self, fn: str, code: int, msg: str):
@@ -74,6 +79,25 @@ class moe_cache_swap(ctypes.Structure):
                 ("expert_in", ctypes.c_int32), ("expert_out", ctypes.c_int32)]
 
 
+class moe_kv_desc(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("n_layers", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32), ("n_slots", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("refs", ctypes.c_void_p), ("free_pages", ctypes.c_void_p), ("n_free", ctypes.c_void_p)]
+
+
+class moe_kv_rows(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("n_rows", ctypes.c_int32), ("slots", ctypes.c_void_p),
+                ("row_start", ctypes.c_void_p)]
+
+
+class moe_attn_args(ctypes.Structure):
+    _fields_ = [("Hq", ctypes.c_int32), ("scale", ctypes.c_float), ("window", ctypes.c_int32),
+                ("n_sink", ctypes.c_int32), ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("o", ctypes.c_void_p), ("lse", ctypes.c_void_p)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -90,6 +114,7 @@ def load(path: str = LIB_PATH):
         L = ctypes.CDLL(path)
         P, i32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
         D = ctypes.POINTER(moe_layer_desc)
+        KV, KR, KA = (ctypes.POINTER(s) for s in (moe_kv_desc, moe_kv_rows, moe_attn_args))
         sig = {
             "moe_router_logits": ([P, i32, P, i32, i32, i32, P, P], i32),
             "moe_route": ([P, i32, i32, i32, P, P, P, P], i32),
@@ -140,6 +165,15 @@ def load(path: str = LIB_PATH):
             "moe_mailbox_inject": ([P, ctypes.c_int32], i32),
             "moe_mailbox_add": ([P, P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, P, P],
                                 i32),
+            "moe_kv_workspace_bytes": ([KV, ctypes.c_int32, ctypes.c_int32], sz),
+            "moe_kv_append": ([KV, ctypes.c_int32, KR, P, P, ctypes.c_int64, P, sz, P], i32),
+            "moe_attn_decode": ([KV, ctypes.c_int32, KR, KA, P, sz, P], i32),
+            "moe_attn_chunk": ([KV, ctypes.c_int32, KR, KA, P, sz, P], i32),
+            "moe_kv_grow": ([KV, P, P, ctypes.c_int32, P, sz, P], i32),
+            "moe_kv_fork": ([KV, P, P, ctypes.c_int32, P, sz, P], i32),
+            "moe_kv_free": ([KV, P, ctypes.c_int32, P, sz, P], i32),
+            "moe_kv_compact": ([KV, P, P, sz, P], i32),
+            "moe_kv_copy_pages": ([KV, P, P, ctypes.c_int32, P, sz, P], i32),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -269,6 +303,44 @@ def moe_read_status(ws, stream=None):
     if code == MOE_ERR_CUDA:
         _check("moe_read_status", code)
     return code, int(out.value)
+
+
+def moe_kv_workspace_bytes(desc, Hq, max_rows) -> int:
+    return int(load().moe_kv_workspace_bytes(ctypes.byref(desc), Hq, max_rows))
+
+
+# The cache calls take references to the structs (ctypes.byref) and raw
+# pointers: a decode step makes two of them per layer, so they stay thin.
+def moe_kv_append(desc, layer, rows, k, v, row_stride, ws, ws_bytes, stream=None):
+    _check("moe_kv_append", load().moe_kv_append(desc, layer, rows, k, v, row_stride, ws, ws_bytes, _stream(stream)))
+
+
+def moe_attn_decode(desc, layer, rows, args, ws, ws_bytes, stream=None):
+    _check("moe_attn_decode", load().moe_attn_decode(desc, layer, rows, args, ws, ws_bytes, _stream(stream)))
+
+
+def moe_attn_chunk(desc, layer, rows, args, ws, ws_bytes, stream=None):
+    _check("moe_attn_chunk", load().moe_attn_chunk(desc, layer, rows, args, ws, ws_bytes, _stream(stream)))
+
+
+def moe_kv_grow(desc, slots, add, n, ws, ws_bytes, stream=None):
+    _check("moe_kv_grow", load().moe_kv_grow(desc, slots, add, n, ws, ws_bytes, _stream(stream)))
+
+
+def moe_kv_fork(desc, src, dst, n, ws, ws_bytes, stream=None):
+    _check("moe_kv_fork", load().moe_kv_fork(desc, src, dst, n, ws, ws_bytes, _stream(stream)))
+
+
+def moe_kv_free(desc, slots, n, ws, ws_bytes, stream=None):
+    _check("moe_kv_free", load().moe_kv_free(desc, slots, n, ws, ws_bytes, _stream(stream)))
+
+
+def moe_kv_compact(desc, n_moved, ws, ws_bytes, stream=None):
+    _check("moe_kv_compact", load().moe_kv_compact(desc, _ptr(n_moved), ws, ws_bytes, _stream(stream)))
+
+
+def moe_kv_copy_pages(desc, src, dst, n, ws, ws_bytes, stream=None):
+    _check("moe_kv_copy_pages", load().moe_kv_copy_pages(desc, src, dst, n, ws, ws_bytes, _stream(stream)))
 
 
 def moe_last_launch_count() -> int:

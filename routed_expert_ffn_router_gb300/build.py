@@ -37,7 +37,7 @@ def sources():
 
 def _headers():
     hs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    return hs + [os.path.join(INCLUDE, "moe.h")]
+    return hs + [os.path.join(INCLUDE, f) for f in ("moe.h", "moe_kv.h")]
 
 
 def up_to_date() -> bool:

@@ -10,6 +10,7 @@
 namespace moe {
 
 static thread_local int32_t g_launches = 0;
+void launch_count_reset() { g_launches = 0; }
 
 // ---- optional kernel timing: an event pair around every launch
 namespace {
@@ -259,7 +260,8 @@ moe_status moe_profile_totals(int32_t kind, double* total_ms, int64_t* count) {
 const char* moe_profile_kind_name(int32_t kind) {
   static const char* names[K_NUM_KINDS] = {"router_logits", "route", "permute", "x_prep",
                                            "gateup", "down", "combine", "fused_decode",
-                                           "fused_stack"};
+                                           "fused_stack", "kv_append", "kv_pages", "kv_move",
+                                           "attn_rows", "attn_decode", "attn_chunk"};
   if (kind < 0 || kind >= K_NUM_KINDS) return "";
   return names[kind];
 }

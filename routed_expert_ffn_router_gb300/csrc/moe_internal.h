@@ -13,6 +13,7 @@ namespace moe {
 enum KernelKind : int {
   K_ROUTER_LOGITS = 0, K_ROUTE, K_PERMUTE, K_X_PREP, K_GATEUP, K_DOWN, K_COMBINE, K_FUSED,
   K_FUSED_STACK,
+  K_KV_APPEND, K_KV_PAGES, K_KV_MOVE, K_ATTN_ROWS, K_ATTN_DECODE, K_ATTN_CHUNK,
   K_NUM_KINDS
 };
 
@@ -20,6 +21,7 @@ enum KernelKind : int {
 // timing is enabled, record a CUDA event pair on the launching stream.
 void launch_begin(int kind, cudaStream_t st);
 void launch_end(cudaStream_t st);
+void launch_count_reset();  // at the start of every entry point that launches
 
 // Sizes the host validated; everything a launch needs besides pointers.
 struct Shape {
