@@ -61,9 +61,12 @@ Rows rows_of(const moe_kv_rows* r) {
 // The workspace: the head that moe_workspace_init zeroes, then one region that
 // every call lays out for itself.
 size_t region_bytes(const moe_kv_desc* d, int32_t Hq, int32_t max_rows) {
-  (void)Hq;
-  (void)max_rows;
-  return pages_ws_bytes(d->n_pages, d->n_slots);
+  size_t n = pages_ws_bytes(d->n_pages, d->n_slots);
+  if (d->D == 64 || d->D == 128) {
+    const size_t m = decode_ws_bytes(d->page_size, d->max_pages, d->Hkv, Hq / d->Hkv, d->D, max_rows);
+    n = m > n ? m : n;
+  }
+  return n;
 }
 
 moe_status check_ws(const void* ws, size_t ws_bytes, size_t region) {
@@ -74,6 +77,7 @@ moe_status check_ws(const void* ws, size_t ws_bytes, size_t region) {
 moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 int32_t* status_of(void* ws) { return static_cast<int32_t*>(ws); }
+int32_t* sync_of(void* ws) { return reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + 512); }  // kSyncInts counters
 void* region_of(void* ws) { return static_cast<uint8_t*>(ws) + kWsHeadBytes; }
 
 moe_status attention(const moe_kv_desc* d, int32_t layer, const moe_kv_rows* r, const moe_attn_args* a, void* ws,
@@ -99,7 +103,11 @@ moe_status attention(const moe_kv_desc* d, int32_t layer, const moe_kv_rows* r, 
   at.q_stride = a->q_stride;
   at.o = static_cast<uint16_t*>(a->o);
   at.lse = a->lse;
-  return cuda_status(launch_attn_rows(c, rw, at, d->dtype == MOE_KV_F16, status_of(ws), static_cast<cudaStream_t>(stream)));
+  const bool f16 = d->dtype == MOE_KV_F16;
+  if (decode && decode_supported(d->D, d->page_size, d->Hkv, at.G, rw.n_q, d->max_pages))
+    return cuda_status(launch_attn_decode(c, rw, at, f16, status_of(ws), sync_of(ws), region_of(ws),
+                                          static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_attn_rows(c, rw, at, f16, status_of(ws), static_cast<cudaStream_t>(stream)));
 }
 
 // Checks shared by the page operations over n slots.

@@ -1,0 +1,807 @@
+// Attention of a decode window over the paged cache: one launch, bound by the
+// HBM read of the visible keys and values.
+//
+// Items and spans. An item is (sequence, tile of 16 query rows, KV head): the
+// rows are the window's new tokens times the query heads of the KV head, and
+// the item's keys and values are read once for all of them. An item's visible
+// 64-token tiles (first tokens that stay visible, then the window) are cut
+// into spans of 2^k tiles, 2^k the smallest with tiles <= 16 4^k, so both the
+// spans' length and their number grow as the square root of the length. Every
+// span is computed by itself and the spans are folded in order,
+//   M' = max(M, m),  L' = L 2^(M - M') + l 2^(m - M'),  O' = O 2^(M - M') + o 2^(m - M'),
+// so a row's result depends on its own sequence only, not on the other
+// sequences nor on how the spans fall on the CTAs.
+//
+// CTAs. Two per SM, each a producer warp and four consumer warps around a
+// 96 KB ring of tiles (K and V of 64 tokens, TMA boxes of a page's rows, 128-byte
+// swizzle). The list of all items' tiles is divided evenly; a CTA takes the
+// spans that start in its part. It folds consecutive spans of an item in
+// registers; an item that lies in several CTAs is joined, through partials in
+// the workspace, by the CTA that finishes last.
+//
+// A tile. Warp w multiplies Q (16 rows, registers) with keys 16 w .. 16 w + 15
+// (mma m16n8k16), the scores meet in shared memory, every warp holds the same
+// row maxima and probabilities, and warp w accumulates columns w D / 4 .. of O.
+// A probability enters the product with V as a sum of two values of the
+// cache's type (rounding 2^-17 for bf16 instead of 2^-8; the second product
+// costs nothing next to the HBM read). Keys that only some rows see are added
+// with scalar products, keys that no row sees get a zero value row: nothing
+// that lies in a masked place reaches a result, NaN and infinities included.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "kv_internal.h"
+#include "kv_tma.h"
+
+namespace moe {
+namespace kv {
+
+namespace {
+
+constexpr int kTile = 64;
+constexpr int kDecThreads = 160;
+constexpr int kRing = 96 * 1024;
+constexpr int kSPitch = kTile + 4;      // fp32 scores per row of a tile
+constexpr int kSeqCap = 256;            // sequences per launch
+constexpr int kCntBase = 2048;          // this kernel's counters in the workspace head
+
+struct DecArgs {
+  CUtensorMap tm_k, tm_v;
+  Cache c;
+  Rows r;
+  Attn a;
+  int b0;             // first sequence of this launch; r.B the sequences in it
+  int RT;             // row tiles per sequence
+  int logP;           // log2 of a box's rows: min(page, 64)
+  int logpage;
+  int max_span;       // spans of an item at most
+  float* part;        // [keys][max_span][R][D + 2]
+  int R;              // rows of a partial: 8 or 16
+  int32_t *status, *cnt;
+};
+
+__host__ __device__ inline int span_tiles(int nvis) {
+  int k = 0;
+  while (nvis > (16LL << (2 * k))) ++k;
+  return 1 << k;
+}
+
+// (m, l, o) of a span folded into (M, L, O): written with explicit rounding so
+// that the fold in registers and the join give the same bits.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void fold_ml(float& M, float& L, float m, float l, float& a, float& b) {
+  const float n = fmaxf(M, m), z = n == -INFINITY ? 0.f : n;
+  a = ex2(M - z);
+  b = ex2(m - z);
+  L = __fmaf_rn(l, b, __fmul_rn(L, a));
+  M = n;
+}
+__device__ __forceinline__ float fold_o(float O, float o, float a, float b) { return __fmaf_rn(o, b, __fmul_rn(O, a)); }
+
+// One item as every role sees it.
+struct Item {
+  int slot, len;
+  int pf, pl;        // tokens of its first and last row (pl < 0: nothing is seen)
+  int ns, wt, nvis;  // tiles of first tokens, first window tile, visible tiles
+  int sp, nspan;
+  __device__ int tile(int v) const { return v < ns ? v : v - ns + wt; }
+};
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  if constexpr (F16) {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+template <bool F16>
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+  if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2*>(&v));
+  else return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+template <bool F16>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  if constexpr (F16) mma_f16_16816(d, a0, a1, a2, a3, b0, b1);
+  else mma_bf16_16816(d, a0, a1, a2, a3, b0, b1);
+}
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+
+template <bool F16, int D>
+__global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_constant__ DecArgs g) {
+  constexpr int kStage = kTile * D * 4;      // K and V of a tile
+  constexpr int kStages = kRing / kStage;
+  constexpr int NT = D / 32;                 // 8-column tiles of a warp's part of O
+  constexpr int KK = D / 16;
+  extern __shared__ __align__(1024) uint8_t smem_dec[];
+  __shared__ __align__(8) uint64_t s_bar[2 * kStages];
+  __shared__ uint32_t s_badbox[kStages];
+  __shared__ int s_off[kSeqCap + 1], s_len[kSeqCap], s_slot[kSeqCap];
+  __shared__ __align__(16) float s_x[2][16][kSPitch];  // read and written in pairs
+  __shared__ int s_scan[8];
+  __shared__ int s_last;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int B = g.r.B, G = g.a.G, n_q = g.r.n_q, W = g.a.window, S = g.a.n_sink, Hkv = g.c.Hkv;
+  const uint32_t ring = (smem_u32(smem_dec) + 1023u) & ~1023u;
+  const uint32_t full = smem_u32(s_bar), empty = full + 8 * kStages;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 4);
+    }
+    fence_barrier_init();
+  }
+  griddep_wait();  // the rows' keys and values of an append before this launch
+
+  auto item_of = [&](int slot, int len, int rt) {
+    Item it;
+    it.slot = slot;
+    it.len = len;
+    const int r1 = min(n_q * G, rt * 16 + 16);
+    it.pf = len - n_q + rt * 16 / G;
+    it.pl = slot < 0 ? -1 : len - n_q + (r1 - 1) / G;
+    it.ns = it.wt = it.nvis = 0;
+    if (it.pl >= 0) {
+      const int from = W > 0 ? max(0, max(0, it.pf) - W + 1) : 0;
+      it.ns = (min(S, from) + kTile - 1) / kTile;
+      it.wt = max(from / kTile, it.ns);
+      it.nvis = it.ns + it.pl / kTile - it.wt + 1;
+    }
+    it.sp = span_tiles(it.nvis);
+    it.nspan = max(1, (it.nvis + it.sp - 1) / it.sp);
+    return it;
+  };
+
+  // the sequences' lengths and where their tiles start in the list of all tiles
+  int base = 0;
+  for (int b0 = 0; b0 < B; b0 += kDecThreads) {
+    const int b = b0 + tid;
+    int w = 0;
+    if (b < B) {
+      const Seq s = load_seq(g.c, g.r, b, g.status);
+      s_len[b] = s.len;
+      s_slot[b] = s.slot;
+      for (int rt = 0; rt < g.RT; ++rt) w += max(1, item_of(s.slot, s.len, rt).nvis);
+      w *= Hkv;
+    }
+    int x = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_scan[warp] = x;
+    __syncthreads();
+    int before = 0, sum = 0;
+#pragma unroll
+    for (int i = 0; i < kDecThreads / 32; ++i) {
+      before += i < warp ? s_scan[i] : 0;
+      sum += s_scan[i];
+    }
+    if (b < B) s_off[b] = base + before + x - w;
+    base += sum;
+    __syncthreads();
+  }
+  const int total = base;
+  if (tid == 0) s_off[B] = total;
+  __syncthreads();
+
+  // the list's division: CTA i takes the spans that start in [lo(i), lo(i + 1))
+  const int nc = gridDim.x, tq = total / nc, tr = total - tq * nc;
+  auto lo_of = [&](int i) { return i * tq + min(i, tr); };
+  auto cta_of = [&](int off) { return off < tr * (tq + 1) ? off / (tq + 1) : tr + (off - tr * (tq + 1)) / tq; };
+  const int lo = lo_of(blockIdx.x), hi = lo_of(blockIdx.x + 1);
+
+  // the walk over this CTA's spans, the same in every role
+  int b = 0, rt = 0, hk = 0, span = 0, ioff = 0;
+  Item it;
+  {
+    int l = 0, h = B - 1;
+    while (l < h) {
+      const int m = (l + h + 1) >> 1;
+      if (s_off[m] <= lo) l = m;
+      else h = m - 1;
+    }
+    b = l;
+    ioff = s_off[b];
+    it = item_of(s_slot[b], s_len[b], 0);
+    while (true) {
+      const int w = max(1, it.nvis);
+      if (lo - ioff < w * Hkv || rt + 1 == g.RT) {
+        hk = min(Hkv - 1, (lo - ioff) / w);
+        ioff += hk * w;
+        span = (lo - ioff + it.sp - 1) / it.sp;
+        break;
+      }
+      ioff += w * Hkv;
+      it = item_of(s_slot[b], s_len[b], ++rt);
+    }
+  }
+  auto next_item = [&] {  // -> false past the last item
+    ioff += max(1, it.nvis);
+    span = 0;
+    if (++hk < Hkv) return true;
+    hk = 0;
+    if (++rt == g.RT) {
+      rt = 0;
+      if (++b == B) return false;
+    }
+    it = item_of(s_slot[b], s_len[b], rt);
+    return true;
+  };
+  bool more = lo < hi;
+  if (more && span >= it.nspan) more = next_item();
+
+  if (warp == 4) {
+    // ================= producer =================
+    const int P = 1 << g.logP, nbox = kTile >> g.logP, box = P * D * 2;
+    int st = 0, ph = 1;
+    bool ok = true;
+    while (more && ok && ioff + span * it.sp < hi) {
+      const int v0 = span * it.sp, v1 = min(it.nvis, v0 + it.sp);
+      const int from = W > 0 ? max(0, max(0, it.pf) - W + 1) : 0, first = min(S, from);
+      const int32_t* tab = g.c.table + (long long)it.slot * g.c.max_pages;
+      // page numbers of 32 boxes at a time, one per lane
+      const int per = 32 >> (6 - g.logP);  // tiles whose boxes fill the lanes
+      for (int vb = v0; vb < v1 && ok; vb += per) {
+        int row = -1;       // the box's first row in the pool; -1 not needed, -2 bad page
+        {
+          const int v = vb + lane / nbox;
+          if (v < v1) {
+            const int j = it.tile(v) * kTile + (lane & (nbox - 1)) * P;
+            if (j <= it.pl && (j + P > from || j < first)) {
+              const int pg = tab[j >> g.logpage];
+              if (pg >= 0 && pg < g.c.n_pages) {
+                row = ((pg * Hkv + hk) << g.logpage) + (j & (g.c.page - 1));
+              } else {
+                row = -2;
+                atomicOr(g.status, DEV_BAD_SLOT);
+              }
+            }
+          }
+        }
+        for (int t = 0; t < per && vb + t < v1; ++t) {
+          ok = mbar_wait_short(empty + 8 * st, ph, g.status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          const int mine = __shfl_sync(0xffffffffu, row, t * nbox + (lane & (nbox - 1)));
+          const unsigned load = __ballot_sync(0xffffffffu, lane < nbox && mine >= 0);
+          const unsigned bad = __ballot_sync(0xffffffffu, lane < nbox && mine == -2);
+          if (lane == 0) {
+            s_badbox[st] = bad;
+            mbar_expect_tx(full + 8 * st, 2 * __popc(load) * box);
+          }
+          __syncwarp();
+          if (load >> lane & 1) {
+            const uint32_t dst = ring + st * kStage + lane * box;
+            tma_load_3d(dst, &g.tm_k, 0, mine, 0, full + 8 * st);
+            tma_load_3d(dst + kStage / 2, &g.tm_v, 0, mine, 0, full + 8 * st);
+          }
+          if (++st == kStages) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      if (++span >= it.nspan) more = next_item();
+    }
+    return;
+  }
+
+  // ================= consumers =================
+  const int qr = lane >> 2, qc = 2 * (lane & 3);
+  const int P = 1 << g.logP;
+  const bool two = n_q * G > 8;  // some tile has rows 8 .. 15
+  // score product: this lane's ldmatrix row of the warp's 16 keys
+  const int krow = warp * 16 + ((lane >> 4) << 3) + (lane & 7);
+  const uint32_t kaddr = (uint32_t)((krow >> g.logP) * P * D * 2 + (krow & (P - 1)) * 128);
+  const uint32_t kxor = (uint32_t)(krow & 7) << 4;
+  const uint32_t kch = ((lane >> 3) & 1) << 4;
+  // value product: this lane's ldmatrix row within 16 keys, its column chunk
+  const int vrow = lane & 15;
+  const uint32_t vxor = (uint32_t)(lane & 7) << 4;
+  const int vch0 = warp * NT + (lane >> 4);
+  int st = 0, ph = 0, sbuf = 0;
+
+  uint32_t q[KK][4];
+  int pos0 = -1, pos1 = -1;      // tokens of this lane's two rows (-1: no row, or before the first token)
+  float M0 = -INFINITY, M1 = -INFINITY, L0 = 0.f, L1 = 0.f, O[NT][4];
+  int run0 = -1;                 // first span of the current run of spans of one item
+
+  const int items = B * Hkv * g.RT;
+  const long long pstride = (long long)g.R * (D + 2);
+  // partials of an item split over CTAs: [span][m of R rows, l of R rows, o [R][D]]
+  auto part_of = [&](int key, int s) { return g.part + ((long long)key * g.max_span + s) * pstride; };
+  auto put = [&](float* p, float m0, float m1, float l0, float l1, const float (&o)[NT][4]) {
+    if (warp == 0 && (lane & 3) == 0) {
+      p[qr] = m0;
+      p[g.R + qr] = l0;
+      if (two) {
+        p[qr + 8] = m1;
+        p[g.R + qr + 8] = l1;
+      }
+    }
+    float* po = p + 2 * g.R + warp * (D / 4) + qc;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      *reinterpret_cast<float2*>(po + qr * D + n * 8) = make_float2(o[n][0], o[n][1]);
+      if (two) *reinterpret_cast<float2*>(po + (qr + 8) * D + n * 8) = make_float2(o[n][2], o[n][3]);
+    }
+  };
+  // rows of the item: token i and head of local row r, -1 if there is none
+  auto row_of = [&](int r) {
+    const int rr = rt * 16 + r;
+    return rr < n_q * G ? rr : -1;
+  };
+  auto out_rows = [&](float m0, float m1, float l0, float l1, const float (&o)[NT][4]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int rr = row_of(qr + 8 * h);
+      if (rr < 0) continue;
+      const long long t = (long long)b * n_q + rr / G;
+      const int hq = hk * G + rr % G;
+      const float l = h ? l1 : l0, m = h ? m1 : m0;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      uint16_t* po = g.a.o + (t * g.a.Hq + hq) * D + warp * (D / 4) + qc;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        *reinterpret_cast<uint32_t*>(po + n * 8) = pack2<F16>(o[n][2 * h] * inv, o[n][2 * h + 1] * inv);
+      if (g.a.lse && warp == 0 && (lane & 3) == 0)
+        g.a.lse[t * g.a.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    }
+  };
+
+  bool ok = true;
+  while (more && ioff + span * it.sp < hi) {
+    if (run0 < 0) {  // a new item: its query rows
+      run0 = span;
+      pos0 = pos1 = -1;
+      const uint16_t* qp[2] = {nullptr, nullptr};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int rr = row_of(qr + 8 * h);
+        if (rr < 0 || it.slot < 0) continue;
+        const int i = rr / G;
+        (h ? pos1 : pos0) = it.len - n_q + i;
+        qp[h] = g.a.q + ((long long)b * n_q + i) * g.a.q_stride + (hk * G + rr % G) * D + qc;
+      }
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          q[kk][e] = qp[e & 1] ? __ldg(reinterpret_cast<const uint32_t*>(qp[e & 1] + kk * 16 + (e >> 1) * 8)) : 0u;
+    }
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, o[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+    const int v1 = min(it.nvis, (span + 1) * it.sp);
+    for (int v = span * it.sp; v < v1; ++v) {
+      const int j0 = it.tile(v) * kTile;
+      // after an expired wait (the status word says that the results are
+      // incomplete) a warp goes on without waiting, so that all meet at every barrier
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_short(full + 8 * st, ph, g.status));
+      const uint32_t bad = *(volatile uint32_t*)&s_badbox[st];
+      const uint32_t sk = ring + st * kStage, sv = sk + kStage / 2;
+      // ---- scores of this warp's 16 keys
+      float x[2][4] = {};
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) {
+        uint32_t kf[4];
+        ldsm4(sk + kaddr + (kk / 4) * (P * 128) + ((((kk & 3) << 5) | kch) ^ kxor), kf);
+        mma<F16>(x[0], q[kk][0], q[kk][1], q[kk][2], q[kk][3], kf[0], kf[1]);
+        mma<F16>(x[1], q[kk][0], q[kk][1], q[kk][2], q[kk][3], kf[2], kf[3]);
+      }
+      const float sc = g.a.scale * 1.4426950408889634f;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        *reinterpret_cast<float2*>(&s_x[sbuf][qr][warp * 16 + n * 8 + qc]) = make_float2(x[n][0] * sc, x[n][1] * sc);
+        if (two)
+          *reinterpret_cast<float2*>(&s_x[sbuf][qr + 8][warp * 16 + n * 8 + qc]) = make_float2(x[n][2] * sc, x[n][3] * sc);
+      }
+      named_bar_sync(1, 128);
+      // ---- all 64 scores of the lane's rows: columns 16 kk + {qc, qc + 1, qc + 8, qc + 9}
+      float s0[16], s1[16];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 t = *reinterpret_cast<const float2*>(&s_x[sbuf][qr][i * 8 + qc]);
+        s0[2 * i] = t.x;
+        s0[2 * i + 1] = t.y;
+        if (two) {
+          const float2 u = *reinterpret_cast<const float2*>(&s_x[sbuf][qr + 8][i * 8 + qc]);
+          s1[2 * i] = u.x;
+          s1[2 * i + 1] = u.y;
+        }
+      }
+      const bool plain = bad == 0 && it.pf >= 0 && j0 + kTile - 1 <= it.pf &&
+                         (W == 0 || j0 > it.pl - W || j0 + kTile <= S);
+      if (!plain) {
+        auto see = [&](int p, int j) {
+          return j <= p && (W == 0 || j > p - W || j < S) && !(bad >> ((j - j0) >> g.logP) & 1);
+        };
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int j = j0 + (i >> 1) * 8 + qc + (i & 1);
+          if (!see(pos0, j)) s0[i] = -INFINITY;
+          if (two && !see(pos1, j)) s1[i] = -INFINITY;
+        }
+      }
+      // ---- running maximum, probabilities
+      float t0 = s0[0], t1 = two ? s1[0] : -INFINITY;
+#pragma unroll
+      for (int i = 1; i < 16; ++i) t0 = fmaxf(t0, s0[i]);
+      if (two) {
+#pragma unroll
+        for (int i = 1; i < 16; ++i) t1 = fmaxf(t1, s1[i]);
+      }
+      t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
+      t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
+      t0 = fmaxf(m0, t0);
+      const float z0 = t0 == -INFINITY ? 0.f : t0, al0 = ex2(m0 - z0);
+      m0 = t0;
+      l0 *= al0;
+      float z1 = 0.f, al1 = 1.f;
+      if (two) {
+        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
+        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
+        t1 = fmaxf(m1, t1);
+        z1 = t1 == -INFINITY ? 0.f : t1;
+        al1 = ex2(m1 - z1);
+        m1 = t1;
+        l1 *= al1;
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        o[n][0] *= al0;
+        o[n][1] *= al0;
+        o[n][2] *= al1;
+        o[n][3] *= al1;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s0[i] = ex2(s0[i] - z0);
+        l0 += s0[i];
+        if (two) {
+          s1[i] = ex2(s1[i] - z1);
+          l1 += s1[i];
+        }
+      }
+      if (!plain) {
+        // which keys no row sees, and which only some see (bit = key of the tile)
+        const int pf = max(0, it.pf);
+        unsigned none[2], some[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int j = j0 + 32 * h + lane;
+          const bool good = !(bad >> ((32 * h + lane) >> g.logP) & 1);
+          const bool any = good && j <= it.pl && (W == 0 || j > pf - W || j < S);
+          const bool all = good && j <= pf && (W == 0 || j > it.pl - W || j < S);
+          none[h] = __ballot_sync(0xffffffffu, !any);
+          some[h] = __ballot_sync(0xffffffffu, any && !all);
+        }
+        auto vptr = [&](int key, int col) {  // address of V[key][col]
+          const int c = col >> 3, r = key & (P - 1);
+          return sv + (key >> g.logP) * (P * D * 2) + (c >> 3) * (P * 128) + r * 128 +
+                 (((uint32_t)((c & 7) ^ (r & 7)) << 4) | ((col & 7) << 1));
+        };
+        for (int h = 0; h < 2; ++h)
+          for (unsigned ms = some[h]; ms; ms &= ms - 1) {
+            const int key = 32 * h + __ffs(ms) - 1, j = j0 + key;
+            const bool v0 = j <= pos0 && (W == 0 || j > pos0 - W || j < S);
+            const bool v1 = j <= pos1 && (W == 0 || j > pos1 - W || j < S);
+            const float p0 = v0 ? ex2(s_x[sbuf][qr][key] - z0) : 0.f;
+            const float p1 = two && v1 ? ex2(s_x[sbuf][qr + 8][key] - z1) : 0.f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const float2 vv = unpack2<F16>(ld_s32(vptr(key, warp * (D / 4) + n * 8 + qc)));
+              if (v0) {
+                o[n][0] = fmaf(p0, vv.x, o[n][0]);
+                o[n][1] = fmaf(p0, vv.y, o[n][1]);
+              }
+              if (two && v1) {
+                o[n][2] = fmaf(p1, vv.x, o[n][2]);
+                o[n][3] = fmaf(p1, vv.y, o[n][3]);
+              }
+            }
+          }
+        __syncwarp();
+        // zero rows in this warp's columns: a lane writes 16 bytes
+        for (int i = lane; i < kTile * NT; i += 32) {
+          const int key = i / NT, c = i - key * NT;
+          const unsigned cut = (key < 32 ? none[0] | some[0] : none[1] | some[1]) >> (key & 31) & 1;
+          if (cut)
+            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vptr(key, (warp * NT + c) * 8)), "r"(0) : "memory");
+        }
+        __syncwarp();
+      }
+      // ---- O += P V, P as a sum of two values of the type
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        uint32_t hi4[4], lo4[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = 4 * kk + (e >> 1) * 2;  // e: 0 row, 1 row + 8, 2 row (k + 8), 3 row + 8 (k + 8)
+          const bool up = e & 1;
+          if (up && !two) {
+            hi4[e] = lo4[e] = 0u;
+            continue;
+          }
+          const float p = up ? s1[i] : s0[i], r = up ? s1[i + 1] : s0[i + 1];
+          hi4[e] = pack2<F16>(p, r);
+          const float2 h = unpack2<F16>(hi4[e]);
+          lo4[e] = pack2<F16>(p - h.x, r - h.y);
+        }
+        const int row = kk * 16 + vrow;
+        const uint32_t va = sv + (row >> g.logP) * (P * D * 2) + (row & (P - 1)) * 128;
+#pragma unroll
+        for (int n = 0; n < NT; n += 2) {
+          uint32_t vf[4];
+          const int c = vch0 + n;
+          ldsm4t(va + (c >> 3) * (P * 128) + (((uint32_t)(c & 7) << 4) ^ vxor), vf);
+          mma<F16>(o[n], hi4[0], hi4[1], hi4[2], hi4[3], vf[0], vf[1]);
+          mma<F16>(o[n + 1], hi4[0], hi4[1], hi4[2], hi4[3], vf[2], vf[3]);
+          mma<F16>(o[n], lo4[0], lo4[1], lo4[2], lo4[3], vf[0], vf[1]);
+          mma<F16>(o[n + 1], lo4[0], lo4[1], lo4[2], lo4[3], vf[2], vf[3]);
+        }
+      }
+      if (!plain) fence_proxy_async_shared();  // the zeros before the next TMA box
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + 8 * st);
+      sbuf ^= 1;
+      if (++st == kStages) {
+        st = 0;
+        ph ^= 1;
+      }
+    }
+    // ---- the span's sums, folded onto the spans before it
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    if (two) {
+      l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    }
+    const int c0 = cta_of(ioff);
+    const int key = items <= nc ? (b * g.RT + rt) * Hkv + hk : c0;
+    if (run0 != 0) {
+      put(part_of(key, span), m0, m1, l0, l1, o);
+    } else if (span == 0) {
+      M0 = m0; M1 = m1; L0 = l0; L1 = l1;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) O[n][e] = o[n][e];
+    } else {
+      float a0, b0, a1, b1;
+      fold_ml(M0, L0, m0, l0, a0, b0);
+      fold_ml(M1, L1, m1, l1, a1, b1);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        O[n][0] = fold_o(O[n][0], o[n][0], a0, b0);
+        O[n][1] = fold_o(O[n][1], o[n][1], a0, b0);
+        O[n][2] = fold_o(O[n][2], o[n][2], a1, b1);
+        O[n][3] = fold_o(O[n][3], o[n][3], a1, b1);
+      }
+    }
+    const bool item_end = span + 1 == it.nspan, run_end = item_end || ioff + (span + 1) * it.sp >= hi;
+    if (run_end && run0 == 0 && item_end) {
+      out_rows(M0, M1, L0, L1, O);
+    } else if (run_end) {
+      if (run0 == 0) put(part_of(key, span), M0, M1, L0, L1, O);
+      __threadfence();
+      named_bar_sync(1, 128);
+      if (tid == 0) {
+        const int mine = span - run0 + 1;
+        s_last = atomicAdd(g.cnt + c0, mine) + mine == it.nspan;
+        if (s_last) g.cnt[c0] = 0;  // ready for the next call
+        __threadfence();
+      }
+      named_bar_sync(1, 128);
+      if (s_last) {
+        // every span is there: the fold in order, from the first run's last span
+        const int n0 = min(it.nspan, (lo_of(c0 + 1) - ioff + it.sp - 1) / it.sp);
+        auto get = [&](int s, float (&ml)[4], float (&w)[NT][4]) {
+          const float* p = part_of(key, s);
+          ml[0] = ldg_cg_f32(p + qr);
+          ml[2] = ldg_cg_f32(p + g.R + qr);
+          ml[1] = two ? ldg_cg_f32(p + qr + 8) : -INFINITY;
+          ml[3] = two ? ldg_cg_f32(p + g.R + qr + 8) : 0.f;
+          const float* po = p + 2 * g.R + warp * (D / 4) + qc;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const float2 u = __ldcg(reinterpret_cast<const float2*>(po + qr * D + n * 8));
+            w[n][0] = u.x;
+            w[n][1] = u.y;
+            const float2 y = two ? __ldcg(reinterpret_cast<const float2*>(po + (qr + 8) * D + n * 8)) : make_float2(0.f, 0.f);
+            w[n][2] = y.x;
+            w[n][3] = y.y;
+          }
+        };
+        float ml[4];
+        get(n0 - 1, ml, O);
+        M0 = ml[0]; M1 = ml[1]; L0 = ml[2]; L1 = ml[3];
+        constexpr int U = 4;
+        for (int s = n0; s < it.nspan; s += U) {
+          float w[U][NT][4], mls[U][4];
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (s + u < it.nspan) get(s + u, mls[u], w[u]);
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (s + u < it.nspan) {
+              float a0, b0, a1, b1;
+              fold_ml(M0, L0, mls[u][0], mls[u][2], a0, b0);
+              fold_ml(M1, L1, mls[u][1], mls[u][3], a1, b1);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                O[n][0] = fold_o(O[n][0], w[u][n][0], a0, b0);
+                O[n][1] = fold_o(O[n][1], w[u][n][1], a0, b0);
+                O[n][2] = fold_o(O[n][2], w[u][n][2], a1, b1);
+                O[n][3] = fold_o(O[n][3], w[u][n][3], a1, b1);
+              }
+            }
+        }
+        out_rows(M0, M1, L0, L1, O);
+      }
+    }
+    if (item_end) {
+      run0 = -1;
+      more = next_item();
+    } else {
+      ++span;
+    }
+  }
+}
+
+int log2_of(int v) {
+  int k = 0;
+  while ((1 << k) < v) ++k;
+  return k;
+}
+
+int sm_count(int* dev_out) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return 0;
+  }
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  *dev_out = dev;
+  return sms > 0 ? sms : 1;
+}
+
+constexpr int kMaxCtas = 2 * 304;  // counters and partials of the largest grid
+
+template <bool F16, int D>
+cudaError_t launch_one(DecArgs& g, int sms, int dev, cudaStream_t st) {
+  constexpr int smem = kRing + 1024;
+  static std::mutex mu;
+  static bool configured[64] = {};
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (!configured[dev]) {
+      const cudaError_t e = cudaFuncSetAttribute(decode_kernel<F16, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) {
+        cudaGetLastError();
+        return e;
+      }
+      configured[dev] = true;
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * sms < kMaxCtas ? 2 * sms : kMaxCtas);
+  cfg.blockDim = dim3(kDecThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  launch_begin(K_ATTN_DECODE, st);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_kernel<F16, D>, g);
+  launch_end(st);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+bool decode_supported(int D, int page, int Hkv, int G, int n_q, int max_pages) {
+  if (D != 64 && D != 128) return false;
+  if (page < 8 || (page & (page - 1))) return false;
+  if (!encode_fn()) return false;
+  // the tiles of one sequence count in int32
+  const long long RT = (n_q * (long long)G + 15) / 16, tiles = ((long long)max_pages * page + kTile - 1) / kTile;
+  return Hkv * RT * (tiles + 1) < (1LL << 30);
+}
+
+// Spans of an item at most, for tables of max_pages pages.
+int decode_max_span(int page, int max_pages) {
+  const int tiles = (int)(((long long)max_pages * page + kTile - 1) / kTile);
+  int most = 16;
+  for (int k = 0;; ++k) {
+    const long long hi = 16LL << (2 * k);
+    const long long t = tiles < hi ? tiles : hi;
+    const long long n = (t + (1LL << k) - 1) >> k;
+    if (n > most) most = (int)n;
+    if (hi >= tiles) return most;
+  }
+}
+
+size_t decode_ws_bytes(int page, int max_pages, int Hkv, int G, int D, int max_rows) {
+  // an item split over CTAs has its partials at its own place when there are
+  // no more items than CTAs, else at the place of its first CTA
+  const long long rows = max_rows < 16 ? max_rows : 16;
+  long long items = 0;  // over every split of max_rows rows into sequences
+  for (int n_q = 1; n_q <= rows; ++n_q) {
+    const long long n = (max_rows / n_q) * ((n_q * (long long)G + 15) / 16) * Hkv;
+    items = n > items ? n : items;
+  }
+  const long long keys = items < kMaxCtas ? items : kMaxCtas;
+  const int R = rows * G > 8 ? 16 : 8;
+  return align256((size_t)keys * decode_max_span(page, max_pages) * R * (D + 2) * 4);
+}
+
+cudaError_t launch_attn_decode(const Cache& c, const Rows& r, const Attn& a, bool f16, int32_t* status, int32_t* sync,
+                               void* scratch, cudaStream_t st) {
+  int dev = 0;
+  const int sms = sm_count(&dev);
+  if (!sms) return cudaErrorInvalidDevice;
+  DecArgs g;
+  if (!pool_maps(c, &g.tm_k, &g.tm_v, c.page < kTile ? c.page : kTile)) return cudaErrorInvalidValue;
+  g.c = c;
+  g.a = a;
+  g.RT = (r.n_q * a.G + 15) / 16;
+  g.logpage = log2_of(c.page);
+  g.logP = g.logpage < 6 ? g.logpage : 6;
+  g.max_span = decode_max_span(c.page, c.max_pages);
+  g.part = static_cast<float*>(scratch);
+  g.R = r.n_q * a.G > 8 ? 16 : 8;
+  g.status = status;
+  g.cnt = sync + kCntBase;
+  const long long tiles = ((long long)c.max_pages * c.page + kTile - 1) / kTile + 1;
+  long long per = ((1LL << 30)) / (c.Hkv * (long long)g.RT * tiles);  // sequences whose tiles count in int32
+  per = per < 1 ? 1 : per > kSeqCap ? kSeqCap : per;
+  for (int b0 = 0; b0 < r.B; b0 += (int)per) {
+    g.r = r;
+    g.r.B = (int)(r.B - b0 < per ? r.B - b0 : per);
+    if (r.slots) {
+      g.r.slots = r.slots + b0;
+    } else if (b0) {  // sequence b is slot b: shift the slots' arrays
+      g.c.table = c.table + (long long)b0 * c.max_pages;
+      g.c.lens = c.lens + b0;
+      g.c.n_slots = c.n_slots - b0;
+    }
+    const long long row0 = (long long)b0 * r.n_q;
+    g.r.n_rows = g.r.B * r.n_q;
+    g.a.q = a.q + row0 * a.q_stride;
+    g.a.o = a.o + row0 * a.Hq * c.D;
+    g.a.lse = a.lse ? a.lse + row0 * a.Hq : nullptr;
+    cudaError_t e;
+    if (c.D == 128) e = f16 ? launch_one<true, 128>(g, sms, dev, st) : launch_one<false, 128>(g, sms, dev, st);
+    else e = f16 ? launch_one<true, 64>(g, sms, dev, st) : launch_one<false, 64>(g, sms, dev, st);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace kv
+}  // namespace moe

@@ -1,0 +1,20 @@
+// TMA descriptors of the cache's pools (host side).
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "kv_internal.h"
+
+namespace moe {
+namespace kv {
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
+
+// One layer's pools as [D / 64][rows][64], rows = n_pages * Hkv * page, with
+// boxes of box_rows rows of all D columns: a box arrives as D / 64 blocks of
+// box_rows rows of 128 bytes, 128-byte swizzle.
+bool pool_maps(const Cache& c, CUtensorMap* k, CUtensorMap* v, int box_rows);
+
+}  // namespace kv
+}  // namespace moe
