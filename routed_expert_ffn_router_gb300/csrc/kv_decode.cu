@@ -5,9 +5,8 @@
 // rows are the window's new tokens times the query heads of the KV head, and
 // the item's keys and values are read once for all of them. An item's visible
 // 64-token tiles (first tokens that stay visible, then the window) are cut
-// into spans of 2^k tiles, 2^k the smallest with tiles <= 16 4^k, so both the
-// spans' length and their number grow as the square root of the length. Every
-// span is computed by itself and the spans are folded in order,
+// into spans (span_tiles). Every span is computed by itself and the spans are
+// folded in order,
 //   M' = max(M, m),  L' = L 2^(M - M') + l 2^(m - M'),  O' = O 2^(M - M') + o 2^(m - M'),
 // so a row's result depends on its own sequence only, not on the other
 // sequences nor on how the spans fall on the CTAs.
@@ -19,7 +18,7 @@
 // registers; an item that lies in several CTAs is joined, through partials in
 // the workspace, by the CTA that finishes last.
 //
-// A tile. Warp w multiplies Q (16 rows, registers) with keys 16 w .. 16 w + 15
+// A tile. Warp w multiplies Q (16 rows) with keys 16 w .. 16 w + 15
 // (mma m16n8k16), the scores meet in shared memory, every warp holds the same
 // row maxima and probabilities, and warp w accumulates columns w D / 4 .. of O.
 // A probability enters the product with V as a sum of two values of the
@@ -44,7 +43,7 @@ constexpr int kTile = 64;
 constexpr int kDecThreads = 160;
 constexpr int kRing = 96 * 1024;
 constexpr int kSPitch = kTile + 4;      // fp32 scores per row of a tile
-constexpr int kSeqCap = 256;            // sequences per launch
+constexpr int kSeqCap = 128;            // sequences per launch
 constexpr int kCntBase = 2048;          // this kernel's counters in the workspace head
 
 struct DecArgs {
@@ -57,14 +56,18 @@ struct DecArgs {
   int logP;           // log2 of a box's rows: min(page, 64)
   int logpage;
   int max_span;       // spans of an item at most
+  int most_spans;     // the same, as the rule for their length takes it
   float* part;        // [keys][max_span][R][D + 2]
   int R;              // rows of a partial: 8 or 16
   int32_t *status, *cnt;
 };
 
-__host__ __device__ inline int span_tiles(int nvis) {
+// Tiles of a span, by the item's own length and the call's heads: 2^k, the
+// smallest with at most 16 2^k spans (their number and their length both grow
+// as the square root of the length) and at most most_spans.
+__host__ __device__ inline int span_tiles(int nvis, int most_spans) {
   int k = 0;
-  while (nvis > (16LL << (2 * k))) ++k;
+  while (nvis > (16LL << (2 * k)) || nvis > ((long long)most_spans << k)) ++k;
   return 1 << k;
 }
 
@@ -127,6 +130,63 @@ __device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
                : "memory");
 }
 
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// A split item whose spans are all there.
+struct Join {
+  int b, rt, hk, n;   // n partials
+  const float* p;
+};
+
+// The fold of n partials of one row (from p on, pstride apart) in order, in the
+// fragment's columns col, col + 8, ..; eight partials in flight per lane.
+template <bool F16, int D>
+__device__ __forceinline__ void join_row(const float* p, long long pstride, int n, int R, int row, int col, uint16_t* o,
+                                      float* lse) {
+  constexpr int NT = D / 32, U = 8;
+  float M = 0.f, L = 0.f, O[NT][2];
+  const float* po = p + 2 * R + row * D + col;
+  for (int s = 0; s < n; s += U) {
+    float m[U], l[U];
+    float2 w[U][NT];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (s + u < n) {
+        m[u] = ldg_cg_f32(p + (s + u) * pstride + row);
+        l[u] = ldg_cg_f32(p + (s + u) * pstride + R + row);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) w[u][i] = __ldcg(reinterpret_cast<const float2*>(po + (s + u) * pstride + i * 8));
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (s + u < n) {
+        if (s + u == 0) {
+          M = m[u];
+          L = l[u];
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            O[i][0] = w[u][i].x;
+            O[i][1] = w[u][i].y;
+          }
+        } else {
+          float a, b;
+          fold_ml(M, L, m[u], l[u], a, b);
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            O[i][0] = fold_o(O[i][0], w[u][i].x, a, b);
+            O[i][1] = fold_o(O[i][1], w[u][i].y, a, b);
+          }
+        }
+      }
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) *reinterpret_cast<uint32_t*>(o + col + i * 8) = pack2<F16>(O[i][0] * inv, O[i][1] * inv);
+  if (lse) *lse = lse_of(M, L);
+}
+
 template <bool F16, int D>
 __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_constant__ DecArgs g) {
   constexpr int kStage = kTile * D * 4;      // K and V of a tile
@@ -138,8 +198,10 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_con
   __shared__ uint32_t s_badbox[kStages];
   __shared__ int s_off[kSeqCap + 1], s_len[kSeqCap], s_slot[kSeqCap];
   __shared__ __align__(16) float s_x[2][16][kSPitch];  // read and written in pairs
+  __shared__ __align__(16) uint16_t s_q[16][D + 8];  // the item's query rows (pitch: no bank conflicts)
   __shared__ int s_scan[8];
-  __shared__ int s_last;
+  __shared__ Join s_join[2];  // split items that this CTA completes: its first and its last at most
+  __shared__ int s_njoin;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int B = g.r.B, G = g.a.G, n_q = g.r.n_q, W = g.a.window, S = g.a.n_sink, Hkv = g.c.Hkv;
@@ -151,6 +213,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_con
       mbar_init(empty + 8 * i, 4);
     }
     fence_barrier_init();
+    s_njoin = 0;
   }
   griddep_wait();  // the rows' keys and values of an append before this launch
 
@@ -168,7 +231,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_con
       it.wt = max(from / kTile, it.ns);
       it.nvis = it.ns + it.pl / kTile - it.wt + 1;
     }
-    it.sp = span_tiles(it.nvis);
+    it.sp = span_tiles(it.nvis, g.most_spans);
     it.nspan = max(1, (it.nvis + it.sp - 1) / it.sp);
     return it;
   };
@@ -323,7 +386,8 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_con
   const int vch0 = warp * NT + (lane >> 4);
   int st = 0, ph = 0, sbuf = 0;
 
-  uint32_t q[KK][4];
+  // query rows: this lane's ldmatrix row and column half
+  const uint32_t qaddr = smem_u32(&s_q[lane & 15][(lane >> 4) * 8]);
   int pos0 = -1, pos1 = -1;      // tokens of this lane's two rows (-1: no row, or before the first token)
   float M0 = -INFINITY, M1 = -INFINITY, L0 = 0.f, L1 = 0.f, O[NT][4];
   int run0 = -1;                 // first span of the current run of spans of one item
@@ -367,7 +431,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_con
       for (int n = 0; n < NT; ++n)
         *reinterpret_cast<uint32_t*>(po + n * 8) = pack2<F16>(o[n][2 * h] * inv, o[n][2 * h + 1] * inv);
       if (g.a.lse && warp == 0 && (lane & 3) == 0)
-        g.a.lse[t * g.a.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        g.a.lse[t * g.a.Hq + hq] = lse_of(m, l);
     }
   };
 
@@ -376,20 +440,20 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_con
     if (run0 < 0) {  // a new item: its query rows
       run0 = span;
       pos0 = pos1 = -1;
-      const uint16_t* qp[2] = {nullptr, nullptr};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int rr = row_of(qr + 8 * h);
-        if (rr < 0 || it.slot < 0) continue;
-        const int i = rr / G;
-        (h ? pos1 : pos0) = it.len - n_q + i;
-        qp[h] = g.a.q + ((long long)b * n_q + i) * g.a.q_stride + (hk * G + rr % G) * D + qc;
+      if (it.slot >= 0) {
+        const int r0 = row_of(qr), r1 = row_of(qr + 8);
+        if (r0 >= 0) pos0 = it.len - n_q + r0 / G;
+        if (r1 >= 0) pos1 = it.len - n_q + r1 / G;
       }
-#pragma unroll
-      for (int kk = 0; kk < KK; ++kk)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          q[kk][e] = qp[e & 1] ? __ldg(reinterpret_cast<const uint32_t*>(qp[e & 1] + kk * 16 + (e >> 1) * 8)) : 0u;
+      named_bar_sync(1, 128);  // the last item's rows are not read any more
+      for (int i = tid; i < 16 * (D / 8); i += 128) {
+        const int r = i / (D / 8), c8 = i - r * (D / 8), rr = row_of(r);
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (rr >= 0)
+          v = ldg_nc_v4(g.a.q + ((long long)b * n_q + rr / G) * g.a.q_stride + (hk * G + rr % G) * D + c8 * 8);
+        *reinterpret_cast<uint4*>(&s_q[r][c8 * 8]) = v;
+      }
+      named_bar_sync(1, 128);
     }
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, o[NT][4];
 #pragma unroll
@@ -406,10 +470,11 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_con
       float x[2][4] = {};
 #pragma unroll
       for (int kk = 0; kk < KK; ++kk) {
-        uint32_t kf[4];
+        uint32_t q[4], kf[4];
+        ldsm4(qaddr + kk * 32, q);
         ldsm4(sk + kaddr + (kk / 4) * (P * 128) + ((((kk & 3) << 5) | kch) ^ kxor), kf);
-        mma<F16>(x[0], q[kk][0], q[kk][1], q[kk][2], q[kk][3], kf[0], kf[1]);
-        mma<F16>(x[1], q[kk][0], q[kk][1], q[kk][2], q[kk][3], kf[2], kf[3]);
+        mma<F16>(x[0], q[0], q[1], q[2], q[3], kf[0], kf[1]);
+        mma<F16>(x[1], q[0], q[1], q[2], q[3], kf[2], kf[3]);
       }
       const float sc = g.a.scale * 1.4426950408889634f;
 #pragma unroll
@@ -610,56 +675,13 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_con
       named_bar_sync(1, 128);
       if (tid == 0) {
         const int mine = span - run0 + 1;
-        s_last = atomicAdd(g.cnt + c0, mine) + mine == it.nspan;
-        if (s_last) g.cnt[c0] = 0;  // ready for the next call
-        __threadfence();
-      }
-      named_bar_sync(1, 128);
-      if (s_last) {
-        // every span is there: the fold in order, from the first run's last span
-        const int n0 = min(it.nspan, (lo_of(c0 + 1) - ioff + it.sp - 1) / it.sp);
-        auto get = [&](int s, float (&ml)[4], float (&w)[NT][4]) {
-          const float* p = part_of(key, s);
-          ml[0] = ldg_cg_f32(p + qr);
-          ml[2] = ldg_cg_f32(p + g.R + qr);
-          ml[1] = two ? ldg_cg_f32(p + qr + 8) : -INFINITY;
-          ml[3] = two ? ldg_cg_f32(p + g.R + qr + 8) : 0.f;
-          const float* po = p + 2 * g.R + warp * (D / 4) + qc;
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const float2 u = __ldcg(reinterpret_cast<const float2*>(po + qr * D + n * 8));
-            w[n][0] = u.x;
-            w[n][1] = u.y;
-            const float2 y = two ? __ldcg(reinterpret_cast<const float2*>(po + (qr + 8) * D + n * 8)) : make_float2(0.f, 0.f);
-            w[n][2] = y.x;
-            w[n][3] = y.y;
-          }
-        };
-        float ml[4];
-        get(n0 - 1, ml, O);
-        M0 = ml[0]; M1 = ml[1]; L0 = ml[2]; L1 = ml[3];
-        constexpr int U = 4;
-        for (int s = n0; s < it.nspan; s += U) {
-          float w[U][NT][4], mls[U][4];
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-            if (s + u < it.nspan) get(s + u, mls[u], w[u]);
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-            if (s + u < it.nspan) {
-              float a0, b0, a1, b1;
-              fold_ml(M0, L0, mls[u][0], mls[u][2], a0, b0);
-              fold_ml(M1, L1, mls[u][1], mls[u][3], a1, b1);
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                O[n][0] = fold_o(O[n][0], w[u][n][0], a0, b0);
-                O[n][1] = fold_o(O[n][1], w[u][n][1], a0, b0);
-                O[n][2] = fold_o(O[n][2], w[u][n][2], a1, b1);
-                O[n][3] = fold_o(O[n][3], w[u][n][3], a1, b1);
-              }
-            }
+        if (atomicAdd(g.cnt + c0, mine) + mine == it.nspan) {
+          g.cnt[c0] = 0;  // ready for the next call
+          // the first run's last span holds the fold of the spans before it
+          const int n0 = min(it.nspan, (lo_of(c0 + 1) - ioff + it.sp - 1) / it.sp) - 1;
+          Join& jn = s_join[s_njoin++];
+          jn = {b, rt, hk, it.nspan - n0, part_of(key, n0)};
         }
-        out_rows(M0, M1, L0, L1, O);
       }
     }
     if (item_end) {
@@ -667,6 +689,19 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_con
       more = next_item();
     } else {
       ++span;
+    }
+  }
+  // ---- joins, after the loop over tiles: they would take registers from it
+  named_bar_sync(1, 128);
+  __threadfence();
+  for (int i = 0; i < s_njoin; ++i) {
+    const Join jn = s_join[i];
+    for (int h = 0; h < (two ? 2 : 1); ++h) {
+      const int rr = jn.rt * 16 + qr + 8 * h;
+      if (rr >= n_q * G) continue;
+      const long long at = ((long long)jn.b * n_q + rr / G) * g.a.Hq + jn.hk * G + rr % G;
+      join_row<F16, D>(jn.p, pstride, jn.n, g.R, qr + 8 * h, warp * (D / 4) + qc, g.a.o + at * D,
+                       g.a.lse && warp == 0 && (lane & 3) == 0 ? g.a.lse + at : nullptr);
     }
   }
 }
@@ -733,16 +768,23 @@ bool decode_supported(int D, int page, int Hkv, int G, int n_q, int max_pages) {
   return Hkv * RT * (tiles + 1) < (1LL << 30);
 }
 
+// Spans that fill the GPU with one sequence's items; more would only lengthen the join.
+int most_spans_of(int Hkv, int RT) {
+  const int n = 256 / (Hkv * RT);
+  return n > 8 ? n : 8;
+}
+
 // Spans of an item at most, for tables of max_pages pages.
-int decode_max_span(int page, int max_pages) {
+int max_span_of(int page, int max_pages, int most_spans) {
   const int tiles = (int)(((long long)max_pages * page + kTile - 1) / kTile);
-  int most = 16;
-  for (int k = 0;; ++k) {
-    const long long hi = 16LL << (2 * k);
-    const long long t = tiles < hi ? tiles : hi;
+  int most = 1;
+  for (int k = 0;; ++k) {  // the longest item with spans of 2^k tiles
+    long long t = 16LL << (2 * k);
+    if (t > ((long long)most_spans << k)) t = (long long)most_spans << k;
+    if (t > tiles) t = tiles;
     const long long n = (t + (1LL << k) - 1) >> k;
     if (n > most) most = (int)n;
-    if (hi >= tiles) return most;
+    if (t == tiles) return most;
   }
 }
 
@@ -750,14 +792,14 @@ size_t decode_ws_bytes(int page, int max_pages, int Hkv, int G, int D, int max_r
   // an item split over CTAs has its partials at its own place when there are
   // no more items than CTAs, else at the place of its first CTA
   const long long rows = max_rows < 16 ? max_rows : 16;
-  long long items = 0;  // over every split of max_rows rows into sequences
+  size_t most = 0;
   for (int n_q = 1; n_q <= rows; ++n_q) {
-    const long long n = (max_rows / n_q) * ((n_q * (long long)G + 15) / 16) * Hkv;
-    items = n > items ? n : items;
+    const int RT = (n_q * G + 15) / 16;
+    const long long items = (max_rows / n_q) * (long long)RT * Hkv, keys = items < kMaxCtas ? items : kMaxCtas;
+    const size_t n = (size_t)keys * max_span_of(page, max_pages, most_spans_of(Hkv, RT)) * (n_q * G > 8 ? 16 : 8);
+    most = n > most ? n : most;
   }
-  const long long keys = items < kMaxCtas ? items : kMaxCtas;
-  const int R = rows * G > 8 ? 16 : 8;
-  return align256((size_t)keys * decode_max_span(page, max_pages) * R * (D + 2) * 4);
+  return align256(most * (D + 2) * 4);
 }
 
 cudaError_t launch_attn_decode(const Cache& c, const Rows& r, const Attn& a, bool f16, int32_t* status, int32_t* sync,
@@ -772,7 +814,8 @@ cudaError_t launch_attn_decode(const Cache& c, const Rows& r, const Attn& a, boo
   g.RT = (r.n_q * a.G + 15) / 16;
   g.logpage = log2_of(c.page);
   g.logP = g.logpage < 6 ? g.logpage : 6;
-  g.max_span = decode_max_span(c.page, c.max_pages);
+  g.most_spans = most_spans_of(c.Hkv, g.RT);
+  g.max_span = max_span_of(c.page, c.max_pages, g.most_spans);
   g.part = static_cast<float*>(scratch);
   g.R = r.n_q * a.G > 8 ? 16 : 8;
   g.status = status;
