@@ -65,6 +65,7 @@ size_t region_bytes(const moe_kv_desc* d, int32_t Hq, int32_t max_rows) {
   if (d->D == 64 || d->D == 128) {
     const size_t m = decode_ws_bytes(d->page_size, d->max_pages, d->Hkv, Hq / d->Hkv, d->D, max_rows);
     n = m > n ? m : n;
+    n = chunk_ws_bytes(d->D) > n ? chunk_ws_bytes(d->D) : n;
   }
   return n;
 }
@@ -107,6 +108,8 @@ moe_status attention(const moe_kv_desc* d, int32_t layer, const moe_kv_rows* r, 
   if (decode && decode_supported(d->D, d->page_size, d->Hkv, at.G, rw.n_q, d->max_pages))
     return cuda_status(launch_attn_decode(c, rw, at, f16, status_of(ws), sync_of(ws), region_of(ws),
                                           static_cast<cudaStream_t>(stream)));
+  if (!decode && chunk_supported(d->D, d->page_size, at.G, at.scale))
+    return cuda_status(launch_attn_chunk(c, rw, at, f16, status_of(ws), region_of(ws), static_cast<cudaStream_t>(stream)));
   return cuda_status(launch_attn_rows(c, rw, at, f16, status_of(ws), static_cast<cudaStream_t>(stream)));
 }
 

@@ -1,0 +1,791 @@
+// Attention of prompt chunks over the paged cache on the 5th-generation tensor
+// cores: S = Q K^T and O += P V as tcgen05 products with S, P and O in tensor
+// memory, the online softmax between them in registers. Bound by the tensor
+// cores at D = 128 (two products of 128 x 128 x 128 per tile and block of 128
+// keys, 1,024 cycles) and by the softmax at D = 64.
+//
+// Units and blocks. A tile is 128 query rows: 128 / G tokens (rounded down)
+// times the G query heads of one KV head, so the heads of a group share one
+// read of their keys. A unit is two tiles in a row of one sequence and KV head;
+// its blocks are the 128-token blocks of keys that some row sees (first tokens
+// that stay visible, then the window). The list of all units' blocks is
+// divided evenly over one CTA per SM: a causal chunk's later tiles see more
+// keys than its early ones, and few rows over a long context are work for all
+// SMs. A unit that lies in several CTAs leaves partial sums (m, l, o in fp32),
+// which combine_kernel joins in the order of the keys.
+//
+// Warps. 0-3 and 4-7: the softmax of tile 0 and of tile 1 (a thread is a row);
+// 8: issues the products; 9: TMA of Q, K and V; 10: zeroes the value rows that
+// no row sees (whatever lies there must not meet a zero probability). While a
+// softmax group works on its scores, the tensor cores run the other tile's
+// products:  S0 S1 | PV0 S0' | PV1 S1' | PV0' ...
+//
+// The running maximum is only raised when a row's scores pass it by more than
+// 2^8 (probabilities up to 256 lose nothing in bf16 or fp16, whose relative
+// rounding is the same there), so the accumulators in tensor memory are seldom
+// rescaled. Probabilities are rounded to the cache's type for the product
+// (half a step, 2^-8 for bf16 and 2^-11 for fp16, independent per key); their
+// sum is kept in fp32 before that rounding.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "kv_internal.h"
+#include "kv_tma.h"
+#include "moe_tc.cuh"
+
+namespace moe {
+namespace kv {
+
+using namespace tc;
+
+namespace {
+
+constexpr int kBlk = 128;               // keys per block
+constexpr int kChunkThreads = 384;
+constexpr int kLaunchRegs = 168;        // registers per thread at launch; the groups share 3 x 168
+constexpr int kSoftRegs = 208, kRestRegs = 88;
+constexpr int kChunkSeqs = 256;         // sequences per launch
+constexpr int kMaxGrid = 304;
+constexpr int kBadRing = 8;
+
+struct ChunkArgs {
+  CUtensorMap tm_q, tm_k, tm_v;
+  Cache c;
+  Rows r;
+  Attn a;
+  int b0, nseq;       // sequences of this launch
+  int tq;             // tokens per tile
+  int logP, logpage;  // rows of a TMA box: min(page, 128)
+  float* part;        // [2 grid][2 tiles][D / 4][128][4]
+  float* pml;         // [2 grid][2 tiles][m, l][128]
+  int32_t* status;
+};
+
+// The two tiles of a unit and the blocks they see.
+struct Unit {
+  int b, qb, hk;
+  int slot, len, n, row0;
+  int pf, pl;              // tokens of the first and the last row (pl < 0: nothing is seen)
+  int from, first;         // the window's first token; first tokens below it that stay visible
+  int ns, wt, nb;          // blocks of first tokens, first window block, blocks
+  __device__ int block(int u) const { return u < ns ? u : u - ns + wt; }
+};
+
+__device__ __forceinline__ void unit_blocks(Unit& x, int tq, int W, int S) {
+  const int i0 = x.qb * 2 * tq;
+  x.pf = x.len - x.n + i0;
+  x.pl = x.slot < 0 ? -1 : x.len - x.n + min(x.n, i0 + 2 * tq) - 1;
+  x.from = x.first = x.ns = x.wt = x.nb = 0;
+  if (x.pl >= 0) {
+    x.from = W > 0 ? max(0, max(0, x.pf) - W + 1) : 0;
+    x.first = min(S, x.from);
+    x.ns = (x.first + kBlk - 1) / kBlk;
+    x.wt = max(x.from / kBlk, x.ns);
+    x.nb = x.ns + x.pl / kBlk - x.wt + 1;
+  }
+}
+
+// The sequences of a launch and the division of their blocks, in shared memory.
+struct Plan {
+  long long off[kChunkSeqs + 1];   // blocks before each sequence (an empty unit counts as one)
+  int slot[kChunkSeqs], len[kChunkSeqs], n[kChunkSeqs], row0[kChunkSeqs];
+  long long total;
+  int nc;                          // CTAs that share the list
+};
+
+__device__ __forceinline__ Unit unit_at(const Plan& p, const ChunkArgs& g, int b, int qb, int hk) {
+  Unit x;
+  x.b = b; x.qb = qb; x.hk = hk;
+  x.slot = p.slot[b]; x.len = p.len[b]; x.n = p.n[b]; x.row0 = p.row0[b];
+  unit_blocks(x, g.tq, g.a.window, g.a.n_sink);
+  return x;
+}
+
+// All threads of the CTA; ends with a barrier.
+__device__ void make_plan(Plan& p, const ChunkArgs& g, int32_t* status) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nw = blockDim.x >> 5;
+  for (int b = tid; b < g.nseq; b += blockDim.x) {
+    const Seq s = load_seq(g.c, g.r, g.b0 + b, status);
+    p.slot[b] = s.slot; p.len[b] = s.len; p.n[b] = s.n; p.row0[b] = s.row0;
+  }
+  __syncthreads();
+  for (int b = warp; b < g.nseq; b += nw) {
+    const int nq = (p.n[b] + 2 * g.tq - 1) / (2 * g.tq);
+    long long w = 0;
+    for (int q = lane; q < nq; q += 32) w += max(1, unit_at(p, g, b, q, 0).nb);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+    if (lane == 0) p.off[b + 1] = w * g.c.Hkv;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    long long base = 0, units = 0;
+    for (int b0 = 0; b0 < g.nseq; b0 += 32) {
+      const int b = b0 + lane;
+      long long x = b < g.nseq ? p.off[b + 1] : 0;
+      long long u = b < g.nseq ? (long long)((p.n[b] + 2 * g.tq - 1) / (2 * g.tq)) * g.c.Hkv : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+      __syncwarp();
+      if (b < g.nseq) p.off[b + 1] = base + x;
+      base += __shfl_sync(0xffffffffu, x, 31);
+      units += u;
+    }
+    if (lane == 0) {
+      p.off[0] = 0;
+      p.total = base;
+      // a CTA per unit, or per four blocks where units are longer than that
+      long long nc = (base + 3) / 4;
+      nc = nc > units ? nc : units;
+      nc = nc < kMaxGrid ? nc : kMaxGrid;
+      p.nc = (int)nc;
+    }
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ long long lo_of(const Plan& p, int nc, int i) { return p.total * i / nc; }
+__device__ __forceinline__ int cta_of(const Plan& p, int nc, long long off) {  // the last i with lo_of(i) <= off
+  return (int)(((off + 1) * nc - 1) / p.total);
+}
+
+// The unit that holds list position `at`, and its first position (one warp).
+__device__ Unit find_unit(const Plan& p, const ChunkArgs& g, long long at, long long* start) {
+  const int lane = threadIdx.x & 31;
+  int l = 0, h = g.nseq - 1;  // the last sequence that starts at or before `at`
+  while (l < h) {
+    const int m = (l + h + 1) >> 1;
+    if (p.off[m] <= at) l = m;
+    else h = m - 1;
+  }
+  const int b = l;
+  long long base = p.off[b];
+  const int nq = (p.n[b] + 2 * g.tq - 1) / (2 * g.tq);
+  for (int q0 = 0;; q0 += 32) {
+    const int q = q0 + lane;
+    const long long w = q < nq ? (long long)max(1, unit_at(p, g, b, q, 0).nb) * g.c.Hkv : 0;
+    long long x = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    const unsigned in = __ballot_sync(0xffffffffu, q < nq && at < base + x);
+    if (in || q0 + 32 >= nq) {
+      const int src = in ? __ffs(in) - 1 : 31;
+      const long long before = __shfl_sync(0xffffffffu, base + x - w, src);
+      const int qb = q0 + src;
+      Unit u = unit_at(p, g, b, qb, 0);
+      const int per = max(1, u.nb);
+      u.hk = (int)((at - before) / per);
+      *start = before + (long long)u.hk * per;
+      return u;
+    }
+    base += __shfl_sync(0xffffffffu, x, 31);
+  }
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  if constexpr (F16) {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+template <int D>
+__host__ __device__ constexpr int stages() { return D == 128 ? 4 : 8; }
+template <int D>
+__host__ __device__ constexpr int chunk_smem() { return 1024 + 2 * kBlk * D * 2 + stages<D>() * kBlk * D * 2; }
+
+template <bool F16, int D>
+__global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_constant__ ChunkArgs g) {
+  constexpr int NH = D / 64;               // halves of 64 columns
+  constexpr int kTileB = kBlk * D * 2;     // bytes of a Q tile, or of a K or V block
+  constexpr int kHalf = kBlk * 128;
+  constexpr int NST = stages<D>();
+  extern __shared__ __align__(1024) uint8_t smem_chunk[];
+  __shared__ Plan s_plan;
+  __shared__ __align__(8) uint64_t s_bar[3 * NST + 12];
+  __shared__ uint32_t s_bad[kBadRing];
+  __shared__ Unit s_unit;
+  __shared__ long long s_start;
+  __shared__ uint32_t s_tmem;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t sq = (smem_u32(smem_chunk) + 1023u) & ~1023u, ring = sq + 2 * kTileB;
+  const uint32_t kv_full = smem_u32(s_bar), kv_empty = kv_full + 8 * NST, v_ready = kv_empty + 8 * NST;
+  const uint32_t q_full = v_ready + 8 * NST, q_empty = q_full + 8;
+  const uint32_t s_full = q_empty + 8, p_full = s_full + 16, pv_done = p_full + 16, o_free = pv_done + 16;
+  const uint32_t drained = o_free + 16;
+  if (tid == 0) {
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(kv_full + 8 * i, 1);
+      mbar_init(kv_empty + 8 * i, 1);
+      mbar_init(v_ready + 8 * i, 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(s_full + 8 * t, 1);
+      mbar_init(p_full + 8 * t, 4);
+      mbar_init(pv_done + 8 * t, 1);
+      mbar_init(o_free + 8 * t, 4);
+    }
+    mbar_init(drained, 1);
+    fence_barrier_init();
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  griddep_wait();
+  make_plan(s_plan, g, blockIdx.x == 0 ? g.status : nullptr);
+  const Plan& p = s_plan;
+  const int nc = min(p.nc, (int)gridDim.x);
+  const bool work = p.total > 0 && (int)blockIdx.x < nc;
+  const long long lo = work ? lo_of(p, nc, blockIdx.x) : 0, hi = work ? lo_of(p, nc, blockIdx.x + 1) : 0;
+  if (warp == 0 && lo < hi) {
+    long long start;
+    const Unit u = find_unit(p, g, lo, &start);
+    if (lane == 0) {
+      s_unit = u;
+      s_start = start;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  griddep_launch_dependents();
+  const uint32_t tmem = s_tmem;
+  const int W = g.a.window, S = g.a.n_sink, G = g.a.G, tq = g.tq;
+
+  // the walk over this CTA's segments, the same in every role
+  Unit x;
+  long long ustart = 0;
+  int u0 = 0, u1 = 0;            // the segment's blocks [u0, u1) of its unit
+  bool more = lo < hi;
+  if (more) {
+    x = s_unit;
+    ustart = s_start;
+  }
+  auto set_blocks = [&] {
+    u0 = (int)(lo > ustart ? lo - ustart : 0);
+    const long long e = hi - ustart;
+    u1 = e < x.nb ? (int)e : x.nb;
+  };
+  if (more) set_blocks();
+  auto next_seg = [&] {
+    ustart += max(1, x.nb);
+    if (ustart >= hi) {
+      more = false;
+      return;
+    }
+    if (++x.hk == g.c.Hkv) {
+      int b = x.b, qb = x.qb + 1;
+      while (qb * 2 * tq >= p.n[b]) {
+        ++b;
+        qb = 0;
+      }
+      x = unit_at(p, g, b, qb, 0);
+    }
+    set_blocks();
+  };
+  // tokens of tile t: [tf, tl], tl < tf if it has none
+  auto tile_tokens = [&](int t, int& tf, int& tl) {
+    const int i0 = x.qb * 2 * tq + t * tq;
+    tf = x.len - x.n + i0;
+    tl = x.len - x.n + min(x.n, i0 + tq) - 1;
+  };
+  auto takes = [&](int j0, int tf, int tl) {  // whether a tile sees anything of the block at token j0
+    return tl >= tf && j0 <= tl && (W == 0 || j0 + kBlk - 1 > max(tf, 0) - W || j0 < S);
+  };
+  bool dead = false;  // an expired wait: go on without waiting (the status word says so)
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait_short(bar, parity, g.status));
+  };
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs));
+    if (warp == 9) {
+      // ================= TMA producer =================
+      const int P = 1 << g.logP, nbox = kBlk >> g.logP;
+      int st = 0, ph = 1, bad_at = 0, qph = 1;
+      for (; more && !dead; next_seg()) {
+        if (u0 == u1) continue;
+        int tf, tl;
+        tile_tokens(1, tf, tl);
+        const int nt = tl >= tf ? 2 : 1;
+        wait(q_empty, qph);
+        qph ^= 1;
+        if (dead) break;
+        if (lane == 0) {
+          mbar_expect_tx(q_full, (uint32_t)(nt * NH * tq * G * 128));
+          for (int t = 0; t < nt; ++t)
+            for (int h = 0; h < NH; ++h)
+              tma_load_3d(sq + t * kTileB + h * kHalf, &g.tm_q, h * 64, x.hk * G, x.row0 + (x.qb * 2 + t) * tq, q_full);
+        }
+        const int32_t* tab = g.c.table + (long long)x.slot * g.c.max_pages;
+        auto entry = [&](int u) {  // lane's box of block u: its first row in the pool, -1 not needed, -2 bad
+          const int j = x.block(u) * kBlk + lane * P;
+          if (lane >= nbox || j > x.pl || !(j + P > x.from || j < x.first)) return -1;
+          const int pg = tab[j >> g.logpage];
+          if (pg >= 0 && pg < g.c.n_pages) return ((pg * g.c.Hkv + x.hk) << g.logpage) + (j & (g.c.page - 1));
+          atomicOr(g.status, DEV_BAD_SLOT);
+          return -2;
+        };
+        int row = entry(u0);
+        for (int u = u0; u < u1 && !dead; ++u) {
+          const int ahead = u + 1 < u1 ? entry(u + 1) : -1;
+          const unsigned load = __ballot_sync(0xffffffffu, row >= 0), bad = __ballot_sync(0xffffffffu, row == -2);
+          for (int kv = 0; kv < 2; ++kv) {
+            wait(kv_empty + 8 * st, ph);
+            if (dead) break;
+            if (lane == 0) {
+              if (kv == 0) s_bad[bad_at] = bad;
+              mbar_expect_tx(kv_full + 8 * st, (uint32_t)(__popc(load) * NH * P * 128));
+            }
+            __syncwarp();
+            if (row >= 0)
+#pragma unroll
+              for (int h = 0; h < NH; ++h)
+                tma_load_2d(ring + st * kTileB + h * kHalf + lane * P * 128, kv ? &g.tm_v : &g.tm_k, h * 64, row,
+                            kv_full + 8 * st);
+            if (++st == NST) {
+              st = 0;
+              ph ^= 1;
+            }
+          }
+          bad_at = (bad_at + 1) % kBadRing;
+          row = ahead;
+        }
+      }
+    } else if (warp == 10) {
+      // ================= values that no row sees become zeros =================
+      int st = 1, ph = 0, bad_at = 0;
+      for (; more; next_seg()) {
+        for (int u = u0; u < u1; ++u) {
+          const int j0 = x.block(u) * kBlk;
+          wait(kv_full + 8 * st, ph);
+          const uint32_t bad = *(volatile uint32_t*)&s_bad[bad_at];
+          if (bad || j0 + kBlk - 1 > x.pl || (j0 < x.from && j0 + kBlk > x.first)) {
+            for (int r = lane; r < kBlk; r += 32) {
+              const int j = j0 + r;
+              if (j > x.pl || (j < x.from && j >= x.first) || (bad >> (r >> g.logP) & 1))
+                for (int i = 0; i < D / 8; ++i)
+                  st_s128(ring + st * kTileB + (i >> 3) * kHalf + r * 128 + (i & 7) * 16, 0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_shared();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(v_ready + 8 * st);
+          bad_at = (bad_at + 1) % kBadRing;
+          st += 2;
+          if (st >= NST) {
+            st = 1;
+            ph ^= 1;
+          }
+        }
+      }
+    } else if (warp == 8) {
+      // ================= tensor-core products =================
+      const uint32_t lead = elect_lane();
+      const uint32_t id_s = idesc_16(F16, 128, kBlk, false), id_o = idesc_16(F16, 128, D, true);
+      int kst = 0, kph = 0;        // ring slot and phase of the next K block (its V block is the slot after)
+      uint32_t np[2] = {0, 0};     // PV products of each tile so far
+      uint32_t nseg[2] = {0, 0};   // segments in which each tile had blocks so far
+      int nq = 0;
+      for (; more; next_seg()) {
+        if (u0 == u1) continue;
+        int tf[2], tl[2];
+        tile_tokens(0, tf[0], tl[0]);
+        tile_tokens(1, tf[1], tl[1]);
+        bool started[2] = {false, false};
+        wait(q_full, nq & 1);
+        ++nq;
+        tc_fence_after();
+        auto score = [&](int t, int st) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 32;
+            tc_mma_el(tmem + t * kBlk, sdesc_sw128(sq + t * kTileB + o), sdesc_sw128(ring + st * kTileB + o), id_s,
+                      kk > 0, lead);
+          }
+          tc_commit_el(s_full + 8 * t, lead);
+        };
+        auto product = [&](int t, int st) {
+          if (!started[t]) {  // the tile's accumulator has been read by the segment before
+            wait(o_free + 8 * t, (nseg[t] & 1) ^ 1);
+            ++nseg[t];
+          }
+          wait(p_full + 8 * t, np[t] & 1);
+          ++np[t];
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kBlk / 16; ++kk)
+            tc_mma_ts_el(tmem + 256 + t * 128, tmem + t * kBlk + kk * 8,
+                         sdesc_sw128_n(ring + st * kTileB + kk * 2048, kHalf), id_o, started[t] || kk > 0, lead);
+          started[t] = true;
+          tc_commit_el(pv_done + 8 * t, lead);
+        };
+        int j0 = x.block(u0) * kBlk;
+        bool t0 = takes(j0, tf[0], tl[0]), t1 = takes(j0, tf[1], tl[1]);
+        wait(kv_full + 8 * kst, kph);
+        tc_fence_after();
+        if (t0) score(0, kst);
+        if (t1) score(1, kst);
+        tc_commit_el(kv_empty + 8 * kst, lead);
+        for (int u = u0; u < u1; ++u) {
+          const int vst = kst + 1, vph = kph;
+          kst += 2;
+          if (kst == NST) {
+            kst = 0;
+            kph ^= 1;
+          }
+          const bool nx = u + 1 < u1;
+          const int jn = nx ? x.block(u + 1) * kBlk : 0;
+          const bool n0 = nx && takes(jn, tf[0], tl[0]), n1 = nx && takes(jn, tf[1], tl[1]);
+          wait(v_ready + 8 * vst, vph);
+          tc_fence_after();
+          if (t0) product(0, vst);
+          if (nx) {
+            wait(kv_full + 8 * kst, kph);
+            tc_fence_after();
+          }
+          if (n0) score(0, kst);
+          if (t1) product(1, vst);
+          tc_commit_el(kv_empty + 8 * vst, lead);
+          if (n1) score(1, kst);
+          if (nx) tc_commit_el(kv_empty + 8 * kst, lead);
+          t0 = n0;
+          t1 = n1;
+        }
+        tc_commit_el(q_empty, lead);
+      }
+      // every product has ended before tensor memory is given back
+      tc_commit_el(drained, lead);
+      mbar_wait_short(drained, 0, g.status);
+    }
+  } else {
+    // ================= softmax (a thread is a row of its tile) =================
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    const int t = warp >> 2, r = tid & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + t * kBlk, to = tmem + lanes + 256 + t * 128;
+    const float sc = g.a.scale * 1.4426950408889634f;
+    uint32_t nsc = 0;   // score blocks of this tile so far
+    int bad_at = 0;
+    for (; more; next_seg()) {
+      int tf, tl;
+      tile_tokens(t, tf, tl);
+      const int tok = r / G, pos = tok < tq && tf + tok <= tl && x.slot >= 0 ? tf + tok : -1;
+      float m = -INFINITY, l = 0.f;
+      bool any = false;     // the accumulator holds a product of this segment
+      for (int u = u0; u < u1; ++u) {
+        const int j0 = x.block(u) * kBlk;
+        if (!takes(j0, tf, tl)) {
+          bad_at = (bad_at + 1) % kBadRing;
+          continue;
+        }
+        wait(s_full + 8 * t, nsc & 1);
+        tc_fence_after();
+        const uint32_t bad = *(volatile uint32_t*)&s_bad[bad_at];
+        bad_at = (bad_at + 1) % kBadRing;
+        uint32_t s[kBlk];
+#pragma unroll
+        for (int i = 0; i < kBlk / 32; ++i) tc_ld32(ts + 32 * i, s + 32 * i);
+        tc_ld_wait();
+        if (bad || tf < 0 || j0 + kBlk - 1 > tf || !(W == 0 || j0 > tl - W || j0 + kBlk <= S)) {
+          const int last = pos - j0, low = W > 0 ? pos - W - j0 : -1, keep = W > 0 ? S - j0 : 0;
+#pragma unroll
+          for (int i = 0; i < kBlk; ++i) {
+            const bool see = i <= last && (i > low || i < keep) && !(bad >> (i >> g.logP) & 1);
+            if (!see) s[i] = 0xff800000u;  // -inf
+          }
+        }
+        float mx[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
+#pragma unroll
+        for (int i = 4; i < kBlk; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+        const bool raise = top > m + 8.f || (m == -INFINITY && top > m);
+        if (__any_sync(0xffffffffu, raise)) {
+          const float m2 = raise ? top : m;
+          const float f = m == m2 ? 1.f : ex2(m - m2);
+          m = m2;
+          l *= f;
+          if (any) {  // the product before is still running, maybe
+            wait(pv_done + 8 * t, (nsc & 1) ^ 1);
+            tc_fence_after();
+#pragma unroll 1
+            for (int i = 0; i < D; i += 32) {
+              uint32_t o[32];
+              tc_ld32(to + i, o);
+              tc_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tc_st32(to + i, o);
+            }
+          }
+        }
+        const float z = m == -INFINITY ? 0.f : m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < kBlk / 64; ++c) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float a0 = ex2(fmaf(__uint_as_float(s[64 * c + 2 * i]), sc, -z));
+            const float a1 = ex2(fmaf(__uint_as_float(s[64 * c + 2 * i + 1]), sc, -z));
+            sum[(2 * i) & 3] += a0;
+            sum[(2 * i + 1) & 3] += a1;
+            pk[i] = pack2<F16>(a0, a1);
+          }
+          tc_st32(ts + 32 * c, pk);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tc_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + 8 * t);
+        ++nsc;
+        any = true;
+      }
+      // ---- the segment's end: the tile's rows out
+      const bool whole = u0 == 0 && u1 == x.nb;
+      if (any) {
+        wait(pv_done + 8 * t, (nsc & 1) ^ 1);
+        tc_fence_after();
+      }
+      if (whole) {
+        const bool real = tok < tq && tf + tok <= tl;
+        const int row = x.row0 + (x.qb * 2 + t) * tq + tok, hq = x.hk * G + r - tok * G;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        uint16_t* po = g.a.o + ((long long)row * g.a.Hq + hq) * D;
+#pragma unroll 1
+        for (int i = 0; i < D; i += 32) {
+          uint32_t o[32];
+          if (any) {
+            tc_ld32(to + i, o);
+            tc_ld_wait();
+          }
+          if (real) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = l == 0.f ? 0u
+                                : pack2<F16>(__uint_as_float(o[8 * e + 2 * k]) * inv, __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
+              *reinterpret_cast<uint4*>(po + i + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        if (real && g.a.lse)
+          g.a.lse[(long long)row * g.a.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      } else {
+        // a part of the unit: place 2 i + 1 if it holds the unit's first block, else 2 i
+        const int slot = 2 * blockIdx.x + (u0 == 0 ? 1 : 0);
+        float* pm = g.pml + (slot * 2 + t) * 256;
+        pm[r] = m;
+        pm[128 + r] = l;
+        if (any) {
+          float* pp = g.part + (long long)(slot * 2 + t) * D * 128 + r * 4;
+#pragma unroll 1
+          for (int i = 0; i < D; i += 32) {
+            uint32_t o[32];
+            tc_ld32(to + i, o);
+            tc_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<uint4*>(pp + (long long)(i / 4 + e) * 512) =
+                  make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+        }
+      }
+      if (any) {  // the accumulator may be written again
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_free + 8 * t);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// Units that lie in several CTAs: their parts folded in the order of the keys.
+// Block (i, y): the unit with CTA i's first position strictly inside it, if i
+// is the unit's second CTA; 32 of its 256 rows, four threads per row.
+template <bool F16, int D>
+__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ ChunkArgs g, int grid) {
+  __shared__ Plan s_plan;
+  __shared__ Unit s_unit;
+  __shared__ long long s_start;
+  const int tid = threadIdx.x;
+  griddep_wait();
+  make_plan(s_plan, g, nullptr);
+  const Plan& p = s_plan;
+  const int nc = min(p.nc, grid), i = blockIdx.x + 1;
+  if (p.total == 0 || i >= nc) return;
+  const long long at = lo_of(p, nc, i);
+  if (tid < 32) {
+    long long start;
+    const Unit u = find_unit(p, g, at, &start);
+    if (tid == 0) {
+      s_unit = u;
+      s_start = start;
+    }
+  }
+  __syncthreads();
+  const Unit x = s_unit;
+  if (s_start == at) return;
+  const int c0 = cta_of(p, nc, s_start), c1 = cta_of(p, nc, s_start + x.nb - 1);
+  if (c0 + 1 != i) return;
+  const int row = blockIdx.y * 32 + (tid >> 2), t = row >> 7, r = row & 127, q = tid & 3;
+  const int tok = r / g.a.G, local = x.qb * 2 * g.tq + t * g.tq + tok;
+  if (tok >= g.tq || local >= x.n) return;
+  auto ml = [&](int c, int k) { return __ldcg(g.pml + ((2 * c + (c == c0 ? 1 : 0)) * 2 + t) * 256 + k * 128 + r); };
+  float m = -INFINITY;
+  for (int c = c0; c <= c1; ++c)
+    if (ml(c, 1) != 0.f) m = fmaxf(m, ml(c, 0));
+  const float z = m == -INFINITY ? 0.f : m;
+  float l = 0.f, o[D / 4];
+#pragma unroll
+  for (int k = 0; k < D / 4; ++k) o[k] = 0.f;
+  for (int c = c0; c <= c1; ++c) {
+    const float lc = ml(c, 1);
+    if (lc == 0.f) continue;  // this part's rows saw nothing (no accumulator was written)
+    const float f = ex2(ml(c, 0) - z);
+    l = fmaf(lc, f, l);
+    const float* pp = g.part + (long long)((2 * c + (c == c0 ? 1 : 0)) * 2 + t) * D * 128 + r * 4;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(pp + (long long)(q * (D / 16) + k) * 512));
+      o[4 * k] = fmaf(v.x, f, o[4 * k]);
+      o[4 * k + 1] = fmaf(v.y, f, o[4 * k + 1]);
+      o[4 * k + 2] = fmaf(v.z, f, o[4 * k + 2]);
+      o[4 * k + 3] = fmaf(v.w, f, o[4 * k + 3]);
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const long long at_row = (long long)(x.row0 + local) * g.a.Hq + x.hk * g.a.G + r - tok * g.a.G;
+  uint16_t* po = g.a.o + at_row * D + q * (D / 4);
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k)
+    *reinterpret_cast<uint4*>(po + 8 * k) =
+        make_uint4(pack2<F16>(o[8 * k] * inv, o[8 * k + 1] * inv), pack2<F16>(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                   pack2<F16>(o[8 * k + 4] * inv, o[8 * k + 5] * inv), pack2<F16>(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+  if (q == 0 && g.a.lse) g.a.lse[at_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+template <bool F16, int D>
+cudaError_t launch_one(ChunkArgs& g, int grid, int dev, cudaStream_t st) {
+  constexpr int smem = chunk_smem<D>();
+  static std::mutex mu;
+  static bool configured[64] = {};
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (!configured[dev]) {
+      cudaError_t e = cudaFuncSetAttribute(chunk_kernel<F16, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      cudaFuncAttributes fa;
+      if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, chunk_kernel<F16, D>);
+      // the register shares add up to what the block is launched with
+      if (e == cudaSuccess && fa.numRegs < kLaunchRegs) e = cudaErrorInvalidConfiguration;
+      if (e != cudaSuccess) {
+        cudaGetLastError();
+        return e;
+      }
+      configured[dev] = true;
+    }
+  }
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kChunkThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  launch_begin(K_ATTN_CHUNK, st);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, chunk_kernel<F16, D>, g);
+  launch_end(st);
+  if (e != cudaSuccess || grid < 2) return e;
+  cfg.gridDim = dim3(grid - 1, 8);
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
+  launch_begin(K_ATTN_COMBINE, st);
+  e = cudaLaunchKernelEx(&cfg, combine_kernel<F16, D>, g, grid);
+  launch_end(st);
+  return e;
+}
+
+int chunk_grid(int* dev) {
+  int sms = 0;
+  if (cudaGetDevice(dev) != cudaSuccess || *dev < 0 || *dev >= 64) {
+    cudaGetLastError();
+    return 0;
+  }
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, *dev);
+  return sms < 1 ? 1 : sms < kMaxGrid ? sms : kMaxGrid;
+}
+
+}  // namespace
+
+bool chunk_supported(int D, int page, int G, float scale) {
+  // a scale above zero: the largest product is then the largest score
+  return (D == 64 || D == 128) && page >= 8 && (page & (page - 1)) == 0 && G <= 128 && scale > 0.f && encode_fn();
+}
+
+size_t chunk_ws_bytes(int D) { return (size_t)2 * kMaxGrid * 2 * 128 * (D + 2) * 4; }
+
+cudaError_t launch_attn_chunk(const Cache& c, const Rows& r, const Attn& a, bool f16, int32_t* status, void* scratch,
+                              cudaStream_t st) {
+  int dev = 0;
+  const int grid = chunk_grid(&dev);
+  if (!grid) return cudaErrorInvalidDevice;
+  ChunkArgs g;
+  g.c = c;
+  g.r = r;
+  g.a = a;
+  g.tq = 128 / a.G;
+  g.logpage = 0;
+  while ((1 << g.logpage) < c.page) ++g.logpage;
+  g.logP = g.logpage < 7 ? g.logpage : 7;
+  g.part = static_cast<float*>(scratch);
+  g.pml = g.part + (size_t)2 * kMaxGrid * 2 * 128 * c.D;
+  g.status = status;
+  if (!pool_maps_2d(c, &g.tm_k, &g.tm_v, 1 << g.logP) || !query_map(a, c.D, r.n_rows, g.tq, &g.tm_q))
+    return cudaErrorInvalidValue;
+  for (g.b0 = 0; g.b0 < r.B; g.b0 += kChunkSeqs) {
+    g.nseq = r.B - g.b0 < kChunkSeqs ? r.B - g.b0 : kChunkSeqs;
+    cudaError_t e;
+    if (c.D == 128) e = f16 ? launch_one<true, 128>(g, grid, dev, st) : launch_one<false, 128>(g, grid, dev, st);
+    else e = f16 ? launch_one<true, 64>(g, grid, dev, st) : launch_one<false, 64>(g, grid, dev, st);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace kv
+}  // namespace moe

@@ -82,6 +82,13 @@ bool decode_supported(int D, int page, int Hkv, int G, int n_q, int max_pages);
 size_t decode_ws_bytes(int page, int max_pages, int Hkv, int G, int D, int max_rows);
 cudaError_t launch_attn_decode(const Cache& c, const Rows& r, const Attn& a, bool f16, int32_t* status, int32_t* sync,
                                void* scratch, cudaStream_t st);
+// The tensor-core prompt-chunk kernels (kv_chunk.cu): D 64 or 128, pages of a
+// power of two of at least 8 tokens, up to 128 query heads per KV head, a scale
+// above zero.
+bool chunk_supported(int D, int page, int G, float scale);
+size_t chunk_ws_bytes(int D);
+cudaError_t launch_attn_chunk(const Cache& c, const Rows& r, const Attn& a, bool f16, int32_t* status, void* scratch,
+                              cudaStream_t st);
 cudaError_t launch_grow(const Cache& c, const int32_t* slots, const int32_t* add, int n, int32_t* status, void* scratch,
                         cudaStream_t st);
 cudaError_t launch_fork(const Cache& c, const int32_t* src, const int32_t* dst, int n, int32_t* status, void* scratch,

@@ -261,7 +261,8 @@ const char* moe_profile_kind_name(int32_t kind) {
   static const char* names[K_NUM_KINDS] = {"router_logits", "route", "permute", "x_prep",
                                            "gateup", "down", "combine", "fused_decode",
                                            "fused_stack", "kv_append", "kv_pages", "kv_move",
-                                           "attn_rows", "attn_decode", "attn_chunk"};
+                                           "attn_rows", "attn_decode", "attn_chunk",
+                                           "attn_combine"};
   if (kind < 0 || kind >= K_NUM_KINDS) return "";
   return names[kind];
 }

@@ -14,6 +14,7 @@ enum KernelKind : int {
   K_ROUTER_LOGITS = 0, K_ROUTE, K_PERMUTE, K_X_PREP, K_GATEUP, K_DOWN, K_COMBINE, K_FUSED,
   K_FUSED_STACK,
   K_KV_APPEND, K_KV_PAGES, K_KV_MOVE, K_ATTN_ROWS, K_ATTN_DECODE, K_ATTN_CHUNK,
+  K_ATTN_COMBINE,
   K_NUM_KINDS
 };
 
