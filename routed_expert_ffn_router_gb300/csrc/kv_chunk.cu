@@ -48,7 +48,16 @@ constexpr int kLaunchRegs = 168;        // registers per thread at launch; the g
 constexpr int kSoftRegs = 208, kRestRegs = 88;
 constexpr int kChunkSeqs = 256;         // sequences per launch
 constexpr int kMaxGrid = 304;
+constexpr int kUnitCost = 2;            // a unit's start and end, in blocks, for the division among the CTAs
 constexpr int kBadRing = 8;
+constexpr int kOutPitch = 80;           // bytes per row of a warp's output buffer (64 and a pad)
+
+// A unit that lies in CTAs c0 .. c1, kept at CTA c0 + 1's place (else c0 = -1).
+struct Split {
+  int c0, c1;
+  int row0, rows;     // its first row (token) and how many
+  int hk;
+};
 
 struct ChunkArgs {
   CUtensorMap tm_q, tm_k, tm_v;
@@ -60,6 +69,7 @@ struct ChunkArgs {
   int logP, logpage;  // rows of a TMA box: min(page, 128)
   float* part;        // [2 grid][2 tiles][D / 4][128][4]
   float* pml;         // [2 grid][2 tiles][m, l][128]
+  Split* split;       // [grid]
   int32_t* status;
 };
 
@@ -89,11 +99,23 @@ __device__ __forceinline__ void unit_blocks(Unit& x, int tq, int W, int S) {
 
 // The sequences of a launch and the division of their blocks, in shared memory.
 struct Plan {
-  long long off[kChunkSeqs + 1];   // blocks before each sequence (an empty unit counts as one)
+  int off[kChunkSeqs + 1];         // list positions before each sequence
+  int nq[kChunkSeqs];              // pairs of tiles
   int slot[kChunkSeqs], len[kChunkSeqs], n[kChunkSeqs], row0[kChunkSeqs];
-  long long total;
+  int total;
   int nc;                          // CTAs that share the list
 };
+
+// A unit's positions in the list, and the block at which a CTA boundary that
+// falls `at` positions into it cuts it: at its start or its end where the piece
+// would be no more than its own cost.
+__device__ __forceinline__ int weight(int nb) { return max(1, nb) + kUnitCost; }
+__device__ __forceinline__ int cut_at(int nb, int at) {
+  if (at <= 0) return 0;
+  if (nb < 2) return max(1, nb);  // one piece (an empty unit counts as one block): where it starts
+  const int x = at - kUnitCost;
+  return x <= 0 ? 0 : x >= nb - 1 ? nb : x;
+}
 
 __device__ __forceinline__ Unit unit_at(const Plan& p, const ChunkArgs& g, int b, int qb, int hk) {
   Unit x;
@@ -104,31 +126,31 @@ __device__ __forceinline__ Unit unit_at(const Plan& p, const ChunkArgs& g, int b
 }
 
 // All threads of the CTA; ends with a barrier.
-__device__ void make_plan(Plan& p, const ChunkArgs& g, int32_t* status) {
+__device__ void make_plan(Plan& p, const ChunkArgs& g, int grid, int32_t* status) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nw = blockDim.x >> 5;
   for (int b = tid; b < g.nseq; b += blockDim.x) {
     const Seq s = load_seq(g.c, g.r, g.b0 + b, status);
     p.slot[b] = s.slot; p.len[b] = s.len; p.n[b] = s.n; p.row0[b] = s.row0;
+    p.nq[b] = (s.n + 2 * g.tq - 1) / (2 * g.tq);
   }
   __syncthreads();
   for (int b = warp; b < g.nseq; b += nw) {
-    const int nq = (p.n[b] + 2 * g.tq - 1) / (2 * g.tq);
-    long long w = 0;
-    for (int q = lane; q < nq; q += 32) w += max(1, unit_at(p, g, b, q, 0).nb);
+    int w = 0;
+    for (int q = lane; q < p.nq[b]; q += 32) w += weight(unit_at(p, g, b, q, 0).nb);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
     if (lane == 0) p.off[b + 1] = w * g.c.Hkv;
   }
   __syncthreads();
   if (warp == 0) {
-    long long base = 0, units = 0;
+    int base = 0, units = 0;
     for (int b0 = 0; b0 < g.nseq; b0 += 32) {
       const int b = b0 + lane;
-      long long x = b < g.nseq ? p.off[b + 1] : 0;
-      long long u = b < g.nseq ? (long long)((p.n[b] + 2 * g.tq - 1) / (2 * g.tq)) * g.c.Hkv : 0;
+      int x = b < g.nseq ? p.off[b + 1] : 0;
+      int u = b < g.nseq ? p.nq[b] * g.c.Hkv : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
       }
 #pragma unroll
@@ -142,50 +164,50 @@ __device__ void make_plan(Plan& p, const ChunkArgs& g, int32_t* status) {
       p.off[0] = 0;
       p.total = base;
       // a CTA per unit, or per four blocks where units are longer than that
-      long long nc = (base + 3) / 4;
-      nc = nc > units ? nc : units;
-      nc = nc < kMaxGrid ? nc : kMaxGrid;
-      p.nc = (int)nc;
+      p.nc = min(min(max((base + 3 + kUnitCost) / (4 + kUnitCost), units), kMaxGrid), grid);
     }
   }
   __syncthreads();
 }
 
-__device__ __forceinline__ long long lo_of(const Plan& p, int nc, int i) { return p.total * i / nc; }
-__device__ __forceinline__ int cta_of(const Plan& p, int nc, long long off) {  // the last i with lo_of(i) <= off
-  return (int)(((off + 1) * nc - 1) / p.total);
+// CTA i's part starts at lo_of(i); cta_of(at) is the last i with lo_of(i) <= at.
+__device__ __forceinline__ int lo_of(const Plan& p, int i) {
+  const int q = p.total / p.nc, r = p.total - q * p.nc;
+  return i * q + min(i, r);
+}
+__device__ __forceinline__ int cta_of(const Plan& p, int at) {
+  const int q = p.total / p.nc, r = p.total - q * p.nc;
+  return at < r * (q + 1) ? at / (q + 1) : r + (at - r * (q + 1)) / q;
 }
 
 // The unit that holds list position `at`, and its first position (one warp).
-__device__ Unit find_unit(const Plan& p, const ChunkArgs& g, long long at, long long* start) {
+__device__ Unit find_unit(const Plan& p, const ChunkArgs& g, int at, int* start) {
   const int lane = threadIdx.x & 31;
-  int l = 0, h = g.nseq - 1;  // the last sequence that starts at or before `at`
-  while (l < h) {
-    const int m = (l + h + 1) >> 1;
-    if (p.off[m] <= at) l = m;
+  int b = 0, h = g.nseq - 1;  // the last sequence that starts at or before `at`
+  while (b < h) {
+    const int m = (b + h + 1) >> 1;
+    if (p.off[m] <= at) b = m;
     else h = m - 1;
   }
-  const int b = l;
-  long long base = p.off[b];
-  const int nq = (p.n[b] + 2 * g.tq - 1) / (2 * g.tq);
+  int base = p.off[b];
+  const int nq = p.nq[b];
   for (int q0 = 0;; q0 += 32) {
     const int q = q0 + lane;
-    const long long w = q < nq ? (long long)max(1, unit_at(p, g, b, q, 0).nb) * g.c.Hkv : 0;
-    long long x = w;
+    const int w = q < nq ? weight(unit_at(p, g, b, q, 0).nb) * g.c.Hkv : 0;
+    int x = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
     const unsigned in = __ballot_sync(0xffffffffu, q < nq && at < base + x);
     if (in || q0 + 32 >= nq) {
       const int src = in ? __ffs(in) - 1 : 31;
-      const long long before = __shfl_sync(0xffffffffu, base + x - w, src);
-      const int qb = q0 + src;
-      Unit u = unit_at(p, g, b, qb, 0);
-      const int per = max(1, u.nb);
-      u.hk = (int)((at - before) / per);
-      *start = before + (long long)u.hk * per;
+      const int before = __shfl_sync(0xffffffffu, base + x - w, src);
+      Unit u = unit_at(p, g, b, q0 + src, 0);
+      const int per = weight(u.nb);
+      u.hk = (at - before) / per;
+      *start = before + u.hk * per;
       return u;
     }
     base += __shfl_sync(0xffffffffu, x, 31);
@@ -208,10 +230,39 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
   }
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 w, x, y;\n"
+      " mov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// The n lowest bits (none below 0, all from 32 on).
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+// Scores I .. I + 63 of keys that the row does not see become -inf.
+template <int I>
+__device__ __forceinline__ void cut(uint32_t (&s)[kBlk], const uint32_t (&vis)[4]) {
+#pragma unroll
+  for (int i = I; i < I + 64; ++i) s[i] = vis[i / 32] & (1u << (i % 32)) ? s[i] : 0xff800000u;
+}
+
 template <int D>
 __host__ __device__ constexpr int stages() { return D == 128 ? 4 : 8; }
 template <int D>
-__host__ __device__ constexpr int chunk_smem() { return 1024 + 2 * kBlk * D * 2 + stages<D>() * kBlk * D * 2; }
+__host__ __device__ constexpr int chunk_smem() {
+  return 1024 + 2 * kBlk * D * 2 + stages<D>() * kBlk * D * 2 + 8 * 32 * kOutPitch;
+}
 
 template <bool F16, int D>
 __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_constant__ ChunkArgs g) {
@@ -221,17 +272,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
   constexpr int NST = stages<D>();
   extern __shared__ __align__(1024) uint8_t smem_chunk[];
   __shared__ Plan s_plan;
-  __shared__ __align__(8) uint64_t s_bar[3 * NST + 12];
+  __shared__ __align__(8) uint64_t s_bar[3 * NST + 13];
   __shared__ uint32_t s_bad[kBadRing];
   __shared__ Unit s_unit;
-  __shared__ long long s_start;
+  __shared__ int s_start;
   __shared__ uint32_t s_tmem;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int W = g.a.window, S = g.a.n_sink, G = g.a.G, tq = g.tq;
   const uint32_t sq = (smem_u32(smem_chunk) + 1023u) & ~1023u, ring = sq + 2 * kTileB;
   const uint32_t kv_full = smem_u32(s_bar), kv_empty = kv_full + 8 * NST, v_ready = kv_empty + 8 * NST;
   const uint32_t q_full = v_ready + 8 * NST, q_empty = q_full + 8;
-  const uint32_t s_full = q_empty + 8, p_full = s_full + 16, pv_done = p_full + 16, o_free = pv_done + 16;
+  const uint32_t s_full = q_empty + 8, p_full = s_full + 16, pv_done = p_full + 32, o_free = pv_done + 16;
   const uint32_t drained = o_free + 16;
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
@@ -243,69 +295,96 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     mbar_init(q_empty, 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(s_full + 8 * t, 1);
-      mbar_init(p_full + 8 * t, 4);
+      mbar_init(p_full + 16 * t, 4);
+      mbar_init(p_full + 16 * t + 8, 4);
       mbar_init(pv_done + 8 * t, 1);
       mbar_init(o_free + 8 * t, 4);
     }
     mbar_init(drained, 1);
     fence_barrier_init();
   }
+  if (tid == 32 * 9) {
+    prefetch_tensormap(&g.tm_q);
+    prefetch_tensormap(&g.tm_k);
+    prefetch_tensormap(&g.tm_v);
+  }
   if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   griddep_wait();
-  make_plan(s_plan, g, blockIdx.x == 0 ? g.status : nullptr);
+  make_plan(s_plan, g, gridDim.x, blockIdx.x == 0 ? g.status : nullptr);
   const Plan& p = s_plan;
-  const int nc = min(p.nc, (int)gridDim.x);
-  const bool work = p.total > 0 && (int)blockIdx.x < nc;
-  const long long lo = work ? lo_of(p, nc, blockIdx.x) : 0, hi = work ? lo_of(p, nc, blockIdx.x + 1) : 0;
-  if (warp == 0 && lo < hi) {
-    long long start;
-    const Unit u = find_unit(p, g, lo, &start);
-    if (lane == 0) {
-      s_unit = u;
-      s_start = start;
+  const bool work = p.total > 0 && (int)blockIdx.x < p.nc;
+  const int lo = work ? lo_of(p, blockIdx.x) : 0, hi = work ? lo_of(p, blockIdx.x + 1) : 0;
+  if (warp == 0) {
+    int start = 0;
+    Split sp;
+    sp.c0 = -1;
+    if (lo < hi) {
+      const Unit u = find_unit(p, g, lo, &start);
+      const int cut = cut_at(u.nb, lo - start);
+      if (cut > 0 && cut < u.nb) {
+        // the CTAs of its first and its last block
+        int c0 = cta_of(p, start + kUnitCost), c1 = cta_of(p, start + kUnitCost + u.nb - 1);
+        while (cut_at(u.nb, lo_of(p, c0 + 1) - start) <= 0) ++c0;
+        while (cut_at(u.nb, lo_of(p, c1) - start) >= u.nb) --c1;
+        sp.c0 = c0 + 1 == (int)blockIdx.x ? c0 : -1;
+        sp.c1 = c1;
+        sp.row0 = u.row0 + u.qb * 2 * tq;
+        sp.rows = min(2 * tq, u.n - u.qb * 2 * tq);
+        sp.hk = u.hk;
+      }
+      if (lane == 0) {
+        s_unit = u;
+        s_start = start;
+      }
     }
+    if (lane == 0) g.split[blockIdx.x] = sp;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   griddep_launch_dependents();
   const uint32_t tmem = s_tmem;
-  const int W = g.a.window, S = g.a.n_sink, G = g.a.G, tq = g.tq;
 
   // the walk over this CTA's segments, the same in every role
   Unit x;
-  long long ustart = 0;
+  int ustart = 0;
   int u0 = 0, u1 = 0;            // the segment's blocks [u0, u1) of its unit
   bool more = lo < hi;
   if (more) {
     x = s_unit;
     ustart = s_start;
   }
-  auto set_blocks = [&] {
-    u0 = (int)(lo > ustart ? lo - ustart : 0);
-    const long long e = hi - ustart;
-    u1 = e < x.nb ? (int)e : x.nb;
-  };
-  if (more) set_blocks();
-  auto next_seg = [&] {
-    ustart += max(1, x.nb);
+  auto next_unit = [&] {
+    ustart += weight(x.nb);
     if (ustart >= hi) {
       more = false;
       return;
     }
     if (++x.hk == g.c.Hkv) {
       int b = x.b, qb = x.qb + 1;
-      while (qb * 2 * tq >= p.n[b]) {
+      while (qb >= p.nq[b]) {
         ++b;
         qb = 0;
       }
       x = unit_at(p, g, b, qb, 0);
     }
-    set_blocks();
   };
+  auto settle = [&] {  // this CTA's blocks of the unit, or of the next one of which it has some
+    for (; more; next_unit()) {
+      const int a = cut_at(x.nb, lo - ustart), e = cut_at(x.nb, hi - ustart);
+      u0 = min(a, x.nb);
+      u1 = min(e, x.nb);
+      if (a < e) return;
+    }
+  };
+  auto next_seg = [&] {
+    next_unit();
+    settle();
+  };
+  settle();
   // tokens of tile t: [tf, tl], tl < tf if it has none
   auto tile_tokens = [&](int t, int& tf, int& tl) {
     const int i0 = x.qb * 2 * tq + t * tq;
@@ -331,15 +410,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         int tf, tl;
         tile_tokens(1, tf, tl);
         const int nt = tl >= tf ? 2 : 1;
-        wait(q_empty, qph);
-        qph ^= 1;
-        if (dead) break;
-        if (lane == 0) {
-          mbar_expect_tx(q_full, (uint32_t)(nt * NH * tq * G * 128));
-          for (int t = 0; t < nt; ++t)
-            for (int h = 0; h < NH; ++h)
-              tma_load_3d(sq + t * kTileB + h * kHalf, &g.tm_q, h * 64, x.hk * G, x.row0 + (x.qb * 2 + t) * tq, q_full);
-        }
         const int32_t* tab = g.c.table + (long long)x.slot * g.c.max_pages;
         auto entry = [&](int u) {  // lane's box of block u: its first row in the pool, -1 not needed, -2 bad
           const int j = x.block(u) * kBlk + lane * P;
@@ -348,6 +418,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           if (pg >= 0 && pg < g.c.n_pages) return ((pg * g.c.Hkv + x.hk) << g.logpage) + (j & (g.c.page - 1));
           atomicOr(g.status, DEV_BAD_SLOT);
           return -2;
+        };
+        auto queries = [&] {
+          wait(q_empty, qph);
+          qph ^= 1;
+          if (lane == 0 && !dead) {
+            mbar_expect_tx(q_full, (uint32_t)(nt * NH * tq * G * 128));
+            for (int t = 0; t < nt; ++t)
+              for (int h = 0; h < NH; ++h)
+                tma_load_3d(sq + t * kTileB + h * kHalf, &g.tm_q, h * 64, x.hk * G, x.row0 + (x.qb * 2 + t) * tq, q_full);
+          }
+          __syncwarp();
         };
         int row = entry(u0);
         for (int u = u0; u < u1 && !dead; ++u) {
@@ -370,6 +451,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
               st = 0;
               ph ^= 1;
             }
+            if (u == u0 && kv == 0) queries();  // after the first keys: they need not wait for the last segment's products
           }
           bad_at = (bad_at + 1) % kBadRing;
           row = ahead;
@@ -433,13 +515,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             wait(o_free + 8 * t, (nseg[t] & 1) ^ 1);
             ++nseg[t];
           }
-          wait(p_full + 8 * t, np[t] & 1);
-          ++np[t];
-          tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < kBlk / 16; ++kk)
-            tc_mma_ts_el(tmem + 256 + t * 128, tmem + t * kBlk + kk * 8,
-                         sdesc_sw128_n(ring + st * kTileB + kk * 2048, kHalf), id_o, started[t] || kk > 0, lead);
+          for (int h = 0; h < 2; ++h) {  // the block's first 64 keys, while the others' probabilities are made
+            wait(p_full + 16 * t + 8 * h, np[t] & 1);
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+              tc_mma_ts_el(tmem + 256 + t * 128, tmem + t * kBlk + kk * 8,
+                           sdesc_sw128_n(ring + st * kTileB + kk * 2048, kHalf), id_o, started[t] || kk > 0, lead);
+          }
+          ++np[t];
           started[t] = true;
           tc_commit_el(pv_done + 8 * t, lead);
         };
@@ -488,12 +573,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + t * kBlk, to = tmem + lanes + 256 + t * 128;
     const float sc = g.a.scale * 1.4426950408889634f;
+    const int tok = r / G;
+    int tks[4];         // tokens of the rows that this lane writes out
+#pragma unroll
+    for (int k = 0; k < 4; ++k) tks[k] = ((warp & 3) * 32 + k * 8 + (lane >> 2)) / G;
+    const uint32_t sout = ring + NST * kTileB + warp * 32 * kOutPitch;
     uint32_t nsc = 0;   // score blocks of this tile so far
     int bad_at = 0;
     for (; more; next_seg()) {
       int tf, tl;
       tile_tokens(t, tf, tl);
-      const int tok = r / G, pos = tok < tq && tf + tok <= tl && x.slot >= 0 ? tf + tok : -1;
+      const int pos = tok < tq && tf + tok <= tl && x.slot >= 0 ? tf + tok : -1;
       float m = -INFINITY, l = 0.f;
       bool any = false;     // the accumulator holds a product of this segment
       for (int u = u0; u < u1; ++u) {
@@ -507,22 +597,34 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         const uint32_t bad = *(volatile uint32_t*)&s_bad[bad_at];
         bad_at = (bad_at + 1) % kBadRing;
         uint32_t s[kBlk];
-#pragma unroll
-        for (int i = 0; i < kBlk / 32; ++i) tc_ld32(ts + 32 * i, s + 32 * i);
+        float mx[4];
+        tc_ld32(ts, s);
+        tc_ld32(ts + 32, s + 32);
         tc_ld_wait();
-        if (bad || tf < 0 || j0 + kBlk - 1 > tf || !(W == 0 || j0 > tl - W || j0 + kBlk <= S)) {
+        tc_ld32(ts + 64, s + 64);
+        tc_ld32(ts + 96, s + 96);
+        const bool edge = bad || tf < 0 || j0 + kBlk - 1 > tf || !(W == 0 || j0 > tl - W || j0 + kBlk <= S);
+        uint32_t vis[4];
+        if (edge) {  // bit i: the row sees key i of the block
           const int last = pos - j0, low = W > 0 ? pos - W - j0 : -1, keep = W > 0 ? S - j0 : 0;
 #pragma unroll
-          for (int i = 0; i < kBlk; ++i) {
-            const bool see = i <= last && (i > low || i < keep) && !(bad >> (i >> g.logP) & 1);
-            if (!see) s[i] = 0xff800000u;  // -inf
-          }
+          for (int w = 0; w < 4; ++w)
+            vis[w] = below(last + 1 - 32 * w) & (~below(low + 1 - 32 * w) | below(keep - 32 * w));
+          if (bad)
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+              for (int i = 0; i < 32; i += 8)
+                if (bad >> ((32 * w + i) >> g.logP) & 1) vis[w] &= ~(0xffu << i);
+          cut<0>(s, vis);
         }
-        float mx[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
 #pragma unroll
-        for (int i = 4; i < kBlk; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
+        for (int i = 4; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
+        tc_ld_wait();
+        if (edge) cut<64>(s, vis);
+#pragma unroll
+        for (int i = 64; i < kBlk; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
         const bool raise = top > m + 8.f || (m == -INFINITY && top > m);
         if (__any_sync(0xffffffffu, raise)) {
@@ -545,25 +647,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           }
         }
         const float z = m == -INFINITY ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const float2 sc2 = make_float2(sc, sc), z2 = make_float2(-z, -z);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < kBlk / 64; ++c) {
           uint32_t pk[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const float a0 = ex2(fmaf(__uint_as_float(s[64 * c + 2 * i]), sc, -z));
-            const float a1 = ex2(fmaf(__uint_as_float(s[64 * c + 2 * i + 1]), sc, -z));
-            sum[(2 * i) & 3] += a0;
-            sum[(2 * i + 1) & 3] += a1;
-            pk[i] = pack2<F16>(a0, a1);
+            float2 e = fma2(make_float2(__uint_as_float(s[64 * c + 2 * i]), __uint_as_float(s[64 * c + 2 * i + 1])), sc2, z2);
+            e.x = ex2(e.x);
+            e.y = ex2(e.y);
+            sum[i & 1] = add2(sum[i & 1], e);
+            pk[i] = pack2<F16>(e.x, e.y);
           }
           tc_st32(ts + 32 * c, pk);
+          tc_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full + 16 * t + 8 * c);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tc_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + 8 * t);
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         ++nsc;
         any = true;
       }
@@ -574,10 +677,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         tc_fence_after();
       }
       if (whole) {
-        const bool real = tok < tq && tf + tok <= tl;
-        const int row = x.row0 + (x.qb * 2 + t) * tq + tok, hq = x.hk * G + r - tok * G;
+        // 32 columns at a time through the warp's own buffer: a thread holds a
+        // row, four lanes write 64 bytes of a row
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        uint16_t* po = g.a.o + ((long long)row * g.a.Hq + hq) * D;
+        const int nt = min(tq, tl - tf + 1);  // tokens of the tile
+        uint16_t* po[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int rr = (warp & 3) * 32 + k * 8 + (lane >> 2), tk = tks[k];
+          po[k] = tk < nt ? g.a.o + (((long long)x.row0 + (x.qb * 2 + t) * tq + tk) * g.a.Hq + x.hk * G + rr - tk * G) * D +
+                                (lane & 3) * 8
+                          : nullptr;
+        }
 #pragma unroll 1
         for (int i = 0; i < D; i += 32) {
           uint32_t o[32];
@@ -585,20 +696,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             tc_ld32(to + i, o);
             tc_ld_wait();
           }
-          if (real) {
+          const bool none = !any || l == 0.f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t w[4];
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                w[k] = l == 0.f ? 0u
-                                : pack2<F16>(__uint_as_float(o[8 * e + 2 * k]) * inv, __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
-              *reinterpret_cast<uint4*>(po + i + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            for (int k = 0; k < 4; ++k)
+              w[k] = none ? 0u : pack2<F16>(__uint_as_float(o[8 * e + 2 * k]) * inv, __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
+            st_s128(sout + lane * kOutPitch + e * 16, w[0], w[1], w[2], w[3]);
           }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (po[k])
+              *reinterpret_cast<uint4*>(po[k] + i) = ld_s128(sout + (k * 8 + (lane >> 2)) * kOutPitch + (lane & 3) * 16);
+          __syncwarp();
         }
-        if (real && g.a.lse)
-          g.a.lse[(long long)row * g.a.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        if (g.a.lse && tok < nt)
+          g.a.lse[((long long)x.row0 + (x.qb * 2 + t) * tq + tok) * g.a.Hq + x.hk * G + r - tok * G] =
+              l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
       } else {
         // a part of the unit: place 2 i + 1 if it holds the unit's first block, else 2 i
         const int slot = 2 * blockIdx.x + (u0 == 0 ? 1 : 0);
@@ -633,50 +749,29 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
 }
 
 // Units that lie in several CTAs: their parts folded in the order of the keys.
-// Block (i, y): the unit with CTA i's first position strictly inside it, if i
-// is the unit's second CTA; 32 of its 256 rows, four threads per row.
+// Block (i, y): the unit recorded at CTA i's place; 32 of its 256 rows, four
+// threads per row.
 template <bool F16, int D>
-__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ ChunkArgs g, int grid) {
-  __shared__ Plan s_plan;
-  __shared__ Unit s_unit;
-  __shared__ long long s_start;
-  const int tid = threadIdx.x;
+__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ ChunkArgs g) {
   griddep_wait();
-  make_plan(s_plan, g, nullptr);
-  const Plan& p = s_plan;
-  const int nc = min(p.nc, grid), i = blockIdx.x + 1;
-  if (p.total == 0 || i >= nc) return;
-  const long long at = lo_of(p, nc, i);
-  if (tid < 32) {
-    long long start;
-    const Unit u = find_unit(p, g, at, &start);
-    if (tid == 0) {
-      s_unit = u;
-      s_start = start;
-    }
-  }
-  __syncthreads();
-  const Unit x = s_unit;
-  if (s_start == at) return;
-  const int c0 = cta_of(p, nc, s_start), c1 = cta_of(p, nc, s_start + x.nb - 1);
-  if (c0 + 1 != i) return;
-  const int row = blockIdx.y * 32 + (tid >> 2), t = row >> 7, r = row & 127, q = tid & 3;
-  const int tok = r / g.a.G, local = x.qb * 2 * g.tq + t * g.tq + tok;
-  if (tok >= g.tq || local >= x.n) return;
-  auto ml = [&](int c, int k) { return __ldcg(g.pml + ((2 * c + (c == c0 ? 1 : 0)) * 2 + t) * 256 + k * 128 + r); };
+  const Split sp = g.split[blockIdx.x + 1];
+  if (sp.c0 < 0) return;
+  const int row = blockIdx.y * 32 + (threadIdx.x >> 2), t = row >> 7, r = row & 127, q = threadIdx.x & 3;
+  const int tok = r / g.a.G, local = t * g.tq + tok;
+  if (tok >= g.tq || local >= sp.rows) return;
+  auto ml = [&](int c, int k) { return __ldcg(g.pml + ((2 * c + (c == sp.c0 ? 1 : 0)) * 2 + t) * 256 + k * 128 + r); };
   float m = -INFINITY;
-  for (int c = c0; c <= c1; ++c)
-    if (ml(c, 1) != 0.f) m = fmaxf(m, ml(c, 0));
+  for (int c = sp.c0; c <= sp.c1; ++c) m = fmaxf(m, ml(c, 0));
   const float z = m == -INFINITY ? 0.f : m;
   float l = 0.f, o[D / 4];
 #pragma unroll
   for (int k = 0; k < D / 4; ++k) o[k] = 0.f;
-  for (int c = c0; c <= c1; ++c) {
+  for (int c = sp.c0; c <= sp.c1; ++c) {
     const float lc = ml(c, 1);
-    if (lc == 0.f) continue;  // this part's rows saw nothing (no accumulator was written)
+    if (lc == 0.f) continue;  // the row saw nothing here (its accumulator may not have been written)
     const float f = ex2(ml(c, 0) - z);
     l = fmaf(lc, f, l);
-    const float* pp = g.part + (long long)((2 * c + (c == c0 ? 1 : 0)) * 2 + t) * D * 128 + r * 4;
+    const float* pp = g.part + (long long)((2 * c + (c == sp.c0 ? 1 : 0)) * 2 + t) * D * 128 + r * 4;
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
       const float4 v = __ldcg(reinterpret_cast<const float4*>(pp + (long long)(q * (D / 16) + k) * 512));
@@ -687,7 +782,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Ch
     }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  const long long at_row = (long long)(x.row0 + local) * g.a.Hq + x.hk * g.a.G + r - tok * g.a.G;
+  const long long at_row = (long long)(sp.row0 + local) * g.a.Hq + sp.hk * g.a.G + r - tok * g.a.G;
   uint16_t* po = g.a.o + at_row * D + q * (D / 4);
 #pragma unroll
   for (int k = 0; k < D / 32; ++k)
@@ -735,7 +830,7 @@ cudaError_t launch_one(ChunkArgs& g, int grid, int dev, cudaStream_t st) {
   cfg.blockDim = dim3(128);
   cfg.dynamicSmemBytes = 0;
   launch_begin(K_ATTN_COMBINE, st);
-  e = cudaLaunchKernelEx(&cfg, combine_kernel<F16, D>, g, grid);
+  e = cudaLaunchKernelEx(&cfg, combine_kernel<F16, D>, g);
   launch_end(st);
   return e;
 }
@@ -752,12 +847,18 @@ int chunk_grid(int* dev) {
 
 }  // namespace
 
-bool chunk_supported(int D, int page, int G, float scale) {
+bool chunk_supported(int D, int page, int Hkv, int G, int B, int n_rows, int max_pages, float scale) {
+  if (G < 1 || G > 128) return false;
+  // the list of all units' blocks counts in int32
+  const long long units = (n_rows / (2 * (128 / G)) + (long long)B) * Hkv, blocks = (long long)max_pages * page / kBlk + 2;
+  if (units * blocks >= (1LL << 31)) return false;
   // a scale above zero: the largest product is then the largest score
-  return (D == 64 || D == 128) && page >= 8 && (page & (page - 1)) == 0 && G <= 128 && scale > 0.f && encode_fn();
+  return (D == 64 || D == 128) && page >= 8 && (page & (page - 1)) == 0 && scale > 0.f && encode_fn();
 }
 
-size_t chunk_ws_bytes(int D) { return (size_t)2 * kMaxGrid * 2 * 128 * (D + 2) * 4; }
+size_t chunk_ws_bytes(int D) {
+  return align256((size_t)2 * kMaxGrid * 2 * 128 * (D + 2) * 4 + kMaxGrid * sizeof(Split));
+}
 
 cudaError_t launch_attn_chunk(const Cache& c, const Rows& r, const Attn& a, bool f16, int32_t* status, void* scratch,
                               cudaStream_t st) {
@@ -774,6 +875,7 @@ cudaError_t launch_attn_chunk(const Cache& c, const Rows& r, const Attn& a, bool
   g.logP = g.logpage < 7 ? g.logpage : 7;
   g.part = static_cast<float*>(scratch);
   g.pml = g.part + (size_t)2 * kMaxGrid * 2 * 128 * c.D;
+  g.split = reinterpret_cast<Split*>(g.pml + (size_t)2 * kMaxGrid * 2 * 256);
   g.status = status;
   if (!pool_maps_2d(c, &g.tm_k, &g.tm_v, 1 << g.logP) || !query_map(a, c.D, r.n_rows, g.tq, &g.tm_q))
     return cudaErrorInvalidValue;

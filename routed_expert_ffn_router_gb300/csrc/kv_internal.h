@@ -85,7 +85,7 @@ cudaError_t launch_attn_decode(const Cache& c, const Rows& r, const Attn& a, boo
 // The tensor-core prompt-chunk kernels (kv_chunk.cu): D 64 or 128, pages of a
 // power of two of at least 8 tokens, up to 128 query heads per KV head, a scale
 // above zero.
-bool chunk_supported(int D, int page, int G, float scale);
+bool chunk_supported(int D, int page, int Hkv, int G, int B, int n_rows, int max_pages, float scale);
 size_t chunk_ws_bytes(int D);
 cudaError_t launch_attn_chunk(const Cache& c, const Rows& r, const Attn& a, bool f16, int32_t* status, void* scratch,
                               cudaStream_t st);
