@@ -15,7 +15,7 @@
 // which combine_kernel joins in the order of the keys.
 //
 // Warps. 0-3 and 4-7: the softmax of tile 0 and of tile 1 (a thread is a row);
-// 8: issues the products; 9: TMA of Q, K and V; 10: zeroes the value rows that
+// 8: issues the products; 9: TMA of Q, K and V; 10, 11: zero the value rows that
 // no row sees (whatever lies there must not meet a zero probability). While a
 // softmax group works on its scores, the tensor cores run the other tile's
 // products:  S0 S1 | PV0 S0' | PV1 S1' | PV0' ...
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     for (int i = 0; i < NST; ++i) {
       mbar_init(kv_full + 8 * i, 1);
       mbar_init(kv_empty + 8 * i, 1);
-      mbar_init(v_ready + 8 * i, 1);
+      mbar_init(v_ready + 8 * i, 2);
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
   };
   bool dead = false;  // an expired wait: go on without waiting (the status word says so)
   auto wait = [&](uint32_t bar, uint32_t parity) {
-    if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait_short(bar, parity, g.status));
+    if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait_sleep(bar, parity, g.status));
   };
 
   if (warp >= 8) {
@@ -430,6 +430,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           }
           __syncwarp();
         };
+        const bool opening = qph == 1 && st == 0 && ph == 1;  // the CTA's first segment: the queries first
+        if (opening) queries();
         int row = entry(u0);
         for (int u = u0; u < u1 && !dead; ++u) {
           const int ahead = u + 1 < u1 ? entry(u + 1) : -1;
@@ -451,26 +453,28 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
               st = 0;
               ph ^= 1;
             }
-            if (u == u0 && kv == 0) queries();  // after the first keys: they need not wait for the last segment's products
+            // later ones after the first keys, which need not wait for the last segment's products
+            if (u == u0 && kv == 0 && !opening) queries();
           }
           bad_at = (bad_at + 1) % kBadRing;
           row = ahead;
         }
       }
-    } else if (warp == 10) {
+    } else if (warp >= 10) {
       // ================= values that no row sees become zeros =================
-      int st = 1, ph = 0, bad_at = 0;
+      int st = 1, ph = 0, bad_at = 0;  // the two warps take the even and the odd rows
       for (; more; next_seg()) {
         for (int u = u0; u < u1; ++u) {
           const int j0 = x.block(u) * kBlk;
           wait(kv_full + 8 * st, ph);
           const uint32_t bad = *(volatile uint32_t*)&s_bad[bad_at];
           if (bad || j0 + kBlk - 1 > x.pl || (j0 < x.from && j0 + kBlk > x.first)) {
-            for (int r = lane; r < kBlk; r += 32) {
+            for (int r = warp - 10 + 2 * (lane >> 3); r < kBlk; r += 8) {  // eight lanes a row of 128 bytes
               const int j = j0 + r;
               if (j > x.pl || (j < x.from && j >= x.first) || (bad >> (r >> g.logP) & 1))
-                for (int i = 0; i < D / 8; ++i)
-                  st_s128(ring + st * kTileB + (i >> 3) * kHalf + r * 128 + (i & 7) * 16, 0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int h = 0; h < NH; ++h)
+                  st_s128(ring + st * kTileB + h * kHalf + r * 128 + (lane & 7) * 16, 0u, 0u, 0u, 0u);
             }
             fence_proxy_async_shared();
           }
