@@ -15,10 +15,12 @@
 // which combine_kernel joins in the order of the keys.
 //
 // Warps. 0-3 and 4-7: the softmax of tile 0 and of tile 1 (a thread is a row);
-// 8: issues the products; 9: TMA of Q, K and V; 10, 11: zero the value rows that
-// no row sees (whatever lies there must not meet a zero probability). While a
-// softmax group works on its scores, the tensor cores run the other tile's
-// products:  S0 S1 | PV0 S0' | PV1 S1' | PV0' ...
+// 8: issues the products; 9: TMA of Q, K and V; 10: zeroes the value rows that
+// no row sees (whatever lies there must not meet a zero probability); 11:
+// divides the list and hands out this CTA's segments (a unit, a range of its
+// blocks) through a small ring, ahead of the others. While a softmax group
+// works on its scores, the tensor cores run the other tile's products:
+//   S0 S1 | PV0 S0' | PV1 S1' | PV0' ...
 //
 // The running maximum is only raised when a row's scores pass it by more than
 // 2^8 (probabilities up to 256 lose nothing in bf16 or fp16, whose relative
@@ -45,11 +47,13 @@ namespace {
 constexpr int kBlk = 128;               // keys per block
 constexpr int kChunkThreads = 384;
 constexpr int kLaunchRegs = 168;        // registers per thread at launch; the groups share 3 x 168
-constexpr int kSoftRegs = 208, kRestRegs = 88;
+constexpr int kSoftRegs = 224, kRestRegs = 56;
 constexpr int kChunkSeqs = 256;         // sequences per launch
 constexpr int kMaxGrid = 304;
 constexpr int kUnitCost = 2;            // a unit's start and end, in blocks, for the division among the CTAs
 constexpr int kBadRing = 8;
+constexpr int kSegRing = 4;
+constexpr int kSegReaders = 11;         // warps 0 .. 10
 constexpr int kOutPitch = 80;           // bytes per row of a warp's output buffer (64 and a pad)
 
 // A unit that lies in CTAs c0 .. c1, kept at CTA c0 + 1's place (else c0 = -1).
@@ -76,34 +80,25 @@ struct ChunkArgs {
 // The two tiles of a unit and the blocks they see.
 struct Unit {
   int b, qb, hk;
-  int slot, len, n, row0;
-  int pf, pl;              // tokens of the first and the last row (pl < 0: nothing is seen)
+  int slot, row0, nt;      // first row (token) of the call and tokens
+  int pf, pl;              // positions of the first and the last token; pl = -1 if nothing is seen
   int from, first;         // the window's first token; first tokens below it that stay visible
   int ns, wt, nb;          // blocks of first tokens, first window block, blocks
+  int u0, u1;              // this CTA's blocks of it
+  int more;                // 0: no unit, the end of the list
   __device__ int block(int u) const { return u < ns ? u : u - ns + wt; }
-};
-
-__device__ __forceinline__ void unit_blocks(Unit& x, int tq, int W, int S) {
-  const int i0 = x.qb * 2 * tq;
-  x.pf = x.len - x.n + i0;
-  x.pl = x.slot < 0 ? -1 : x.len - x.n + min(x.n, i0 + 2 * tq) - 1;
-  x.from = x.first = x.ns = x.wt = x.nb = 0;
-  if (x.pl >= 0) {
-    x.from = W > 0 ? max(0, max(0, x.pf) - W + 1) : 0;
-    x.first = min(S, x.from);
-    x.ns = (x.first + kBlk - 1) / kBlk;
-    x.wt = max(x.from / kBlk, x.ns);
-    x.nb = x.ns + x.pl / kBlk - x.wt + 1;
+  // tokens' positions of tile t: [tf, tl], tl < tf if it has none
+  __device__ void tile(int t, int tq, int& tf, int& tl) const {
+    tf = pf + t * tq;
+    tl = pf + min(nt, (t + 1) * tq) - 1;
   }
-}
+};
 
 // The sequences of a launch and the division of their blocks, in shared memory.
 struct Plan {
   int off[kChunkSeqs + 1];         // list positions before each sequence
-  int nq[kChunkSeqs];              // pairs of tiles
+  int nq[kChunkSeqs];              // units of one KV head
   int slot[kChunkSeqs], len[kChunkSeqs], n[kChunkSeqs], row0[kChunkSeqs];
-  int total;
-  int nc;                          // CTAs that share the list
 };
 
 // A unit's positions in the list, and the block at which a CTA boundary that
@@ -119,99 +114,159 @@ __device__ __forceinline__ int cut_at(int nb, int at) {
 
 __device__ __forceinline__ Unit unit_at(const Plan& p, const ChunkArgs& g, int b, int qb, int hk) {
   Unit x;
+  const int W = g.a.window, i0 = qb * 2 * g.tq;
   x.b = b; x.qb = qb; x.hk = hk;
-  x.slot = p.slot[b]; x.len = p.len[b]; x.n = p.n[b]; x.row0 = p.row0[b];
-  unit_blocks(x, g.tq, g.a.window, g.a.n_sink);
+  x.slot = p.slot[b];
+  x.row0 = p.row0[b] + i0;
+  x.nt = min(p.n[b] - i0, 2 * g.tq);
+  x.pf = p.len[b] - p.n[b] + i0;
+  x.pl = x.slot < 0 ? -1 : x.pf + x.nt - 1;
+  x.from = x.first = x.ns = x.wt = x.nb = 0;
+  if (x.pl >= 0) {
+    x.from = W > 0 ? max(0, max(0, x.pf) - W + 1) : 0;
+    x.first = min(g.a.n_sink, x.from);
+    x.ns = (x.first + kBlk - 1) / kBlk;
+    x.wt = max(x.from / kBlk, x.ns);
+    x.nb = x.ns + x.pl / kBlk - x.wt + 1;
+  }
   return x;
 }
 
-// All threads of the CTA; ends with a barrier.
-__device__ void make_plan(Plan& p, const ChunkArgs& g, int grid, int32_t* status) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nw = blockDim.x >> 5;
-  for (int b = tid; b < g.nseq; b += blockDim.x) {
-    const Seq s = load_seq(g.c, g.r, g.b0 + b, status);
-    p.slot[b] = s.slot; p.len[b] = s.len; p.n[b] = s.n; p.row0[b] = s.row0;
-    p.nq[b] = (s.n + 2 * g.tq - 1) / (2 * g.tq);
+// CTA i's part of `total` positions among nc CTAs starts at lo(i); cta(at) is
+// the last i with lo(i) <= at.
+struct Division {
+  int q, r;
+  __device__ Division(int total, int nc) : q(total / nc), r(total - total / nc * nc) {}
+  __device__ int lo(int i) const { return i * q + min(i, r); }
+  __device__ int cta(int at) const { return at < r * (q + 1) ? at / (q + 1) : r + (at - r * (q + 1)) / q; }
+};
+
+__device__ __forceinline__ int warp_scan(int v, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
   }
-  __syncthreads();
-  for (int b = warp; b < g.nseq; b += nw) {
+  return v;
+}
+
+// The whole of warp 11: the division, then this CTA's segments into the ring.
+__device__ __forceinline__ void schedule(Plan& p, const ChunkArgs& g, Unit* ring, uint32_t full, uint32_t empty) {
+  const int lane = threadIdx.x & 31, Hkv = g.c.Hkv;
+  // the sequences, and the list positions of the units of each
+  int total = 0, units = 0;
+  for (int b0 = 0; b0 < g.nseq; b0 += 32) {
+    const int b = b0 + lane;
+    int nq = 0;
+    if (b < g.nseq) {
+      const Seq s = load_seq(g.c, g.r, g.b0 + b, blockIdx.x == 0 ? g.status : nullptr);
+      nq = (s.n + 2 * g.tq - 1) / (2 * g.tq);
+      p.slot[b] = s.slot; p.len[b] = s.len; p.n[b] = s.n; p.row0[b] = s.row0; p.nq[b] = nq;
+    }
+    __syncwarp();
+    // a lane per sequence, or for few sequences a lane per unit
     int w = 0;
-    for (int q = lane; q < p.nq[b]; q += 32) w += weight(unit_at(p, g, b, q, 0).nb);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-    if (lane == 0) p.off[b + 1] = w * g.c.Hkv;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    int base = 0, units = 0;
-    for (int b0 = 0; b0 < g.nseq; b0 += 32) {
-      const int b = b0 + lane;
-      int x = b < g.nseq ? p.off[b + 1] : 0;
-      int u = b < g.nseq ? p.nq[b] * g.c.Hkv : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+    if (g.nseq >= 8) {
+      for (int q = 0; q < nq; ++q) w += weight(unit_at(p, g, b, q, 0).nb);
+    } else {
+      for (int k = 0; k < g.nseq; ++k) {
+        int part = 0;
+        for (int q = lane; q < p.nq[k]; q += 32) part += weight(unit_at(p, g, k, q, 0).nb);
+        part = __reduce_add_sync(0xffffffffu, part);
+        if (lane == k) w = part;
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-      __syncwarp();
-      if (b < g.nseq) p.off[b + 1] = base + x;
-      base += __shfl_sync(0xffffffffu, x, 31);
-      units += u;
     }
+    const int x = warp_scan(w * Hkv, lane);
+    if (b < g.nseq) p.off[b] = total + x - w * Hkv;
+    total += __shfl_sync(0xffffffffu, x, 31);
+    units += __reduce_add_sync(0xffffffffu, nq) * Hkv;
+  }
+  if (lane == 0) p.off[g.nseq] = total;
+  __syncwarp();
+  // a CTA per unit, or per four blocks where units are longer than that
+  const int nc = min(max((total + 3 + kUnitCost) / (4 + kUnitCost), units), (int)gridDim.x);
+  const bool work = (int)blockIdx.x < nc;
+  const Division dv(total, max(nc, 1));
+  const int lo = work ? dv.lo(blockIdx.x) : 0, hi = work ? dv.lo(blockIdx.x + 1) : 0;
+  Split sp;
+  sp.c0 = -1;
+  Unit x;
+  int start = 0;
+  if (lo < hi) {
+    // the unit that holds position lo
+    int b = 0, h = g.nseq - 1;  // the last sequence that starts at or before it
+    while (b < h) {
+      const int m = (b + h + 1) >> 1;
+      if (p.off[m] <= lo) b = m;
+      else h = m - 1;
+    }
+    start = p.off[b];
+    int qb = 0;
+    for (int q0 = 0;; q0 += 32) {
+      const int q = q0 + lane;
+      const int w = q < p.nq[b] ? weight(unit_at(p, g, b, q, 0).nb) * Hkv : 0;
+      const int s = warp_scan(w, lane);
+      const unsigned in = __ballot_sync(0xffffffffu, lo < start + s);
+      if (in || q0 + 32 >= p.nq[b]) {
+        const int src = in ? __ffs(in) - 1 : 31;
+        qb = q0 + src;
+        start += __shfl_sync(0xffffffffu, s - w, src);
+        break;
+      }
+      start += __shfl_sync(0xffffffffu, s, 31);
+    }
+    x = unit_at(p, g, b, qb, 0);
+    x.hk = (lo - start) / weight(x.nb);
+    start += x.hk * weight(x.nb);
+    const int cut = cut_at(x.nb, lo - start);
+    if (cut > 0 && cut < x.nb) {
+      // a split unit: the CTAs of its first and its last block
+      int c0 = dv.cta(start + kUnitCost), c1 = dv.cta(start + kUnitCost + x.nb - 1);
+      while (cut_at(x.nb, dv.lo(c0 + 1) - start) <= 0) ++c0;
+      while (cut_at(x.nb, dv.lo(c1) - start) >= x.nb) --c1;
+      sp.c0 = c0 + 1 == (int)blockIdx.x ? c0 : -1;
+      sp.c1 = c1;
+      sp.row0 = x.row0;
+      sp.rows = x.nt;
+      sp.hk = x.hk;
+    }
+  }
+  int i = 0, ph = 1;
+  auto put = [&](int more) {
+    if (!__all_sync(0xffffffffu, mbar_wait_sleep(empty + 8 * i, ph, g.status))) return false;
+    x.more = more;
     if (lane == 0) {
-      p.off[0] = 0;
-      p.total = base;
-      // a CTA per unit, or per four blocks where units are longer than that
-      p.nc = min(min(max((base + 3 + kUnitCost) / (4 + kUnitCost), units), kMaxGrid), grid);
+      ring[i] = x;
+      mbar_arrive(full + 8 * i);
+    }
+    __syncwarp();
+    if (++i == kSegRing) {
+      i = 0;
+      ph ^= 1;
+    }
+    return true;
+  };
+  bool ok = true;
+  while (ok && start < hi) {
+    const int a = cut_at(x.nb, lo - start), e = cut_at(x.nb, hi - start);
+    if (a < e) {  // this CTA has a part of it
+      x.u0 = min(a, x.nb);
+      x.u1 = min(e, x.nb);
+      ok = put(1);
+    }
+    start += weight(x.nb);
+    if (start >= hi) break;
+    if (++x.hk == Hkv) {
+      int b = x.b, qb = x.qb + 1;
+      while (qb >= p.nq[b]) {
+        ++b;
+        qb = 0;
+      }
+      x = unit_at(p, g, b, qb, 0);
     }
   }
-  __syncthreads();
-}
-
-// CTA i's part starts at lo_of(i); cta_of(at) is the last i with lo_of(i) <= at.
-__device__ __forceinline__ int lo_of(const Plan& p, int i) {
-  const int q = p.total / p.nc, r = p.total - q * p.nc;
-  return i * q + min(i, r);
-}
-__device__ __forceinline__ int cta_of(const Plan& p, int at) {
-  const int q = p.total / p.nc, r = p.total - q * p.nc;
-  return at < r * (q + 1) ? at / (q + 1) : r + (at - r * (q + 1)) / q;
-}
-
-// The unit that holds list position `at`, and its first position (one warp).
-__device__ Unit find_unit(const Plan& p, const ChunkArgs& g, int at, int* start) {
-  const int lane = threadIdx.x & 31;
-  int b = 0, h = g.nseq - 1;  // the last sequence that starts at or before `at`
-  while (b < h) {
-    const int m = (b + h + 1) >> 1;
-    if (p.off[m] <= at) b = m;
-    else h = m - 1;
-  }
-  int base = p.off[b];
-  const int nq = p.nq[b];
-  for (int q0 = 0;; q0 += 32) {
-    const int q = q0 + lane;
-    const int w = q < nq ? weight(unit_at(p, g, b, q, 0).nb) * g.c.Hkv : 0;
-    int x = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    const unsigned in = __ballot_sync(0xffffffffu, q < nq && at < base + x);
-    if (in || q0 + 32 >= nq) {
-      const int src = in ? __ffs(in) - 1 : 31;
-      const int before = __shfl_sync(0xffffffffu, base + x - w, src);
-      Unit u = unit_at(p, g, b, q0 + src, 0);
-      const int per = weight(u.nb);
-      u.hk = (at - before) / per;
-      *start = before + u.hk * per;
-      return u;
-    }
-    base += __shfl_sync(0xffffffffu, x, 31);
-  }
+  if (ok) put(0);
+  if (lane == 0) g.split[blockIdx.x] = sp;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -272,11 +327,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
   constexpr int NST = stages<D>();
   extern __shared__ __align__(1024) uint8_t smem_chunk[];
   __shared__ Plan s_plan;
-  __shared__ __align__(8) uint64_t s_bar[3 * NST + 13];
+  __shared__ __align__(8) uint64_t s_bar[3 * NST + 2 * kSegRing + 13];
   __shared__ uint32_t s_bad[kBadRing];
-  __shared__ Unit s_unit;
-  __shared__ int s_start;
+  __shared__ __align__(16) Unit s_seg[kSegRing];
   __shared__ uint32_t s_tmem;
+  __shared__ int s_tok[kBlk];      // token of each row of a tile
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int W = g.a.window, S = g.a.n_sink, G = g.a.G, tq = g.tq;
@@ -284,12 +339,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
   const uint32_t kv_full = smem_u32(s_bar), kv_empty = kv_full + 8 * NST, v_ready = kv_empty + 8 * NST;
   const uint32_t q_full = v_ready + 8 * NST, q_empty = q_full + 8;
   const uint32_t s_full = q_empty + 8, p_full = s_full + 16, pv_done = p_full + 32, o_free = pv_done + 16;
-  const uint32_t drained = o_free + 16;
+  const uint32_t drained = o_free + 16, seg_full = drained + 8, seg_empty = seg_full + 8 * kSegRing;
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
       mbar_init(kv_full + 8 * i, 1);
       mbar_init(kv_empty + 8 * i, 1);
-      mbar_init(v_ready + 8 * i, 2);
+      mbar_init(v_ready + 8 * i, 1);
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
@@ -301,8 +356,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       mbar_init(o_free + 8 * t, 4);
     }
     mbar_init(drained, 1);
+    for (int i = 0; i < kSegRing; ++i) {
+      mbar_init(seg_full + 8 * i, 1);
+      mbar_init(seg_empty + 8 * i, kSegReaders);
+    }
     fence_barrier_init();
   }
+  if (tid < kBlk) s_tok[tid] = tid / G;
   if (tid == 32 * 9) {
     prefetch_tensormap(&g.tm_q);
     prefetch_tensormap(&g.tm_k);
@@ -312,91 +372,33 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  griddep_wait();
-  make_plan(s_plan, g, gridDim.x, blockIdx.x == 0 ? g.status : nullptr);
-  const Plan& p = s_plan;
-  const bool work = p.total > 0 && (int)blockIdx.x < p.nc;
-  const int lo = work ? lo_of(p, blockIdx.x) : 0, hi = work ? lo_of(p, blockIdx.x + 1) : 0;
-  if (warp == 0) {
-    int start = 0;
-    Split sp;
-    sp.c0 = -1;
-    if (lo < hi) {
-      const Unit u = find_unit(p, g, lo, &start);
-      const int cut = cut_at(u.nb, lo - start);
-      if (cut > 0 && cut < u.nb) {
-        // the CTAs of its first and its last block
-        int c0 = cta_of(p, start + kUnitCost), c1 = cta_of(p, start + kUnitCost + u.nb - 1);
-        while (cut_at(u.nb, lo_of(p, c0 + 1) - start) <= 0) ++c0;
-        while (cut_at(u.nb, lo_of(p, c1) - start) >= u.nb) --c1;
-        sp.c0 = c0 + 1 == (int)blockIdx.x ? c0 : -1;
-        sp.c1 = c1;
-        sp.row0 = u.row0 + u.qb * 2 * tq;
-        sp.rows = min(2 * tq, u.n - u.qb * 2 * tq);
-        sp.hk = u.hk;
-      }
-      if (lane == 0) {
-        s_unit = u;
-        s_start = start;
-      }
-    }
-    if (lane == 0) g.split[blockIdx.x] = sp;
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  griddep_launch_dependents();
   const uint32_t tmem = s_tmem;
+  griddep_wait();  // an append's rows, and the workspace of the launch before
 
-  // the walk over this CTA's segments, the same in every role
-  Unit x;
-  int ustart = 0;
-  int u0 = 0, u1 = 0;            // the segment's blocks [u0, u1) of its unit
-  bool more = lo < hi;
-  if (more) {
-    x = s_unit;
-    ustart = s_start;
-  }
-  auto next_unit = [&] {
-    ustart += weight(x.nb);
-    if (ustart >= hi) {
-      more = false;
-      return;
-    }
-    if (++x.hk == g.c.Hkv) {
-      int b = x.b, qb = x.qb + 1;
-      while (qb >= p.nq[b]) {
-        ++b;
-        qb = 0;
-      }
-      x = unit_at(p, g, b, qb, 0);
-    }
-  };
-  auto settle = [&] {  // this CTA's blocks of the unit, or of the next one of which it has some
-    for (; more; next_unit()) {
-      const int a = cut_at(x.nb, lo - ustart), e = cut_at(x.nb, hi - ustart);
-      u0 = min(a, x.nb);
-      u1 = min(e, x.nb);
-      if (a < e) return;
-    }
-  };
-  auto next_seg = [&] {
-    next_unit();
-    settle();
-  };
-  settle();
-  // tokens of tile t: [tf, tl], tl < tf if it has none
-  auto tile_tokens = [&](int t, int& tf, int& tl) {
-    const int i0 = x.qb * 2 * tq + t * tq;
-    tf = x.len - x.n + i0;
-    tl = x.len - x.n + min(x.n, i0 + tq) - 1;
-  };
   auto takes = [&](int j0, int tf, int tl) {  // whether a tile sees anything of the block at token j0
     return tl >= tf && j0 <= tl && (W == 0 || j0 + kBlk - 1 > max(tf, 0) - W || j0 < S);
   };
   bool dead = false;  // an expired wait: go on without waiting (the status word says so)
   auto wait = [&](uint32_t bar, uint32_t parity) {
     if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait_sleep(bar, parity, g.status));
+  };
+  // this CTA's segments: next_seg() waits for one (false: there are no more),
+  // done_seg() gives its place back
+  int seg_i = 0, seg_ph = 0;
+  auto next_seg = [&] {
+    wait(seg_full + 8 * seg_i, seg_ph);
+    return !dead && s_seg[seg_i].more != 0;
+  };
+  auto done_seg = [&] {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(seg_empty + 8 * seg_i);
+    if (++seg_i == kSegRing) {
+      seg_i = 0;
+      seg_ph ^= 1;
+    }
   };
 
   if (warp >= 8) {
@@ -405,11 +407,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       // ================= TMA producer =================
       const int P = 1 << g.logP, nbox = kBlk >> g.logP;
       int st = 0, ph = 1, bad_at = 0, qph = 1;
-      for (; more && !dead; next_seg()) {
-        if (u0 == u1) continue;
-        int tf, tl;
-        tile_tokens(1, tf, tl);
-        const int nt = tl >= tf ? 2 : 1;
+      bool opening = true;
+      while (next_seg()) {
+        const Unit x = s_seg[seg_i];
+        done_seg();
+        if (x.u0 == x.u1) continue;
+        const int nt = x.nt > tq ? 2 : 1;
         const int32_t* tab = g.c.table + (long long)x.slot * g.c.max_pages;
         auto entry = [&](int u) {  // lane's box of block u: its first row in the pool, -1 not needed, -2 bad
           const int j = x.block(u) * kBlk + lane * P;
@@ -426,15 +429,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             mbar_expect_tx(q_full, (uint32_t)(nt * NH * tq * G * 128));
             for (int t = 0; t < nt; ++t)
               for (int h = 0; h < NH; ++h)
-                tma_load_3d(sq + t * kTileB + h * kHalf, &g.tm_q, h * 64, x.hk * G, x.row0 + (x.qb * 2 + t) * tq, q_full);
+                tma_load_3d(sq + t * kTileB + h * kHalf, &g.tm_q, h * 64, x.hk * G, x.row0 + t * tq, q_full);
           }
           __syncwarp();
         };
-        const bool opening = qph == 1 && st == 0 && ph == 1;  // the CTA's first segment: the queries first
-        if (opening) queries();
-        int row = entry(u0);
-        for (int u = u0; u < u1 && !dead; ++u) {
-          const int ahead = u + 1 < u1 ? entry(u + 1) : -1;
+        if (opening) queries();  // the CTA's first segment: the queries first
+        int row = entry(x.u0);
+        for (int u = x.u0; u < x.u1 && !dead; ++u) {
+          const int ahead = u + 1 < x.u1 ? entry(u + 1) : -1;
           const unsigned load = __ballot_sync(0xffffffffu, row >= 0), bad = __ballot_sync(0xffffffffu, row == -2);
           for (int kv = 0; kv < 2; ++kv) {
             wait(kv_empty + 8 * st, ph);
@@ -454,22 +456,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
               ph ^= 1;
             }
             // later ones after the first keys, which need not wait for the last segment's products
-            if (u == u0 && kv == 0 && !opening) queries();
+            if (u == x.u0 && kv == 0 && !opening) queries();
           }
           bad_at = (bad_at + 1) % kBadRing;
           row = ahead;
         }
+        opening = false;
       }
-    } else if (warp >= 10) {
+    } else if (warp == 10) {
       // ================= values that no row sees become zeros =================
-      int st = 1, ph = 0, bad_at = 0;  // the two warps take the even and the odd rows
-      for (; more; next_seg()) {
-        for (int u = u0; u < u1; ++u) {
+      int st = 1, ph = 0, bad_at = 0;
+      while (next_seg()) {
+        const Unit x = s_seg[seg_i];
+        done_seg();
+        for (int u = x.u0; u < x.u1; ++u) {
           const int j0 = x.block(u) * kBlk;
           wait(kv_full + 8 * st, ph);
           const uint32_t bad = *(volatile uint32_t*)&s_bad[bad_at];
           if (bad || j0 + kBlk - 1 > x.pl || (j0 < x.from && j0 + kBlk > x.first)) {
-            for (int r = warp - 10 + 2 * (lane >> 3); r < kBlk; r += 8) {  // eight lanes a row of 128 bytes
+            for (int r = lane >> 3; r < kBlk; r += 4) {  // eight lanes a row of 128 bytes
               const int j = j0 + r;
               if (j > x.pl || (j < x.from && j >= x.first) || (bad >> (r >> g.logP) & 1))
 #pragma unroll
@@ -492,61 +497,67 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       // ================= tensor-core products =================
       const uint32_t lead = elect_lane();
       const uint32_t id_s = idesc_16(F16, 128, kBlk, false), id_o = idesc_16(F16, 128, D, true);
+      // descriptors of the first tiles; the others differ by their address / 16
+      // in the low field (no carry: shared addresses < 256 KB)
+      const uint64_t qd0 = sdesc_sw128(sq), kd0 = sdesc_sw128(ring), vd0 = sdesc_sw128_n(ring, kHalf);
       int kst = 0, kph = 0;        // ring slot and phase of the next K block (its V block is the slot after)
-      uint32_t np[2] = {0, 0};     // PV products of each tile so far
-      uint32_t nseg[2] = {0, 0};   // segments in which each tile had blocks so far
+      uint32_t np = 0, nseg = 3;   // bit t: parity of tile t's products so far; of its segments (for o_free)
       int nq = 0;
-      for (; more; next_seg()) {
-        if (u0 == u1) continue;
+      while (next_seg()) {
+        const Unit x = s_seg[seg_i];
+        done_seg();
+        if (x.u0 == x.u1) continue;
         int tf[2], tl[2];
-        tile_tokens(0, tf[0], tl[0]);
-        tile_tokens(1, tf[1], tl[1]);
-        bool started[2] = {false, false};
+        x.tile(0, tq, tf[0], tl[0]);
+        x.tile(1, tq, tf[1], tl[1]);
         wait(q_full, nq & 1);
         ++nq;
         tc_fence_after();
+        bool started[2] = {false, false};
         auto score = [&](int t, int st) {
+          const uint64_t qd = qd0 + (uint32_t)(t * kTileB >> 4), kd = kd0 + (uint32_t)(st * kTileB >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 32;
-            tc_mma_el(tmem + t * kBlk, sdesc_sw128(sq + t * kTileB + o), sdesc_sw128(ring + st * kTileB + o), id_s,
-                      kk > 0, lead);
+            const uint32_t o = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+            tc_mma_el(tmem + t * kBlk, qd + o, kd + o, id_s, kk > 0, lead);
           }
           tc_commit_el(s_full + 8 * t, lead);
         };
         auto product = [&](int t, int st) {
           if (!started[t]) {  // the tile's accumulator has been read by the segment before
-            wait(o_free + 8 * t, (nseg[t] & 1) ^ 1);
-            ++nseg[t];
+            wait(o_free + 8 * t, nseg >> t & 1);
+            nseg ^= 1u << t;
           }
+          const uint64_t vd = vd0 + (uint32_t)(st * kTileB >> 4);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {  // the block's first 64 keys, while the others' probabilities are made
-            wait(p_full + 16 * t + 8 * h, np[t] & 1);
+            wait(p_full + 16 * t + 8 * h, np >> t & 1);
             tc_fence_after();
 #pragma unroll
             for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-              tc_mma_ts_el(tmem + 256 + t * 128, tmem + t * kBlk + kk * 8,
-                           sdesc_sw128_n(ring + st * kTileB + kk * 2048, kHalf), id_o, started[t] || kk > 0, lead);
+              tc_mma_ts_el(tmem + 256 + t * 128, tmem + t * kBlk + kk * 8, vd + kk * (2048 >> 4), id_o,
+                           started[t] || kk > 0, lead);
           }
-          ++np[t];
+          np ^= 1u << t;
           started[t] = true;
           tc_commit_el(pv_done + 8 * t, lead);
         };
-        int j0 = x.block(u0) * kBlk;
+        int j0 = x.block(x.u0) * kBlk;
         bool t0 = takes(j0, tf[0], tl[0]), t1 = takes(j0, tf[1], tl[1]);
         wait(kv_full + 8 * kst, kph);
         tc_fence_after();
         if (t0) score(0, kst);
         if (t1) score(1, kst);
         tc_commit_el(kv_empty + 8 * kst, lead);
-        for (int u = u0; u < u1; ++u) {
+        if (x.u0 + 1 == x.u1) tc_commit_el(q_empty, lead);
+        for (int u = x.u0; u < x.u1; ++u) {
           const int vst = kst + 1, vph = kph;
           kst += 2;
           if (kst == NST) {
             kst = 0;
             kph ^= 1;
           }
-          const bool nx = u + 1 < u1;
+          const bool nx = u + 1 < x.u1;
           const int jn = nx ? x.block(u + 1) * kBlk : 0;
           const bool n0 = nx && takes(jn, tf[0], tl[0]), n1 = nx && takes(jn, tf[1], tl[1]);
           wait(v_ready + 8 * vst, vph);
@@ -560,15 +571,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           if (t1) product(1, vst);
           tc_commit_el(kv_empty + 8 * vst, lead);
           if (n1) score(1, kst);
-          if (nx) tc_commit_el(kv_empty + 8 * kst, lead);
+          if (nx) {
+            tc_commit_el(kv_empty + 8 * kst, lead);
+            if (u + 2 == x.u1) tc_commit_el(q_empty, lead);  // the segment's last product with Q
+          }
           t0 = n0;
           t1 = n1;
         }
-        tc_commit_el(q_empty, lead);
       }
       // every product has ended before tensor memory is given back
       tc_commit_el(drained, lead);
       mbar_wait_short(drained, 0, g.status);
+    }
+    else {
+      // ================= the division and this CTA's segments =================
+      schedule(s_plan, g, s_seg, seg_full, seg_empty);
     }
   } else {
     // ================= softmax (a thread is a row of its tile) =================
@@ -577,21 +594,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + t * kBlk, to = tmem + lanes + 256 + t * 128;
     const float sc = g.a.scale * 1.4426950408889634f;
-    const int tok = r / G;
-    int tks[4];         // tokens of the rows that this lane writes out
-#pragma unroll
-    for (int k = 0; k < 4; ++k) tks[k] = ((warp & 3) * 32 + k * 8 + (lane >> 2)) / G;
     const uint32_t sout = ring + NST * kTileB + warp * 32 * kOutPitch;
     uint32_t nsc = 0;   // score blocks of this tile so far
     int bad_at = 0;
-    for (; more; next_seg()) {
+    while (next_seg()) {
+      const Unit& x = s_seg[seg_i];  // read again at the segment's end: few registers are left in the loop
       int tf, tl;
-      tile_tokens(t, tf, tl);
+      x.tile(t, tq, tf, tl);
+      const int tok = s_tok[r];
       const int pos = tok < tq && tf + tok <= tl && x.slot >= 0 ? tf + tok : -1;
       float m = -INFINITY, l = 0.f;
       bool any = false;     // the accumulator holds a product of this segment
-      for (int u = u0; u < u1; ++u) {
-        const int j0 = x.block(u) * kBlk;
+      const int ns = x.ns, wt = x.wt, u1 = x.u1;
+      for (int u = x.u0; u < u1; ++u) {
+        const int j0 = (u < ns ? u : u - ns + wt) * kBlk;
         if (!takes(j0, tf, tl)) {
           bad_at = (bad_at + 1) % kBadRing;
           continue;
@@ -675,7 +691,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         any = true;
       }
       // ---- the segment's end: the tile's rows out
-      const bool whole = u0 == 0 && u1 == x.nb;
+      const bool whole = x.u0 == 0 && x.u1 == x.nb;
       if (any) {
         wait(pv_done + 8 * t, (nsc & 1) ^ 1);
         tc_fence_after();
@@ -688,8 +704,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         uint16_t* po[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int rr = (warp & 3) * 32 + k * 8 + (lane >> 2), tk = tks[k];
-          po[k] = tk < nt ? g.a.o + (((long long)x.row0 + (x.qb * 2 + t) * tq + tk) * g.a.Hq + x.hk * G + rr - tk * G) * D +
+          const int rr = (warp & 3) * 32 + k * 8 + (lane >> 2), tk = s_tok[rr];
+          po[k] = tk < nt ? g.a.o + (((long long)x.row0 + t * tq + tk) * g.a.Hq + x.hk * G + rr - tk * G) * D +
                                 (lane & 3) * 8
                           : nullptr;
         }
@@ -717,11 +733,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           __syncwarp();
         }
         if (g.a.lse && tok < nt)
-          g.a.lse[((long long)x.row0 + (x.qb * 2 + t) * tq + tok) * g.a.Hq + x.hk * G + r - tok * G] =
+          g.a.lse[((long long)x.row0 + t * tq + tok) * g.a.Hq + x.hk * G + r - tok * G] =
               l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
       } else {
         // a part of the unit: place 2 i + 1 if it holds the unit's first block, else 2 i
-        const int slot = 2 * blockIdx.x + (u0 == 0 ? 1 : 0);
+        const int slot = 2 * blockIdx.x + (x.u0 == 0 ? 1 : 0);
         float* pm = g.pml + (slot * 2 + t) * 256;
         pm[r] = m;
         pm[128 + r] = l;
@@ -744,11 +760,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         __syncwarp();
         if (lane == 0) mbar_arrive(o_free + 8 * t);
       }
+      done_seg();
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  griddep_launch_dependents();
   if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
