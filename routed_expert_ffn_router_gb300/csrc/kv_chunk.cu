@@ -50,13 +50,15 @@ constexpr int kLaunchRegs = 168;        // registers per thread at launch; the g
 constexpr int kSoftRegs = 224, kRestRegs = 56;
 constexpr int kChunkSeqs = 256;         // sequences per launch
 constexpr int kMaxGrid = 304;
-constexpr int kUnitCost = 2;            // a unit's start and end, in blocks, for the division among the CTAs
+constexpr int kUnitCost = 3;            // a unit's start and end, in blocks, for the division among the CTAs
+constexpr int kSnap = 2;                // a piece of so many blocks or fewer is not cut off
 constexpr int kBadRing = 8;
+constexpr int kJoinMost = 6;            // parts that a unit's last CTA joins; combine_kernel takes more
 constexpr int kSegRing = 4;
 constexpr int kSegReaders = 11;         // warps 0 .. 10
 constexpr int kOutPitch = 80;           // bytes per row of a warp's output buffer (64 and a pad)
 
-// A unit that lies in CTAs c0 .. c1, kept at CTA c0 + 1's place (else c0 = -1).
+// A unit for combine_kernel, in CTAs c0 .. c1, kept at CTA c0 + 1's place (else c0 = -1).
 struct Split {
   int c0, c1;
   int row0, rows;     // its first row (token) and how many
@@ -71,6 +73,8 @@ struct ChunkArgs {
   int b0, nseq;       // sequences of this launch
   int tq;             // tokens per tile
   int logP, logpage;  // rows of a TMA box: min(page, 128)
+  int combine;        // whether combine_kernel follows
+  int32_t* cnt;       // [grid][2 tiles][4 warps]: parts of the unit that starts in a CTA, zero between calls
   float* part;        // [2 grid][2 tiles][D / 4][128][4]
   float* pml;         // [2 grid][2 tiles][m, l][128]
   Split* split;       // [grid]
@@ -85,6 +89,7 @@ struct Unit {
   int from, first;         // the window's first token; first tokens below it that stay visible
   int ns, wt, nb;          // blocks of first tokens, first window block, blocks
   int u0, u1;              // this CTA's blocks of it
+  int c0, c1;              // the CTAs that share it
   int more;                // 0: no unit, the end of the list
   __device__ int block(int u) const { return u < ns ? u : u - ns + wt; }
   // tokens' positions of tile t: [tf, tl], tl < tf if it has none
@@ -103,13 +108,13 @@ struct Plan {
 
 // A unit's positions in the list, and the block at which a CTA boundary that
 // falls `at` positions into it cuts it: at its start or its end where the piece
-// would be no more than its own cost.
+// would be small (a cut costs both sides a start, an end and the join).
 __device__ __forceinline__ int weight(int nb) { return max(1, nb) + kUnitCost; }
 __device__ __forceinline__ int cut_at(int nb, int at) {
   if (at <= 0) return 0;
   if (nb < 2) return max(1, nb);  // one piece (an empty unit counts as one block): where it starts
   const int x = at - kUnitCost;
-  return x <= 0 ? 0 : x >= nb - 1 ? nb : x;
+  return x <= min(kSnap, nb / 2) ? 0 : x >= nb - kSnap ? nb : x;
 }
 
 __device__ __forceinline__ Unit unit_at(const Plan& p, const ChunkArgs& g, int b, int qb, int hk) {
@@ -188,8 +193,6 @@ __device__ __forceinline__ void schedule(Plan& p, const ChunkArgs& g, Unit* ring
   const bool work = (int)blockIdx.x < nc;
   const Division dv(total, max(nc, 1));
   const int lo = work ? dv.lo(blockIdx.x) : 0, hi = work ? dv.lo(blockIdx.x + 1) : 0;
-  Split sp;
-  sp.c0 = -1;
   Unit x;
   int start = 0;
   if (lo < hi) {
@@ -218,18 +221,6 @@ __device__ __forceinline__ void schedule(Plan& p, const ChunkArgs& g, Unit* ring
     x = unit_at(p, g, b, qb, 0);
     x.hk = (lo - start) / weight(x.nb);
     start += x.hk * weight(x.nb);
-    const int cut = cut_at(x.nb, lo - start);
-    if (cut > 0 && cut < x.nb) {
-      // a split unit: the CTAs of its first and its last block
-      int c0 = dv.cta(start + kUnitCost), c1 = dv.cta(start + kUnitCost + x.nb - 1);
-      while (cut_at(x.nb, dv.lo(c0 + 1) - start) <= 0) ++c0;
-      while (cut_at(x.nb, dv.lo(c1) - start) >= x.nb) --c1;
-      sp.c0 = c0 + 1 == (int)blockIdx.x ? c0 : -1;
-      sp.c1 = c1;
-      sp.row0 = x.row0;
-      sp.rows = x.nt;
-      sp.hk = x.hk;
-    }
   }
   int i = 0, ph = 1;
   auto put = [&](int more) {
@@ -246,12 +237,23 @@ __device__ __forceinline__ void schedule(Plan& p, const ChunkArgs& g, Unit* ring
     }
     return true;
   };
+  Split sp;
+  sp.c0 = -1;
   bool ok = true;
   while (ok && start < hi) {
     const int a = cut_at(x.nb, lo - start), e = cut_at(x.nb, hi - start);
     if (a < e) {  // this CTA has a part of it
       x.u0 = min(a, x.nb);
       x.u1 = min(e, x.nb);
+      x.c0 = x.c1 = blockIdx.x;
+      if (x.u0 > 0 || x.u1 < x.nb) {  // a split unit: the CTAs of its first and its last block
+        x.c0 = dv.cta(start + kUnitCost);
+        x.c1 = dv.cta(start + kUnitCost + x.nb - 1);
+        while (cut_at(x.nb, dv.lo(x.c0 + 1) - start) <= 0) ++x.c0;
+        while (cut_at(x.nb, dv.lo(x.c1) - start) >= x.nb) --x.c1;
+        if (g.combine && x.c1 - x.c0 >= kJoinMost && x.c0 + 1 == (int)blockIdx.x)
+          sp = {x.c0, x.c1, x.row0, x.nt, x.hk};
+      }
       ok = put(1);
     }
     start += weight(x.nb);
@@ -266,7 +268,7 @@ __device__ __forceinline__ void schedule(Plan& p, const ChunkArgs& g, Unit* ring
     }
   }
   if (ok) put(0);
-  if (lane == 0) g.split[blockIdx.x] = sp;
+  if (lane == 0 && g.combine) g.split[blockIdx.x] = sp;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -414,13 +416,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         if (x.u0 == x.u1) continue;
         const int nt = x.nt > tq ? 2 : 1;
         const int32_t* tab = g.c.table + (long long)x.slot * g.c.max_pages;
-        auto entry = [&](int u) {  // lane's box of block u: its first row in the pool, -1 not needed, -2 bad
+        // lane's box of block u: its first row in the pool; for a box that no row
+        // sees, or of a bad page, the row past the pool's end, from where TMA
+        // fills in zeros
+        const int past = g.c.n_pages * g.c.Hkv << g.logpage;
+        auto entry = [&](int u) {
           const int j = x.block(u) * kBlk + lane * P;
-          if (lane >= nbox || j > x.pl || !(j + P > x.from || j < x.first)) return -1;
+          if (lane >= nbox || j > x.pl || !(j + P > x.from || j < x.first)) return past;
           const int pg = tab[j >> g.logpage];
           if (pg >= 0 && pg < g.c.n_pages) return ((pg * g.c.Hkv + x.hk) << g.logpage) + (j & (g.c.page - 1));
           atomicOr(g.status, DEV_BAD_SLOT);
-          return -2;
+          return past + 1;
         };
         auto queries = [&] {
           wait(q_empty, qph);
@@ -436,17 +442,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         if (opening) queries();  // the CTA's first segment: the queries first
         int row = entry(x.u0);
         for (int u = x.u0; u < x.u1 && !dead; ++u) {
-          const int ahead = u + 1 < x.u1 ? entry(u + 1) : -1;
-          const unsigned load = __ballot_sync(0xffffffffu, row >= 0), bad = __ballot_sync(0xffffffffu, row == -2);
+          const int ahead = u + 1 < x.u1 ? entry(u + 1) : past;
+          const unsigned bad = __ballot_sync(0xffffffffu, row == past + 1);
           for (int kv = 0; kv < 2; ++kv) {
             wait(kv_empty + 8 * st, ph);
             if (dead) break;
             if (lane == 0) {
               if (kv == 0) s_bad[bad_at] = bad;
-              mbar_expect_tx(kv_full + 8 * st, (uint32_t)(__popc(load) * NH * P * 128));
+              mbar_expect_tx(kv_full + 8 * st, kTileB);
             }
             __syncwarp();
-            if (row >= 0)
+            if (lane < nbox)
 #pragma unroll
               for (int h = 0; h < NH; ++h)
                 tma_load_2d(ring + st * kTileB + h * kHalf + lane * P * 128, kv ? &g.tm_v : &g.tm_k, h * 64, row,
@@ -465,27 +471,36 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       }
     } else if (warp == 10) {
       // ================= values that no row sees become zeros =================
-      int st = 1, ph = 0, bad_at = 0;
+      const int P = 1 << g.logP;
+      int st = 1, ph = 0;
       while (next_seg()) {
         const Unit x = s_seg[seg_i];
         done_seg();
         for (int u = x.u0; u < x.u1; ++u) {
           const int j0 = x.block(u) * kBlk;
           wait(kv_full + 8 * st, ph);
-          const uint32_t bad = *(volatile uint32_t*)&s_bad[bad_at];
-          if (bad || j0 + kBlk - 1 > x.pl || (j0 < x.from && j0 + kBlk > x.first)) {
-            for (int r = lane >> 3; r < kBlk; r += 4) {  // eight lanes a row of 128 bytes
-              const int j = j0 + r;
-              if (j > x.pl || (j < x.from && j >= x.first) || (bad >> (r >> g.logP) & 1))
+          // rows [a, e) of the block's boxes that some row sees and some rows of
+          // which none does: past the last token, before the window
+          auto zero = [&](int a, int e) {
+            for (int r = a + (lane >> 3); r < e; r += 4)  // eight lanes a row of 128 bytes
 #pragma unroll
-                for (int h = 0; h < NH; ++h)
-                  st_s128(ring + st * kTileB + h * kHalf + r * 128 + (lane & 7) * 16, 0u, 0u, 0u, 0u);
+              for (int h = 0; h < NH; ++h) st_s128(ring + st * kTileB + h * kHalf + r * 128 + (lane & 7) * 16, 0u, 0u, 0u, 0u);
+          };
+          auto box_end = [&](int r) { return (r + P - 1) & ~(P - 1); };
+          const bool tail = j0 + kBlk - 1 > x.pl, head = j0 < x.from && j0 + kBlk > x.first;
+          if (tail) zero(x.pl + 1 - j0, box_end(x.pl + 1 - j0));
+          if (head) {
+            const int a = max(0, x.first - j0), e = min(kBlk, x.from - j0);  // unseen rows
+            if (box_end(a) >= e) {
+              zero(a, e);
+            } else {
+              zero(a, box_end(a));
+              zero(e & ~(P - 1), e);
             }
-            fence_proxy_async_shared();
           }
+          if (tail || head) fence_proxy_async_shared();
           __syncwarp();
           if (lane == 0) mbar_arrive(v_ready + 8 * st);
-          bad_at = (bad_at + 1) % kBadRing;
           st += 2;
           if (st >= NST) {
             st = 1;
@@ -589,6 +604,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     }
   } else {
     // ================= softmax (a thread is a row of its tile) =================
+    constexpr int CW = 64;  // columns of O at a time in the segment's end
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     const int t = warp >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -696,64 +712,140 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         wait(pv_done + 8 * t, (nsc & 1) ^ 1);
         tc_fence_after();
       }
-      if (whole) {
-        // 32 columns at a time through the warp's own buffer: a thread holds a
-        // row, four lanes write 64 bytes of a row
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+      // A unit in several CTAs: all but the last to end leave their part (place
+      // 2 c + 1 if it holds the unit's first block, else 2 c); the last one adds
+      // the parts up in the order of the keys, its own from tensor memory.
+      const int c0 = x.c0, c1 = x.c1, me = blockIdx.x;
+      auto place = [&](int c) { return (2 * c + (c == c0 ? 1 : 0)) * 2 + t; };
+      bool last = whole;
+      if (!whole) {
+        const bool here = !(g.combine && c1 - c0 >= kJoinMost);
+        int32_t* cnt = g.cnt + c0 * 8 + (warp & 7);
+        if (here) last = __shfl_sync(0xffffffffu, lane == 0 ? ld_acquire_gpu(cnt) : 0, 0) == c1 - c0;
+        if (!last) {
+          float* pm = g.pml + place(me) * 256;
+          pm[r] = m;
+          pm[128 + r] = l;
+          if (any) {
+            float* pp = g.part + (long long)place(me) * D * 128 + r * 4;
+#pragma unroll 1
+            for (int i = 0; i < D; i += 32) {
+              uint32_t o[32];
+              tc_ld32(to + i, o);
+              tc_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                *reinterpret_cast<uint4*>(pp + (long long)(i / 4 + e) * 512) =
+                    make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            }
+          }
+          if (here) {
+            __threadfence();
+            __syncwarp();
+            last = __shfl_sync(0xffffffffu, lane == 0 ? atomicAdd(cnt, 1) : 0, 0) == c1 - c0;
+          }
+        }
+        if (last) {
+          if (lane == 0) *cnt = 0;  // ready for the next call
+          __threadfence();
+        }
+      }
+      if (last) {
+        float mt = m, lt = l;
+        if (!whole) {
+          for (int c = c0; c <= c1; ++c)
+            if (c != me) mt = fmaxf(mt, __ldcg(g.pml + place(c) * 256 + r));
+          lt = 0.f;
+        }
+        const float zt = mt == -INFINITY ? 0.f : mt;
+        if (!whole)
+          for (int c = c0; c <= c1; ++c) {
+            const float mc = c == me ? m : __ldcg(g.pml + place(c) * 256 + r);
+            const float lc = c == me ? l : __ldcg(g.pml + place(c) * 256 + 128 + r);
+            lt = fmaf(lc, ex2(mc - zt), lt);
+          }
+        const float inv = lt == 0.f ? 0.f : 1.f / lt;
+        // a thread holds a row; 32 columns at a time through the warp's own
+        // buffer, from which four lanes write 64 bytes of a row
         const int nt = min(tq, tl - tf + 1);  // tokens of the tile
         uint16_t* po[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int rr = (warp & 3) * 32 + k * 8 + (lane >> 2), tk = s_tok[rr];
-          po[k] = tk < nt ? g.a.o + (((long long)x.row0 + t * tq + tk) * g.a.Hq + x.hk * G + rr - tk * G) * D +
-                                (lane & 3) * 8
+          po[k] = tk < nt ? g.a.o + (((long long)x.row0 + t * tq + tk) * g.a.Hq + x.hk * G + rr - tk * G) * D + (lane & 3) * 8
                           : nullptr;
         }
+        const bool none = lt == 0.f;  // the row sees nothing
 #pragma unroll 1
-        for (int i = 0; i < D; i += 32) {
-          uint32_t o[32];
-          if (any) {
-            tc_ld32(to + i, o);
-            tc_ld_wait();
-          }
-          const bool none = !any || l == 0.f;
+        for (int i = 0; i < D; i += CW) {
+          float y[CW];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t w[4];
+          for (int e = 0; e < CW; ++e) y[e] = 0.f;
+          if (whole) {
+            if (any) {
+#pragma unroll
+              for (int e = 0; e < CW; e += 16) {
+                uint32_t o[16];
+                tc_ld16(to + i + e, o);
+                tc_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) y[e + k] = __uint_as_float(o[k]);
+              }
+            }
+          } else {
+#pragma unroll 1
+            for (int c = c0; c <= c1; ++c) {
+              if (c == me) {
+                if (!any) continue;
+                const float f = l != 0.f ? ex2(m - zt) : 0.f;
+#pragma unroll
+                for (int e = 0; e < CW; e += 16) {
+                  uint32_t o[16];
+                  tc_ld16(to + i + e, o);
+                  tc_ld_wait();
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) y[e + k] = fmaf(__uint_as_float(o[k]), f, y[e + k]);
+                }
+              } else {
+                float4 v[CW / 4];
+                const float* pp = g.part + (long long)place(c) * D * 128 + i * 128 + r * 4;
+#pragma unroll
+                for (int e = 0; e < CW / 4; ++e) v[e] = __ldcg(reinterpret_cast<const float4*>(pp + e * 512));
+                const float lc = __ldcg(g.pml + place(c) * 256 + 128 + r), mc = __ldcg(g.pml + place(c) * 256 + r);
+                if (lc == 0.f) continue;  // the row saw nothing there (it may have left no accumulator)
+                const float f = ex2(mc - zt);
+#pragma unroll
+                for (int e = 0; e < CW / 4; ++e) {
+                  y[4 * e] = fmaf(v[e].x, f, y[4 * e]);
+                  y[4 * e + 1] = fmaf(v[e].y, f, y[4 * e + 1]);
+                  y[4 * e + 2] = fmaf(v[e].z, f, y[4 * e + 2]);
+                  y[4 * e + 3] = fmaf(v[e].w, f, y[4 * e + 3]);
+                }
+              }
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < CW; q += 32) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = none ? 0u
+                            : pack2<F16>(y[q + 8 * e + 2 * k] * inv, y[q + 8 * e + 2 * k + 1] * inv);
+              st_s128(sout + lane * kOutPitch + e * 16, w[0], w[1], w[2], w[3]);
+            }
+            __syncwarp();
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              w[k] = none ? 0u : pack2<F16>(__uint_as_float(o[8 * e + 2 * k]) * inv, __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
-            st_s128(sout + lane * kOutPitch + e * 16, w[0], w[1], w[2], w[3]);
+              if (po[k])
+                *reinterpret_cast<uint4*>(po[k] + i + q) = ld_s128(sout + (k * 8 + (lane >> 2)) * kOutPitch + (lane & 3) * 16);
+            __syncwarp();
           }
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (po[k])
-              *reinterpret_cast<uint4*>(po[k] + i) = ld_s128(sout + (k * 8 + (lane >> 2)) * kOutPitch + (lane & 3) * 16);
-          __syncwarp();
         }
         if (g.a.lse && tok < nt)
           g.a.lse[((long long)x.row0 + t * tq + tok) * g.a.Hq + x.hk * G + r - tok * G] =
-              l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-      } else {
-        // a part of the unit: place 2 i + 1 if it holds the unit's first block, else 2 i
-        const int slot = 2 * blockIdx.x + (x.u0 == 0 ? 1 : 0);
-        float* pm = g.pml + (slot * 2 + t) * 256;
-        pm[r] = m;
-        pm[128 + r] = l;
-        if (any) {
-          float* pp = g.part + (long long)(slot * 2 + t) * D * 128 + r * 4;
-#pragma unroll 1
-          for (int i = 0; i < D; i += 32) {
-            uint32_t o[32];
-            tc_ld32(to + i, o);
-            tc_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<uint4*>(pp + (long long)(i / 4 + e) * 512) =
-                  make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          }
-        }
+              lt == 0.f ? -INFINITY : (mt + log2f(lt)) * 0.6931471805599453f;
       }
       if (any) {  // the accumulator may be written again
         tc_fence_before();
@@ -847,7 +939,7 @@ cudaError_t launch_one(ChunkArgs& g, int grid, int dev, cudaStream_t st) {
   launch_begin(K_ATTN_CHUNK, st);
   cudaError_t e = cudaLaunchKernelEx(&cfg, chunk_kernel<F16, D>, g);
   launch_end(st);
-  if (e != cudaSuccess || grid < 2) return e;
+  if (e != cudaSuccess || !g.combine) return e;
   cfg.gridDim = dim3(grid - 1, 8);
   cfg.blockDim = dim3(128);
   cfg.dynamicSmemBytes = 0;
@@ -882,8 +974,8 @@ size_t chunk_ws_bytes(int D) {
   return align256((size_t)2 * kMaxGrid * 2 * 128 * (D + 2) * 4 + kMaxGrid * sizeof(Split));
 }
 
-cudaError_t launch_attn_chunk(const Cache& c, const Rows& r, const Attn& a, bool f16, int32_t* status, void* scratch,
-                              cudaStream_t st) {
+cudaError_t launch_attn_chunk(const Cache& c, const Rows& r, const Attn& a, bool f16, int32_t* status, int32_t* sync,
+                              void* scratch, cudaStream_t st) {
   int dev = 0;
   const int grid = chunk_grid(&dev);
   if (!grid) return cudaErrorInvalidDevice;
@@ -895,6 +987,7 @@ cudaError_t launch_attn_chunk(const Cache& c, const Rows& r, const Attn& a, bool
   g.logpage = 0;
   while ((1 << g.logpage) < c.page) ++g.logpage;
   g.logP = g.logpage < 7 ? g.logpage : 7;
+  g.cnt = sync;
   g.part = static_cast<float*>(scratch);
   g.pml = g.part + (size_t)2 * kMaxGrid * 2 * 128 * c.D;
   g.split = reinterpret_cast<Split*>(g.pml + (size_t)2 * kMaxGrid * 2 * 256);
@@ -903,6 +996,11 @@ cudaError_t launch_attn_chunk(const Cache& c, const Rows& r, const Attn& a, bool
     return cudaErrorInvalidValue;
   for (g.b0 = 0; g.b0 < r.B; g.b0 += kChunkSeqs) {
     g.nseq = r.B - g.b0 < kChunkSeqs ? r.B - g.b0 : kChunkSeqs;
+    // Which calls can have a unit in many CTAs: where one sequence's units fill
+    // the GPU, the longest is at most about twice the mean and lies in a few.
+    // Elsewhere (few rows over a long context, sequences of very different
+    // lengths) the kernel that joins many parts follows. Either way is right.
+    g.combine = !(r.B == 1 && 3LL * ((r.n_rows + 2 * g.tq - 1) / (2 * g.tq)) * c.Hkv >= 2LL * grid);
     cudaError_t e;
     if (c.D == 128) e = f16 ? launch_one<true, 128>(g, grid, dev, st) : launch_one<false, 128>(g, grid, dev, st);
     else e = f16 ? launch_one<true, 64>(g, grid, dev, st) : launch_one<false, 64>(g, grid, dev, st);

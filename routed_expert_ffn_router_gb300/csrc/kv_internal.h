@@ -87,8 +87,8 @@ cudaError_t launch_attn_decode(const Cache& c, const Rows& r, const Attn& a, boo
 // above zero.
 bool chunk_supported(int D, int page, int Hkv, int G, int B, int n_rows, int max_pages, float scale);
 size_t chunk_ws_bytes(int D);
-cudaError_t launch_attn_chunk(const Cache& c, const Rows& r, const Attn& a, bool f16, int32_t* status, void* scratch,
-                              cudaStream_t st);
+cudaError_t launch_attn_chunk(const Cache& c, const Rows& r, const Attn& a, bool f16, int32_t* status, int32_t* sync,
+                              void* scratch, cudaStream_t st);
 cudaError_t launch_grow(const Cache& c, const int32_t* slots, const int32_t* add, int n, int32_t* status, void* scratch,
                         cudaStream_t st);
 cudaError_t launch_fork(const Cache& c, const int32_t* src, const int32_t* dst, int n, int32_t* status, void* scratch,
