@@ -18,14 +18,18 @@
 // registers; an item that lies in several CTAs is joined, through partials in
 // the workspace, by the CTA that finishes last.
 //
-// A tile. Warp w multiplies Q (16 rows) with keys 16 w .. 16 w + 15
-// (mma m16n8k16), the scores meet in shared memory, every warp holds the same
-// row maxima and probabilities, and warp w accumulates columns w D / 4 .. of O.
-// A probability enters the product with V as a sum of two values of the
+// A tile. Warp w has its keys 16 w .. 16 w + 15 to itself: S^T = K Q^T (mma
+// m16n8k16, the 8 query rows of a block as N, so no half of the product is
+// padding), the softmax of its 16 x 8 scores in registers, P^T turned into the B
+// operand by movmatrix, O^T += V^T P^T over all of D. The warps meet only at a
+// span's end, where their (m, l, o) are added up through shared memory in warp
+// order. A probability enters the product with V as a sum of two values of the
 // cache's type (rounding 2^-17 for bf16 instead of 2^-8; the second product
-// costs nothing next to the HBM read). Keys that only some rows see are added
-// with scalar products, keys that no row sees get a zero value row: nothing
-// that lies in a masked place reaches a result, NaN and infinities included.
+// costs nothing next to the HBM read). The running maximum is raised only by
+// more than 2^8 (sums are in fp32), so O is seldom rescaled. Keys that only some
+// rows see are added with scalar products, keys that no row sees get a zero
+// value row: nothing that lies in a masked place reaches a result, NaN and
+// infinities included.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -42,7 +46,7 @@ namespace {
 constexpr int kTile = 64;
 constexpr int kDecThreads = 160;
 constexpr int kRing = 96 * 1024;
-constexpr int kSPitch = kTile + 4;      // fp32 scores per row of a tile
+constexpr int kOPitch = 64 + 4;         // floats per row of the buffer in which the warps' O meet
 constexpr int kSeqCap = 128;            // sequences per launch
 constexpr int kCntBase = 2048;          // this kernel's counters in the workspace head
 
@@ -87,6 +91,10 @@ __device__ __forceinline__ void fold_ml(float& M, float& L, float m, float l, fl
 }
 __device__ __forceinline__ float fold_o(float O, float o, float a, float b) { return __fmaf_rn(o, b, __fmul_rn(O, a)); }
 
+__device__ __forceinline__ float4 fold_o4(const float4& O, const float4& o, float a, float b) {
+  return make_float4(fold_o(O.x, o.x, a, b), fold_o(O.y, o.y, a, b), fold_o(O.z, o.z, a, b), fold_o(O.w, o.w, a, b));
+}
+
 // One item as every role sees it.
 struct Item {
   int slot, len;
@@ -123,6 +131,11 @@ __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
                : "r"(a)
                : "memory");
 }
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  return d;
+}
 __device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -134,6 +147,17 @@ __device__ __forceinline__ float lse_of(float m, float l) {
   return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
+// A row's result: columns 64 h .. + 3 of o.
+template <bool F16, int D>
+__device__ __forceinline__ void put_row(float m, float l, const float4 (&O)[D / 64], uint16_t* o, float* lse) {
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int h = 0; h < D / 64; ++h)
+    *reinterpret_cast<uint2*>(o + 64 * h) =
+        make_uint2(pack2<F16>(O[h].x * inv, O[h].y * inv), pack2<F16>(O[h].z * inv, O[h].w * inv));
+  if (lse) *lse = lse_of(m, l);
+}
+
 // A split item whose spans are all there.
 struct Join {
   int b, rt, hk, n;   // n partials
@@ -141,23 +165,24 @@ struct Join {
 };
 
 // The fold of n partials of one row (from p on, pstride apart) in order, in the
-// fragment's columns col, col + 8, ..; eight partials in flight per lane.
+// columns col + 64 h .. + 3; eight partials in flight per lane.
 template <bool F16, int D>
 __device__ __forceinline__ void join_row(const float* p, long long pstride, int n, int R, int row, int col, uint16_t* o,
-                                      float* lse) {
-  constexpr int NT = D / 32, U = 8;
-  float M = 0.f, L = 0.f, O[NT][2];
+                                         float* lse) {
+  constexpr int NH = D / 64, U = 8;
+  float M = 0.f, L = 0.f;
+  float4 O[NH];
   const float* po = p + 2 * R + row * D + col;
   for (int s = 0; s < n; s += U) {
     float m[U], l[U];
-    float2 w[U][NT];
+    float4 w[U][NH];
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (s + u < n) {
         m[u] = ldg_cg_f32(p + (s + u) * pstride + row);
         l[u] = ldg_cg_f32(p + (s + u) * pstride + R + row);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) w[u][i] = __ldcg(reinterpret_cast<const float2*>(po + (s + u) * pstride + i * 8));
+        for (int h = 0; h < NH; ++h) w[u][h] = __ldcg(reinterpret_cast<const float4*>(po + (s + u) * pstride + 64 * h));
       }
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -166,39 +191,30 @@ __device__ __forceinline__ void join_row(const float* p, long long pstride, int 
           M = m[u];
           L = l[u];
 #pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            O[i][0] = w[u][i].x;
-            O[i][1] = w[u][i].y;
-          }
+          for (int h = 0; h < NH; ++h) O[h] = w[u][h];
         } else {
           float a, b;
           fold_ml(M, L, m[u], l[u], a, b);
 #pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            O[i][0] = fold_o(O[i][0], w[u][i].x, a, b);
-            O[i][1] = fold_o(O[i][1], w[u][i].y, a, b);
-          }
+          for (int h = 0; h < NH; ++h) O[h] = fold_o4(O[h], w[u][h], a, b);
         }
       }
   }
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-#pragma unroll
-  for (int i = 0; i < NT; ++i) *reinterpret_cast<uint32_t*>(o + col + i * 8) = pack2<F16>(O[i][0] * inv, O[i][1] * inv);
-  if (lse) *lse = lse_of(M, L);
+  put_row<F16, D>(M, L, O, o + col, lse);
 }
 
-template <bool F16, int D>
+// NB: blocks of 8 query rows of an item.
+template <bool F16, int D, int NB>
 __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_constant__ DecArgs g) {
   constexpr int kStage = kTile * D * 4;      // K and V of a tile
   constexpr int kStages = kRing / kStage;
-  constexpr int NT = D / 32;                 // 8-column tiles of a warp's part of O
-  constexpr int KK = D / 16;
+  constexpr int KK = D / 16, NH = D / 64;
   extern __shared__ __align__(1024) uint8_t smem_dec[];
   __shared__ __align__(8) uint64_t s_bar[2 * kStages];
   __shared__ uint32_t s_badbox[kStages];
   __shared__ int s_off[kSeqCap + 1], s_len[kSeqCap], s_slot[kSeqCap];
-  __shared__ __align__(16) float s_x[2][16][kSPitch];  // read and written in pairs
-  __shared__ __align__(16) uint16_t s_q[16][D + 8];  // the item's query rows (pitch: no bank conflicts)
+  __shared__ __align__(16) float s_o[4][8][kOPitch];  // the warps' O: 8 rows, 64 columns at a time
+  __shared__ float s_ml[2][4][8 * NB];                // the warps' maxima and sums
   __shared__ int s_scan[8];
   __shared__ Join s_join[2];  // split items that this CTA completes: its first and its last at most
   __shared__ int s_njoin;
@@ -372,305 +388,301 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_con
   }
 
   // ================= consumers =================
-  const int qr = lane >> 2, qc = 2 * (lane & 3);
-  const int P = 1 << g.logP;
-  const bool two = n_q * G > 8;  // some tile has rows 8 .. 15
-  // score product: this lane's ldmatrix row of the warp's 16 keys
-  const int krow = warp * 16 + ((lane >> 4) << 3) + (lane & 7);
-  const uint32_t kaddr = (uint32_t)((krow >> g.logP) * P * D * 2 + (krow & (P - 1)) * 128);
-  const uint32_t kxor = (uint32_t)(krow & 7) << 4;
-  const uint32_t kch = ((lane >> 3) & 1) << 4;
-  // value product: this lane's ldmatrix row within 16 keys, its column chunk
-  const int vrow = lane & 15;
-  const uint32_t vxor = (uint32_t)(lane & 7) << 4;
-  const int vch0 = warp * NT + (lane >> 4);
-  int st = 0, ph = 0, sbuf = 0;
+  const int P = 1 << g.logP, boxb = P * D * 2, halfb = P * 128;
+  // score product: this lane's ldmatrix row of the warp's keys; value product: the same
+  const int kr = warp * 16 + (lane & 15), vr = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
+  const uint32_t koff = (kr >> g.logP) * boxb + (kr & (P - 1)) * 128, voff = (vr >> g.logP) * boxb + (vr & (P - 1)) * 128;
+  const uint32_t kx = (uint32_t)((lane >> 4) ^ (lane & 7)) << 4, vx = (uint32_t)(((lane >> 3) & 1) ^ (lane & 7)) << 4;
+  const int key0 = warp * 16 + (lane >> 2);  // scores: keys key0, key0 + 8; rows 8 nb + ra, + 1
+  const int ra = 2 * (lane & 3);
+  const int mrow = lane >> 2, mcol = warp * 16 + 4 * (lane & 3);  // merged: row 8 nb + mrow, columns 64 h + mcol .. + 3
+  const float sc = g.a.scale * 1.4426950408889634f;
+  int st = 0, ph = 0;
 
-  // query rows: this lane's ldmatrix row and column half
-  const uint32_t qaddr = smem_u32(&s_q[lane & 15][(lane >> 4) * 8]);
-  int pos0 = -1, pos1 = -1;      // tokens of this lane's two rows (-1: no row, or before the first token)
-  float M0 = -INFINITY, M1 = -INFINITY, L0 = 0.f, L1 = 0.f, O[NT][4];
+  uint32_t q[NB][KK][2];
+  int pos[NB][2];                // tokens of this lane's score rows (-1: no row, or before the first token)
+  float M[NB], L[NB];
+  float4 O[NB][NH];
   int run0 = -1;                 // first span of the current run of spans of one item
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    M[nb] = -INFINITY;
+    L[nb] = 0.f;
+  }
 
   const int items = B * Hkv * g.RT;
   const long long pstride = (long long)g.R * (D + 2);
   // partials of an item split over CTAs: [span][m of R rows, l of R rows, o [R][D]]
   auto part_of = [&](int key, int s) { return g.part + ((long long)key * g.max_span + s) * pstride; };
-  auto put = [&](float* p, float m0, float m1, float l0, float l1, const float (&o)[NT][4]) {
-    if (warp == 0 && (lane & 3) == 0) {
-      p[qr] = m0;
-      p[g.R + qr] = l0;
-      if (two) {
-        p[qr + 8] = m1;
-        p[g.R + qr + 8] = l1;
-      }
-    }
-    float* po = p + 2 * g.R + warp * (D / 4) + qc;
+  auto put = [&](float* p, const float (&m)[NB], const float (&l)[NB], const float4 (&o)[NB][NH]) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      *reinterpret_cast<float2*>(po + qr * D + n * 8) = make_float2(o[n][0], o[n][1]);
-      if (two) *reinterpret_cast<float2*>(po + (qr + 8) * D + n * 8) = make_float2(o[n][2], o[n][3]);
+    for (int nb = 0; nb < NB; ++nb) {
+      const int r = 8 * nb + mrow;
+      if (warp == 0 && (lane & 3) == 0) {
+        p[r] = m[nb];
+        p[g.R + r] = l[nb];
+      }
+#pragma unroll
+      for (int h = 0; h < NH; ++h) *reinterpret_cast<float4*>(p + 2 * g.R + r * D + 64 * h + mcol) = o[nb][h];
     }
   };
-  // rows of the item: token i and head of local row r, -1 if there is none
+  // index of the item's local row r among the sequence's rows, -1 if there is none
   auto row_of = [&](int r) {
     const int rr = rt * 16 + r;
     return rr < n_q * G ? rr : -1;
   };
-  auto out_rows = [&](float m0, float m1, float l0, float l1, const float (&o)[NT][4]) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int rr = row_of(qr + 8 * h);
-      if (rr < 0) continue;
-      const long long t = (long long)b * n_q + rr / G;
-      const int hq = hk * G + rr % G;
-      const float l = h ? l1 : l0, m = h ? m1 : m0;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      uint16_t* po = g.a.o + (t * g.a.Hq + hq) * D + warp * (D / 4) + qc;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        *reinterpret_cast<uint32_t*>(po + n * 8) = pack2<F16>(o[n][2 * h] * inv, o[n][2 * h + 1] * inv);
-      if (g.a.lse && warp == 0 && (lane & 3) == 0)
-        g.a.lse[t * g.a.Hq + hq] = lse_of(m, l);
-    }
-  };
 
   bool ok = true;
   while (more && ioff + span * it.sp < hi) {
-    if (run0 < 0) {  // a new item: its query rows
+    if (run0 < 0) {  // a new item: its query rows as B operands
       run0 = span;
-      pos0 = pos1 = -1;
-      if (it.slot >= 0) {
-        const int r0 = row_of(qr), r1 = row_of(qr + 8);
-        if (r0 >= 0) pos0 = it.len - n_q + r0 / G;
-        if (r1 >= 0) pos1 = it.len - n_q + r1 / G;
-      }
-      named_bar_sync(1, 128);  // the last item's rows are not read any more
-      for (int i = tid; i < 16 * (D / 8); i += 128) {
-        const int r = i / (D / 8), c8 = i - r * (D / 8), rr = row_of(r);
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (rr >= 0)
-          v = ldg_nc_v4(g.a.q + ((long long)b * n_q + rr / G) * g.a.q_stride + (hk * G + rr % G) * D + c8 * 8);
-        *reinterpret_cast<uint4*>(&s_q[r][c8 * 8]) = v;
-      }
-      named_bar_sync(1, 128);
-    }
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, o[NT][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+      for (int nb = 0; nb < NB; ++nb) {
+        const int rr = row_of(8 * nb + (lane >> 2));
+        const uint16_t* qp = g.a.q + ((long long)b * n_q + rr / G) * g.a.q_stride + (hk * G + rr % G) * D + ra;
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            q[nb][kk][e] = rr >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(qp + kk * 16 + e * 8)) : 0u;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = row_of(8 * nb + ra + e);
+          pos[nb][e] = r >= 0 && it.slot >= 0 ? it.len - n_q + r / G : -1;
+        }
+      }
+    }
+    float m[NB][2], l[NB][2], o[NB][KK][4];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      m[nb][0] = m[nb][1] = -INFINITY;
+      l[nb][0] = l[nb][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < KK; ++i) o[nb][i][0] = o[nb][i][1] = o[nb][i][2] = o[nb][i][3] = 0.f;
+    }
     const int v1 = min(it.nvis, (span + 1) * it.sp);
     for (int v = span * it.sp; v < v1; ++v) {
-      const int j0 = it.tile(v) * kTile;
+      const int j0 = it.tile(v) * kTile + warp * 16;  // the warp's first key
       // after an expired wait (the status word says that the results are
       // incomplete) a warp goes on without waiting, so that all meet at every barrier
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait_short(full + 8 * st, ph, g.status));
       const uint32_t bad = *(volatile uint32_t*)&s_badbox[st];
-      const uint32_t sk = ring + st * kStage, sv = sk + kStage / 2;
-      // ---- scores of this warp's 16 keys
-      float x[2][4] = {};
+      const uint32_t sk = ring + st * kStage + koff, sv = ring + st * kStage + kStage / 2;
+      // ---- scores
+      float x[NB][2][4] = {};
 #pragma unroll
       for (int kk = 0; kk < KK; ++kk) {
-        uint32_t q[4], kf[4];
-        ldsm4(qaddr + kk * 32, q);
-        ldsm4(sk + kaddr + (kk / 4) * (P * 128) + ((((kk & 3) << 5) | kch) ^ kxor), kf);
-        mma<F16>(x[0], q[0], q[1], q[2], q[3], kf[0], kf[1]);
-        mma<F16>(x[1], q[0], q[1], q[2], q[3], kf[2], kf[3]);
-      }
-      const float sc = g.a.scale * 1.4426950408889634f;
+        uint32_t kf[4];
+        ldsm4(sk + (kk >> 2) * halfb + (((kk & 3) << 5) ^ kx), kf);
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        *reinterpret_cast<float2*>(&s_x[sbuf][qr][warp * 16 + n * 8 + qc]) = make_float2(x[n][0] * sc, x[n][1] * sc);
-        if (two)
-          *reinterpret_cast<float2*>(&s_x[sbuf][qr + 8][warp * 16 + n * 8 + qc]) = make_float2(x[n][2] * sc, x[n][3] * sc);
+        for (int nb = 0; nb < NB; ++nb) mma<F16>(x[nb][kk & 1], kf[0], kf[1], kf[2], kf[3], q[nb][kk][0], q[nb][kk][1]);
       }
-      named_bar_sync(1, 128);
-      // ---- all 64 scores of the lane's rows: columns 16 kk + {qc, qc + 1, qc + 8, qc + 9}
-      float s0[16], s1[16];
+      float s[NB][4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 t = *reinterpret_cast<const float2*>(&s_x[sbuf][qr][i * 8 + qc]);
-        s0[2 * i] = t.x;
-        s0[2 * i + 1] = t.y;
-        if (two) {
-          const float2 u = *reinterpret_cast<const float2*>(&s_x[sbuf][qr + 8][i * 8 + qc]);
-          s1[2 * i] = u.x;
-          s1[2 * i + 1] = u.y;
-        }
-      }
-      const bool plain = bad == 0 && it.pf >= 0 && j0 + kTile - 1 <= it.pf &&
-                         (W == 0 || j0 > it.pl - W || j0 + kTile <= S);
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nb][e] = (x[nb][0][e] + x[nb][1][e]) * sc;
+      const bool plain = bad == 0 && it.pf >= 0 && j0 + 15 <= it.pf && (W == 0 || j0 > it.pl - W || j0 + 16 <= S);
       if (!plain) {
-        auto see = [&](int p, int j) {
-          return j <= p && (W == 0 || j > p - W || j < S) && !(bad >> ((j - j0) >> g.logP) & 1);
-        };
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int j = j0 + (i >> 1) * 8 + qc + (i & 1);
-          if (!see(pos0, j)) s0[i] = -INFINITY;
-          if (two && !see(pos1, j)) s1[i] = -INFINITY;
-        }
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int k = key0 + (e >> 1) * 8, j = j0 - warp * 16 + k, p = pos[nb][e & 1];
+            if (!(j <= p && (W == 0 || j > p - W || j < S)) || (bad >> (k >> g.logP) & 1)) s[nb][e] = -INFINITY;
+          }
       }
       // ---- running maximum, probabilities
-      float t0 = s0[0], t1 = two ? s1[0] : -INFINITY;
+      bool raise = false;
+      float top[NB][2];
 #pragma unroll
-      for (int i = 1; i < 16; ++i) t0 = fmaxf(t0, s0[i]);
-      if (two) {
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int i = 1; i < 16; ++i) t1 = fmaxf(t1, s1[i]);
-      }
-      t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
-      t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
-      t0 = fmaxf(m0, t0);
-      const float z0 = t0 == -INFINITY ? 0.f : t0, al0 = ex2(m0 - z0);
-      m0 = t0;
-      l0 *= al0;
-      float z1 = 0.f, al1 = 1.f;
-      if (two) {
-        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
-        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
-        t1 = fmaxf(m1, t1);
-        z1 = t1 == -INFINITY ? 0.f : t1;
-        al1 = ex2(m1 - z1);
-        m1 = t1;
-        l1 *= al1;
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        o[n][0] *= al0;
-        o[n][1] *= al0;
-        o[n][2] *= al1;
-        o[n][3] *= al1;
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s0[i] = ex2(s0[i] - z0);
-        l0 += s0[i];
-        if (two) {
-          s1[i] = ex2(s1[i] - z1);
-          l1 += s1[i];
+        for (int e = 0; e < 2; ++e) {
+          float y = fmaxf(s[nb][e], s[nb][e + 2]);
+          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+          top[nb][e] = y;
+          raise = raise || y > m[nb][e] + 8.f || (m[nb][e] == -INFINITY && y > m[nb][e]);
         }
-      }
-      if (!plain) {
-        // which keys no row sees, and which only some see (bit = key of the tile)
-        const int pf = max(0, it.pf);
-        unsigned none[2], some[2];
+      if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int j = j0 + 32 * h + lane;
-          const bool good = !(bad >> ((32 * h + lane) >> g.logP) & 1);
-          const bool any = good && j <= it.pl && (W == 0 || j > pf - W || j < S);
-          const bool all = good && j <= pf && (W == 0 || j > it.pl - W || j < S);
-          none[h] = __ballot_sync(0xffffffffu, !any);
-          some[h] = __ballot_sync(0xffffffffu, any && !all);
-        }
-        auto vptr = [&](int key, int col) {  // address of V[key][col]
-          const int c = col >> 3, r = key & (P - 1);
-          return sv + (key >> g.logP) * (P * D * 2) + (c >> 3) * (P * 128) + r * 128 +
-                 (((uint32_t)((c & 7) ^ (r & 7)) << 4) | ((col & 7) << 1));
-        };
-        for (int h = 0; h < 2; ++h)
-          for (unsigned ms = some[h]; ms; ms &= ms - 1) {
-            const int key = 32 * h + __ffs(ms) - 1, j = j0 + key;
-            const bool v0 = j <= pos0 && (W == 0 || j > pos0 - W || j < S);
-            const bool v1 = j <= pos1 && (W == 0 || j > pos1 - W || j < S);
-            const float p0 = v0 ? ex2(s_x[sbuf][qr][key] - z0) : 0.f;
-            const float p1 = two && v1 ? ex2(s_x[sbuf][qr + 8][key] - z1) : 0.f;
+        for (int nb = 0; nb < NB; ++nb) {
+          float f[2];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const float2 vv = unpack2<F16>(ld_s32(vptr(key, warp * (D / 4) + n * 8 + qc)));
-              if (v0) {
-                o[n][0] = fmaf(p0, vv.x, o[n][0]);
-                o[n][1] = fmaf(p0, vv.y, o[n][1]);
-              }
-              if (two && v1) {
-                o[n][2] = fmaf(p1, vv.x, o[n][2]);
-                o[n][3] = fmaf(p1, vv.y, o[n][3]);
-              }
-            }
+          for (int e = 0; e < 2; ++e) {
+            const bool up = top[nb][e] > m[nb][e] + 8.f || (m[nb][e] == -INFINITY && top[nb][e] > m[nb][e]);
+            f[e] = up ? ex2(m[nb][e] - top[nb][e]) : 1.f;
+            m[nb][e] = up ? top[nb][e] : m[nb][e];
+            l[nb][e] *= f[e];
           }
-        __syncwarp();
-        // zero rows in this warp's columns: a lane writes 16 bytes
-        for (int i = lane; i < kTile * NT; i += 32) {
-          const int key = i / NT, c = i - key * NT;
-          const unsigned cut = (key < 32 ? none[0] | some[0] : none[1] | some[1]) >> (key & 31) & 1;
-          if (cut)
-            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vptr(key, (warp * NT + c) * 8)), "r"(0) : "memory");
-        }
-        __syncwarp();
-      }
-      // ---- O += P V, P as a sum of two values of the type
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        uint32_t hi4[4], lo4[4];
+          for (int i = 0; i < KK; ++i) {
+            o[nb][i][0] *= f[0];
+            o[nb][i][1] *= f[1];
+            o[nb][i][2] *= f[0];
+            o[nb][i][3] *= f[1];
+          }
+        }
+      }
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int i = 4 * kk + (e >> 1) * 2;  // e: 0 row, 1 row + 8, 2 row (k + 8), 3 row + 8 (k + 8)
-          const bool up = e & 1;
-          if (up && !two) {
-            hi4[e] = lo4[e] = 0u;
-            continue;
-          }
-          const float p = up ? s1[i] : s0[i], r = up ? s1[i + 1] : s0[i + 1];
-          hi4[e] = pack2<F16>(p, r);
-          const float2 h = unpack2<F16>(hi4[e]);
-          lo4[e] = pack2<F16>(p - h.x, r - h.y);
+          const float z = m[nb][e & 1] == -INFINITY ? 0.f : m[nb][e & 1];
+          s[nb][e] = ex2(s[nb][e] - z);
+          l[nb][e & 1] += s[nb][e];
         }
-        const int row = kk * 16 + vrow;
-        const uint32_t va = sv + (row >> g.logP) * (P * D * 2) + (row & (P - 1)) * 128;
+      if (!plain) {
+        // which keys no row sees, and which only some see (bit = key of the warp)
+        const int pf = max(0, it.pf), j = j0 + (lane & 15), k = warp * 16 + (lane & 15);
+        const bool good = !(bad >> (k >> g.logP) & 1);
+        const bool any = good && j <= it.pl && (W == 0 || j > pf - W || j < S);
+        const bool all = good && j <= pf && (W == 0 || j > it.pl - W || j < S);
+        const unsigned cut = __ballot_sync(0xffffffffu, !all) & 0xffffu, some = __ballot_sync(0xffffffffu, any && !all) & 0xffffu;
+        auto vptr = [&](int key, int c) {  // address of 16 bytes: columns 8 c .. of V[key]
+          const int r = key & (P - 1);
+          return sv + (key >> g.logP) * boxb + (c >> 3) * halfb + r * 128 + ((uint32_t)((c & 7) ^ (r & 7)) << 4);
+        };
+        for (unsigned ms = some; ms; ms &= ms - 1) {
+          const int i = __ffs(ms) - 1, jj = j0 + i, src = (i & 7) * 4 + (lane & 3);
 #pragma unroll
-        for (int n = 0; n < NT; n += 2) {
-          uint32_t vf[4];
-          const int c = vch0 + n;
-          ldsm4t(va + (c >> 3) * (P * 128) + (((uint32_t)(c & 7) << 4) ^ vxor), vf);
-          mma<F16>(o[n], hi4[0], hi4[1], hi4[2], hi4[3], vf[0], vf[1]);
-          mma<F16>(o[n + 1], hi4[0], hi4[1], hi4[2], hi4[3], vf[2], vf[3]);
-          mma<F16>(o[n], lo4[0], lo4[1], lo4[2], lo4[3], vf[0], vf[1]);
-          mma<F16>(o[n + 1], lo4[0], lo4[1], lo4[2], lo4[3], vf[2], vf[3]);
+          for (int nb = 0; nb < NB; ++nb) {
+            const float pa = __shfl_sync(0xffffffffu, i < 8 ? s[nb][0] : s[nb][2], src);
+            const float pb = __shfl_sync(0xffffffffu, i < 8 ? s[nb][1] : s[nb][3], src);
+            const bool va = jj <= pos[nb][0] && (W == 0 || jj > pos[nb][0] - W || jj < S);
+            const bool vb = jj <= pos[nb][1] && (W == 0 || jj > pos[nb][1] - W || jj < S);
+#pragma unroll
+            for (int d = 0; d < KK; ++d)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                uint16_t bits;
+                asm volatile("ld.shared.b16 %0, [%1];" : "=h"(bits) : "r"(vptr(warp * 16 + i, 2 * d + e) + 2 * (lane >> 2)));
+                const float vv = unpack2<F16>(bits).x;
+                if (va) o[nb][d][2 * e] = fmaf(pa, vv, o[nb][d][2 * e]);
+                if (vb) o[nb][d][2 * e + 1] = fmaf(pb, vv, o[nb][d][2 * e + 1]);
+              }
+          }
+        }
+        __syncwarp();
+        for (int i = lane; i < 16 * (D / 8); i += 32) {
+          const int key = i / (D / 8);
+          if (cut >> key & 1)
+            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vptr(warp * 16 + key, i % (D / 8))), "r"(0) : "memory");
+        }
+        __syncwarp();
+      }
+      // ---- O^T += V^T P^T, P as a sum of two values of the type
+      uint32_t hi[NB][2], lw[NB][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t h = pack2<F16>(s[nb][2 * e], s[nb][2 * e + 1]);
+          const float2 f = unpack2<F16>(h);
+          hi[nb][e] = transpose8x8(h);
+          lw[nb][e] = transpose8x8(pack2<F16>(s[nb][2 * e] - f.x, s[nb][2 * e + 1] - f.y));
+        }
+#pragma unroll
+      for (int d = 0; d < KK; ++d) {
+        uint32_t vf[4];
+        ldsm4t(sv + voff + (d >> 2) * halfb + (((d & 3) << 5) ^ vx), vf);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          mma<F16>(o[nb][d], vf[0], vf[1], vf[2], vf[3], hi[nb][0], hi[nb][1]);
+          mma<F16>(o[nb][d], vf[0], vf[1], vf[2], vf[3], lw[nb][0], lw[nb][1]);
         }
       }
       if (!plain) fence_proxy_async_shared();  // the zeros before the next TMA box
       __syncwarp();
       if (lane == 0) mbar_arrive(empty + 8 * st);
-      sbuf ^= 1;
       if (++st == kStages) {
         st = 0;
         ph ^= 1;
       }
     }
-    // ---- the span's sums, folded onto the spans before it
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-    if (two) {
-      l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    // ---- the span's end: the warps' sums added up in warp order
+    float ms[NB], ls[NB];
+    float4 os[NB][NH];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], d);
+        if (lane < 4) {
+          s_ml[0][warp][8 * nb + ra + e] = m[nb][e];
+          s_ml[1][warp][8 * nb + ra + e] = l[nb][e];
+        }
+      }
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      float f[4];
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s_o[warp][ra + (e & 1)][16 * d + 8 * (e >> 1) + (lane >> 2)] = o[nb][4 * h + d][e];
+        named_bar_sync(1, 128);
+        if (h == 0) {
+          float top = s_ml[0][0][8 * nb + mrow];
+#pragma unroll
+          for (int w = 1; w < 4; ++w) top = fmaxf(top, s_ml[0][w][8 * nb + mrow]);
+          const float z = top == -INFINITY ? 0.f : top;
+          ms[nb] = top;
+          ls[nb] = 0.f;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            f[w] = ex2(s_ml[0][w][8 * nb + mrow] - z);
+            ls[nb] = __fmaf_rn(s_ml[1][w][8 * nb + mrow], f[w], ls[nb]);
+          }
+        }
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float4 u = *reinterpret_cast<const float4*>(&s_o[w][mrow][mcol]);
+          y = make_float4(__fmaf_rn(u.x, f[w], y.x), __fmaf_rn(u.y, f[w], y.y), __fmaf_rn(u.z, f[w], y.z),
+                          __fmaf_rn(u.w, f[w], y.w));
+        }
+        os[nb][h] = y;
+        named_bar_sync(1, 128);  // before the buffer is written again
+      }
     }
+    // ---- folded onto the spans before it
     const int c0 = cta_of(ioff);
     const int key = items <= nc ? (b * g.RT + rt) * Hkv + hk : c0;
     if (run0 != 0) {
-      put(part_of(key, span), m0, m1, l0, l1, o);
-    } else if (span == 0) {
-      M0 = m0; M1 = m1; L0 = l0; L1 = l1;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) O[n][e] = o[n][e];
+      put(part_of(key, span), ms, ls, os);
     } else {
-      float a0, b0, a1, b1;
-      fold_ml(M0, L0, m0, l0, a0, b0);
-      fold_ml(M1, L1, m1, l1, a1, b1);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        O[n][0] = fold_o(O[n][0], o[n][0], a0, b0);
-        O[n][1] = fold_o(O[n][1], o[n][1], a0, b0);
-        O[n][2] = fold_o(O[n][2], o[n][2], a1, b1);
-        O[n][3] = fold_o(O[n][3], o[n][3], a1, b1);
+      for (int nb = 0; nb < NB; ++nb) {
+        if (span == 0) {
+          M[nb] = ms[nb];
+          L[nb] = ls[nb];
+#pragma unroll
+          for (int h = 0; h < NH; ++h) O[nb][h] = os[nb][h];
+        } else {
+          float fa, fb;
+          fold_ml(M[nb], L[nb], ms[nb], ls[nb], fa, fb);
+#pragma unroll
+          for (int h = 0; h < NH; ++h) O[nb][h] = fold_o4(O[nb][h], os[nb][h], fa, fb);
+        }
       }
     }
     const bool item_end = span + 1 == it.nspan, run_end = item_end || ioff + (span + 1) * it.sp >= hi;
     if (run_end && run0 == 0 && item_end) {
-      out_rows(M0, M1, L0, L1, O);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const int rr = row_of(8 * nb + mrow);
+        if (rr < 0) continue;
+        const long long at = ((long long)b * n_q + rr / G) * g.a.Hq + hk * G + rr % G;
+        put_row<F16, D>(M[nb], L[nb], O[nb], g.a.o + at * D + mcol,
+                        g.a.lse && warp == 0 && (lane & 3) == 0 ? g.a.lse + at : nullptr);
+      }
     } else if (run_end) {
-      if (run0 == 0) put(part_of(key, span), M0, M1, L0, L1, O);
+      if (run0 == 0) put(part_of(key, span), M, L, O);
       __threadfence();
       named_bar_sync(1, 128);
       if (tid == 0) {
@@ -696,11 +708,11 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_con
   __threadfence();
   for (int i = 0; i < s_njoin; ++i) {
     const Join jn = s_join[i];
-    for (int h = 0; h < (two ? 2 : 1); ++h) {
-      const int rr = jn.rt * 16 + qr + 8 * h;
+    for (int nb = 0; nb < NB; ++nb) {
+      const int rr = jn.rt * 16 + 8 * nb + mrow;
       if (rr >= n_q * G) continue;
       const long long at = ((long long)jn.b * n_q + rr / G) * g.a.Hq + jn.hk * G + rr % G;
-      join_row<F16, D>(jn.p, pstride, jn.n, g.R, qr + 8 * h, warp * (D / 4) + qc, g.a.o + at * D,
+      join_row<F16, D>(jn.p, pstride, jn.n, g.R, 8 * nb + mrow, mcol, g.a.o + at * D,
                        g.a.lse && warp == 0 && (lane & 3) == 0 ? g.a.lse + at : nullptr);
     }
   }
@@ -725,15 +737,15 @@ int sm_count(int* dev_out) {
 
 constexpr int kMaxCtas = 2 * 304;  // counters and partials of the largest grid
 
-template <bool F16, int D>
-cudaError_t launch_one(DecArgs& g, int sms, int dev, cudaStream_t st) {
+template <bool F16, int D, int NB>
+cudaError_t launch_nb(DecArgs& g, int sms, int dev, cudaStream_t st) {
   constexpr int smem = kRing + 1024;
   static std::mutex mu;
   static bool configured[64] = {};
   {
     std::lock_guard<std::mutex> lk(mu);
     if (!configured[dev]) {
-      const cudaError_t e = cudaFuncSetAttribute(decode_kernel<F16, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      const cudaError_t e = cudaFuncSetAttribute(decode_kernel<F16, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (e != cudaSuccess) {
         cudaGetLastError();
         return e;
@@ -752,9 +764,14 @@ cudaError_t launch_one(DecArgs& g, int sms, int dev, cudaStream_t st) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   launch_begin(K_ATTN_DECODE, st);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_kernel<F16, D>, g);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_kernel<F16, D, NB>, g);
   launch_end(st);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <bool F16, int D>
+cudaError_t launch_one(DecArgs& g, int sms, int dev, cudaStream_t st) {
+  return g.R > 8 ? launch_nb<F16, D, 2>(g, sms, dev, st) : launch_nb<F16, D, 1>(g, sms, dev, st);
 }
 
 }  // namespace
