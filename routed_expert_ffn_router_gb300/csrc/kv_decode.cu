@@ -4,23 +4,24 @@
 // Items and spans. An item is (sequence, tile of 16 query rows, KV head): the
 // rows are the window's new tokens times the query heads of the KV head, and
 // the item's keys and values are read once for all of them. An item's visible
-// 64-token tiles (first tokens that stay visible, then the window) are cut
-// into spans (span_tiles). Every span is computed by itself and the spans are
+// tiles (first tokens that stay visible, then the window) are cut into
+// spans (span_log). Every span is computed by itself and the spans are
 // folded in order,
 //   M' = max(M, m),  L' = L 2^(M - M') + l 2^(m - M'),  O' = O 2^(M - M') + o 2^(m - M'),
 // so a row's result depends on its own sequence only, not on the other
 // sequences nor on how the spans fall on the CTAs.
 //
-// CTAs. Two per SM, each a producer warp and four consumer warps around a
-// 96 KB ring of tiles (K and V of 64 tokens, TMA boxes of a page's rows, 128-byte
-// swizzle). The list of all items' tiles is divided evenly; a CTA takes the
+// CTAs. A producer warp and, for each 8 query rows of a tile, a group of four
+// consumer warps around a ring of tiles (K and V of 64 or 128 tokens, TMA boxes of
+// a page's rows, 128-byte swizzle): items of up to 8 rows run two
+// CTAs per SM with 96 KB of tiles each, items of 16 rows one CTA with 192 KB. The list of all items' tiles is divided evenly; a CTA takes the
 // spans that start in its part. It folds consecutive spans of an item in
 // registers; an item that lies in several CTAs is joined, through partials in
 // the workspace, by the CTA that finishes last.
 //
-// A tile. Warp w has its keys 16 w .. 16 w + 15 to itself: S^T = K Q^T (mma
-// m16n8k16, the 8 query rows of a block as N, so no half of the product is
-// padding), the softmax of its 16 x 8 scores in registers, P^T turned into the B
+// A tile. A warp has a quarter of its keys, in blocks of 16, to itself: S^T =
+// K Q^T (mma m16n8k16 with its group's 8 query rows as N, so no half of the
+// product is padding), the softmax of its 16 x 8 scores in registers, P^T turned into the B
 // operand by movmatrix, O^T += V^T P^T over all of D. The warps meet only at a
 // span's end, where their (m, l, o) are added up through shared memory in warp
 // order. A probability enters the product with V as a sum of two values of the
@@ -43,9 +44,16 @@ namespace kv {
 
 namespace {
 
-constexpr int kTile = 64;
-constexpr int kDecThreads = 160;
-constexpr int kRing = 96 * 1024;
+// Tokens of a tile for RG groups of rows: a warp has 16 or 32 keys of it. With 32
+// its chain of products and reductions is paid half as often (what one CTA per
+// SM, or 16 KB of keys and values per 64 tokens, needs to keep up with the HBM).
+__host__ __device__ constexpr int tile_of(int D, int RG) { return D == 128 && RG == 1 ? 64 : 128; }
+// RG groups of four consumer warps and the producer.
+template <int RG>
+__host__ __device__ constexpr int dec_threads() { return 32 * (4 * RG + 1); }
+template <int RG>
+__host__ __device__ constexpr int dec_ring() { return RG * 96 * 1024; }
+constexpr int kPairBar = 4;             // named barriers 4 .. 7: the warps of two groups with the same keys (1, 2: a group's)
 constexpr int kOPitch = 64 + 4;         // floats per row of the buffer in which the warps' O meet
 constexpr int kSeqCap = 128;            // sequences per launch
 constexpr int kCntBase = 2048;          // this kernel's counters in the workspace head
@@ -57,22 +65,22 @@ struct DecArgs {
   Attn a;
   int b0;             // first sequence of this launch; r.B the sequences in it
   int RT;             // row tiles per sequence
-  int logP;           // log2 of a box's rows: min(page, 64)
+  int logP;           // log2 of a box's rows: min(page, tile)
   int logpage;
   int max_span;       // spans of an item at most
-  int most_spans;     // the same, as the rule for their length takes it
+  int span_c, most_spans;  // the rule for their length
   float* part;        // [keys][max_span][R][D + 2]
   int R;              // rows of a partial: 8 or 16
   int32_t *status, *cnt;
 };
 
-// Tiles of a span, by the item's own length and the call's heads: 2^k, the
-// smallest with at most 16 2^k spans (their number and their length both grow
+// log2 of a span's tiles, by the item's own length and the call's heads: the
+// smallest k with at most c 2^k spans (their number and their length both grow
 // as the square root of the length) and at most most_spans.
-__host__ __device__ inline int span_tiles(int nvis, int most_spans) {
+__host__ __device__ inline int span_log(int nvis, int c, int most_spans) {
   int k = 0;
-  while (nvis > (16LL << (2 * k)) || nvis > ((long long)most_spans << k)) ++k;
-  return 1 << k;
+  while (nvis > ((long long)c << (2 * k)) || nvis > ((long long)most_spans << k)) ++k;
+  return k;
 }
 
 // (m, l, o) of a span folded into (M, L, O): written with explicit rounding so
@@ -81,6 +89,11 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ int add_acq_rel_gpu(int* p, int v) {
+  int old;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
 }
 __device__ __forceinline__ void fold_ml(float& M, float& L, float m, float l, float& a, float& b) {
   const float n = fmaxf(M, m), z = n == -INFINITY ? 0.f : n;
@@ -100,7 +113,7 @@ struct Item {
   int slot, len;
   int pf, pl;        // tokens of its first and last row (pl < 0: nothing is seen)
   int ns, wt, nvis;  // tiles of first tokens, first window tile, visible tiles
-  int sp, nspan;
+  int ks, nspan;     // spans of 2^ks tiles
   __device__ int tile(int v) const { return v < ns ? v : v - ns + wt; }
 };
 
@@ -165,59 +178,68 @@ struct Join {
 };
 
 // The fold of n partials of one row (from p on, pstride apart) in order, in the
-// columns col + 64 h .. + 3; eight partials in flight per lane.
+// columns col + 64 h .. + 3; the next four partials are on their way while four
+// are folded.
 template <bool F16, int D>
 __device__ __forceinline__ void join_row(const float* p, long long pstride, int n, int R, int row, int col, uint16_t* o,
                                          float* lse) {
-  constexpr int NH = D / 64, U = 8;
+  constexpr int NH = D / 64, U = 4;
   float M = 0.f, L = 0.f;
   float4 O[NH];
-  const float* po = p + 2 * R + row * D + col;
-  for (int s = 0; s < n; s += U) {
-    float m[U], l[U];
-    float4 w[U][NH];
+  float m[2][U], l[2][U];
+  float4 w[2][U][NH];
+  auto get = [&](int s, float (&m)[U], float (&l)[U], float4 (&w)[U][NH]) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (s + u < n) {
-        m[u] = ldg_cg_f32(p + (s + u) * pstride + row);
-        l[u] = ldg_cg_f32(p + (s + u) * pstride + R + row);
+    for (int u = 0; u < U; ++u) {
+      const float* q = p + min(s + u, n - 1) * pstride;
+      m[u] = ldg_cg_f32(q + row);
+      l[u] = ldg_cg_f32(q + R + row);
 #pragma unroll
-        for (int h = 0; h < NH; ++h) w[u][h] = __ldcg(reinterpret_cast<const float4*>(po + (s + u) * pstride + 64 * h));
-      }
+      for (int h = 0; h < NH; ++h) w[u][h] = __ldcg(reinterpret_cast<const float4*>(q + 2 * R + row * D + col + 64 * h));
+    }
+  };
+  get(0, m[0], l[0], w[0]);
+  for (int s0 = 0; s0 < n; s0 += 2 * U)
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (s + u < n) {
+    for (int k = 0; k < 2; ++k) {
+      const int s = s0 + k * U;
+      if (s >= n) break;
+      if (s + U < n) get(s + U, m[k ^ 1], l[k ^ 1], w[k ^ 1]);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (s + u >= n) break;
         if (s + u == 0) {
-          M = m[u];
-          L = l[u];
+          M = m[k][u];
+          L = l[k][u];
 #pragma unroll
-          for (int h = 0; h < NH; ++h) O[h] = w[u][h];
+          for (int h = 0; h < NH; ++h) O[h] = w[k][u][h];
         } else {
           float a, b;
-          fold_ml(M, L, m[u], l[u], a, b);
+          fold_ml(M, L, m[k][u], l[k][u], a, b);
 #pragma unroll
-          for (int h = 0; h < NH; ++h) O[h] = fold_o4(O[h], w[u][h], a, b);
+          for (int h = 0; h < NH; ++h) O[h] = fold_o4(O[h], w[k][u][h], a, b);
         }
       }
-  }
+    }
   put_row<F16, D>(M, L, O, o + col, lse);
 }
 
-// NB: blocks of 8 query rows of an item.
-template <bool F16, int D, int NB>
-__global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_constant__ DecArgs g) {
+template <bool F16, int D, int RG>
+__global__ void __launch_bounds__(dec_threads<RG>(), 3 - RG) decode_kernel(const __grid_constant__ DecArgs g) {
+  constexpr int kDecThreads = dec_threads<RG>();
+  constexpr int kTile = tile_of(D, RG), KB = kTile / 64;  // KB blocks of 16 keys per warp
   constexpr int kStage = kTile * D * 4;      // K and V of a tile
-  constexpr int kStages = kRing / kStage;
+  constexpr int kStages = dec_ring<RG>() / kStage;
   constexpr int KK = D / 16, NH = D / 64;
   extern __shared__ __align__(1024) uint8_t smem_dec[];
   __shared__ __align__(8) uint64_t s_bar[2 * kStages];
   __shared__ uint32_t s_badbox[kStages];
   __shared__ int s_off[kSeqCap + 1], s_len[kSeqCap], s_slot[kSeqCap];
-  __shared__ __align__(16) float s_o[4][8][kOPitch];  // the warps' O: 8 rows, 64 columns at a time
-  __shared__ float s_ml[2][4][8 * NB];                // the warps' maxima and sums
-  __shared__ int s_scan[8];
-  __shared__ Join s_join[2];  // split items that this CTA completes: its first and its last at most
-  __shared__ int s_njoin;
+  __shared__ __align__(16) float s_o[RG][4][8][kOPitch];  // the warps' O: 8 rows, 64 columns at a time
+  __shared__ float s_ml[RG][2][4][8];                     // the warps' maxima and sums
+  __shared__ int s_scan[4 * RG + 1];
+  __shared__ Join s_join[RG][2];  // split items that this CTA completes: its first and its last at most
+  __shared__ int s_njoin[RG];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int B = g.r.B, G = g.a.G, n_q = g.r.n_q, W = g.a.window, S = g.a.n_sink, Hkv = g.c.Hkv;
@@ -226,10 +248,10 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_con
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, 4);
+      mbar_init(empty + 8 * i, 4 * RG);
     }
     fence_barrier_init();
-    s_njoin = 0;
+    for (int i = 0; i < RG; ++i) s_njoin[i] = 0;
   }
   griddep_wait();  // the rows' keys and values of an append before this launch
 
@@ -238,8 +260,8 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_con
     it.slot = slot;
     it.len = len;
     const int r1 = min(n_q * G, rt * 16 + 16);
-    it.pf = len - n_q + rt * 16 / G;
-    it.pl = slot < 0 ? -1 : len - n_q + (r1 - 1) / G;
+    it.pf = len - n_q + (rt ? rt * 16 / G : 0);
+    it.pl = slot < 0 ? -1 : len - n_q + (r1 == n_q * G ? n_q - 1 : (r1 - 1) / G);
     it.ns = it.wt = it.nvis = 0;
     if (it.pl >= 0) {
       const int from = W > 0 ? max(0, max(0, it.pf) - W + 1) : 0;
@@ -247,8 +269,8 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_con
       it.wt = max(from / kTile, it.ns);
       it.nvis = it.ns + it.pl / kTile - it.wt + 1;
     }
-    it.sp = span_tiles(it.nvis, g.most_spans);
-    it.nspan = max(1, (it.nvis + it.sp - 1) / it.sp);
+    it.ks = span_log(it.nvis, g.span_c, g.most_spans);
+    it.nspan = max(1, (it.nvis + (1 << it.ks) - 1) >> it.ks);
     return it;
   };
 
@@ -310,7 +332,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_con
       if (lo - ioff < w * Hkv || rt + 1 == g.RT) {
         hk = min(Hkv - 1, (lo - ioff) / w);
         ioff += hk * w;
-        span = (lo - ioff + it.sp - 1) / it.sp;
+        span = (lo - ioff + (1 << it.ks) - 1) >> it.ks;
         break;
       }
       ioff += w * Hkv;
@@ -332,17 +354,17 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_con
   bool more = lo < hi;
   if (more && span >= it.nspan) more = next_item();
 
-  if (warp == 4) {
+  if (warp == 4 * RG) {
     // ================= producer =================
     const int P = 1 << g.logP, nbox = kTile >> g.logP, box = P * D * 2;
     int st = 0, ph = 1;
     bool ok = true;
-    while (more && ok && ioff + span * it.sp < hi) {
-      const int v0 = span * it.sp, v1 = min(it.nvis, v0 + it.sp);
+    while (more && ok && ioff + (span << it.ks) < hi) {
+      const int v0 = span << it.ks, v1 = min(it.nvis, v0 + (1 << it.ks));
       const int from = W > 0 ? max(0, max(0, it.pf) - W + 1) : 0, first = min(S, from);
       const int32_t* tab = g.c.table + (long long)it.slot * g.c.max_pages;
       // page numbers of 32 boxes at a time, one per lane
-      const int per = 32 >> (6 - g.logP);  // tiles whose boxes fill the lanes
+      const int per = 32 / nbox;  // tiles whose boxes fill the lanes
       for (int vb = v0; vb < v1 && ok; vb += per) {
         int row = -1;       // the box's first row in the pool; -1 not needed, -2 bad page
         {
@@ -388,210 +410,212 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_con
   }
 
   // ================= consumers =================
+  const int grp = warp >> 2, wg = warp & 3, bar_id = 1 + grp;  // the group's rows: 8 grp .. of the item
   const int P = 1 << g.logP, boxb = P * D * 2, halfb = P * 128;
   // score product: this lane's ldmatrix row of the warp's keys; value product: the same
-  const int kr = warp * 16 + (lane & 15), vr = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
-  const uint32_t koff = (kr >> g.logP) * boxb + (kr & (P - 1)) * 128, voff = (vr >> g.logP) * boxb + (vr & (P - 1)) * 128;
+  uint32_t koff[KB], voff[KB];
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb) {
+    const int k0 = (wg * KB + kb) * 16, kr = k0 + (lane & 15), vr = k0 + (lane & 7) + ((lane >> 4) << 3);
+    koff[kb] = (kr >> g.logP) * boxb + (kr & (P - 1)) * 128;
+    voff[kb] = (vr >> g.logP) * boxb + (vr & (P - 1)) * 128;
+  }
   const uint32_t kx = (uint32_t)((lane >> 4) ^ (lane & 7)) << 4, vx = (uint32_t)(((lane >> 3) & 1) ^ (lane & 7)) << 4;
-  const int key0 = warp * 16 + (lane >> 2);  // scores: keys key0, key0 + 8; rows 8 nb + ra, + 1
   const int ra = 2 * (lane & 3);
-  const int mrow = lane >> 2, mcol = warp * 16 + 4 * (lane & 3);  // merged: row 8 nb + mrow, columns 64 h + mcol .. + 3
+  const int mrow = lane >> 2, mcol = wg * 16 + 4 * (lane & 3);  // merged: row mrow, columns 64 h + mcol .. + 3
   const float sc = g.a.scale * 1.4426950408889634f;
   int st = 0, ph = 0;
 
-  uint32_t q[NB][KK][2];
-  int pos[NB][2];                // tokens of this lane's score rows (-1: no row, or before the first token)
-  float M[NB], L[NB];
-  float4 O[NB][NH];
+  uint32_t q[KK][2];
+  int pos[2];                    // tokens of this lane's score rows ra, ra + 1 (-1: no row, or before the first token)
+  float M = -INFINITY, L = 0.f;
+  float4 O[NH];
   int run0 = -1;                 // first span of the current run of spans of one item
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    M[nb] = -INFINITY;
-    L[nb] = 0.f;
-  }
 
   const int items = B * Hkv * g.RT;
   const long long pstride = (long long)g.R * (D + 2);
   // partials of an item split over CTAs: [span][m of R rows, l of R rows, o [R][D]]
   auto part_of = [&](int key, int s) { return g.part + ((long long)key * g.max_span + s) * pstride; };
-  auto put = [&](float* p, const float (&m)[NB], const float (&l)[NB], const float4 (&o)[NB][NH]) {
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const int r = 8 * nb + mrow;
-      if (warp == 0 && (lane & 3) == 0) {
-        p[r] = m[nb];
-        p[g.R + r] = l[nb];
-      }
-#pragma unroll
-      for (int h = 0; h < NH; ++h) *reinterpret_cast<float4*>(p + 2 * g.R + r * D + 64 * h + mcol) = o[nb][h];
+  // an item's place among the partials
+  auto key_of = [&] { return items <= nc ? (b * g.RT + rt) * Hkv + hk : cta_of(ioff); };
+  auto put = [&](float* p, float m, float l, const float4 (&o)[NH]) {
+    const int r = 8 * grp + mrow;
+    if (wg == 0 && (lane & 3) == 0) {
+      p[r] = m;
+      p[g.R + r] = l;
     }
+#pragma unroll
+    for (int h = 0; h < NH; ++h) *reinterpret_cast<float4*>(p + 2 * g.R + r * D + 64 * h + mcol) = o[h];
   };
-  // index of the item's local row r among the sequence's rows, -1 if there is none
+  // token of a sequence's row, and the row's place in a tensor [row][Hq]
+  auto token_of = [&](int rr) { return n_q == 1 ? 0 : rr / G; };
+  auto place_of = [&](int b, int hk, int rr) {
+    const int i = token_of(rr);
+    return ((long long)b * n_q + i) * g.a.Hq + hk * G + rr - i * G;
+  };
+  // index of the group's row r among the sequence's rows, -1 if there is none
   auto row_of = [&](int r) {
-    const int rr = rt * 16 + r;
+    const int rr = rt * 16 + 8 * grp + r;
     return rr < n_q * G ? rr : -1;
   };
 
   bool ok = true;
-  while (more && ioff + span * it.sp < hi) {
+  while (more && ioff + (span << it.ks) < hi) {
     if (run0 < 0) {  // a new item: its query rows as B operands
       run0 = span;
+      const int rr = row_of(lane >> 2), qi = token_of(rr);
+      const uint16_t* qp = g.a.q + ((long long)b * n_q + qi) * g.a.q_stride + (hk * G + rr - qi * G) * D + ra;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        const int rr = row_of(8 * nb + (lane >> 2));
-        const uint16_t* qp = g.a.q + ((long long)b * n_q + rr / G) * g.a.q_stride + (hk * G + rr % G) * D + ra;
+      for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk)
+        for (int e = 0; e < 2; ++e)
+          q[kk][e] = rr >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(qp + kk * 16 + e * 8)) : 0u;
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            q[nb][kk][e] = rr >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(qp + kk * 16 + e * 8)) : 0u;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = row_of(8 * nb + ra + e);
-          pos[nb][e] = r >= 0 && it.slot >= 0 ? it.len - n_q + r / G : -1;
-        }
+      for (int e = 0; e < 2; ++e) {
+        const int r = row_of(ra + e);
+        pos[e] = r >= 0 && it.slot >= 0 ? it.len - n_q + token_of(r) : -1;
       }
     }
-    float m[NB][2], l[NB][2], o[NB][KK][4];
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[KK][4];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      m[nb][0] = m[nb][1] = -INFINITY;
-      l[nb][0] = l[nb][1] = 0.f;
-#pragma unroll
-      for (int i = 0; i < KK; ++i) o[nb][i][0] = o[nb][i][1] = o[nb][i][2] = o[nb][i][3] = 0.f;
-    }
-    const int v1 = min(it.nvis, (span + 1) * it.sp);
-    for (int v = span * it.sp; v < v1; ++v) {
-      const int j0 = it.tile(v) * kTile + warp * 16;  // the warp's first key
+    for (int i = 0; i < KK; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    const int v1 = min(it.nvis, (span + 1) << it.ks);
+    for (int v = span << it.ks; v < v1; ++v) {
+      const int j0 = it.tile(v) * kTile + wg * 16 * KB;  // the warp's first key
       // after an expired wait (the status word says that the results are
       // incomplete) a warp goes on without waiting, so that all meet at every barrier
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait_short(full + 8 * st, ph, g.status));
       const uint32_t bad = *(volatile uint32_t*)&s_badbox[st];
-      const uint32_t sk = ring + st * kStage + koff, sv = ring + st * kStage + kStage / 2;
-      // ---- scores
-      float x[NB][2][4] = {};
+      const uint32_t sk = ring + st * kStage, sv = sk + kStage / 2;
+      // ---- scores: keys 16 kb + lane / 4, + 8; rows ra, ra + 1
+      float s[KB][4];
 #pragma unroll
-      for (int kk = 0; kk < KK; ++kk) {
-        uint32_t kf[4];
-        ldsm4(sk + (kk >> 2) * halfb + (((kk & 3) << 5) ^ kx), kf);
+      for (int kb = 0; kb < KB; ++kb) {
+        float x[2][4] = {};
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) mma<F16>(x[nb][kk & 1], kf[0], kf[1], kf[2], kf[3], q[nb][kk][0], q[nb][kk][1]);
+        for (int kk = 0; kk < KK; ++kk) {
+          uint32_t kf[4];
+          ldsm4(sk + koff[kb] + (kk >> 2) * halfb + (((kk & 3) << 5) ^ kx), kf);
+          mma<F16>(x[kk & 1], kf[0], kf[1], kf[2], kf[3], q[kk][0], q[kk][1]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[kb][e] = (x[0][e] + x[1][e]) * sc;
       }
-      float s[NB][4];
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[nb][e] = (x[nb][0][e] + x[nb][1][e]) * sc;
-      const bool plain = bad == 0 && it.pf >= 0 && j0 + 15 <= it.pf && (W == 0 || j0 > it.pl - W || j0 + 16 <= S);
+      const bool plain =
+          bad == 0 && it.pf >= 0 && j0 + 16 * KB - 1 <= it.pf && (W == 0 || j0 > it.pl - W || j0 + 16 * KB <= S);
       if (!plain) {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+        for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int k = key0 + (e >> 1) * 8, j = j0 - warp * 16 + k, p = pos[nb][e & 1];
-            if (!(j <= p && (W == 0 || j > p - W || j < S)) || (bad >> (k >> g.logP) & 1)) s[nb][e] = -INFINITY;
+            const int k = 16 * kb + 8 * (e >> 1) + (lane >> 2), j = j0 + k, p = pos[e & 1];
+            if (!(j <= p && (W == 0 || j > p - W || j < S)) || (bad >> ((wg * 16 * KB + k) >> g.logP) & 1))
+              s[kb][e] = -INFINITY;
           }
       }
       // ---- running maximum, probabilities
-      bool raise = false;
-      float top[NB][2];
+      float top[2];
+      bool up[2];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int e = 0; e < 2; ++e) {
+        float y = fmaxf(s[0][e], s[0][e + 2]);
+#pragma unroll
+        for (int kb = 1; kb < KB; ++kb) y = fmaxf(y, fmaxf(s[kb][e], s[kb][e + 2]));
+        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+        top[e] = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+        up[e] = top[e] > m[e] + 8.f || (m[e] == -INFINITY && top[e] > m[e]);
+      }
+      if (__any_sync(0xffffffffu, up[0] || up[1])) {
+        float f[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float y = fmaxf(s[nb][e], s[nb][e + 2]);
-          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
-          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
-          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
-          top[nb][e] = y;
-          raise = raise || y > m[nb][e] + 8.f || (m[nb][e] == -INFINITY && y > m[nb][e]);
+          f[e] = up[e] ? ex2(m[e] - top[e]) : 1.f;
+          m[e] = up[e] ? top[e] : m[e];
+          l[e] *= f[e];
         }
-      if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          float f[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const bool up = top[nb][e] > m[nb][e] + 8.f || (m[nb][e] == -INFINITY && top[nb][e] > m[nb][e]);
-            f[e] = up ? ex2(m[nb][e] - top[nb][e]) : 1.f;
-            m[nb][e] = up ? top[nb][e] : m[nb][e];
-            l[nb][e] *= f[e];
-          }
-#pragma unroll
-          for (int i = 0; i < KK; ++i) {
-            o[nb][i][0] *= f[0];
-            o[nb][i][1] *= f[1];
-            o[nb][i][2] *= f[0];
-            o[nb][i][3] *= f[1];
-          }
+        for (int i = 0; i < KK; ++i) {
+          o[i][0] *= f[0];
+          o[i][1] *= f[1];
+          o[i][2] *= f[0];
+          o[i][3] *= f[1];
         }
       }
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int e = 0; e < 4; ++e) {
+        const float z = m[e & 1] == -INFINITY ? 0.f : m[e & 1];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float z = m[nb][e & 1] == -INFINITY ? 0.f : m[nb][e & 1];
-          s[nb][e] = ex2(s[nb][e] - z);
-          l[nb][e & 1] += s[nb][e];
+        for (int kb = 0; kb < KB; ++kb) {
+          s[kb][e] = ex2(s[kb][e] - z);
+          l[e & 1] += s[kb][e];
         }
+      }
       if (!plain) {
-        // which keys no row sees, and which only some see (bit = key of the warp)
-        const int pf = max(0, it.pf), j = j0 + (lane & 15), k = warp * 16 + (lane & 15);
-        const bool good = !(bad >> (k >> g.logP) & 1);
+        // which keys no row of the item sees, and which only some see (bit = key of the warp)
+        const int pf = max(0, it.pf), kl = lane & (16 * KB - 1), j = j0 + kl;
+        const bool good = !(bad >> ((wg * 16 * KB + kl) >> g.logP) & 1);
         const bool any = good && j <= it.pl && (W == 0 || j > pf - W || j < S);
         const bool all = good && j <= pf && (W == 0 || j > it.pl - W || j < S);
-        const unsigned cut = __ballot_sync(0xffffffffu, !all) & 0xffffu, some = __ballot_sync(0xffffffffu, any && !all) & 0xffffu;
-        auto vptr = [&](int key, int c) {  // address of 16 bytes: columns 8 c .. of V[key]
-          const int r = key & (P - 1);
+        constexpr unsigned kKeys = KB == 2 ? 0xffffffffu : 0xffffu;
+        const unsigned cut = __ballot_sync(0xffffffffu, !all) & kKeys, some = __ballot_sync(0xffffffffu, any && !all) & kKeys;
+        auto vptr = [&](int k, int c) {  // address of 16 bytes: columns 8 c .. of V of the warp's key k
+          const int key = wg * 16 * KB + k, r = key & (P - 1);
           return sv + (key >> g.logP) * boxb + (c >> 3) * halfb + r * 128 + ((uint32_t)((c & 7) ^ (r & 7)) << 4);
         };
         for (unsigned ms = some; ms; ms &= ms - 1) {
           const int i = __ffs(ms) - 1, jj = j0 + i, src = (i & 7) * 4 + (lane & 3);
+          float pa = 0.f, pb = 0.f;
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            const float pa = __shfl_sync(0xffffffffu, i < 8 ? s[nb][0] : s[nb][2], src);
-            const float pb = __shfl_sync(0xffffffffu, i < 8 ? s[nb][1] : s[nb][3], src);
-            const bool va = jj <= pos[nb][0] && (W == 0 || jj > pos[nb][0] - W || jj < S);
-            const bool vb = jj <= pos[nb][1] && (W == 0 || jj > pos[nb][1] - W || jj < S);
+          for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-            for (int d = 0; d < KK; ++d)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                uint16_t bits;
-                asm volatile("ld.shared.b16 %0, [%1];" : "=h"(bits) : "r"(vptr(warp * 16 + i, 2 * d + e) + 2 * (lane >> 2)));
-                const float vv = unpack2<F16>(bits).x;
-                if (va) o[nb][d][2 * e] = fmaf(pa, vv, o[nb][d][2 * e]);
-                if (vb) o[nb][d][2 * e + 1] = fmaf(pb, vv, o[nb][d][2 * e + 1]);
+            for (int e = 0; e < 2; ++e)
+              if (i >> 3 == 2 * kb + e) {
+                pa = s[kb][2 * e];
+                pb = s[kb][2 * e + 1];
               }
-          }
+          pa = __shfl_sync(0xffffffffu, pa, src);
+          pb = __shfl_sync(0xffffffffu, pb, src);
+          const bool va = jj <= pos[0] && (W == 0 || jj > pos[0] - W || jj < S);
+          const bool vb = jj <= pos[1] && (W == 0 || jj > pos[1] - W || jj < S);
+#pragma unroll
+          for (int d = 0; d < KK; ++d)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              uint16_t bits;
+              asm volatile("ld.shared.b16 %0, [%1];" : "=h"(bits) : "r"(vptr(i, 2 * d + e) + 2 * (lane >> 2)));
+              const float vv = unpack2<F16>(bits).x;
+              if (va) o[d][2 * e] = fmaf(pa, vv, o[d][2 * e]);
+              if (vb) o[d][2 * e + 1] = fmaf(pb, vv, o[d][2 * e + 1]);
+            }
         }
-        __syncwarp();
-        for (int i = lane; i < 16 * (D / 8); i += 32) {
-          const int key = i / (D / 8);
-          if (cut >> key & 1)
-            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vptr(warp * 16 + key, i % (D / 8))), "r"(0) : "memory");
+        // the other group's warp of these keys has added them too (it comes here for the same tiles)
+        if constexpr (RG > 1) named_bar_sync(kPairBar + wg, 64);
+        else __syncwarp();
+        for (int i = lane; i < 16 * KB * (D / 8); i += 32) {
+          const int k = i / (D / 8);
+          if (cut >> k & 1)
+            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vptr(k, i % (D / 8))), "r"(0) : "memory");
         }
         __syncwarp();
       }
       // ---- O^T += V^T P^T, P as a sum of two values of the type
-      uint32_t hi[NB][2], lw[NB][2];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int kb = 0; kb < KB; ++kb) {
+        uint32_t ph2[2], pl2[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const uint32_t h = pack2<F16>(s[nb][2 * e], s[nb][2 * e + 1]);
+          const uint32_t h = pack2<F16>(s[kb][2 * e], s[kb][2 * e + 1]);
           const float2 f = unpack2<F16>(h);
-          hi[nb][e] = transpose8x8(h);
-          lw[nb][e] = transpose8x8(pack2<F16>(s[nb][2 * e] - f.x, s[nb][2 * e + 1] - f.y));
+          ph2[e] = transpose8x8(h);
+          pl2[e] = transpose8x8(pack2<F16>(s[kb][2 * e] - f.x, s[kb][2 * e + 1] - f.y));
         }
 #pragma unroll
-      for (int d = 0; d < KK; ++d) {
-        uint32_t vf[4];
-        ldsm4t(sv + voff + (d >> 2) * halfb + (((d & 3) << 5) ^ vx), vf);
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          mma<F16>(o[nb][d], vf[0], vf[1], vf[2], vf[3], hi[nb][0], hi[nb][1]);
-          mma<F16>(o[nb][d], vf[0], vf[1], vf[2], vf[3], lw[nb][0], lw[nb][1]);
+        for (int d = 0; d < KK; ++d) {
+          uint32_t vf[4];
+          ldsm4t(sv + voff[kb] + (d >> 2) * halfb + (((d & 3) << 5) ^ vx), vf);
+          mma<F16>(o[d], vf[0], vf[1], vf[2], vf[3], ph2[0], ph2[1]);
+          mma<F16>(o[d], vf[0], vf[1], vf[2], vf[3], pl2[0], pl2[1]);
         }
       }
       if (!plain) fence_proxy_async_shared();  // the zeros before the next TMA box
@@ -602,97 +626,77 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_con
         ph ^= 1;
       }
     }
-    // ---- the span's end: the warps' sums added up in warp order
-    float ms[NB], ls[NB];
-    float4 os[NB][NH];
+    // ---- the span's end: the group's sums added up in warp order
+    float ms = -INFINITY, ls = 0.f, f[4];
+    float4 os[NH];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+    for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], d);
-        if (lane < 4) {
-          s_ml[0][warp][8 * nb + ra + e] = m[nb][e];
-          s_ml[1][warp][8 * nb + ra + e] = l[nb][e];
-        }
+      for (int d = 4; d < 32; d <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], d);
+      if (lane < 4) {
+        s_ml[grp][0][wg][ra + e] = m[e];
+        s_ml[grp][1][wg][ra + e] = l[e];
       }
+    }
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      float f[4];
+    for (int h = 0; h < NH; ++h) {
 #pragma unroll
-      for (int h = 0; h < NH; ++h) {
+      for (int d = 0; d < 4; ++d)
 #pragma unroll
-        for (int d = 0; d < 4; ++d)
+        for (int e = 0; e < 4; ++e) s_o[grp][wg][ra + (e & 1)][16 * d + 8 * (e >> 1) + (lane >> 2)] = o[4 * h + d][e];
+      named_bar_sync(bar_id, 128);
+      if (h == 0) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s_o[warp][ra + (e & 1)][16 * d + 8 * (e >> 1) + (lane >> 2)] = o[nb][4 * h + d][e];
-        named_bar_sync(1, 128);
-        if (h == 0) {
-          float top = s_ml[0][0][8 * nb + mrow];
-#pragma unroll
-          for (int w = 1; w < 4; ++w) top = fmaxf(top, s_ml[0][w][8 * nb + mrow]);
-          const float z = top == -INFINITY ? 0.f : top;
-          ms[nb] = top;
-          ls[nb] = 0.f;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            f[w] = ex2(s_ml[0][w][8 * nb + mrow] - z);
-            ls[nb] = __fmaf_rn(s_ml[1][w][8 * nb + mrow], f[w], ls[nb]);
-          }
-        }
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < 4; ++w) ms = fmaxf(ms, s_ml[grp][0][w][mrow]);
+        const float z = ms == -INFINITY ? 0.f : ms;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const float4 u = *reinterpret_cast<const float4*>(&s_o[w][mrow][mcol]);
-          y = make_float4(__fmaf_rn(u.x, f[w], y.x), __fmaf_rn(u.y, f[w], y.y), __fmaf_rn(u.z, f[w], y.z),
-                          __fmaf_rn(u.w, f[w], y.w));
+          f[w] = ex2(s_ml[grp][0][w][mrow] - z);
+          ls = __fmaf_rn(s_ml[grp][1][w][mrow], f[w], ls);
         }
-        os[nb][h] = y;
-        named_bar_sync(1, 128);  // before the buffer is written again
       }
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float4 u = *reinterpret_cast<const float4*>(&s_o[grp][w][mrow][mcol]);
+        y = make_float4(__fmaf_rn(u.x, f[w], y.x), __fmaf_rn(u.y, f[w], y.y), __fmaf_rn(u.z, f[w], y.z),
+                        __fmaf_rn(u.w, f[w], y.w));
+      }
+      os[h] = y;
+      named_bar_sync(bar_id, 128);  // before the buffer is written again
     }
     // ---- folded onto the spans before it
-    const int c0 = cta_of(ioff);
-    const int key = items <= nc ? (b * g.RT + rt) * Hkv + hk : c0;
     if (run0 != 0) {
-      put(part_of(key, span), ms, ls, os);
+      put(part_of(key_of(), span), ms, ls, os);
+    } else if (span == 0) {
+      M = ms;
+      L = ls;
+#pragma unroll
+      for (int h = 0; h < NH; ++h) O[h] = os[h];
     } else {
+      float fa, fb;
+      fold_ml(M, L, ms, ls, fa, fb);
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        if (span == 0) {
-          M[nb] = ms[nb];
-          L[nb] = ls[nb];
-#pragma unroll
-          for (int h = 0; h < NH; ++h) O[nb][h] = os[nb][h];
-        } else {
-          float fa, fb;
-          fold_ml(M[nb], L[nb], ms[nb], ls[nb], fa, fb);
-#pragma unroll
-          for (int h = 0; h < NH; ++h) O[nb][h] = fold_o4(O[nb][h], os[nb][h], fa, fb);
-        }
-      }
+      for (int h = 0; h < NH; ++h) O[h] = fold_o4(O[h], os[h], fa, fb);
     }
-    const bool item_end = span + 1 == it.nspan, run_end = item_end || ioff + (span + 1) * it.sp >= hi;
+    const bool item_end = span + 1 == it.nspan, run_end = item_end || ioff + ((span + 1) << it.ks) >= hi;
     if (run_end && run0 == 0 && item_end) {
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        const int rr = row_of(8 * nb + mrow);
-        if (rr < 0) continue;
-        const long long at = ((long long)b * n_q + rr / G) * g.a.Hq + hk * G + rr % G;
-        put_row<F16, D>(M[nb], L[nb], O[nb], g.a.o + at * D + mcol,
-                        g.a.lse && warp == 0 && (lane & 3) == 0 ? g.a.lse + at : nullptr);
+      const int rr = row_of(mrow);
+      if (rr >= 0) {
+        const long long at = place_of(b, hk, rr);
+        put_row<F16, D>(M, L, O, g.a.o + at * D + mcol, g.a.lse && wg == 0 && (lane & 3) == 0 ? g.a.lse + at : nullptr);
       }
     } else if (run_end) {
-      if (run0 == 0) put(part_of(key, span), M, L, O);
-      __threadfence();
-      named_bar_sync(1, 128);
-      if (tid == 0) {
-        const int mine = span - run0 + 1;
-        if (atomicAdd(g.cnt + c0, mine) + mine == it.nspan) {
-          g.cnt[c0] = 0;  // ready for the next call
+      if (run0 == 0) put(part_of(key_of(), span), M, L, O);
+      named_bar_sync(bar_id, 128);  // the group's partials before the count, which releases them
+      if ((tid & 127) == 0) {
+        const int c0 = cta_of(ioff), mine = span - run0 + 1;
+        int32_t* cnt = g.cnt + 2 * c0 + grp;
+        if (add_acq_rel_gpu(cnt, mine) + mine == it.nspan) {
+          *cnt = 0;  // ready for the next call
           // the first run's last span holds the fold of the spans before it
-          const int n0 = min(it.nspan, (lo_of(c0 + 1) - ioff + it.sp - 1) / it.sp) - 1;
-          Join& jn = s_join[s_njoin++];
-          jn = {b, rt, hk, it.nspan - n0, part_of(key, n0)};
+          const int n0 = min(it.nspan, (lo_of(c0 + 1) - ioff + (1 << it.ks) - 1) >> it.ks) - 1;
+          s_join[grp][s_njoin[grp]++] = {b, rt, hk, it.nspan - n0, part_of(key_of(), n0)};
         }
       }
     }
@@ -704,17 +708,14 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_con
     }
   }
   // ---- joins, after the loop over tiles: they would take registers from it
-  named_bar_sync(1, 128);
-  __threadfence();
-  for (int i = 0; i < s_njoin; ++i) {
-    const Join jn = s_join[i];
-    for (int nb = 0; nb < NB; ++nb) {
-      const int rr = jn.rt * 16 + 8 * nb + mrow;
-      if (rr >= n_q * G) continue;
-      const long long at = ((long long)jn.b * n_q + rr / G) * g.a.Hq + jn.hk * G + rr % G;
-      join_row<F16, D>(jn.p, pstride, jn.n, g.R, 8 * nb + mrow, mcol, g.a.o + at * D,
-                       g.a.lse && warp == 0 && (lane & 3) == 0 ? g.a.lse + at : nullptr);
-    }
+  named_bar_sync(bar_id, 128);
+  for (int i = 0; i < s_njoin[grp]; ++i) {
+    const Join jn = s_join[grp][i];
+    const int rr = jn.rt * 16 + 8 * grp + mrow;
+    if (rr >= n_q * G) continue;
+    const long long at = place_of(jn.b, jn.hk, rr);
+    join_row<F16, D>(jn.p, pstride, jn.n, g.R, 8 * grp + mrow, mcol, g.a.o + at * D,
+                     g.a.lse && wg == 0 && (lane & 3) == 0 ? g.a.lse + at : nullptr);
   }
 }
 
@@ -737,15 +738,15 @@ int sm_count(int* dev_out) {
 
 constexpr int kMaxCtas = 2 * 304;  // counters and partials of the largest grid
 
-template <bool F16, int D, int NB>
-cudaError_t launch_nb(DecArgs& g, int sms, int dev, cudaStream_t st) {
-  constexpr int smem = kRing + 1024;
+template <bool F16, int D, int RG>
+cudaError_t launch_rg(DecArgs& g, int sms, int dev, cudaStream_t st) {
+  constexpr int smem = dec_ring<RG>() + 1024;
   static std::mutex mu;
   static bool configured[64] = {};
   {
     std::lock_guard<std::mutex> lk(mu);
     if (!configured[dev]) {
-      const cudaError_t e = cudaFuncSetAttribute(decode_kernel<F16, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      const cudaError_t e = cudaFuncSetAttribute(decode_kernel<F16, D, RG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (e != cudaSuccess) {
         cudaGetLastError();
         return e;
@@ -754,8 +755,9 @@ cudaError_t launch_nb(DecArgs& g, int sms, int dev, cudaStream_t st) {
     }
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * sms < kMaxCtas ? 2 * sms : kMaxCtas);
-  cfg.blockDim = dim3(kDecThreads);
+  const int ctas = (3 - RG) * sms;
+  cfg.gridDim = dim3(ctas < kMaxCtas ? ctas : kMaxCtas);
+  cfg.blockDim = dim3(dec_threads<RG>());
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -764,14 +766,14 @@ cudaError_t launch_nb(DecArgs& g, int sms, int dev, cudaStream_t st) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   launch_begin(K_ATTN_DECODE, st);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_kernel<F16, D, NB>, g);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_kernel<F16, D, RG>, g);
   launch_end(st);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <bool F16, int D>
 cudaError_t launch_one(DecArgs& g, int sms, int dev, cudaStream_t st) {
-  return g.R > 8 ? launch_nb<F16, D, 2>(g, sms, dev, st) : launch_nb<F16, D, 1>(g, sms, dev, st);
+  return g.R > 8 ? launch_rg<F16, D, 2>(g, sms, dev, st) : launch_rg<F16, D, 1>(g, sms, dev, st);
 }
 
 }  // namespace
@@ -781,22 +783,28 @@ bool decode_supported(int D, int page, int Hkv, int G, int n_q, int max_pages) {
   if (page < 8 || (page & (page - 1))) return false;
   if (!encode_fn()) return false;
   // the tiles of one sequence count in int32
-  const long long RT = (n_q * (long long)G + 15) / 16, tiles = ((long long)max_pages * page + kTile - 1) / kTile;
+  const long long RT = (n_q * (long long)G + 15) / 16, tiles = ((long long)max_pages * page + 63) / 64;
   return Hkv * RT * (tiles + 1) < (1LL << 30);
 }
 
-// Spans that fill the GPU with one sequence's items; more would only lengthen the join.
+// The rule for the spans of an item: with few items per sequence more spans, so
+// that one sequence fills the GPU; with many only as many as that takes, since
+// every span costs its end and the join.
+int span_c_of(int Hkv, int RT) {
+  const int c = 32 / (Hkv * RT);
+  return c < 4 ? 4 : c;
+}
 int most_spans_of(int Hkv, int RT) {
   const int n = 256 / (Hkv * RT);
   return n > 8 ? n : 8;
 }
 
 // Spans of an item at most, for tables of max_pages pages.
-int max_span_of(int page, int max_pages, int most_spans) {
-  const int tiles = (int)(((long long)max_pages * page + kTile - 1) / kTile);
+int max_span_of(int page, int max_pages, int tile, int span_c, int most_spans) {
+  const int tiles = (int)(((long long)max_pages * page + tile - 1) / tile);
   int most = 1;
   for (int k = 0;; ++k) {  // the longest item with spans of 2^k tiles
-    long long t = 16LL << (2 * k);
+    long long t = (long long)span_c << (2 * k);
     if (t > ((long long)most_spans << k)) t = (long long)most_spans << k;
     if (t > tiles) t = tiles;
     const long long n = (t + (1LL << k) - 1) >> k;
@@ -813,7 +821,7 @@ size_t decode_ws_bytes(int page, int max_pages, int Hkv, int G, int D, int max_r
   for (int n_q = 1; n_q <= rows; ++n_q) {
     const int RT = (n_q * G + 15) / 16;
     const long long items = (max_rows / n_q) * (long long)RT * Hkv, keys = items < kMaxCtas ? items : kMaxCtas;
-    const size_t n = (size_t)keys * max_span_of(page, max_pages, most_spans_of(Hkv, RT)) * (n_q * G > 8 ? 16 : 8);
+    const size_t n = (size_t)keys * max_span_of(page, max_pages, tile_of(D, n_q * G > 8 ? 2 : 1), span_c_of(Hkv, RT), most_spans_of(Hkv, RT)) * (n_q * G > 8 ? 16 : 8);
     most = n > most ? n : most;
   }
   return align256(most * (D + 2) * 4);
@@ -824,20 +832,23 @@ cudaError_t launch_attn_decode(const Cache& c, const Rows& r, const Attn& a, boo
   int dev = 0;
   const int sms = sm_count(&dev);
   if (!sms) return cudaErrorInvalidDevice;
+  const int tile = tile_of(c.D, r.n_q * a.G > 8 ? 2 : 1);
   DecArgs g;
-  if (!pool_maps(c, &g.tm_k, &g.tm_v, c.page < kTile ? c.page : kTile)) return cudaErrorInvalidValue;
+  if (!pool_maps(c, &g.tm_k, &g.tm_v, c.page < tile ? c.page : tile)) return cudaErrorInvalidValue;
   g.c = c;
   g.a = a;
   g.RT = (r.n_q * a.G + 15) / 16;
   g.logpage = log2_of(c.page);
-  g.logP = g.logpage < 6 ? g.logpage : 6;
+  g.logP = log2_of(tile);
+  if (g.logpage < g.logP) g.logP = g.logpage;
+  g.span_c = span_c_of(c.Hkv, g.RT);
   g.most_spans = most_spans_of(c.Hkv, g.RT);
-  g.max_span = max_span_of(c.page, c.max_pages, g.most_spans);
+  g.max_span = max_span_of(c.page, c.max_pages, tile, g.span_c, g.most_spans);
   g.part = static_cast<float*>(scratch);
   g.R = r.n_q * a.G > 8 ? 16 : 8;
   g.status = status;
   g.cnt = sync + kCntBase;
-  const long long tiles = ((long long)c.max_pages * c.page + kTile - 1) / kTile + 1;
+  const long long tiles = ((long long)c.max_pages * c.page + tile - 1) / tile + 1;
   long long per = ((1LL << 30)) / (c.Hkv * (long long)g.RT * tiles);  // sequences whose tiles count in int32
   per = per < 1 ? 1 : per > kSeqCap ? kSeqCap : per;
   for (int b0 = 0; b0 < r.B; b0 += (int)per) {
