@@ -53,6 +53,9 @@ template <int RG>
 __host__ __device__ constexpr int dec_threads() { return 32 * (4 * RG + 1); }
 template <int RG>
 __host__ __device__ constexpr int dec_ring() { return RG * 96 * 1024; }
+template <int RG>
+__host__ __device__ constexpr int dec_ctas() { return 3 - RG; }  // per SM
+constexpr int kAllBar = 3;              // named barrier of all consumer warps
 constexpr int kPairBar = 4;             // named barriers 4 .. 7: the warps of two groups with the same keys (1, 2: a group's)
 constexpr int kOPitch = 64 + 4;         // floats per row of the buffer in which the warps' O meet
 constexpr int kSeqCap = 128;            // sequences per launch
@@ -69,8 +72,7 @@ struct DecArgs {
   int logpage;
   int max_span;       // spans of an item at most
   int span_c, most_spans;  // the rule for their length
-  float* part;        // [keys][max_span][R][D + 2]
-  int R;              // rows of a partial: 8 or 16
+  float* part;        // [keys][max_span][RG] partials
   int32_t *status, *cnt;
 };
 
@@ -177,55 +179,71 @@ struct Join {
   const float* p;
 };
 
-// The fold of n partials of one row (from p on, pstride apart) in order, in the
-// columns col + 64 h .. + 3; the next four partials are on their way while four
-// are folded.
-template <bool F16, int D>
-__device__ __forceinline__ void join_row(const float* p, long long pstride, int n, int R, int row, int col, uint16_t* o,
-                                         float* lse) {
-  constexpr int NH = D / 64, U = 4;
-  float M = 0.f, L = 0.f;
+// A group's part of a span's partial: m and l of its 8 rows, o [8][D].
+template <int D>
+__host__ __device__ constexpr int part_floats() { return 16 + 8 * D; }
+
+// The fold of n partials of a group's rows (from p on, pstride floats apart) in
+// order, for row `row` and the columns col + 64 h .. + 3, by the group's 128
+// threads. The partials come through shared memory (BUF bytes from buf), U at a
+// time while U are folded: a join reads some 100 KB that other SMs wrote, and
+// what it waits for is the latency of those reads.
+template <bool F16, int D, int BUF>
+__device__ __forceinline__ void join_rows(const float* p, long long pstride, int n, uint32_t buf, int bar_id, int row, int col,
+                                          uint16_t* o, float* lse) {
+  constexpr int NH = D / 64, kVecs = part_floats<D>() / 4, kBytes = part_floats<D>() * 4;
+  constexpr int kFit = BUF / (2 * kBytes), U = kFit < 8 ? kFit : 8;
+  static_assert(U >= 4);
+  const int t = threadIdx.x & 127;
+  auto fetch = [&](int s0) {  // partials s0 .. s0 + U - 1 into their half of the buffer
+    for (int u = 0; u < U && s0 + u < n; ++u) {
+      const float* q = p + (s0 + u) * pstride;
+      const uint32_t d = buf + ((s0 / U & 1) * U + u) * kBytes;
+      for (int i = t; i < kVecs; i += 128)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + 16 * i), "l"(q + 4 * i) : "memory");
+    }
+    cp_async_commit();
+  };
+  float M = -INFINITY, L = 0.f;
   float4 O[NH];
-  float m[2][U], l[2][U];
-  float4 w[2][U][NH];
-  auto get = [&](int s, float (&m)[U], float (&l)[U], float4 (&w)[U][NH]) {
+#pragma unroll
+  for (int h = 0; h < NH; ++h) O[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+  fetch(0);
+  for (int s0 = 0; s0 < n; s0 += U) {
+    fetch(s0 + U);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    named_bar_sync(bar_id, 128);
+    // past the last partial: m = -inf and zeros, which the fold leaves as it is
+    float m[U], l[U];
+    float4 w[U][NH];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const float* q = p + min(s + u, n - 1) * pstride;
-      m[u] = ldg_cg_f32(q + row);
-      l[u] = ldg_cg_f32(q + R + row);
+      const uint32_t d = buf + ((s0 / U & 1) * U + u) * kBytes;
+      const bool in = s0 + u < n;
+      m[u] = in ? __uint_as_float(ld_s32(d + row * 4)) : -INFINITY;
+      l[u] = in ? __uint_as_float(ld_s32(d + 32 + row * 4)) : 0.f;
 #pragma unroll
-      for (int h = 0; h < NH; ++h) w[u][h] = __ldcg(reinterpret_cast<const float4*>(q + 2 * R + row * D + col + 64 * h));
-    }
-  };
-  get(0, m[0], l[0], w[0]);
-  for (int s0 = 0; s0 < n; s0 += 2 * U)
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int s = s0 + k * U;
-      if (s >= n) break;
-      if (s + U < n) get(s + U, m[k ^ 1], l[k ^ 1], w[k ^ 1]);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (s + u >= n) break;
-        if (s + u == 0) {
-          M = m[k][u];
-          L = l[k][u];
-#pragma unroll
-          for (int h = 0; h < NH; ++h) O[h] = w[k][u][h];
-        } else {
-          float a, b;
-          fold_ml(M, L, m[k][u], l[k][u], a, b);
-#pragma unroll
-          for (int h = 0; h < NH; ++h) O[h] = fold_o4(O[h], w[k][u][h], a, b);
-        }
+      for (int h = 0; h < NH; ++h) {
+        const uint4 v = ld_s128(d + 64 + (row * D + col + 64 * h) * 4);
+        w[u][h] = in ? make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w))
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
       }
     }
-  put_row<F16, D>(M, L, O, o + col, lse);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float a, b;
+      fold_ml(M, L, m[u], l[u], a, b);
+#pragma unroll
+      for (int h = 0; h < NH; ++h) O[h] = fold_o4(O[h], w[u][h], a, b);
+    }
+    named_bar_sync(bar_id, 128);  // before this half is filled again
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (o) put_row<F16, D>(M, L, O, o + col, lse);
 }
 
 template <bool F16, int D, int RG>
-__global__ void __launch_bounds__(dec_threads<RG>(), 3 - RG) decode_kernel(const __grid_constant__ DecArgs g) {
+__global__ void __launch_bounds__(dec_threads<RG>(), dec_ctas<RG>()) decode_kernel(const __grid_constant__ DecArgs g) {
   constexpr int kDecThreads = dec_threads<RG>();
   constexpr int kTile = tile_of(D, RG), KB = kTile / 64;  // KB blocks of 16 keys per warp
   constexpr int kStage = kTile * D * 4;      // K and V of a tile
@@ -243,7 +261,7 @@ __global__ void __launch_bounds__(dec_threads<RG>(), 3 - RG) decode_kernel(const
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int B = g.r.B, G = g.a.G, n_q = g.r.n_q, W = g.a.window, S = g.a.n_sink, Hkv = g.c.Hkv;
-  const uint32_t ring = (smem_u32(smem_dec) + 1023u) & ~1023u;
+  const uint32_t ring = smem_u32(smem_dec);  // aligned as declared: a swizzled box starts on 1 KB
   const uint32_t full = smem_u32(s_bar), empty = full + 8 * kStages;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -433,19 +451,20 @@ __global__ void __launch_bounds__(dec_threads<RG>(), 3 - RG) decode_kernel(const
   int run0 = -1;                 // first span of the current run of spans of one item
 
   const int items = B * Hkv * g.RT;
-  const long long pstride = (long long)g.R * (D + 2);
-  // partials of an item split over CTAs: [span][m of R rows, l of R rows, o [R][D]]
-  auto part_of = [&](int key, int s) { return g.part + ((long long)key * g.max_span + s) * pstride; };
+  // the group's partials of an item split over CTAs
+  constexpr long long pstride = RG * part_floats<D>();
+  auto part_of = [&](int key, int s) {
+    return g.part + ((long long)key * g.max_span + s) * pstride + grp * part_floats<D>();
+  };
   // an item's place among the partials
   auto key_of = [&] { return items <= nc ? (b * g.RT + rt) * Hkv + hk : cta_of(ioff); };
   auto put = [&](float* p, float m, float l, const float4 (&o)[NH]) {
-    const int r = 8 * grp + mrow;
     if (wg == 0 && (lane & 3) == 0) {
-      p[r] = m;
-      p[g.R + r] = l;
+      p[mrow] = m;
+      p[8 + mrow] = l;
     }
 #pragma unroll
-    for (int h = 0; h < NH; ++h) *reinterpret_cast<float4*>(p + 2 * g.R + r * D + 64 * h + mcol) = o[h];
+    for (int h = 0; h < NH; ++h) *reinterpret_cast<float4*>(p + 16 + mrow * D + 64 * h + mcol) = o[h];
   };
   // token of a sequence's row, and the row's place in a tensor [row][Hq]
   auto token_of = [&](int rr) { return n_q == 1 ? 0 : rr / G; };
@@ -668,12 +687,13 @@ __global__ void __launch_bounds__(dec_threads<RG>(), 3 - RG) decode_kernel(const
     // ---- folded onto the spans before it
     if (run0 != 0) {
       put(part_of(key_of(), span), ms, ls, os);
-    } else if (span == 0) {
-      M = ms;
-      L = ls;
-#pragma unroll
-      for (int h = 0; h < NH; ++h) O[h] = os[h];
     } else {
+      if (span == 0) {
+        M = -INFINITY;
+        L = 0.f;
+#pragma unroll
+        for (int h = 0; h < NH; ++h) O[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
       float fa, fb;
       fold_ml(M, L, ms, ls, fa, fb);
 #pragma unroll
@@ -707,15 +727,16 @@ __global__ void __launch_bounds__(dec_threads<RG>(), 3 - RG) decode_kernel(const
       ++span;
     }
   }
-  // ---- joins, after the loop over tiles: they would take registers from it
-  named_bar_sync(bar_id, 128);
+  // ---- joins, after the loop over tiles: they would take registers from it,
+  // and the ring is free once every group is here
+  named_bar_sync(kAllBar, 128 * RG);
   for (int i = 0; i < s_njoin[grp]; ++i) {
     const Join jn = s_join[grp][i];
     const int rr = jn.rt * 16 + 8 * grp + mrow;
-    if (rr >= n_q * G) continue;
-    const long long at = place_of(jn.b, jn.hk, rr);
-    join_row<F16, D>(jn.p, pstride, jn.n, g.R, 8 * grp + mrow, mcol, g.a.o + at * D,
-                     g.a.lse && wg == 0 && (lane & 3) == 0 ? g.a.lse + at : nullptr);
+    const bool real = rr < n_q * G;
+    const long long at = real ? place_of(jn.b, jn.hk, rr) : 0;
+    join_rows<F16, D, dec_ring<RG>() / RG>(jn.p, pstride, jn.n, ring + grp * (dec_ring<RG>() / RG), bar_id, mrow, mcol,
+                      real ? g.a.o + at * D : nullptr, g.a.lse && wg == 0 && (lane & 3) == 0 ? g.a.lse + at : nullptr);
   }
 }
 
@@ -740,7 +761,7 @@ constexpr int kMaxCtas = 2 * 304;  // counters and partials of the largest grid
 
 template <bool F16, int D, int RG>
 cudaError_t launch_rg(DecArgs& g, int sms, int dev, cudaStream_t st) {
-  constexpr int smem = dec_ring<RG>() + 1024;
+  constexpr int smem = dec_ring<RG>();
   static std::mutex mu;
   static bool configured[64] = {};
   {
@@ -755,7 +776,7 @@ cudaError_t launch_rg(DecArgs& g, int sms, int dev, cudaStream_t st) {
     }
   }
   cudaLaunchConfig_t cfg = {};
-  const int ctas = (3 - RG) * sms;
+  const int ctas = dec_ctas<RG>() * sms;
   cfg.gridDim = dim3(ctas < kMaxCtas ? ctas : kMaxCtas);
   cfg.blockDim = dim3(dec_threads<RG>());
   cfg.dynamicSmemBytes = smem;
@@ -773,7 +794,7 @@ cudaError_t launch_rg(DecArgs& g, int sms, int dev, cudaStream_t st) {
 
 template <bool F16, int D>
 cudaError_t launch_one(DecArgs& g, int sms, int dev, cudaStream_t st) {
-  return g.R > 8 ? launch_rg<F16, D, 2>(g, sms, dev, st) : launch_rg<F16, D, 1>(g, sms, dev, st);
+  return g.r.n_q * g.a.G > 8 ? launch_rg<F16, D, 2>(g, sms, dev, st) : launch_rg<F16, D, 1>(g, sms, dev, st);
 }
 
 }  // namespace
@@ -821,10 +842,12 @@ size_t decode_ws_bytes(int page, int max_pages, int Hkv, int G, int D, int max_r
   for (int n_q = 1; n_q <= rows; ++n_q) {
     const int RT = (n_q * G + 15) / 16;
     const long long items = (max_rows / n_q) * (long long)RT * Hkv, keys = items < kMaxCtas ? items : kMaxCtas;
-    const size_t n = (size_t)keys * max_span_of(page, max_pages, tile_of(D, n_q * G > 8 ? 2 : 1), span_c_of(Hkv, RT), most_spans_of(Hkv, RT)) * (n_q * G > 8 ? 16 : 8);
+    const int RG = n_q * G > 8 ? 2 : 1;
+    const size_t n = (size_t)keys * RG *
+                     max_span_of(page, max_pages, tile_of(D, RG), span_c_of(Hkv, RT), most_spans_of(Hkv, RT));
     most = n > most ? n : most;
   }
-  return align256(most * (D + 2) * 4);
+  return align256(most * (D == 128 ? part_floats<128>() : part_floats<64>()) * 4);
 }
 
 cudaError_t launch_attn_decode(const Cache& c, const Rows& r, const Attn& a, bool f16, int32_t* status, int32_t* sync,
@@ -845,7 +868,6 @@ cudaError_t launch_attn_decode(const Cache& c, const Rows& r, const Attn& a, boo
   g.most_spans = most_spans_of(c.Hkv, g.RT);
   g.max_span = max_span_of(c.page, c.max_pages, tile, g.span_c, g.most_spans);
   g.part = static_cast<float*>(scratch);
-  g.R = r.n_q * a.G > 8 ? 16 : 8;
   g.status = status;
   g.cnt = sync + kCntBase;
   const long long tiles = ((long long)c.max_pages * c.page + tile - 1) / tile + 1;
