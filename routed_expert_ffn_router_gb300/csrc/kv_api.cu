@@ -179,7 +179,7 @@ moe_status moe_kv_free(const moe_kv_desc* d, const int32_t* slots, int32_t n, vo
   moe_status s = check_pages(d, n, ws, ws_bytes);
   if (s != MOE_OK || n == 0) return s;
   if (!slots || !aligned(slots, 4)) return MOE_ERR_INVALID;
-  return cuda_status(launch_free(cache_of(d, 0), slots, n, status_of(ws), region_of(ws), static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_free(cache_of(d, 0), slots, n, status_of(ws), static_cast<cudaStream_t>(stream)));
 }
 
 moe_status moe_kv_compact(const moe_kv_desc* d, int32_t* n_moved, void* ws, size_t ws_bytes, void* stream) {
@@ -196,7 +196,7 @@ moe_status moe_kv_copy_pages(const moe_kv_desc* d, const int32_t* src, const int
   if (n < 0 || n > d->n_pages) return MOE_ERR_INVALID;
   if (n == 0) return MOE_OK;
   if (!src || !dst || !aligned(src, 4) || !aligned(dst, 4)) return MOE_ERR_INVALID;
-  return cuda_status(launch_copy_pages(cache_of(d, 0), src, dst, n, status_of(ws), region_of(ws),
+  return cuda_status(launch_copy_pages(cache_of(d, 0), src, dst, n, status_of(ws),
                                        static_cast<cudaStream_t>(stream)));
 }
 

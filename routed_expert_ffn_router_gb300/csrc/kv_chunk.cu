@@ -868,6 +868,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
 template <bool F16, int D>
 __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ ChunkArgs g) {
   griddep_wait();
+  griddep_launch_dependents();
   const Split sp = g.split[blockIdx.x + 1];
   if (sp.c0 < 0) return;
   const int row = blockIdx.y * 32 + (threadIdx.x >> 2), t = row >> 7, r = row & 127, q = threadIdx.x & 3;
@@ -926,27 +927,9 @@ cudaError_t launch_one(ChunkArgs& g, int grid, int dev, cudaStream_t st) {
       configured[dev] = true;
     }
   }
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kChunkThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  launch_begin(K_ATTN_CHUNK, st);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, chunk_kernel<F16, D>, g);
-  launch_end(st);
+  const cudaError_t e = launch_pdl(K_ATTN_CHUNK, chunk_kernel<F16, D>, dim3(grid), kChunkThreads, smem, st, g);
   if (e != cudaSuccess || !g.combine) return e;
-  cfg.gridDim = dim3(grid - 1, 8);
-  cfg.blockDim = dim3(128);
-  cfg.dynamicSmemBytes = 0;
-  launch_begin(K_ATTN_COMBINE, st);
-  e = cudaLaunchKernelEx(&cfg, combine_kernel<F16, D>, g);
-  launch_end(st);
-  return e;
+  return launch_pdl(K_ATTN_COMBINE, combine_kernel<F16, D>, dim3(grid - 1, 8), 128, 0, st, g);
 }
 
 int chunk_grid(int* dev) {

@@ -272,6 +272,7 @@ __global__ void __launch_bounds__(dec_threads<RG>(), dec_ctas<RG>()) decode_kern
     for (int i = 0; i < RG; ++i) s_njoin[i] = 0;
   }
   griddep_wait();  // the rows' keys and values of an append before this launch
+  griddep_launch_dependents();
 
   auto item_of = [&](int slot, int len, int rt) {
     Item it;
@@ -488,7 +489,7 @@ __global__ void __launch_bounds__(dec_threads<RG>(), dec_ctas<RG>()) decode_kern
       for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          q[kk][e] = rr >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(qp + kk * 16 + e * 8)) : 0u;
+          q[kk][e] = rr >= 0 ? *reinterpret_cast<const uint32_t*>(qp + kk * 16 + e * 8) : 0u;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = row_of(ra + e);
@@ -775,21 +776,9 @@ cudaError_t launch_rg(DecArgs& g, int sms, int dev, cudaStream_t st) {
       configured[dev] = true;
     }
   }
-  cudaLaunchConfig_t cfg = {};
   const int ctas = dec_ctas<RG>() * sms;
-  cfg.gridDim = dim3(ctas < kMaxCtas ? ctas : kMaxCtas);
-  cfg.blockDim = dim3(dec_threads<RG>());
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  launch_begin(K_ATTN_DECODE, st);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_kernel<F16, D, RG>, g);
-  launch_end(st);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return launch_pdl(K_ATTN_DECODE, decode_kernel<F16, D, RG>, dim3(ctas < kMaxCtas ? ctas : kMaxCtas), dec_threads<RG>(),
+                    smem, st, g);
 }
 
 template <bool F16, int D>

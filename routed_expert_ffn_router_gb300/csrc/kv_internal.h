@@ -72,6 +72,28 @@ __device__ __forceinline__ Seq load_seq(const Cache& c, const Rows& r, int b, in
   return s;
 }
 
+// Launch that may be scheduled before the stream's previous kernel has ended:
+// a kernel launched this way waits (griddep_wait) before it touches memory and
+// then lets its own successor be scheduled, so that in a chain of short calls
+// a kernel's launch latency and prologue are paid during the one before.
+template <class... P, class... A>
+cudaError_t launch_pdl(int kind, void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  launch_begin(kind, st);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(a)...);
+  launch_end(st);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 cudaError_t launch_append(const Cache& c, const Rows& r, const uint16_t* k, const uint16_t* v, long long stride,
                           int32_t* status, cudaStream_t st);
 cudaError_t launch_attn_rows(const Cache& c, const Rows& r, const Attn& a, bool f16, int32_t* status,
@@ -93,10 +115,10 @@ cudaError_t launch_grow(const Cache& c, const int32_t* slots, const int32_t* add
                         cudaStream_t st);
 cudaError_t launch_fork(const Cache& c, const int32_t* src, const int32_t* dst, int n, int32_t* status, void* scratch,
                         cudaStream_t st);
-cudaError_t launch_free(const Cache& c, const int32_t* slots, int n, int32_t* status, void* scratch, cudaStream_t st);
+cudaError_t launch_free(const Cache& c, const int32_t* slots, int n, int32_t* status, cudaStream_t st);
 cudaError_t launch_compact(const Cache& c, int32_t* n_moved, int32_t* status, void* scratch, cudaStream_t st);
 cudaError_t launch_copy_pages(const Cache& c, const int32_t* src, const int32_t* dst, int n, int32_t* status,
-                              void* scratch, cudaStream_t st);
+                              cudaStream_t st);
 
 }  // namespace kv
 }  // namespace moe

@@ -61,14 +61,28 @@ __device__ int block_scan(int v, int* sum, int* sh) {
   return (warp ? sh[warp - 1] : 0) + x - v;
 }
 
+// The first thing of every kernel here (launch_pdl).
+__device__ __forceinline__ void start() {
+  griddep_wait();
+  griddep_launch_dependents();
+}
+
 __device__ __forceinline__ int pages_of(int len, int page) { return (int)(((long long)len + page - 1) / page); }
 
 // ------------------------------------------------------------------ append
 // One CTA per row; a thread moves 16-byte pieces of the row's keys and values.
-__global__ void __launch_bounds__(128) append_kernel(Cache c, Rows r, const uint16_t* __restrict__ k,
-                                                     const uint16_t* __restrict__ v, long long stride,
-                                                     int32_t* status) {
+__global__ void __launch_bounds__(128) append_kernel(Cache c, Rows r, const uint16_t* k, const uint16_t* v,
+                                                     long long stride, int32_t* status) {
   const int t = blockIdx.x;
+  start();
+  const int vd = c.D >> 3, per = c.Hkv * vd;
+  auto src = [&](int i) {
+    const int j = i < per ? i : i - per;
+    return reinterpret_cast<const uint4*>((i < per ? k : v) + (long long)t * stride) + j;
+  };
+  // the thread's first piece is on its way while the row's page is looked up
+  uint4 x = make_uint4(0, 0, 0, 0);
+  if (threadIdx.x < 2 * per) x = *src(threadIdx.x);
   int b;
   if (r.row_start) {  // the last sequence that starts at or before row t
     int lo = 0, hi = r.B - 1;
@@ -90,14 +104,13 @@ __global__ void __launch_bounds__(128) append_kernel(Cache c, Rows r, const uint
     if (threadIdx.x == 0) atomicOr(status, DEV_BAD_SLOT);
     return;
   }
-  const int vd = c.D >> 3, per = c.Hkv * vd;
   const long long base = (long long)pg * c.Hkv * c.page + tok % c.page;
   for (int i = threadIdx.x; i < 2 * per; i += blockDim.x) {
+    if (i != threadIdx.x) x = *src(i);
     const int j = i < per ? i : i - per;
     const int h = j / vd, d = (j - h * vd) * 8;
-    const uint16_t* src = (i < per ? k : v) + (long long)t * stride + h * c.D + d;
     uint16_t* dst = (i < per ? c.k : c.v) + (base + (long long)h * c.page) * c.D + d;
-    *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
+    *reinterpret_cast<uint4*>(dst) = x;
   }
 }
 
@@ -107,6 +120,7 @@ __global__ void __launch_bounds__(kPlanThreads) grow_kernel(Cache c, const int32
   __shared__ int sh[32];
   __shared__ int bad;
   const int tid = threadIdx.x;
+  start();
   if (tid == 0) bad = 0;
   __syncthreads();
   const long long cap = (long long)c.max_pages * c.page;
@@ -158,6 +172,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(Cache c, const 
   __shared__ int sh[32];
   __shared__ int bad;
   const int tid = threadIdx.x;
+  start();
   if (tid == 0) bad = 0;
   __syncthreads();
   const long long cap = (long long)c.max_pages * c.page;
@@ -201,59 +216,75 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(Cache c, const 
 }
 
 // Copy `vecs` 16-byte pieces by one warp, eight loads in flight per lane.
-__device__ __forceinline__ void warp_copy(uint4* __restrict__ dst, const uint4* __restrict__ src, int vecs) {
+constexpr int kPiece = 256;
+__device__ __forceinline__ void warp_copy(uint4* dst, const uint4* src, int vecs) {
   const int lane = threadIdx.x & 31;
-  int j = lane;
-  for (; j + 32 * 7 < vecs; j += 32 * 8) {
+  for (int j = lane; j < vecs; j += kPiece) {
     uint4 t[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) t[u] = ldg_nc_v4(src + j + 32 * u);
+    for (int u = 0; u < 8; ++u)
+      if (j + 32 * u < vecs) t[u] = __ldcs(src + j + 32 * u);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) dst[j + 32 * u] = t[u];
+    for (int u = 0; u < 8; ++u)
+      if (j + 32 * u < vecs) __stcs(dst + j + 32 * u, t[u]);
   }
-  for (; j < vecs; j += 32) dst[j] = ldg_nc_v4(src + j);
 }
+
+// The walk of a warp over (move, plane, part): plane 2 l + (0 keys, 1 values) of
+// layer l, `parts` pieces of a page each. One division per warp, then additions.
+struct Walk {
+  long long m, dm;
+  int pl, part, dpl, dpart, planes, parts;
+  __device__ Walk(int planes_, int parts_) : planes(planes_), parts(parts_) {
+    const unsigned w = blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5), nw = gridDim.x * (kMoveThreads / 32);
+    split(w, m, pl, part);
+    split(nw, dm, dpl, dpart);
+  }
+  __device__ void split(unsigned w, long long& a, int& b, int& c) const {
+    const unsigned t = w / parts;
+    c = (int)(w - t * parts);
+    a = t / planes;
+    b = (int)(t - (unsigned)a * planes);
+  }
+  __device__ void next() {
+    part += dpart;
+    pl += dpl;
+    m += dm;
+    if (part >= parts) part -= parts, ++pl;
+    if (pl >= planes) pl -= planes, ++m;
+  }
+};
 
 // Pages moved whole: a page's rows of all heads are contiguous in a layer's
 // pool; a warp copies pieces of 4 KB of it.
-constexpr int kPiece = 256;  // 16-byte vectors
 __device__ void move_pages(const Cache& c, const int32_t* msrc, const int32_t* mdst, long long n, int32_t* status) {
   const long long vecs = (long long)c.Hkv * c.page * c.D / 8;  // of a page in one pool
-  const long long pieces = (vecs + kPiece - 1) / kPiece;
-  const long long items = n * 2 * c.n_layers * pieces;
-  const long long nw = (long long)gridDim.x * (kMoveThreads / 32);
-  for (long long it = (long long)blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5); it < items; it += nw) {
-    const long long t = it / pieces, p = it - t * pieces;
-    const long long m = t / (2 * c.n_layers);
-    const int pl = (int)(t - m * 2 * c.n_layers);
-    const int a = msrc[m], b = mdst[m];
+  for (Walk w(2 * c.n_layers, (int)((vecs + kPiece - 1) / kPiece)); w.m < n; w.next()) {
+    const int a = msrc[w.m], b = mdst[w.m];
     if (a < 0 || a >= c.n_pages || b < 0 || b >= c.n_pages) {
       if ((threadIdx.x & 31) == 0) atomicOr(status, DEV_BAD_SLOT);
       continue;
     }
-    uint4* pool = reinterpret_cast<uint4*>((pl & 1) ? c.v : c.k) + (long long)(pl >> 1) * c.n_pages * vecs + p * kPiece;
-    const long long left = vecs - p * kPiece;
+    const long long at = (long long)w.part * kPiece, left = vecs - at;
+    uint4* pool = reinterpret_cast<uint4*>((w.pl & 1) ? c.v : c.k) + (long long)(w.pl >> 1) * c.n_pages * vecs + at;
     warp_copy(pool + b * vecs, pool + a * vecs, (int)(left < kPiece ? left : kPiece));
   }
 }
 
 __global__ void __launch_bounds__(kMoveThreads) fork_apply_kernel(Cache c, const int32_t* src, const int32_t* dst, int n,
                                                                   int32_t* status, Scratch s) {
+  start();
   const int moves = s.hdr[0];
   if (moves < 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long gw = (long long)blockIdx.x * (kMoveThreads / 32) + warp, nw = (long long)gridDim.x * (kMoveThreads / 32);
   // a warp copies the rows in use of one head of one layer's keys or values
   const int vd = c.D >> 3;
-  const long long head = (long long)c.page * vd, planes = 2LL * c.n_layers;
-  const long long items = moves * planes * c.Hkv;
-  for (long long it = gw; it < items; it += nw) {
-    const long long t = it / c.Hkv;
-    const int h = (int)(it - t * c.Hkv);
-    const long long m = t / planes;
-    const int pl = (int)(t - m * planes);
-    uint4* pool = reinterpret_cast<uint4*>((pl & 1) ? c.v : c.k) + ((long long)(pl >> 1) * c.n_pages * c.Hkv + h) * head;
-    warp_copy(pool + s.mdst[m] * c.Hkv * head, pool + s.msrc[m] * c.Hkv * head, s.remap[m] * vd);
+  const long long head = (long long)c.page * vd;
+  for (Walk w(2 * c.n_layers, c.Hkv); w.m < moves; w.next()) {
+    uint4* pool = reinterpret_cast<uint4*>((w.pl & 1) ? c.v : c.k) +
+                  ((long long)(w.pl >> 1) * c.n_pages * c.Hkv + w.part) * head;
+    warp_copy(pool + s.mdst[w.m] * c.Hkv * head, pool + s.msrc[w.m] * c.Hkv * head, s.remap[w.m] * vd);
   }
   // a warp rewrites 32 entries of one fork's table row
   const int segs = (c.max_pages + 31) / 32;
@@ -279,6 +310,7 @@ __global__ void __launch_bounds__(kMoveThreads) fork_apply_kernel(Cache c, const
 // second kernel pushes (in page order, so the stack does not depend on timing).
 __global__ void __launch_bounds__(kMoveThreads) free_refs_kernel(Cache c, const int32_t* slots, int n, int32_t* status) {
   const int i = blockIdx.x, q = blockIdx.y * kMoveThreads + threadIdx.x;
+  start();
   const int slot = slots[i];
   if (slot < 0 || slot >= c.n_slots) {
     if (q == 0) atomicOr(status, DEV_BAD_SLOT);
@@ -306,6 +338,7 @@ __global__ void __launch_bounds__(kMoveThreads) free_refs_kernel(Cache c, const 
 __global__ void __launch_bounds__(kPlanThreads) free_push_kernel(Cache c, const int32_t* slots, int n, int32_t* status) {
   __shared__ int sh[32];
   const int tid = threadIdx.x;
+  start();
   const int nf = *c.n_free;
   int at = nf;
   constexpr int kPer = 8;
@@ -339,6 +372,7 @@ __global__ void __launch_bounds__(kPlanThreads) free_push_kernel(Cache c, const 
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(Cache c, Scratch s, int32_t* n_moved) {
   __shared__ int sh[32];
   const int tid = threadIdx.x;
+  start();
   int n_live = 0;
   for (int p = tid; p < c.n_pages; p += kPlanThreads) n_live += c.refs[p] > 0 ? 1 : 0;
   int dummy = n_live;
@@ -384,6 +418,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(Cache c, Scr
 }
 
 __global__ void __launch_bounds__(kMoveThreads) compact_apply_kernel(Cache c, Scratch s, int32_t* status) {
+  start();
   const int moves = s.hdr[0], n_live = s.hdr[1];
   const long long gt = (long long)blockIdx.x * kMoveThreads + threadIdx.x, nt = (long long)gridDim.x * kMoveThreads;
   move_pages(c, s.msrc, s.mdst, moves, status);
@@ -404,6 +439,7 @@ __global__ void __launch_bounds__(kMoveThreads) compact_apply_kernel(Cache c, Sc
 
 __global__ void __launch_bounds__(kMoveThreads) copy_pages_kernel(Cache c, const int32_t* src, const int32_t* dst, int n,
                                                                   int32_t* status) {
+  start();
   move_pages(c, src, dst, n, status);
 }
 
@@ -422,59 +458,39 @@ size_t pages_ws_bytes(int n_pages, int n_slots) {
 
 cudaError_t launch_append(const Cache& c, const Rows& r, const uint16_t* k, const uint16_t* v, long long stride,
                           int32_t* status, cudaStream_t st) {
-  launch_begin(K_KV_APPEND, st);
-  append_kernel<<<r.n_rows, 128, 0, st>>>(c, r, k, v, stride, status);
-  launch_end(st);
-  return cudaGetLastError();
+  return launch_pdl(K_KV_APPEND, append_kernel, dim3(r.n_rows), 128, 0, st, c, r, k, v, stride, status);
 }
 
 cudaError_t launch_grow(const Cache& c, const int32_t* slots, const int32_t* add, int n, int32_t* status, void* scratch,
                         cudaStream_t st) {
-  launch_begin(K_KV_PAGES, st);
-  grow_kernel<<<1, kPlanThreads, 0, st>>>(c, slots, add, n, status, scratch_of(scratch, c.n_pages, c.n_slots));
-  launch_end(st);
-  return cudaGetLastError();
+  return launch_pdl(K_KV_PAGES, grow_kernel, dim3(1), kPlanThreads, 0, st, c, slots, add, n, status,
+                    scratch_of(scratch, c.n_pages, c.n_slots));
 }
 
 cudaError_t launch_fork(const Cache& c, const int32_t* src, const int32_t* dst, int n, int32_t* status, void* scratch,
                         cudaStream_t st) {
   const Scratch s = scratch_of(scratch, c.n_pages, c.n_slots);
-  launch_begin(K_KV_PAGES, st);
-  fork_plan_kernel<<<1, kPlanThreads, 0, st>>>(c, src, dst, n, status, s);
-  launch_end(st);
-  launch_begin(K_KV_MOVE, st);
-  fork_apply_kernel<<<move_grid(), kMoveThreads, 0, st>>>(c, src, dst, n, status, s);
-  launch_end(st);
-  return cudaGetLastError();
+  const cudaError_t e = launch_pdl(K_KV_PAGES, fork_plan_kernel, dim3(1), kPlanThreads, 0, st, c, src, dst, n, status, s);
+  return e != cudaSuccess
+             ? e
+             : launch_pdl(K_KV_MOVE, fork_apply_kernel, dim3(move_grid()), kMoveThreads, 0, st, c, src, dst, n, status, s);
 }
 
-cudaError_t launch_free(const Cache& c, const int32_t* slots, int n, int32_t* status, void* scratch, cudaStream_t st) {
-  launch_begin(K_KV_PAGES, st);
-  free_refs_kernel<<<dim3(n, (c.max_pages + kMoveThreads - 1) / kMoveThreads), kMoveThreads, 0, st>>>(c, slots, n, status);
-  launch_end(st);
-  launch_begin(K_KV_PAGES, st);
-  free_push_kernel<<<1, kPlanThreads, 0, st>>>(c, slots, n, status);
-  launch_end(st);
-  return cudaGetLastError();
+cudaError_t launch_free(const Cache& c, const int32_t* slots, int n, int32_t* status, cudaStream_t st) {
+  const cudaError_t e = launch_pdl(K_KV_PAGES, free_refs_kernel, dim3(n, (c.max_pages + kMoveThreads - 1) / kMoveThreads),
+                                   kMoveThreads, 0, st, c, slots, n, status);
+  return e != cudaSuccess ? e : launch_pdl(K_KV_PAGES, free_push_kernel, dim3(1), kPlanThreads, 0, st, c, slots, n, status);
 }
 
 cudaError_t launch_compact(const Cache& c, int32_t* n_moved, int32_t* status, void* scratch, cudaStream_t st) {
   const Scratch s = scratch_of(scratch, c.n_pages, c.n_slots);
-  launch_begin(K_KV_PAGES, st);
-  compact_plan_kernel<<<1, kPlanThreads, 0, st>>>(c, s, n_moved);
-  launch_end(st);
-  launch_begin(K_KV_MOVE, st);
-  compact_apply_kernel<<<move_grid(), kMoveThreads, 0, st>>>(c, s, status);
-  launch_end(st);
-  return cudaGetLastError();
+  const cudaError_t e = launch_pdl(K_KV_PAGES, compact_plan_kernel, dim3(1), kPlanThreads, 0, st, c, s, n_moved);
+  return e != cudaSuccess ? e : launch_pdl(K_KV_MOVE, compact_apply_kernel, dim3(move_grid()), kMoveThreads, 0, st, c, s, status);
 }
 
 cudaError_t launch_copy_pages(const Cache& c, const int32_t* src, const int32_t* dst, int n, int32_t* status,
-                              void* scratch, cudaStream_t st) {
-  launch_begin(K_KV_MOVE, st);
-  copy_pages_kernel<<<move_grid(), kMoveThreads, 0, st>>>(c, src, dst, n, status);
-  launch_end(st);
-  return cudaGetLastError();
+                              cudaStream_t st) {
+  return launch_pdl(K_KV_MOVE, copy_pages_kernel, dim3(move_grid()), kMoveThreads, 0, st, c, src, dst, n, status);
 }
 
 }  // namespace kv

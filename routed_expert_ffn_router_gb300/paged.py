@@ -25,10 +25,14 @@ from . import _lib
 from ._lib import MOE_KV_BF16, MOE_KV_F16, moe_attn_args, moe_kv_desc, moe_kv_rows
 
 _DTYPES = {torch.bfloat16: MOE_KV_BF16, torch.float16: MOE_KV_F16}
+_I32, _F32 = torch.int32, torch.float32
+# The current stream's handle without the Stream object around it: a decode step
+# makes two calls per layer, and the object costs as much as a launch.
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _i32(t, what, device):
-    if t.dtype != torch.int32 or not t.is_contiguous() or t.device != device:
+    if t.dtype != _I32 or t.device != device or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous int32 tensor on {device}")
     return t
 
@@ -37,7 +41,8 @@ class PagedKV:
     """k, v [n_layers][n_pages][Hkv][page_size][D] (bf16 or fp16), table int32
     [n_slots][max_pages], lens int32 [n_slots], refs int32 [n_pages], free int32
     [n_pages] with n_free int32 [1]. Hq: query heads; max_rows: rows of the
-    largest attention call (sizes the workspace)."""
+    largest attention call (sizes the workspace). One thread at a time: the
+    calls share the argument structs and the workspace."""
 
     def __init__(self, n_layers, n_pages, page_size, Hkv, D, n_slots, max_pages, Hq=None, max_rows=2048,
                  dtype=torch.bfloat16, device="cuda"):
@@ -84,45 +89,53 @@ class PagedKV:
         self._desc_ref = ctypes.byref(d)
         self._rows, self._args = moe_kv_rows(), moe_attn_args()
         self._rows_ref, self._args_ref = ctypes.byref(self._rows), ctypes.byref(self._args)
+        self._args.Hq, self._scale, self._index = Hq, 1.0 / math.sqrt(D), dev.index or 0
 
     # ---- marshalling
+    def _stream(self, stream):
+        if stream is None:
+            return _current_stream(self._index)
+        return stream if isinstance(stream, int) else stream.cuda_stream
+
     def _heads(self, t, heads, what):
         """-> row stride of [rows][heads][D] with contiguous heads."""
-        if t.dtype != self.dtype or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != self.D or t.device != self.device:
-            raise ValueError(f"{what} must be [rows][{heads}][{self.D}] {self.dtype} on {self.device}")
-        s = t.stride()
-        if s[2] != 1 or (s[1] != self.D and heads > 1):
+        shape, D = t.shape, self.D
+        if len(shape) != 3 or shape[1] != heads or shape[2] != D or t.dtype != self.dtype or t.device != self.device:
+            raise ValueError(f"{what} must be [rows][{heads}][{D}] {self.dtype} on {self.device}")
+        s0, s1, s2 = t.stride()
+        if s2 != 1 or (s1 != D and heads > 1):
             raise ValueError(f"{what}: the heads of a row must be contiguous")
-        return s[0] if t.shape[0] > 1 else max(s[0], heads * self.D)
+        return s0 if shape[0] > 1 or s0 > heads * D else heads * D
 
     def _set_rows(self, n_rows, slots, row_start):
         r = self._rows
-        if slots is not None:
-            _i32(slots, "slots", self.device)
-        if row_start is not None:
-            _i32(row_start, "row_start", self.device)
-            B = row_start.numel() - 1
-            if B < 0 or (slots is not None and slots.numel() != B):
-                raise ValueError("row_start has one entry more than there are sequences")
+        if slots is None:
+            B, r.slots = n_rows, None
         else:
-            B = n_rows if slots is None else slots.numel()
+            B, r.slots = _i32(slots, "slots", self.device).numel(), slots.data_ptr()
+        if row_start is None:
+            r.row_start = None
+        else:
+            n = _i32(row_start, "row_start", self.device).numel() - 1
+            if n < 0 or (slots is not None and B != n):
+                raise ValueError("row_start has one entry more than there are sequences")
+            B, r.row_start = n, row_start.data_ptr()
         if (n_rows > 0 and B < 1) or (slots is None and B > self.n_slots):
             raise ValueError("more sequences than slots, or none")
         if n_rows > self.max_rows:
             raise ValueError(f"{n_rows} rows: the workspace is sized for {self.max_rows}")
         r.B, r.n_rows = B, n_rows
-        r.slots = None if slots is None else slots.data_ptr()
-        r.row_start = None if row_start is None else row_start.data_ptr()
 
     # ---- new tokens and attention
     def append(self, layer, k, v, slots=None, row_start=None, stream=None):
         """Write k, v [rows][Hkv][D] of the newest tokens into `layer`'s pages."""
         stride = self._heads(k, self.Hkv, "k")
-        if self._heads(v, self.Hkv, "v") != stride or v.shape[0] != k.shape[0]:
+        n = k.shape[0]
+        if self._heads(v, self.Hkv, "v") != stride or v.shape[0] != n:
             raise ValueError("k and v must have the same rows and row stride")
-        self._set_rows(k.shape[0], slots, row_start)
+        self._set_rows(n, slots, row_start)
         _lib.moe_kv_append(self._desc_ref, layer, self._rows_ref, k.data_ptr(), v.data_ptr(), stride, self.ws_ptr,
-                           self.ws_bytes, stream)
+                           self.ws_bytes, self._stream(stream))
 
     def _attend(self, fn, layer, q, slots, row_start, scale, window, sinks, want_lse, out, lse, stream):
         Hq = self.Hq
@@ -135,14 +148,14 @@ class PagedKV:
             raise ValueError("out must be a contiguous tensor like q")
         if lse is None:
             if want_lse:
-                lse = torch.empty((n, Hq), dtype=torch.float32, device=self.device)
-        elif lse.shape != (n, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != self.device:
+                lse = torch.empty((n, Hq), dtype=_F32, device=self.device)
+        elif lse.shape != (n, Hq) or lse.dtype != _F32 or not lse.is_contiguous() or lse.device != self.device:
             raise ValueError("lse must be a contiguous fp32 [rows][Hq]")
         a = self._args
-        a.Hq, a.scale, a.window, a.n_sink = Hq, (1.0 / math.sqrt(self.D) if scale is None else scale), window, sinks
+        a.scale, a.window, a.n_sink = (self._scale if scale is None else scale), window, sinks
         a.q, a.q_stride, a.o = q.data_ptr(), stride, out.data_ptr()
         a.lse = None if lse is None else lse.data_ptr()
-        fn(self._desc_ref, layer, self._rows_ref, self._args_ref, self.ws_ptr, self.ws_bytes, stream)
+        fn(self._desc_ref, layer, self._rows_ref, self._args_ref, self.ws_ptr, self.ws_bytes, self._stream(stream))
         return out if lse is None else (out, lse)
 
     def decode(self, layer, q, slots=None, scale=None, window=0, sinks=0, want_lse=False, out=None, lse=None,
@@ -164,25 +177,25 @@ class PagedKV:
         _i32(slots, "slots", self.device), _i32(add, "add", self.device)
         if add.numel() != slots.numel():
             raise ValueError("one add per slot")
-        _lib.moe_kv_grow(self._desc_ref, slots.data_ptr(), add.data_ptr(), slots.numel(), self.ws_ptr, self.ws_bytes, stream)
+        _lib.moe_kv_grow(self._desc_ref, slots.data_ptr(), add.data_ptr(), slots.numel(), self.ws_ptr, self.ws_bytes, self._stream(stream))
 
     def fork(self, src, dst, stream=None):
         """Slot dst[i] (empty) becomes a fork of slot src[i]."""
         _i32(src, "src", self.device), _i32(dst, "dst", self.device)
         if src.numel() != dst.numel():
             raise ValueError("one dst per src")
-        _lib.moe_kv_fork(self._desc_ref, src.data_ptr(), dst.data_ptr(), src.numel(), self.ws_ptr, self.ws_bytes, stream)
+        _lib.moe_kv_fork(self._desc_ref, src.data_ptr(), dst.data_ptr(), src.numel(), self.ws_ptr, self.ws_bytes, self._stream(stream))
 
     def free_slots(self, slots, stream=None):
         """Empty the slots; pages that no slot holds any more become free."""
         _i32(slots, "slots", self.device)
-        _lib.moe_kv_free(self._desc_ref, slots.data_ptr(), slots.numel(), self.ws_ptr, self.ws_bytes, stream)
+        _lib.moe_kv_free(self._desc_ref, slots.data_ptr(), slots.numel(), self.ws_ptr, self.ws_bytes, self._stream(stream))
 
     def compact(self, n_moved=None, stream=None):
         """Move the live pages to the lowest page numbers (n_moved: int32 [1], the moves)."""
         if n_moved is not None:
             _i32(n_moved, "n_moved", self.device)
-        _lib.moe_kv_compact(self._desc_ref, n_moved, self.ws_ptr, self.ws_bytes, stream)
+        _lib.moe_kv_compact(self._desc_ref, n_moved, self.ws_ptr, self.ws_bytes, self._stream(stream))
 
     def copy_pages(self, src, dst, stream=None):
         """Copy page src[i] to page dst[i] in every layer."""
@@ -190,11 +203,11 @@ class PagedKV:
         if src.numel() != dst.numel():
             raise ValueError("one dst per src")
         _lib.moe_kv_copy_pages(self._desc_ref, src.data_ptr(), dst.data_ptr(), src.numel(), self.ws_ptr, self.ws_bytes,
-                               stream)
+                               self._stream(stream))
 
     def status(self, stream=None):
         """-> (moe_status code, raw device status bits); waits for the stream."""
-        return _lib.moe_read_status(self.ws_ptr, stream)
+        return _lib.moe_read_status(self.ws_ptr, self._stream(stream))
 
     def clear_status(self, stream=None):
-        _lib.moe_workspace_init(self.ws_ptr, self.ws_bytes, stream)
+        _lib.moe_workspace_init(self.ws_ptr, self.ws_bytes, self._stream(stream))
