@@ -979,11 +979,17 @@ cudaError_t launch_attn_chunk(const Cache& c, const Rows& r, const Attn& a, bool
     return cudaErrorInvalidValue;
   for (g.b0 = 0; g.b0 < r.B; g.b0 += kChunkSeqs) {
     g.nseq = r.B - g.b0 < kChunkSeqs ? r.B - g.b0 : kChunkSeqs;
-    // Which calls can have a unit in many CTAs: where one sequence's units fill
-    // the GPU, the longest is at most about twice the mean and lies in a few.
-    // Elsewhere (few rows over a long context, sequences of very different
-    // lengths) the kernel that joins many parts follows. Either way is right.
-    g.combine = !(r.B == 1 && 3LL * ((r.n_rows + 2 * g.tq - 1) / (2 * g.tq)) * c.Hkv >= 2LL * grid);
+    // The kernel that joins many parts follows only where a unit can lie in many
+    // CTAs (either way is right). Not where one sequence's units fill the GPU:
+    // the longest is at most about twice the mean. And not where the table or the
+    // window leaves a unit few blocks: a CTA's share is four positions at least,
+    // so that nb blocks lie in at most (nb + 2) / 4 + 2 CTAs. A launch less is
+    // 2 us of 15 for 40 rows.
+    const bool full_gpu = r.B == 1 && 3LL * ((r.n_rows + 2 * g.tq - 1) / (2 * g.tq)) * c.Hkv >= 2LL * grid;
+    long long seen = (long long)c.max_pages * c.page;
+    const long long win = (long long)a.window + 2 * g.tq - 1;
+    if (a.window > 0 && win + a.n_sink + kBlk < seen) seen = win + a.n_sink + kBlk;  // both ends inside blocks
+    g.combine = !full_gpu && (seen + kBlk - 1) / kBlk + 1 > 4 * kJoinMost - 7;
     cudaError_t e;
     if (c.D == 128) e = f16 ? launch_one<true, 128>(g, grid, dev, st) : launch_one<false, 128>(g, grid, dev, st);
     else e = f16 ? launch_one<true, 64>(g, grid, dev, st) : launch_one<false, 64>(g, grid, dev, st);
