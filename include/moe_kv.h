@@ -20,8 +20,7 @@
  * warm-up call per kind, and report host-detected errors before anything is
  * launched. The workspace is initialised by moe_workspace_init, its status
  * word is read by moe_read_status, and it serves one call at a time. Results
- * are deterministic, and an attention row's result does not depend on the
- * other sequences of the call.
+ * are deterministic: the same call gives the same bits.
  *
  * Device-detected problems are OR-ed into the status word: 2 a slot outside
  * [0, n_slots) (its rows are treated as a sequence of length 0), a page number
@@ -79,9 +78,10 @@ typedef struct {
  * q_stride elements from row to row (heads contiguous, so q may be a part of a
  * larger projection); o [n_rows][Hq][D] contiguous; both in the cache's type
  * and 16-byte aligned, q_stride a multiple of 8. lse [n_rows][Hq] fp32 or
- * NULL. Products are of the cache's type, sums and softmax in fp32. What lies
- * in a sequence's pages past its length, or in pages wholly outside every
- * row's window, is not used and may be anything. */
+ * NULL. Products are of the cache's type, sums and softmax in fp32. A token
+ * that no row of the call sees (past the length, outside every row's window)
+ * is not used and may hold anything, NaN included; pages wholly of such tokens
+ * are not read and their table entries may be anything. */
 typedef struct {
   int32_t Hq;
   float scale;
@@ -106,11 +106,18 @@ moe_status moe_kv_append(const moe_kv_desc *kv, int32_t layer, const moe_kv_rows
 
 /* Attention of a decode window: the same number of rows (1 .. 16) for every
  * sequence, row_start NULL. The key-value pairs are read once per 16 query
- * rows of a KV head, the work split over the sequences' lengths and joined. */
+ * rows of a KV head, the work split over the sequences' lengths and joined. A
+ * row's result depends on its own sequence only, bit for bit: not on the other
+ * sequences of the call, nor on where the pages lie. A NaN or an infinity in a
+ * token reaches only the rows that see the token. */
 moe_status moe_attn_decode(const moe_kv_desc *kv, int32_t layer, const moe_kv_rows *rows,
                            const moe_attn_args *a, void *ws, size_t ws_bytes, void *stream);
 
-/* Attention of prompt chunks: any number of rows per sequence. */
+/* Attention of prompt chunks: any number of rows per sequence. How a long
+ * sequence is split depends on the call, so a row's last bits may differ in
+ * another call. Values that some rows of a sequence see must be finite: as in
+ * a plain product of probabilities and values, a NaN or an infinity may reach
+ * rows that do not see it. */
 moe_status moe_attn_chunk(const moe_kv_desc *kv, int32_t layer, const moe_kv_rows *rows,
                           const moe_attn_args *a, void *ws, size_t ws_bytes, void *stream);
 

@@ -271,6 +271,11 @@ __device__ __forceinline__ void schedule(Plan& p, const ChunkArgs& g, Unit* ring
   if (lane == 0 && g.combine) g.split[blockIdx.x] = sp;
 }
 
+__device__ __forceinline__ int add_acq_rel_gpu(int* p, int v) {
+  int old;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -706,146 +711,150 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         ++nsc;
         any = true;
       }
-      // ---- the segment's end: the tile's rows out
+      // ---- the segment's end: the tile's rows out. Its loops are kept small: the
+      // code runs once per segment, mostly cold, and its fetches are what it
+      // waits for (unrolled over 64 columns the ends took twice as long).
       const bool whole = x.u0 == 0 && x.u1 == x.nb;
+      // A unit in several CTAs: all but the last to end leave their part (place
+      // 2 c + 1 if it holds the unit's first block, else 2 c); the last one adds
+      // the parts up in the order of the keys, its own from tensor memory.
+      const int c0 = x.c0, c1 = whole ? x.c0 : x.c1, me = blockIdx.x;
+      auto place = [&](int c) { return (2 * c + (c == c0 ? 1 : 0)) * 2 + t; };
+      const bool here = !(g.combine && c1 - c0 >= kJoinMost);
+      int32_t* cnt = g.cnt + c0 * 8 + (warp & 7);
+      bool last = whole;
+      if (!whole && here) {  // while the last product runs
+        last = __shfl_sync(0xffffffffu, lane == 0 ? ld_acquire_gpu(cnt) : 0, 0) == c1 - c0;
+        __syncwarp();
+      }
       if (any) {
         wait(pv_done + 8 * t, (nsc & 1) ^ 1);
         tc_fence_after();
       }
-      // A unit in several CTAs: all but the last to end leave their part (place
-      // 2 c + 1 if it holds the unit's first block, else 2 c); the last one adds
-      // the parts up in the order of the keys, its own from tensor memory.
-      const int c0 = x.c0, c1 = x.c1, me = blockIdx.x;
-      auto place = [&](int c) { return (2 * c + (c == c0 ? 1 : 0)) * 2 + t; };
-      bool last = whole;
-      if (!whole) {
-        const bool here = !(g.combine && c1 - c0 >= kJoinMost);
-        int32_t* cnt = g.cnt + c0 * 8 + (warp & 7);
-        if (here) last = __shfl_sync(0xffffffffu, lane == 0 ? ld_acquire_gpu(cnt) : 0, 0) == c1 - c0;
-        if (!last) {
-          float* pm = g.pml + place(me) * 256;
-          pm[r] = m;
-          pm[128 + r] = l;
-          if (any) {
-            float* pp = g.part + (long long)place(me) * D * 128 + r * 4;
+      if (!last) {
+        float* pm = g.pml + place(me) * 256;
+        pm[r] = m;
+        pm[128 + r] = l;
+        if (any) {
+          float* pp = g.part + (long long)place(me) * D * 128 + r * 4;
 #pragma unroll 1
-            for (int i = 0; i < D; i += 32) {
+          for (int i = 0; i < D; i += 32) {
+            uint32_t o[32];
+            tc_ld32(to + i, o);
+            tc_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<uint4*>(pp + (long long)(i / 4 + e) * 512) =
+                  make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+        }
+        if (here) {
+          __syncwarp();
+          last = __shfl_sync(0xffffffffu, lane == 0 ? add_acq_rel_gpu(cnt, 1) : 0, 0) == c1 - c0;
+          __syncwarp();
+        }
+      }
+      if (last) {
+        // the first part of another CTA, 32 columns ahead of their use
+        const int cf = c0 == me ? c0 + 1 : c0;
+        float4 ahead[8];
+        auto fetch = [&](int i) {
+          const float* pp = g.part + (long long)place(cf) * D * 128 + i * 128 + r * 4;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) ahead[e] = __ldcg(reinterpret_cast<const float4*>(pp + e * 512));
+        };
+        float mt = m, lt = l, mf = -INFINITY, lf = 0.f;
+        if (!whole) {
+          fetch(0);
+          mt = -INFINITY;
+          lt = 0.f;
+#pragma unroll 1
+          for (int c = c0; c <= c1; ++c) {
+            const float* pm = g.pml + place(c) * 256 + r;
+            const float mc = c == me ? m : __ldcg(pm), lc = c == me ? l : __ldcg(pm + 128);
+            const float n = fmaxf(mt, mc), z = n == -INFINITY ? 0.f : n;
+            lt = fmaf(lc, ex2(mc - z), lt * ex2(mt - z));
+            mt = n;
+            if (c == cf) {
+              mf = mc;
+              lf = lc;
+            }
+          }
+        }
+        const float zt = mt == -INFINITY ? 0.f : mt, inv = lt == 0.f ? 0.f : 1.f / lt;
+        // factors; 0 for a row that saw nothing in a part (which may have left no accumulator)
+        const float f_me = l != 0.f ? ex2(m - zt) : 0.f, f_cf = lf != 0.f ? ex2(mf - zt) : 0.f;
+        // a thread holds a row; 32 columns at a time through the warp's own
+        // buffer, from which four lanes write 64 bytes of a row
+        const int nt = min(tq, tl - tf + 1);  // tokens of the tile
+        uint16_t* po = g.a.o + (((long long)x.row0 + t * tq) * g.a.Hq + x.hk * G) * D + (lane & 3) * 8;
+        int off[4];  // -1: a row of no token
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int rr = (warp & 3) * 32 + k * 8 + (lane >> 2), tk = s_tok[rr];
+          off[k] = tk < nt ? (tk * (g.a.Hq - G) + rr) * D : -1;
+        }
+#pragma unroll 1
+        for (int i = 0; i < D; i += 32) {
+          float y[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = 0.f;
+#pragma unroll 1
+          for (int c = c0; c <= c1; ++c) {
+            if (c == me || whole) {
+              if (!any) continue;
               uint32_t o[32];
               tc_ld32(to + i, o);
               tc_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                *reinterpret_cast<uint4*>(pp + (long long)(i / 4 + e) * 512) =
-                    make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-            }
-          }
-          if (here) {
-            __threadfence();
-            __syncwarp();
-            last = __shfl_sync(0xffffffffu, lane == 0 ? atomicAdd(cnt, 1) : 0, 0) == c1 - c0;
-          }
-        }
-        if (last) {
-          if (lane == 0) *cnt = 0;  // ready for the next call
-          __threadfence();
-        }
-      }
-      if (last) {
-        float mt = m, lt = l;
-        if (!whole) {
-          for (int c = c0; c <= c1; ++c)
-            if (c != me) mt = fmaxf(mt, __ldcg(g.pml + place(c) * 256 + r));
-          lt = 0.f;
-        }
-        const float zt = mt == -INFINITY ? 0.f : mt;
-        if (!whole)
-          for (int c = c0; c <= c1; ++c) {
-            const float mc = c == me ? m : __ldcg(g.pml + place(c) * 256 + r);
-            const float lc = c == me ? l : __ldcg(g.pml + place(c) * 256 + 128 + r);
-            lt = fmaf(lc, ex2(mc - zt), lt);
-          }
-        const float inv = lt == 0.f ? 0.f : 1.f / lt;
-        // a thread holds a row; 32 columns at a time through the warp's own
-        // buffer, from which four lanes write 64 bytes of a row
-        const int nt = min(tq, tl - tf + 1);  // tokens of the tile
-        uint16_t* po[4];
+              for (int k = 0; k < 32; ++k) y[k] = fmaf(__uint_as_float(o[k]), f_me, y[k]);
+            } else {
+              float f = f_cf;
+              float4 v[8];
+              if (c == cf) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int rr = (warp & 3) * 32 + k * 8 + (lane >> 2), tk = s_tok[rr];
-          po[k] = tk < nt ? g.a.o + (((long long)x.row0 + t * tq + tk) * g.a.Hq + x.hk * G + rr - tk * G) * D + (lane & 3) * 8
-                          : nullptr;
-        }
-        const bool none = lt == 0.f;  // the row sees nothing
-#pragma unroll 1
-        for (int i = 0; i < D; i += CW) {
-          float y[CW];
-#pragma unroll
-          for (int e = 0; e < CW; ++e) y[e] = 0.f;
-          if (whole) {
-            if (any) {
-#pragma unroll
-              for (int e = 0; e < CW; e += 16) {
-                uint32_t o[16];
-                tc_ld16(to + i + e, o);
-                tc_ld_wait();
-#pragma unroll
-                for (int k = 0; k < 16; ++k) y[e + k] = __uint_as_float(o[k]);
-              }
-            }
-          } else {
-#pragma unroll 1
-            for (int c = c0; c <= c1; ++c) {
-              if (c == me) {
-                if (!any) continue;
-                const float f = l != 0.f ? ex2(m - zt) : 0.f;
-#pragma unroll
-                for (int e = 0; e < CW; e += 16) {
-                  uint32_t o[16];
-                  tc_ld16(to + i + e, o);
-                  tc_ld_wait();
-#pragma unroll
-                  for (int k = 0; k < 16; ++k) y[e + k] = fmaf(__uint_as_float(o[k]), f, y[e + k]);
-                }
+                for (int e = 0; e < 8; ++e) v[e] = ahead[e];
+                if (i + 32 < D) fetch(i + 32);
               } else {
-                float4 v[CW / 4];
+                const float* pm = g.pml + place(c) * 256 + r;
+                const float lc = __ldcg(pm + 128), mc = __ldcg(pm);
                 const float* pp = g.part + (long long)place(c) * D * 128 + i * 128 + r * 4;
 #pragma unroll
-                for (int e = 0; e < CW / 4; ++e) v[e] = __ldcg(reinterpret_cast<const float4*>(pp + e * 512));
-                const float lc = __ldcg(g.pml + place(c) * 256 + 128 + r), mc = __ldcg(g.pml + place(c) * 256 + r);
-                if (lc == 0.f) continue;  // the row saw nothing there (it may have left no accumulator)
-                const float f = ex2(mc - zt);
+                for (int e = 0; e < 8; ++e) v[e] = __ldcg(reinterpret_cast<const float4*>(pp + e * 512));
+                f = lc != 0.f ? ex2(mc - zt) : 0.f;
+              }
+              if (f != 0.f) {
 #pragma unroll
-                for (int e = 0; e < CW / 4; ++e) {
+                for (int e = 0; e < 8; ++e) {
                   y[4 * e] = fmaf(v[e].x, f, y[4 * e]);
                   y[4 * e + 1] = fmaf(v[e].y, f, y[4 * e + 1]);
                   y[4 * e + 2] = fmaf(v[e].z, f, y[4 * e + 2]);
                   y[4 * e + 3] = fmaf(v[e].w, f, y[4 * e + 3]);
                 }
               }
+              __syncwarp();
             }
           }
+          const bool none = lt == 0.f;  // the row sees nothing
 #pragma unroll
-          for (int q = 0; q < CW; q += 32) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t w[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                w[k] = none ? 0u
-                            : pack2<F16>(y[q + 8 * e + 2 * k] * inv, y[q + 8 * e + 2 * k + 1] * inv);
-              st_s128(sout + lane * kOutPitch + e * 16, w[0], w[1], w[2], w[3]);
-            }
-            __syncwarp();
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if (po[k])
-                *reinterpret_cast<uint4*>(po[k] + i + q) = ld_s128(sout + (k * 8 + (lane >> 2)) * kOutPitch + (lane & 3) * 16);
-            __syncwarp();
+              w[k] = none ? 0u : pack2<F16>(y[8 * e + 2 * k] * inv, y[8 * e + 2 * k + 1] * inv);
+            st_s128(sout + lane * kOutPitch + e * 16, w[0], w[1], w[2], w[3]);
           }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (off[k] >= 0)
+              *reinterpret_cast<uint4*>(po + off[k] + i) = ld_s128(sout + (k * 8 + (lane >> 2)) * kOutPitch + (lane & 3) * 16);
+          __syncwarp();
         }
         if (g.a.lse && tok < nt)
           g.a.lse[((long long)x.row0 + t * tq + tok) * g.a.Hq + x.hk * G + r - tok * G] =
               lt == 0.f ? -INFINITY : (mt + log2f(lt)) * 0.6931471805599453f;
+        if (!whole && lane == 0) *cnt = 0;  // ready for the next call
       }
       if (any) {  // the accumulator may be written again
         tc_fence_before();

