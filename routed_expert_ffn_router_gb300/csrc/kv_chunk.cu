@@ -12,7 +12,8 @@
 // divided evenly over one CTA per SM: a causal chunk's later tiles see more
 // keys than its early ones, and few rows over a long context are work for all
 // SMs. A unit that lies in several CTAs leaves partial sums (m, l, o in fp32),
-// which combine_kernel joins in the order of the keys.
+// which the last of them to end joins in the order of the keys, or, of units in
+// many CTAs, combine_kernel.
 //
 // Warps. 0-3 and 4-7: the softmax of tile 0 and of tile 1 (a thread is a row);
 // 8: issues the products; 9: TMA of Q, K and V; 10: zeroes the value rows that
@@ -28,6 +29,15 @@
 // rescaled. Probabilities are rounded to the cache's type for the product
 // (half a step, 2^-8 for bf16 and 2^-11 for fp16, independent per key); their
 // sum is kept in fp32 before that rounding.
+//
+// Measured (head size 128, bf16, append included; of 1,917 TFLOP/s): 2,048 tokens
+// after 30,693, 32 / 8 heads, 719 us, 1,479 TFLOP/s (0.77); a 2,048-token prompt,
+// 16 / 4 heads, 38 us; five chunks of up to 901 tokens with a window of 512, 28 /
+// 4 heads, 68 us. A pair of tiles takes 3,300 to 3,500 cycles per block, 2,048 of
+// them products: the softmax of one tile and the products of the other wait for
+// each other in turn. A short prompt is bound by what stands around its blocks,
+// in cycles: 5,000 until the list is divided and 5,000 until the first scores,
+// 5,000 to 9,000 per segment's end, 2,000 to 4,000 more where it is joined.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -51,9 +61,10 @@ constexpr int kSoftRegs = 224, kRestRegs = 56;
 constexpr int kChunkSeqs = 256;         // sequences per launch
 constexpr int kMaxGrid = 304;
 constexpr int kUnitCost = 3;            // a unit's start and end, in blocks, for the division among the CTAs
-constexpr int kSnap = 2;                // a piece of so many blocks or fewer is not cut off
+constexpr int kSnap = 1;                // a piece of so many blocks or fewer is not cut off (2 is as good)
 constexpr int kBadRing = 8;
-constexpr int kJoinMost = 6;            // parts that a unit's last CTA joins; combine_kernel takes more
+constexpr int kJoinMost = 3;            // parts that a unit's last CTA joins where combine_kernel follows for the others
+constexpr int kFewBlocks = 17;          // a unit of no more blocks: its last CTA joins it
 constexpr int kSegRing = 4;
 constexpr int kSegReaders = 11;         // warps 0 .. 10
 constexpr int kOutPitch = 80;           // bytes per row of a warp's output buffer (64 and a pad)
@@ -188,8 +199,9 @@ __device__ __forceinline__ void schedule(Plan& p, const ChunkArgs& g, Unit* ring
   }
   if (lane == 0) p.off[g.nseq] = total;
   __syncwarp();
-  // a CTA per unit, or per four blocks where units are longer than that
-  const int nc = min(max((total + 3 + kUnitCost) / (4 + kUnitCost), units), (int)gridDim.x);
+  // a CTA per unit, or per two blocks where units are longer than that (512 tokens
+  // 19 us, 20 with four)
+  const int nc = min(max((total + 1 + kUnitCost) / (2 + kUnitCost), units), (int)gridDim.x);
   const bool work = (int)blockIdx.x < nc;
   const Division dv(total, max(nc, 1));
   const int lo = work ? dv.lo(blockIdx.x) : 0, hi = work ? dv.lo(blockIdx.x + 1) : 0;
@@ -247,10 +259,14 @@ __device__ __forceinline__ void schedule(Plan& p, const ChunkArgs& g, Unit* ring
       x.u1 = min(e, x.nb);
       x.c0 = x.c1 = blockIdx.x;
       if (x.u0 > 0 || x.u1 < x.nb) {  // a split unit: the CTAs of its first and its last block
-        x.c0 = dv.cta(start + kUnitCost);
-        x.c1 = dv.cta(start + kUnitCost + x.nb - 1);
-        while (cut_at(x.nb, dv.lo(x.c0 + 1) - start) <= 0) ++x.c0;
-        while (cut_at(x.nb, dv.lo(x.c1) - start) >= x.nb) --x.c1;
+        if (x.u0 > 0) {
+          x.c0 = dv.cta(start + kUnitCost);
+          while (cut_at(x.nb, dv.lo(x.c0 + 1) - start) <= 0) ++x.c0;
+        }
+        if (x.u1 < x.nb) {
+          x.c1 = dv.cta(start + kUnitCost + x.nb - 1);
+          while (cut_at(x.nb, dv.lo(x.c1) - start) >= x.nb) --x.c1;
+        }
         if (g.combine && x.c1 - x.c0 >= kJoinMost && x.c0 + 1 == (int)blockIdx.x)
           sp = {x.c0, x.c1, x.row0, x.nt, x.hk};
       }
@@ -609,7 +625,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     }
   } else {
     // ================= softmax (a thread is a row of its tile) =================
-    constexpr int CW = 64;  // columns of O at a time in the segment's end
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     const int t = warp >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -871,49 +886,69 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
   if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-// Units that lie in several CTAs: their parts folded in the order of the keys.
-// Block (i, y): the unit recorded at CTA i's place; 32 of its 256 rows, four
-// threads per row.
+// Units that lie in many CTAs: their parts folded in the order of the keys. A
+// job is eight columns of a tile of such a unit, a thread per row; the parts
+// come kFold at a time, so that a few reads' latency covers them all (one by one
+// 38 parts took 40 us).
+constexpr int kFold = 8;
 template <bool F16, int D>
-__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ ChunkArgs g) {
+__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ ChunkArgs g, int grid) {
+  __shared__ int s_list[kMaxGrid], s_n;
   griddep_wait();
   griddep_launch_dependents();
-  const Split sp = g.split[blockIdx.x + 1];
-  if (sp.c0 < 0) return;
-  const int row = blockIdx.y * 32 + (threadIdx.x >> 2), t = row >> 7, r = row & 127, q = threadIdx.x & 3;
-  const int tok = r / g.a.G, local = t * g.tq + tok;
-  if (tok >= g.tq || local >= sp.rows) return;
-  auto ml = [&](int c, int k) { return __ldcg(g.pml + ((2 * c + (c == sp.c0 ? 1 : 0)) * 2 + t) * 256 + k * 128 + r); };
-  float m = -INFINITY;
-  for (int c = sp.c0; c <= sp.c1; ++c) m = fmaxf(m, ml(c, 0));
-  const float z = m == -INFINITY ? 0.f : m;
-  float l = 0.f, o[D / 4];
-#pragma unroll
-  for (int k = 0; k < D / 4; ++k) o[k] = 0.f;
-  for (int c = sp.c0; c <= sp.c1; ++c) {
-    const float lc = ml(c, 1);
-    if (lc == 0.f) continue;  // the row saw nothing here (its accumulator may not have been written)
-    const float f = ex2(ml(c, 0) - z);
-    l = fmaf(lc, f, l);
-    const float* pp = g.part + (long long)((2 * c + (c == sp.c0 ? 1 : 0)) * 2 + t) * D * 128 + r * 4;
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(pp + (long long)(q * (D / 16) + k) * 512));
-      o[4 * k] = fmaf(v.x, f, o[4 * k]);
-      o[4 * k + 1] = fmaf(v.y, f, o[4 * k + 1]);
-      o[4 * k + 2] = fmaf(v.z, f, o[4 * k + 2]);
-      o[4 * k + 3] = fmaf(v.w, f, o[4 * k + 3]);
+  const int r = threadIdx.x;
+  if (r < 32) {  // the units
+    int n = 0;
+    for (int i0 = 1; i0 < grid; i0 += 32) {
+      const bool is = i0 + r < grid && __ldcg(&g.split[i0 + r].c0) >= 0;
+      const unsigned all = __ballot_sync(0xffffffffu, is);
+      if (is) s_list[n + __popc(all & ((1u << r) - 1u))] = i0 + r;
+      n += __popc(all);
     }
+    if (r == 0) s_n = n;
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const long long at_row = (long long)(sp.row0 + local) * g.a.Hq + sp.hk * g.a.G + r - tok * g.a.G;
-  uint16_t* po = g.a.o + at_row * D + q * (D / 4);
+  __syncthreads();
+  constexpr int kCols = D / 8;
+  for (int job = blockIdx.x; job < s_n * 2 * kCols; job += gridDim.x) {
+    const Split sp = g.split[s_list[job / (2 * kCols)]];
+    const int t = job / kCols & 1, q = job % kCols;
+    const int tok = r / g.a.G, local = t * g.tq + tok;
+    if (tok >= g.tq || local >= sp.rows) continue;
+    float m = -INFINITY, l = 0.f, o[8];
 #pragma unroll
-  for (int k = 0; k < D / 32; ++k)
-    *reinterpret_cast<uint4*>(po + 8 * k) =
-        make_uint4(pack2<F16>(o[8 * k] * inv, o[8 * k + 1] * inv), pack2<F16>(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
-                   pack2<F16>(o[8 * k + 4] * inv, o[8 * k + 5] * inv), pack2<F16>(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
-  if (q == 0 && g.a.lse) g.a.lse[at_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    for (int k = 0; k < 8; ++k) o[k] = 0.f;
+#pragma unroll 1
+    for (int b = sp.c0; b <= sp.c1; b += kFold) {
+      float mc[kFold], lc[kFold];
+      float4 v[kFold][2];
+#pragma unroll
+      for (int i = 0; i < kFold; ++i) {
+        const int c = min(b + i, sp.c1);
+        const long long place = (2 * c + (c == sp.c0 ? 1 : 0)) * 2 + t;
+        const float* pp = g.part + place * D * 128 + q * 1024 + r * 4;
+        mc[i] = __ldcg(g.pml + place * 256 + r);
+        lc[i] = b + i <= sp.c1 ? __ldcg(g.pml + place * 256 + 128 + r) : 0.f;
+        v[i][0] = __ldcg(reinterpret_cast<const float4*>(pp));
+        v[i][1] = __ldcg(reinterpret_cast<const float4*>(pp + 512));
+      }
+#pragma unroll
+      for (int i = 0; i < kFold; ++i) {
+        if (lc[i] == 0.f) continue;  // the row saw nothing here (its accumulator may not have been written)
+        const float n = fmaxf(m, mc[i]), f = ex2(m - n), e = ex2(mc[i] - n);  // mc is finite
+        m = n;
+        l = fmaf(lc[i], e, l * f);
+        const float w[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] = fmaf(w[k], e, o[k] * f);
+      }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const long long at_row = (long long)(sp.row0 + local) * g.a.Hq + sp.hk * g.a.G + r - tok * g.a.G;
+    *reinterpret_cast<uint4*>(g.a.o + at_row * D + q * 8) =
+        make_uint4(pack2<F16>(o[0] * inv, o[1] * inv), pack2<F16>(o[2] * inv, o[3] * inv),
+                   pack2<F16>(o[4] * inv, o[5] * inv), pack2<F16>(o[6] * inv, o[7] * inv));
+    if (q == 0 && g.a.lse) g.a.lse[at_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  }
 }
 
 template <bool F16, int D>
@@ -938,7 +973,7 @@ cudaError_t launch_one(ChunkArgs& g, int grid, int dev, cudaStream_t st) {
   }
   const cudaError_t e = launch_pdl(K_ATTN_CHUNK, chunk_kernel<F16, D>, dim3(grid), kChunkThreads, smem, st, g);
   if (e != cudaSuccess || !g.combine) return e;
-  return launch_pdl(K_ATTN_COMBINE, combine_kernel<F16, D>, dim3(grid - 1, 8), 128, 0, st, g);
+  return launch_pdl(K_ATTN_COMBINE, combine_kernel<F16, D>, dim3(2 * grid), 128, 0, st, g, grid);
 }
 
 int chunk_grid(int* dev) {
@@ -991,14 +1026,14 @@ cudaError_t launch_attn_chunk(const Cache& c, const Rows& r, const Attn& a, bool
     // The kernel that joins many parts follows only where a unit can lie in many
     // CTAs (either way is right). Not where one sequence's units fill the GPU:
     // the longest is at most about twice the mean. And not where the table or the
-    // window leaves a unit few blocks: a CTA's share is four positions at least,
-    // so that nb blocks lie in at most (nb + 2) / 4 + 2 CTAs. A launch less is
-    // 2 us of 15 for 40 rows.
+    // window leaves a unit few blocks: a launch less is 2 us of 15 for 40 rows.
+    // Joined there, 38 parts of 40 rows over 30,000 tokens are 31 us; 8 parts of
+    // 4,000 tokens 23 us (35 by the last CTA), 256 rows over 16,000 69 (79).
     const bool full_gpu = r.B == 1 && 3LL * ((r.n_rows + 2 * g.tq - 1) / (2 * g.tq)) * c.Hkv >= 2LL * grid;
     long long seen = (long long)c.max_pages * c.page;
     const long long win = (long long)a.window + 2 * g.tq - 1;
     if (a.window > 0 && win + a.n_sink + kBlk < seen) seen = win + a.n_sink + kBlk;  // both ends inside blocks
-    g.combine = !full_gpu && (seen + kBlk - 1) / kBlk + 1 > 4 * kJoinMost - 7;
+    g.combine = !full_gpu && (seen + kBlk - 1) / kBlk + 1 > kFewBlocks;
     cudaError_t e;
     if (c.D == 128) e = f16 ? launch_one<true, 128>(g, grid, dev, st) : launch_one<false, 128>(g, grid, dev, st);
     else e = f16 ? launch_one<true, 64>(g, grid, dev, st) : launch_one<false, 64>(g, grid, dev, st);
