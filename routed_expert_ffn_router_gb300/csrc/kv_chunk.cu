@@ -167,7 +167,8 @@ __device__ __forceinline__ int warp_scan(int v, int lane) {  // inclusive
 }
 
 // The whole of warp 11: the division, then this CTA's segments into the ring.
-__device__ __forceinline__ void schedule(Plan& p, const ChunkArgs& g, Unit* ring, uint32_t full, uint32_t empty) {
+__device__ __forceinline__ void schedule(Plan& p, const ChunkArgs& g, Unit* ring, uint32_t full, uint32_t empty,
+                                         uint32_t shared) {
   const int lane = threadIdx.x & 31, Hkv = g.c.Hkv;
   // the sequences, and the list positions of the units of each
   int total = 0, units = 0;
@@ -243,11 +244,20 @@ __device__ __forceinline__ void schedule(Plan& p, const ChunkArgs& g, Unit* ring
       mbar_arrive(full + 8 * i);
     }
     __syncwarp();
+    return true;
+  };
+  // the CTAs that share the segment's unit follow: its readers need them at its end only
+  auto put_shared = [&] {
+    if (lane == 0) {
+      ring[i].c0 = x.c0;
+      ring[i].c1 = x.c1;
+      mbar_arrive(shared + 8 * i);
+    }
+    __syncwarp();
     if (++i == kSegRing) {
       i = 0;
       ph ^= 1;
     }
-    return true;
   };
   Split sp;
   sp.c0 = -1;
@@ -258,6 +268,7 @@ __device__ __forceinline__ void schedule(Plan& p, const ChunkArgs& g, Unit* ring
       x.u0 = min(a, x.nb);
       x.u1 = min(e, x.nb);
       x.c0 = x.c1 = blockIdx.x;
+      ok = put(1);
       if (x.u0 > 0 || x.u1 < x.nb) {  // a split unit: the CTAs of its first and its last block
         if (x.u0 > 0) {
           x.c0 = dv.cta(start + kUnitCost);
@@ -270,7 +281,7 @@ __device__ __forceinline__ void schedule(Plan& p, const ChunkArgs& g, Unit* ring
         if (g.combine && x.c1 - x.c0 >= kJoinMost && x.c0 + 1 == (int)blockIdx.x)
           sp = {x.c0, x.c1, x.row0, x.nt, x.hk};
       }
-      ok = put(1);
+      if (ok) put_shared();
     }
     start += weight(x.nb);
     if (start >= hi) break;
@@ -350,7 +361,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
   constexpr int NST = stages<D>();
   extern __shared__ __align__(1024) uint8_t smem_chunk[];
   __shared__ Plan s_plan;
-  __shared__ __align__(8) uint64_t s_bar[3 * NST + 2 * kSegRing + 13];
+  __shared__ __align__(8) uint64_t s_bar[3 * NST + 3 * kSegRing + 13];
   __shared__ uint32_t s_bad[kBadRing];
   __shared__ __align__(16) Unit s_seg[kSegRing];
   __shared__ uint32_t s_tmem;
@@ -363,6 +374,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
   const uint32_t q_full = v_ready + 8 * NST, q_empty = q_full + 8;
   const uint32_t s_full = q_empty + 8, p_full = s_full + 16, pv_done = p_full + 32, o_free = pv_done + 16;
   const uint32_t drained = o_free + 16, seg_full = drained + 8, seg_empty = seg_full + 8 * kSegRing;
+  const uint32_t seg_shared = seg_empty + 8 * kSegRing;
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
       mbar_init(kv_full + 8 * i, 1);
@@ -381,6 +393,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     mbar_init(drained, 1);
     for (int i = 0; i < kSegRing; ++i) {
       mbar_init(seg_full + 8 * i, 1);
+      mbar_init(seg_shared + 8 * i, 1);
       mbar_init(seg_empty + 8 * i, kSegReaders);
     }
     fence_barrier_init();
@@ -441,10 +454,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         // sees, or of a bad page, the row past the pool's end, from where TMA
         // fills in zeros
         const int past = g.c.n_pages * g.c.Hkv << g.logpage;
-        auto entry = [&](int u) {
+        // (page() only reads the table: its result is first needed in row_of())
+        auto sees = [&](int j) { return lane < nbox && j <= x.pl && (j + P > x.from || j < x.first); };
+        auto page = [&](int u) {
           const int j = x.block(u) * kBlk + lane * P;
-          if (lane >= nbox || j > x.pl || !(j + P > x.from || j < x.first)) return past;
-          const int pg = tab[j >> g.logpage];
+          return sees(j) ? tab[j >> g.logpage] : 0;
+        };
+        auto row_of = [&](int u, int pg) {
+          const int j = x.block(u) * kBlk + lane * P;
+          if (!sees(j)) return past;
           if (pg >= 0 && pg < g.c.n_pages) return ((pg * g.c.Hkv + x.hk) << g.logpage) + (j & (g.c.page - 1));
           atomicOr(g.status, DEV_BAD_SLOT);
           return past + 1;
@@ -460,10 +478,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           }
           __syncwarp();
         };
+        int pg = page(x.u0);
         if (opening) queries();  // the CTA's first segment: the queries first
-        int row = entry(x.u0);
         for (int u = x.u0; u < x.u1 && !dead; ++u) {
-          const int ahead = u + 1 < x.u1 ? entry(u + 1) : past;
+          const int row = row_of(u, pg);
+          pg = u + 1 < x.u1 ? page(u + 1) : 0;
           const unsigned bad = __ballot_sync(0xffffffffu, row == past + 1);
           for (int kv = 0; kv < 2; ++kv) {
             wait(kv_empty + 8 * st, ph);
@@ -486,7 +505,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             if (u == x.u0 && kv == 0 && !opening) queries();
           }
           bad_at = (bad_at + 1) % kBadRing;
-          row = ahead;
         }
         opening = false;
       }
@@ -621,7 +639,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     }
     else {
       // ================= the division and this CTA's segments =================
-      schedule(s_plan, g, s_seg, seg_full, seg_empty);
+      schedule(s_plan, g, s_seg, seg_full, seg_empty, seg_shared);
     }
   } else {
     // ================= softmax (a thread is a row of its tile) =================
@@ -733,7 +751,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       // A unit in several CTAs: all but the last to end leave their part (place
       // 2 c + 1 if it holds the unit's first block, else 2 c); the last one adds
       // the parts up in the order of the keys, its own from tensor memory.
-      const int c0 = x.c0, c1 = whole ? x.c0 : x.c1, me = blockIdx.x;
+      wait(seg_shared + 8 * seg_i, seg_ph);
+      const int c0 = x.c0, c1 = x.c1, me = blockIdx.x;
       auto place = [&](int c) { return (2 * c + (c == c0 ? 1 : 0)) * 2 + t; };
       const bool here = !(g.combine && c1 - c0 >= kJoinMost);
       int32_t* cnt = g.cnt + c0 * 8 + (warp & 7);
