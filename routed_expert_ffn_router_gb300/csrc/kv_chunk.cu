@@ -65,6 +65,7 @@ constexpr int kSnap = 1;                // a piece of so many blocks or fewer is
 constexpr int kBadRing = 8;
 constexpr int kJoinMost = 3;            // parts that a unit's last CTA joins where combine_kernel follows for the others
 constexpr int kFewBlocks = 17;          // a unit of no more blocks: its last CTA joins it
+constexpr uint32_t kTries = 1u << 22;   // of a wait, each up to a microsecond long
 constexpr int kSegRing = 4;
 constexpr int kSegReaders = 11;         // warps 0 .. 10
 constexpr int kOutPitch = 80;           // bytes per row of a warp's output buffer (64 and a pad)
@@ -417,15 +418,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
   auto takes = [&](int j0, int tf, int tl) {  // whether a tile sees anything of the block at token j0
     return tl >= tf && j0 <= tl && (W == 0 || j0 + kBlk - 1 > max(tf, 0) - W || j0 < S);
   };
+  // A wait is a few instructions: the warp that issues the products runs from a
+  // cold instruction cache between the softmax warps' loops, and a wait that
+  // found its phase complete cost it 270 cycles with the time taken inside.
   bool dead = false;  // an expired wait: go on without waiting (the status word says so)
   auto wait = [&](uint32_t bar, uint32_t parity) {
-    if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait_sleep(bar, parity, g.status));
+    uint32_t n = dead ? 1u : kTries;
+    while (!mbar_try_wait_ns(bar, parity, 1000) && --n) {
+    }
+    dead |= n == 0;
+    __syncwarp();
   };
   // this CTA's segments: next_seg() waits for one (false: there are no more),
   // done_seg() gives its place back
   int seg_i = 0, seg_ph = 0;
   auto next_seg = [&] {
     wait(seg_full + 8 * seg_i, seg_ph);
+    dead = __any_sync(0xffffffffu, dead);
     return !dead && s_seg[seg_i].more != 0;
   };
   auto done_seg = [&] {
@@ -486,7 +495,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           const unsigned bad = __ballot_sync(0xffffffffu, row == past + 1);
           for (int kv = 0; kv < 2; ++kv) {
             wait(kv_empty + 8 * st, ph);
-            if (dead) break;
+            if ((dead = __any_sync(0xffffffffu, dead))) break;
             if (lane == 0) {
               if (kv == 0) s_bad[bad_at] = bad;
               mbar_expect_tx(kv_full + 8 * st, kTileB);
@@ -898,6 +907,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       done_seg();
     }
   }
+  if (dead) atomicOr(g.status, DEV_TIMEOUT);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
