@@ -68,6 +68,7 @@ __host__ __device__ constexpr int dec_ctas() { return 3 - RG; }  // per SM
 constexpr int kAllBar = 3;              // named barrier of all consumer warps
 constexpr int kPairBar = 4;             // named barriers 4 .. 7: the warps of two groups with the same keys (1, 2: a group's)
 constexpr int kOPitch = 64 + 4;         // floats per row of the buffer in which the warps' O meet
+constexpr uint32_t kTries = 1u << 24;   // of a wait, up to 128 ns long each
 constexpr int kSeqCap = 128;            // sequences per launch
 constexpr int kCntBase = 2048;          // this kernel's counters in the workspace head
 
@@ -382,19 +383,29 @@ __global__ void __launch_bounds__(dec_threads<RG>(), dec_ctas<RG>()) decode_kern
   };
   bool more = lo < hi;
   if (more && span >= it.nspan) more = next_item();
+  // A wait on the ring, a few instructions long. After an expired one (the status
+  // word says that the results are incomplete) a warp goes on without waiting,
+  // so that all meet at every barrier.
+  bool dead = false;
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    uint32_t n = dead ? 1u : kTries;
+    while (!mbar_try_wait_ns(bar, parity, 128) && --n) {
+    }
+    dead |= n == 0;
+    __syncwarp();
+  };
 
   if (warp == 4 * RG) {
     // ================= producer =================
     const int P = 1 << g.logP, nbox = kTile >> g.logP, box = P * D * 2;
     int st = 0, ph = 1;
-    bool ok = true;
-    while (more && ok && ioff + (span << it.ks) < hi) {
+    while (more && !dead && ioff + (span << it.ks) < hi) {
       const int v0 = span << it.ks, v1 = min(it.nvis, v0 + (1 << it.ks));
       const int from = W > 0 ? max(0, max(0, it.pf) - W + 1) : 0, first = min(S, from);
       const int32_t* tab = g.c.table + (long long)it.slot * g.c.max_pages;
       // page numbers of 32 boxes at a time, one per lane
       const int per = 32 / nbox;  // tiles whose boxes fill the lanes
-      for (int vb = v0; vb < v1 && ok; vb += per) {
+      for (int vb = v0; vb < v1 && !dead; vb += per) {
         int row = -1;       // the box's first row in the pool; -1 not needed, -2 bad page
         {
           const int v = vb + lane / nbox;
@@ -412,8 +423,8 @@ __global__ void __launch_bounds__(dec_threads<RG>(), dec_ctas<RG>()) decode_kern
           }
         }
         for (int t = 0; t < per && vb + t < v1; ++t) {
-          ok = mbar_wait_short(empty + 8 * st, ph, g.status);
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          wait(empty + 8 * st, ph);
+          if ((dead = __any_sync(0xffffffffu, dead))) break;
           const int mine = __shfl_sync(0xffffffffu, row, t * nbox + (lane & (nbox - 1)));
           const unsigned load = __ballot_sync(0xffffffffu, lane < nbox && mine >= 0);
           const unsigned bad = __ballot_sync(0xffffffffu, lane < nbox && mine == -2);
@@ -435,6 +446,7 @@ __global__ void __launch_bounds__(dec_threads<RG>(), dec_ctas<RG>()) decode_kern
       }
       if (++span >= it.nspan) more = next_item();
     }
+    if (dead) atomicOr(g.status, DEV_TIMEOUT);
     return;
   }
 
@@ -489,7 +501,6 @@ __global__ void __launch_bounds__(dec_threads<RG>(), dec_ctas<RG>()) decode_kern
     return rr < n_q * G ? rr : -1;
   };
 
-  bool ok = true;
   while (more && ioff + (span << it.ks) < hi) {
     if (run0 < 0) {  // a new item: its query rows as B operands
       run0 = span;
@@ -512,9 +523,7 @@ __global__ void __launch_bounds__(dec_threads<RG>(), dec_ctas<RG>()) decode_kern
     const int v1 = min(it.nvis, (span + 1) << it.ks);
     for (int v = span << it.ks; v < v1; ++v) {
       const int j0 = it.tile(v) * kTile + wg * 16 * KB;  // the warp's first key
-      // after an expired wait (the status word says that the results are
-      // incomplete) a warp goes on without waiting, so that all meet at every barrier
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_short(full + 8 * st, ph, g.status));
+      wait(full + 8 * st, ph);
       const uint32_t bad = *(volatile uint32_t*)&s_badbox[st];
       const uint32_t sk = ring + st * kStage, sv = sk + kStage / 2;
       // ---- scores: keys 16 kb + lane / 4, + 8; rows ra, ra + 1
@@ -738,6 +747,7 @@ __global__ void __launch_bounds__(dec_threads<RG>(), dec_ctas<RG>()) decode_kern
       ++span;
     }
   }
+  if (dead) atomicOr(g.status, DEV_TIMEOUT);
   // ---- joins, after the loop over tiles: they would take registers from it,
   // and the ring is free once every group is here
   named_bar_sync(kAllBar, 128 * RG);
