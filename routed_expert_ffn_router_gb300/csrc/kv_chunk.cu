@@ -429,6 +429,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     dead |= n == 0;
     __syncwarp();
   };
+  auto wait2 = [&](uint32_t bar, uint32_t parity, uint32_t bar2, uint32_t parity2) {  // for both
+    uint32_t n = dead ? 1u : kTries;
+    while (true) {
+      const bool a = mbar_try_wait_ns(bar, parity, 1000), b = mbar_try_wait_ns(bar2, parity2, 1000);
+      if ((a && b) || !--n) break;
+    }
+    dead |= n == 0;
+    __syncwarp();
+  };
   // this CTA's segments: next_seg() waits for one (false: there are no more),
   // done_seg() gives its place back
   int seg_i = 0, seg_ph = 0;
@@ -623,13 +632,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           const bool nx = u + 1 < x.u1;
           const int jn = nx ? x.block(u + 1) * kBlk : 0;
           const bool n0 = nx && takes(jn, tf[0], tl[0]), n1 = nx && takes(jn, tf[1], tl[1]);
-          wait(v_ready + 8 * vst, vph);
+          if (nx) wait2(v_ready + 8 * vst, vph, kv_full + 8 * kst, kph);
+          else wait(v_ready + 8 * vst, vph);
           tc_fence_after();
           if (t0) product(0, vst);
-          if (nx) {
-            wait(kv_full + 8 * kst, kph);
-            tc_fence_after();
-          }
           if (n0) score(0, kst);
           if (t1) product(1, vst);
           tc_commit_el(kv_empty + 8 * vst, lead);
