@@ -7,8 +7,11 @@
 // Units and blocks. A tile is 128 query rows: 128 / G tokens (rounded down)
 // times the G query heads of one KV head, so the heads of a group share one
 // read of their keys. A unit is two tiles in a row of one sequence and KV head;
-// its blocks are the 128-token blocks of keys that some row sees (first tokens
-// that stay visible, then the window). The list of all units' blocks is
+// its blocks are 128 keys each, packed from the TMA boxes (a page, or 128 rows of
+// one) that some row sees: first tokens that stay visible, then the window.
+// (With blocks of 128 tokens in a row, a window of 512 and 4 first tokens was
+// seven blocks a unit instead of five, 55 us instead of 48 for the five chunks
+// below.) The list of all units' blocks is
 // divided evenly over one CTA per SM: a causal chunk's later tiles see more
 // keys than its early ones, and few rows over a long context are work for all
 // SMs. A unit that lies in several CTAs leaves partial sums (m, l, o in fp32),
@@ -31,13 +34,18 @@
 // sum is kept in fp32 before that rounding.
 //
 // Measured (head size 128, bf16, append included; of 1,917 TFLOP/s): 2,048 tokens
-// after 30,693, 32 / 8 heads, 719 us, 1,479 TFLOP/s (0.77); a 2,048-token prompt,
-// 16 / 4 heads, 38 us; five chunks of up to 901 tokens with a window of 512, 28 /
-// 4 heads, 68 us. A pair of tiles takes 3,300 to 3,500 cycles per block, 2,048 of
-// them products: the softmax of one tile and the products of the other wait for
-// each other in turn. A short prompt is bound by what stands around its blocks,
-// in cycles: 5,000 until the list is divided and 5,000 until the first scores,
-// 5,000 to 9,000 per segment's end, 2,000 to 4,000 more where it is joined.
+// after 30,693, 32 / 8 heads, 675 us, 1,575 TFLOP/s (0.82); a 2,048-token prompt,
+// 16 / 4 heads, 33 us; five chunks of up to 901 tokens with a window of 512 and 4
+// first tokens, 28 / 4 heads, 48 us. A pair of tiles takes about 3,000 cycles per
+// block, 2,048 of them products; a tile's chain is its softmax (1,700), its two
+// products (1,024) and the barriers between. Steps of 64 keys with two buffers of
+// scores break that chain, but a product of 64 keys takes 51 cycles instead of
+// 32 (both operands come from shared memory): 886 us. So were probabilities
+// taken with the maximum so far while the block's own is found (+8 %), two
+// threads per row (813 us). A short prompt is bound by what stands around its
+// blocks: 10,000 cycles until the first scores (the list's division 5,000), 5,000
+// to 9,000 at a segment's end, 2,000 to 4,000 more where it is joined, most of
+// them instruction fetches of code that runs once.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -99,11 +107,13 @@ struct Unit {
   int slot, row0, nt;      // first row (token) of the call and tokens
   int pf, pl;              // positions of the first and the last token; pl = -1 if nothing is seen
   int from, first;         // the window's first token; first tokens below it that stay visible
-  int ns, wt, nb;          // blocks of first tokens, first window block, blocks
+  // Its keys are the TMA boxes that some row sees, in order: position i of them is
+  // token i below ns (the boxes of the first tokens), token i + gap from there on
+  // (the window's). Block u is positions 128 u .. 128 u + 127.
+  int ns, gap, nb;
   int u0, u1;              // this CTA's blocks of it
   int c0, c1;              // the CTAs that share it
   int more;                // 0: no unit, the end of the list
-  __device__ int block(int u) const { return u < ns ? u : u - ns + wt; }
   // tokens' positions of tile t: [tf, tl], tl < tf if it has none
   __device__ void tile(int t, int tq, int& tf, int& tl) const {
     tf = pf + t * tq;
@@ -138,13 +148,14 @@ __device__ __forceinline__ Unit unit_at(const Plan& p, const ChunkArgs& g, int b
   x.nt = min(p.n[b] - i0, 2 * g.tq);
   x.pf = p.len[b] - p.n[b] + i0;
   x.pl = x.slot < 0 ? -1 : x.pf + x.nt - 1;
-  x.from = x.first = x.ns = x.wt = x.nb = 0;
+  x.from = x.first = x.ns = x.gap = x.nb = 0;
   if (x.pl >= 0) {
     x.from = W > 0 ? max(0, max(0, x.pf) - W + 1) : 0;
     x.first = min(g.a.n_sink, x.from);
-    x.ns = (x.first + kBlk - 1) / kBlk;
-    x.wt = max(x.from / kBlk, x.ns);
-    x.nb = x.ns + x.pl / kBlk - x.wt + 1;
+    const int P = 1 << g.logP;
+    x.ns = (x.first + P - 1) & -P;
+    x.gap = max(x.from & -P, x.ns) - x.ns;
+    x.nb = ((x.pl & -P) + P - x.gap + kBlk - 1) / kBlk;
   }
   return x;
 }
@@ -415,8 +426,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
   const uint32_t tmem = s_tmem;
   griddep_wait();  // an append's rows, and the workspace of the launch before
 
-  auto takes = [&](int j0, int tf, int tl) {  // whether a tile sees anything of the block at token j0
-    return tl >= tf && j0 <= tl && (W == 0 || j0 + kBlk - 1 > max(tf, 0) - W || j0 < S);
+  // The blocks of a unit of which tile t sees something: those below `end` that
+  // are below `early` (first tokens) or not below `win` (the tile's own window).
+  struct Taken {
+    int end, early, win;
+    __device__ bool operator()(int u) const { return u < end && (u < early || u >= win); }
+  };
+  auto taken = [&](const Unit& x, int t) {
+    int tf, tl;
+    x.tile(t, tq, tf, tl);
+    const int last = tl < x.ns ? tl : max(x.ns - 1, tl - x.gap);  // its last token's position
+    Taken k;
+    k.end = tl >= max(tf, 0) ? last / kBlk + 1 : 0;
+    k.early = W > 0 ? (max(x.ns, S - x.gap) + kBlk - 1) / kBlk : 0;
+    k.win = W > 0 ? max(x.ns, max(tf, 0) - W + 1 - x.gap) / kBlk : 0;
+    return k;
   };
   // A wait is a few instructions: the warp that issues the products runs from a
   // cold instruction cache between the softmax warps' loops, and a wait that
@@ -473,14 +497,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         // fills in zeros
         const int past = g.c.n_pages * g.c.Hkv << g.logpage;
         // (page() only reads the table: its result is first needed in row_of())
-        auto sees = [&](int j) { return lane < nbox && j <= x.pl && (j + P > x.from || j < x.first); };
+        auto token = [&](int u) {  // of lane's box, -1 if there is none
+          const int i = u * kBlk + lane * P, j = i < x.ns ? i : i + x.gap;
+          return lane < nbox && j <= x.pl ? j : -1;
+        };
         auto page = [&](int u) {
-          const int j = x.block(u) * kBlk + lane * P;
-          return sees(j) ? tab[j >> g.logpage] : 0;
+          const int j = token(u);
+          return j >= 0 ? tab[j >> g.logpage] : 0;
         };
         auto row_of = [&](int u, int pg) {
-          const int j = x.block(u) * kBlk + lane * P;
-          if (!sees(j)) return past;
+          const int j = token(u);
+          if (j < 0) return past;
           if (pg >= 0 && pg < g.c.n_pages) return ((pg * g.c.Hkv + x.hk) << g.logpage) + (j & (g.c.page - 1));
           atomicOr(g.status, DEV_BAD_SLOT);
           return past + 1;
@@ -534,28 +561,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         const Unit x = s_seg[seg_i];
         done_seg();
         for (int u = x.u0; u < x.u1; ++u) {
-          const int j0 = x.block(u) * kBlk;
+          const int i0 = u * kBlk;
           wait(kv_full + 8 * st, ph);
-          // rows [a, e) of the block's boxes that some row sees and some rows of
-          // which none does: past the last token, before the window
+          // positions [a, e) of the boxes that some row sees and some rows of which
+          // none does: past the last token, after the first tokens, before the window
           auto zero = [&](int a, int e) {
+            a = max(a - i0, 0);
+            e = min(e - i0, kBlk);
             for (int r = a + (lane >> 3); r < e; r += 4)  // eight lanes a row of 128 bytes
 #pragma unroll
               for (int h = 0; h < NH; ++h) st_s128(ring + st * kTileB + h * kHalf + r * 128 + (lane & 7) * 16, 0u, 0u, 0u, 0u);
+            return a < e;
           };
-          auto box_end = [&](int r) { return (r + P - 1) & ~(P - 1); };
-          const bool tail = j0 + kBlk - 1 > x.pl, head = j0 < x.from && j0 + kBlk > x.first;
-          if (tail) zero(x.pl + 1 - j0, box_end(x.pl + 1 - j0));
-          if (head) {
-            const int a = max(0, x.first - j0), e = min(kBlk, x.from - j0);  // unseen rows
-            if (box_end(a) >= e) {
-              zero(a, e);
-            } else {
-              zero(a, box_end(a));
-              zero(e & ~(P - 1), e);
-            }
-          }
-          if (tail || head) fence_proxy_async_shared();
+          const int end = (x.pl < x.ns ? x.pl : x.pl - x.gap) + 1;
+          bool any = zero(end, (end + P - 1) & -P);
+          any |= zero(x.first, min(x.ns, x.from));
+          any |= zero(x.ns, x.from - x.gap);
+          if (any) fence_proxy_async_shared();
           __syncwarp();
           if (lane == 0) mbar_arrive(v_ready + 8 * st);
           st += 2;
@@ -579,9 +601,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         const Unit x = s_seg[seg_i];
         done_seg();
         if (x.u0 == x.u1) continue;
-        int tf[2], tl[2];
-        x.tile(0, tq, tf[0], tl[0]);
-        x.tile(1, tq, tf[1], tl[1]);
         wait(q_full, nq & 1);
         ++nq;
         tc_fence_after();
@@ -614,8 +633,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           started[t] = true;
           tc_commit_el(pv_done + 8 * t, lead);
         };
-        int j0 = x.block(x.u0) * kBlk;
-        bool t0 = takes(j0, tf[0], tl[0]), t1 = takes(j0, tf[1], tl[1]);
+        const Taken k0 = taken(x, 0), k1 = taken(x, 1);
+        bool t0 = k0(x.u0), t1 = k1(x.u0);
         wait(kv_full + 8 * kst, kph);
         tc_fence_after();
         if (t0) score(0, kst);
@@ -630,8 +649,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             kph ^= 1;
           }
           const bool nx = u + 1 < x.u1;
-          const int jn = nx ? x.block(u + 1) * kBlk : 0;
-          const bool n0 = nx && takes(jn, tf[0], tl[0]), n1 = nx && takes(jn, tf[1], tl[1]);
+          const bool n0 = nx && k0(u + 1), n1 = nx && k1(u + 1);
           if (nx) wait2(v_ready + 8 * vst, vph, kv_full + 8 * kst, kph);
           else wait(v_ready + 8 * vst, vph);
           tc_fence_after();
@@ -674,13 +692,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       const int pos = tok < tq && tf + tok <= tl && x.slot >= 0 ? tf + tok : -1;
       float m = -INFINITY, l = 0.f;
       bool any = false;     // the accumulator holds a product of this segment
-      const int ns = x.ns, wt = x.wt, u1 = x.u1;
+      const int ns = x.ns, gap = x.gap, u1 = x.u1;
+      const Taken mine = taken(x, t);
       for (int u = x.u0; u < u1; ++u) {
-        const int j0 = (u < ns ? u : u - ns + wt) * kBlk;
-        if (!takes(j0, tf, tl)) {
+        if (!mine(u)) {
           bad_at = (bad_at + 1) % kBadRing;
           continue;
         }
+        // keys below `cut_k` are the tokens from u * kBlk on, the others those from jw on
+        const int cut_k = ns - u * kBlk, jw = u * kBlk + (cut_k < kBlk ? gap : 0);
+        const bool all = (cut_k <= 0 || cut_k >= kBlk) && jw + kBlk - 1 <= tf && (W == 0 || jw > tl - W || jw + kBlk <= S);
         wait(s_full + 8 * t, nsc & 1);
         tc_fence_after();
         const uint32_t bad = *(volatile uint32_t*)&s_bad[bad_at];
@@ -692,13 +713,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         tc_ld_wait();
         tc_ld32(ts + 64, s + 64);
         tc_ld32(ts + 96, s + 96);
-        const bool edge = bad || tf < 0 || j0 + kBlk - 1 > tf || !(W == 0 || j0 > tl - W || j0 + kBlk <= S);
+        const bool edge = bad || !all;
         uint32_t vis[4];
         if (edge) {  // bit i: the row sees key i of the block
-          const int last = pos - j0, low = W > 0 ? pos - W - j0 : -1, keep = W > 0 ? S - j0 : 0;
+          auto seen = [&](int j0, int w) {
+            const int last = pos - j0, low = W > 0 ? pos - W - j0 : -1, keep = W > 0 ? S - j0 : 0;
+            return below(last + 1 - 32 * w) & (~below(low + 1 - 32 * w) | below(keep - 32 * w));
+          };
 #pragma unroll
-          for (int w = 0; w < 4; ++w)
-            vis[w] = below(last + 1 - 32 * w) & (~below(low + 1 - 32 * w) | below(keep - 32 * w));
+          for (int w = 0; w < 4; ++w) vis[w] = seen(jw, w);
+          if (cut_k > 0 && cut_k < kBlk)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t early = below(cut_k - 32 * w);
+              vis[w] = (vis[w] & ~early) | (seen(u * kBlk, w) & early);
+            }
           if (bad)
 #pragma unroll
             for (int w = 0; w < 4; ++w)
