@@ -34,9 +34,9 @@
 // sum is kept in fp32 before that rounding.
 //
 // Measured (head size 128, bf16, append included; of 1,917 TFLOP/s): 2,048 tokens
-// after 30,693, 32 / 8 heads, 675 us, 1,575 TFLOP/s (0.82); a 2,048-token prompt,
+// after 30,693, 32 / 8 heads, 667 us, 1,595 TFLOP/s (0.83); a 2,048-token prompt,
 // 16 / 4 heads, 33 us; five chunks of up to 901 tokens with a window of 512 and 4
-// first tokens, 28 / 4 heads, 48 us. A pair of tiles takes about 3,000 cycles per
+// first tokens, 28 / 4 heads, 47 us. A pair of tiles takes about 3,000 cycles per
 // block, 2,048 of them products; a tile's chain is its softmax (1,700), its two
 // products (1,024) and the barriers between. Steps of 64 keys with two buffers of
 // scores break that chain, but a product of 64 keys takes 51 cycles instead of

@@ -37,10 +37,10 @@
 // in a masked place reaches a result, NaN and infinities included.
 //
 // Measured (head size 128, bf16, append included; of 6.78 TB/s copied): 64
-// conversations of up to 8,191 tokens, 32 / 8 heads: 202 us, 6.1 TB/s (0.90);
-// one of 131,057 tokens: 91 us, 5.9 TB/s (0.87). Short calls are a chain of
+// conversations of up to 8,191 tokens, 32 / 8 heads: 199 us, 6.2 TB/s (0.92);
+// one of 131,057 tokens: 90 us, 5.9 TB/s (0.87). Short calls are a chain of
 // latencies (division of the list, page table, first tile, the joins): 517
-// tokens 12.6 us, 8 sequences of up to 4,093 tokens 19 us.
+// tokens 9.7 us, 8 sequences of up to 4,093 tokens 17 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

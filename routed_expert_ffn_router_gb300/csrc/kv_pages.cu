@@ -10,10 +10,10 @@
 // HBM, the small calls by the launches; the second launch of a pair is scheduled
 // while the first runs.
 //
-// Measured: freeing and forking 4 slots over 48 layers (a page of 16 tokens
-// each) 11.4 us; 64 forks (82 MB of pages of 32 tokens) 30 us, 5.5 TB/s read and
-// written (0.80 of a measured copy); compacting 2.6 GB of moves 414 us, 6.3 TB/s
-// (0.93).
+// Measured: forking 4 slots over 48 layers (a page of 16 tokens each) and freeing
+// them 10.4 us; 64 forks (82 MB of pages of 32 tokens) and their freeing 28 us,
+// 5.8 TB/s read and written (0.86 of a measured copy); compacting 2.6 GB of moves
+// 408 us, 6.4 TB/s (0.94).
 #include "kv_internal.h"
 
 namespace moe {
