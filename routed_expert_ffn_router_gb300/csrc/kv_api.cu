@@ -111,7 +111,7 @@ moe_status attention(const moe_kv_desc* d, int32_t layer, const moe_kv_rows* r, 
   if (!decode && chunk_supported(d->D, d->page_size, d->Hkv, at.G, rw.B, rw.n_rows, d->max_pages, at.scale))
     return cuda_status(launch_attn_chunk(c, rw, at, f16, status_of(ws), sync_of(ws), region_of(ws),
                                          static_cast<cudaStream_t>(stream)));
-  return cuda_status(launch_attn_rows(c, rw, at, f16, status_of(ws), static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_attn_rows(c, rw, at, f16, decode, status_of(ws), static_cast<cudaStream_t>(stream)));
 }
 
 // Checks shared by the page operations over n slots.

@@ -96,7 +96,7 @@ cudaError_t launch_pdl(int kind, void (*kernel)(P...), dim3 grid, int threads, s
 
 cudaError_t launch_append(const Cache& c, const Rows& r, const uint16_t* k, const uint16_t* v, long long stride,
                           int32_t* status, cudaStream_t st);
-cudaError_t launch_attn_rows(const Cache& c, const Rows& r, const Attn& a, bool f16, int32_t* status,
+cudaError_t launch_attn_rows(const Cache& c, const Rows& r, const Attn& a, bool f16, bool decode, int32_t* status,
                              cudaStream_t st);
 // The one-launch decode kernel (kv_decode.cu): D 64 or 128, pages of a power of
 // two of at least 8 tokens.
