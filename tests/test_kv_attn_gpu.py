@@ -260,3 +260,38 @@ def test_pools_beyond_2_to_the_32_elements():
     check(c2, run(c2, "chunk", kv), c2.reference(), "chunk")
     del k, v
     torch.cuda.empty_cache()
+
+
+# lens, rows, page, window, sinks: boxes of first tokens and of the window packed into one block
+PACKED = {
+    "page_8": ([700, 333], [150, 40], 8, 130, 5),
+    "page_64": ([900, 400], [200, 90], 64, 200, 70),
+    "page_128": ([900, 257], [130, 257], 128, 100, 3),
+    "page_256": ([1200, 513], [300, 100], 256, 260, 300),
+    "first_tokens_end_a_box": ([640, 640], [70, 1], 32, 96, 64),
+    "first_tokens_meet_window": ([300, 300], [64, 33], 16, 200, 90),
+    "one_key_windows": ([500], [129], 16, 1, 129),
+    "window_longer_than_the_sequence": ([200, 90], [200, 17], 32, 512, 4),
+}
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("name", list(PACKED))
+def test_chunk_blocks_of_first_tokens_and_window(name, D):
+    lens, news, page, window, sinks = PACKED[name]
+    c = Case(lens, news, 14, 2, D, page, BF, window, sinks, seed=31)
+    check(c, run(c, "chunk"), c.reference(), name)
+
+
+@pytest.mark.parametrize("op,lens,news,Hq,Hkv,D,page,window,sinks", [
+    ("decode", [2100, 1, 0, 65], [3, 3, 3, 3], 6, 2, 80, 16, 0, 0),
+    ("decode", [1500, 70], [1, 1], 4, 4, 72, 24, 700, 11),
+    ("decode", [900, 4097], [2, 2], 8, 2, 128, 20, 0, 0),
+    ("decode", [333], [16], 4, 1, 256, 7, 50, 60),
+    ("chunk", [1000, 3], [40, 3], 6, 2, 80, 16, 300, 4),
+    ("chunk", [700], [700], 12, 3, 40, 12, 0, 0),
+])
+def test_any_head_and_page_size(op, lens, news, Hq, Hkv, D, page, window, sinks):
+    """Shapes of the kernel whose warps share a row, and of a warp with a row to itself."""
+    c = Case(lens, news, Hq, Hkv, D, page, FP if D == 80 else BF, window, sinks, seed=32)
+    check(c, run(c, op), c.reference(), op)
