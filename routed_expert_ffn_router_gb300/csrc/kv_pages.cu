@@ -11,7 +11,7 @@
 // while the first runs.
 //
 // Measured: forking 4 slots over 48 layers (a page of 16 tokens each) and freeing
-// them 10.4 us; 64 forks (82 MB of pages of 32 tokens) and their freeing 28 us,
+// them 8.6 us; 64 forks (82 MB of pages of 32 tokens) and their freeing 28 us,
 // 5.8 TB/s read and written (0.86 of a measured copy); compacting 2.6 GB of moves
 // 408 us, 6.4 TB/s (0.94).
 #include "kv_internal.h"
@@ -313,24 +313,16 @@ __global__ void __launch_bounds__(kMoveThreads) fork_apply_kernel(Cache c, const
 }
 
 // ------------------------------------------------------------------ free
-// refs - 1 for every page held; a page that reaches 0 is marked -1, which the
-// second kernel pushes (in page order, so the stack does not depend on timing).
-__global__ void __launch_bounds__(kMoveThreads) free_refs_kernel(Cache c, const int32_t* slots, int n, int32_t* status) {
-  const int i = blockIdx.x, q = blockIdx.y * kMoveThreads + threadIdx.x;
-  start();
-  const int slot = slots[i];
-  if (slot < 0 || slot >= c.n_slots) {
-    if (q == 0) atomicOr(status, DEV_BAD_SLOT);
-    return;
-  }
-  if (q >= c.max_pages) return;
+// refs - 1 for page q of slot slots[i]; a page that reaches 0 is marked -1, to
+// be pushed afterwards (in page order, so the stack does not depend on timing).
+__device__ __forceinline__ void release(const Cache& c, int slot, int q, int32_t* status) {
   int32_t* e = c.table + (long long)slot * c.max_pages + q;
   if (q < pages_of(max(0, c.lens[slot]), c.page)) {
     const int pg = *e;
     if (pg >= 0 && pg < c.n_pages) {
       const int old = atomicSub(c.refs + pg, 1);
       if (old == 1) {
-        c.refs[pg] = -1;
+        atomicExch(c.refs + pg, -1);
       } else if (old <= 0) {  // not a held page: the books were wrong
         atomicAdd(c.refs + pg, 1);
         atomicOr(status, DEV_BAD_SLOT);
@@ -342,10 +334,34 @@ __global__ void __launch_bounds__(kMoveThreads) free_refs_kernel(Cache c, const 
   *e = -1;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) free_push_kernel(Cache c, const int32_t* slots, int n, int32_t* status) {
+__global__ void __launch_bounds__(kMoveThreads) free_refs_kernel(Cache c, const int32_t* slots, int n, int32_t* status) {
+  const int i = blockIdx.x, q = blockIdx.y * kMoveThreads + threadIdx.x;
+  start();
+  const int slot = slots[i];
+  if (slot < 0 || slot >= c.n_slots) {
+    if (q == 0) atomicOr(status, DEV_BAD_SLOT);
+  } else if (q < c.max_pages) {
+    release(c, slot, q, status);
+  }
+}
+
+// Few table entries are released here too, by the one CTA that pushes: a launch
+// less (4 slots of 65 entries, with their forks, 8.6 us against 9.1 and 2 us less
+// for the host; 1,040 entries 12.2 against 11.4).
+constexpr int kFewEntries = 512;
+__global__ void __launch_bounds__(kPlanThreads) free_push_kernel(Cache c, const int32_t* slots, int n, int few,
+                                                                 int32_t* status) {
   __shared__ int sh[32];
   const int tid = threadIdx.x;
   start();
+  if (few) {
+    for (int k = tid; k < n * c.max_pages; k += kPlanThreads) {
+      const int i = k / c.max_pages, slot = slots[i], q = k - i * c.max_pages;
+      if (slot >= 0 && slot < c.n_slots) release(c, slot, q, status);
+      else if (q == 0) atomicOr(status, DEV_BAD_SLOT);
+    }
+    __syncthreads();
+  }
   const int nf = *c.n_free;
   int at = nf;
   constexpr int kPer = 8;
@@ -355,7 +371,7 @@ __global__ void __launch_bounds__(kPlanThreads) free_push_kernel(Cache c, const 
     unsigned gone = 0;
 #pragma unroll
     for (int u = 0; u < kPer; ++u)
-      if (top - u >= 0 && c.refs[top - u] == -1) gone |= 1u << u;
+      if (top - u >= 0 && __ldcg(c.refs + top - u) == -1) gone |= 1u << u;
     int sum;
     int x = block_scan(__popc(gone), &sum, sh) + at;
 #pragma unroll
@@ -484,9 +500,13 @@ cudaError_t launch_fork(const Cache& c, const int32_t* src, const int32_t* dst, 
 }
 
 cudaError_t launch_free(const Cache& c, const int32_t* slots, int n, int32_t* status, cudaStream_t st) {
-  const cudaError_t e = launch_pdl(K_KV_PAGES, free_refs_kernel, dim3(n, (c.max_pages + kMoveThreads - 1) / kMoveThreads),
-                                   kMoveThreads, 0, st, c, slots, n, status);
-  return e != cudaSuccess ? e : launch_pdl(K_KV_PAGES, free_push_kernel, dim3(1), kPlanThreads, 0, st, c, slots, n, status);
+  const int few = (long long)n * c.max_pages <= kFewEntries;
+  if (!few) {
+    const cudaError_t e = launch_pdl(K_KV_PAGES, free_refs_kernel, dim3(n, (c.max_pages + kMoveThreads - 1) / kMoveThreads),
+                                     kMoveThreads, 0, st, c, slots, n, status);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(K_KV_PAGES, free_push_kernel, dim3(1), kPlanThreads, 0, st, c, slots, n, few, status);
 }
 
 cudaError_t launch_compact(const Cache& c, int32_t* n_moved, int32_t* status, void* scratch, cudaStream_t st) {
