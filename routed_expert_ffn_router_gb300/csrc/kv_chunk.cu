@@ -884,8 +884,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
               uint32_t o[32];
               tc_ld32(to + i, o);
               tc_ld_wait();
+              if (f_me != 0.f) {
 #pragma unroll
-              for (int k = 0; k < 32; ++k) y[k] = fmaf(__uint_as_float(o[k]), f_me, y[k]);
+                for (int k = 0; k < 32; ++k) y[k] = fmaf(__uint_as_float(o[k]), f_me, y[k]);
+              }
             } else {
               float f = f_cf;
               float4 v[8];
