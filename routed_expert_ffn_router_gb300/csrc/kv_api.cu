@@ -99,7 +99,12 @@ moe_status attention(const moe_kv_desc* d, int32_t layer, const moe_kv_rows* r, 
   const Cache c = cache_of(d, layer);
   const Rows rw = rows_of(r);
   Attn at;
-  at.Hq = a->Hq; at.G = a->Hq / d->Hkv; at.window = a->window; at.n_sink = a->n_sink; at.scale = a->scale;
+  // Neither a window nor first tokens beyond what a table holds mean more than all
+  // of it: bounded so, their sums with tokens' positions stay in int32.
+  const int32_t most = d->max_pages * d->page_size;
+  at.window = a->window < most ? a->window : most;
+  at.n_sink = a->n_sink < most ? a->n_sink : most;
+  at.Hq = a->Hq; at.G = a->Hq / d->Hkv; at.scale = a->scale;
   at.q = static_cast<const uint16_t*>(a->q);
   at.q_stride = a->q_stride;
   at.o = static_cast<uint16_t*>(a->o);

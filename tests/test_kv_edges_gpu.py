@@ -1,0 +1,40 @@
+"""Attention over the paged cache at the edges of its arguments, against the
+64-bit definition: very large windows and first-token counts."""
+import pytest
+import torch
+
+from routed_expert_ffn_router_gb300 import _lib
+from routed_expert_ffn_router_gb300 import build as libbuild
+from tests._kv_ref import Case, check
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+MOST = 2 ** 31 - 1
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    libbuild.build()
+    _lib.load()
+
+
+def run(c, op, kv=None, **kw):
+    kv = c.cache() if kv is None else kv
+    ms = dict(window=c.window, sinks=c.sinks, want_lse=True)
+    if op == "decode":
+        out = kv.decode(0, c.q, slots=c.slots, **ms, **kw)
+    else:
+        out = kv.chunk(0, c.q, slots=c.slots, row_start=c.row_start, **ms, **kw)
+    torch.cuda.synchronize()
+    assert kv.status() == (_lib.MOE_OK, 0)
+    return out
+
+
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 64), (80, 24)])
+@pytest.mark.parametrize("op", ["decode", "chunk"])
+@pytest.mark.parametrize("window,sinks", [(200, MOST), (200, MOST - 127), (1, MOST), (MOST, 0), (MOST, MOST), (MOST, 5)])
+def test_windows_and_first_tokens_without_bound(op, D, page, window, sinks):
+    n = (2, 2) if op == "decode" else (300, 17)
+    c = Case([1500, 40], n, 8, 2, D, page, BF, window, sinks, seed=41)
+    check(c, run(c, op), c.reference(), op)
+
