@@ -595,7 +595,8 @@ __global__ void __launch_bounds__(dec_threads<RG>(), dec_ctas<RG>()) decode_kern
         const int pf = max(0, it.pf), kl = lane & (16 * KB - 1), j = j0 + kl;
         const bool good = !(bad >> ((wg * 16 * KB + kl) >> g.logP) & 1);
         const bool any = good && j <= it.pl && (W == 0 || j > pf - W || j < S);
-        const bool all = good && j <= pf && (W == 0 || j > it.pl - W || j < S);
+        // (a first row before token 0 sees nothing: then no key is seen by all)
+        const bool all = good && j <= it.pf && (W == 0 || j > it.pl - W || j < S);
         constexpr unsigned kKeys = KB == 2 ? 0xffffffffu : 0xffffu;
         const unsigned cut = __ballot_sync(0xffffffffu, !all) & kKeys, some = __ballot_sync(0xffffffffu, any && !all) & kKeys;
         auto vptr = [&](int k, int c) {  // address of 16 bytes: columns 8 c .. of V of the warp's key k

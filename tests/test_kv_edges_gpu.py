@@ -1,5 +1,8 @@
 """Attention over the paged cache at the edges of its arguments, against the
-64-bit definition: very large windows and first-token counts."""
+64-bit definition: very large windows and first-token counts, rows before the
+first token next to values that are not finite."""
+import math
+
 import pytest
 import torch
 
@@ -38,3 +41,14 @@ def test_windows_and_first_tokens_without_bound(op, D, page, window, sinks):
     c = Case([1500, 40], n, 8, 2, D, page, BF, window, sinks, seed=41)
     check(c, run(c, op), c.reference(), op)
 
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("lens,n,Hq,Hkv,D", [([1, 2, 0], 3, 4, 2, 128), ([1, 2, 3, 20], 3, 8, 2, 64),
+                                             ([5, 15, 16], 16, 4, 2, 128), ([1], 2, 4, 2, 80)])
+def test_rows_before_the_first_token_next_to_values_that_are_not_finite(bad, lens, n, Hq, Hkv, D):
+    # the rows of a window that are no tokens see nothing, whatever the first token holds
+    c = Case(lens, [n] * len(lens), Hq, Hkv, D, 16, BF, 0, 0, seed=42)
+    for b, s in enumerate(c.slots.tolist()):
+        if lens[b]:
+            c.v[0, int(c.table[s, 0]), :, 0] = bad
+    check(c, run(c, "decode"), c.reference(), "not finite")
