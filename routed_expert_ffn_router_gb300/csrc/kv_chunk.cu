@@ -27,11 +27,13 @@
 //   S0 S1 | PV0 S0' | PV1 S1' | PV0' ...
 //
 // The running maximum is only raised when a row's scores pass it by more than
-// 2^8 (probabilities up to 256 lose nothing in bf16 or fp16, whose relative
-// rounding is the same there), so the accumulators in tensor memory are seldom
-// rescaled. Probabilities are rounded to the cache's type for the product
-// (half a step, 2^-8 for bf16 and 2^-11 for fp16, independent per key); their
-// sum is kept in fp32 before that rounding.
+// 2^8 (probabilities up to 256 are rounded no worse than those up to 1), so the
+// accumulators in tensor memory are seldom rescaled. Probabilities are rounded to
+// the cache's type for the product (half a step, 2^-8 for bf16 and 2^-11 for fp16,
+// independent per key); their sum is kept in fp32 before that rounding. fp16 has a
+// fixed step below 2^-14: its probabilities are lifted by 2^7 (to 2^15 at most), so
+// that half of that step is 2^-32 of the largest one. Without the lift, keys 2^-25
+// below it vanished from the product and stayed in the sum.
 //
 // Measured (head size 128, bf16, append included; of 1,917 TFLOP/s): 2,048 tokens
 // after 30,693, 32 / 8 heads, 667 us, 1,595 TFLOP/s (0.83); a 2,048-token prompt,
@@ -348,6 +350,10 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
+
+// log2 of the factor that a probability, and so l and o, carry.
+template <bool F16>
+__host__ __device__ constexpr float lift() { return F16 ? 7.f : 0.f; }
 
 // The n lowest bits (none below 0, all from 32 on).
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
@@ -764,7 +770,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             }
           }
         }
-        const float z = m == -INFINITY ? 0.f : m;
+        const float z = m == -INFINITY ? 0.f : m - lift<F16>();
         const float2 sc2 = make_float2(sc, sc), z2 = make_float2(-z, -z);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -933,7 +939,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         }
         if (g.a.lse && tok < nt)
           g.a.lse[((long long)x.row0 + t * tq + tok) * g.a.Hq + x.hk * G + r - tok * G] =
-              lt == 0.f ? -INFINITY : (mt + log2f(lt)) * 0.6931471805599453f;
+              lt == 0.f ? -INFINITY : (mt + (log2f(lt) - lift<F16>())) * 0.6931471805599453f;
         if (!whole && lane == 0) *cnt = 0;  // ready for the next call
       }
       if (any) {  // the accumulator may be written again
@@ -1013,7 +1019,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Ch
     *reinterpret_cast<uint4*>(g.a.o + at_row * D + q * 8) =
         make_uint4(pack2<F16>(o[0] * inv, o[1] * inv), pack2<F16>(o[2] * inv, o[3] * inv),
                    pack2<F16>(o[4] * inv, o[5] * inv), pack2<F16>(o[6] * inv, o[7] * inv));
-    if (q == 0 && g.a.lse) g.a.lse[at_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    if (q == 0 && g.a.lse) g.a.lse[at_row] = l == 0.f ? -INFINITY : (m + (log2f(l) - lift<F16>())) * 0.6931471805599453f;
   }
 }
 

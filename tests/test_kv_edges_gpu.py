@@ -1,6 +1,7 @@
 """Attention over the paged cache at the edges of its arguments, against the
 64-bit definition: very large windows and first-token counts, rows before the
-first token next to values that are not finite."""
+first token next to values that are not finite, probabilities far below the
+largest."""
 import math
 
 import pytest
@@ -11,7 +12,7 @@ from routed_expert_ffn_router_gb300 import build as libbuild
 from tests._kv_ref import Case, check
 
 pytestmark = pytest.mark.gpu
-BF = torch.bfloat16
+BF, FP = torch.bfloat16, torch.float16
 MOST = 2 ** 31 - 1
 
 
@@ -52,3 +53,25 @@ def test_rows_before_the_first_token_next_to_values_that_are_not_finite(bad, len
         if lens[b]:
             c.v[0, int(c.table[s, 0]), :, 0] = bad
     check(c, run(c, "decode"), c.reference(), "not finite")
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("op,n,D", [("chunk", 1, 64), ("chunk", 700, 128), ("chunk", 700, 64)])
+def test_probabilities_far_below_the_largest(dtype, op, n, D):
+    """Every sixteenth key has score 0 and the value 0, the others a score of about
+    -25.5 ln 2 and a large value: only the small probabilities reach the result. A
+    probability in fp16 has a fixed step below the normal range: with the largest lifted
+    to 2^7, half of it is 2^-32 of the largest probability, for each key."""
+    c = Case([1800], [n], 8, 2, D, 16, dtype, 0, 0, seed=43, poison=False)
+    c.q.zero_()
+    c.q[..., 0] = 4.0
+    c.k.zero_()
+    c.k[..., 0] = -17.675 / 4
+    c.k[..., 0::16, :] = 0.0
+    c.v[:] = 1000.0 + 10 * torch.randn(c.v.shape, device="cuda").to(dtype)
+    c.v[..., 0::16, :] = 0.0
+    ro, rl, to, tl = c.reference(scale=1.0)
+    if dtype == FP:
+        to = to + 1.05 * 16 * 2.0 ** -32 * float(c.v.max())   # at most 16 keys for each of the largest ones
+    assert float(ro.min()) > 20 * float(to.max())
+    check(c, run(c, op, scale=1.0), (ro, rl, to, tl), op)
