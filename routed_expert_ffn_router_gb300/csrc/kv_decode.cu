@@ -31,7 +31,9 @@
 // probabilities per tile: 64 conversations 224 us instead of 208.) A probability
 // enters the product with V as a sum of two values of the cache's type (rounding
 // 2^-17 for bf16 instead of 2^-8; the second product costs nothing next to the
-// HBM read). The running maximum is raised only by more than 2^8 (sums are in
+// HBM read). fp16 has a fixed step below 2^-14, where the second value is lost too:
+// its probabilities are lifted by 2^7 (to 2^15 at most), so that half of that step
+// is 2^-32 of the largest one. The running maximum is raised only by more than 2^8 (sums are in
 // fp32), so O is seldom rescaled. Keys that only some rows see are added with
 // scalar products, keys that no row sees get a zero value row: nothing that lies
 // in a masked place reaches a result, NaN and infinities included.
@@ -169,8 +171,13 @@ __device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
                : "memory");
 }
 
+// log2 of the factor that a probability, and so l and o, carry.
+template <bool F16>
+__host__ __device__ constexpr float lift() { return F16 ? 7.f : 0.f; }
+
+template <bool F16>
 __device__ __forceinline__ float lse_of(float m, float l) {
-  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  return l == 0.f ? -INFINITY : (m + (log2f(l) - lift<F16>())) * 0.6931471805599453f;
 }
 
 // A row's result: columns 64 h .. + 3 of o.
@@ -181,7 +188,7 @@ __device__ __forceinline__ void put_row(float m, float l, const float4 (&O)[D / 
   for (int h = 0; h < D / 64; ++h)
     *reinterpret_cast<uint2*>(o + 64 * h) =
         make_uint2(pack2<F16>(O[h].x * inv, O[h].y * inv), pack2<F16>(O[h].z * inv, O[h].w * inv));
-  if (lse) *lse = lse_of(m, l);
+  if (lse) *lse = lse_of<F16>(m, l);
 }
 
 // A split item whose spans are all there.
@@ -583,7 +590,7 @@ __global__ void __launch_bounds__(dec_threads<RG>(), dec_ctas<RG>()) decode_kern
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float z = m[e & 1] == -INFINITY ? 0.f : m[e & 1];
+        const float z = m[e & 1] == -INFINITY ? 0.f : m[e & 1] - lift<F16>();
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
           s[kb][e] = ex2(s[kb][e] - z);

@@ -56,7 +56,8 @@ def test_rows_before_the_first_token_next_to_values_that_are_not_finite(bad, len
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
-@pytest.mark.parametrize("op,n,D", [("chunk", 1, 64), ("chunk", 700, 128), ("chunk", 700, 64)])
+@pytest.mark.parametrize("op,n,D", [("decode", 1, 128), ("decode", 4, 64), ("chunk", 1, 64), ("chunk", 700, 128),
+                                    ("chunk", 700, 64)])
 def test_probabilities_far_below_the_largest(dtype, op, n, D):
     """Every sixteenth key has score 0 and the value 0, the others a score of about
     -25.5 ln 2 and a large value: only the small probabilities reach the result. A
