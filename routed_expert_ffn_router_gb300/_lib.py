@@ -7,6 +7,7 @@ a call fails, an exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -205,6 +206,18 @@ def _stream(stream):
         import torch
         return torch.cuda.current_stream().cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def on_stream(stream):
+    """Makes `stream` (a torch stream or a handle) torch's current one, so that a
+    tensor allocated there is its own: a block of another stream may still be in
+    use there, and is handed out again as soon as it is dropped. None: no change."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 # --------------------------------------------------------------------------- calls

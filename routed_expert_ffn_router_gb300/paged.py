@@ -42,7 +42,10 @@ class PagedKV:
     [n_slots][max_pages], lens int32 [n_slots], refs int32 [n_pages], free int32
     [n_pages] with n_free int32 [1]. Hq: query heads; max_rows: rows of the
     largest attention call (sizes the workspace). One thread at a time: the
-    calls share the argument structs and the workspace."""
+    calls share the argument structs and the workspace. A call works on the
+    current stream, or on `stream` (a torch stream or a handle), whose the results
+    are then; ordering it with other streams, and keeping the arguments alive until
+    it has run, is the caller's."""
 
     def __init__(self, n_layers, n_pages, page_size, Hkv, D, n_slots, max_pages, Hq=None, max_rows=2048,
                  dtype=torch.bfloat16, device="cuda"):
@@ -97,6 +100,12 @@ class PagedKV:
             return _current_stream(self._index)
         return stream if isinstance(stream, int) else stream.cuda_stream
 
+    def _new(self, shape, dtype, stream):
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with _lib.on_stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
     def _heads(self, t, heads, what):
         """-> row stride of [rows][heads][D] with contiguous heads."""
         shape, D = t.shape, self.D
@@ -143,12 +152,12 @@ class PagedKV:
         n = q.shape[0]
         self._set_rows(n, slots, row_start)
         if out is None:
-            out = torch.empty((n, Hq, self.D), dtype=self.dtype, device=self.device)
+            out = self._new((n, Hq, self.D), self.dtype, stream)
         elif out.shape != q.shape or out.dtype != self.dtype or not out.is_contiguous() or out.device != self.device:
             raise ValueError("out must be a contiguous tensor like q")
         if lse is None:
             if want_lse:
-                lse = torch.empty((n, Hq), dtype=_F32, device=self.device)
+                lse = self._new((n, Hq), _F32, stream)
         elif lse.shape != (n, Hq) or lse.dtype != _F32 or not lse.is_contiguous() or lse.device != self.device:
             raise ValueError("lse must be a contiguous fp32 [rows][Hq]")
         a = self._args
