@@ -29,6 +29,7 @@ _I32, _F32 = torch.int32, torch.float32
 # The current stream's handle without the Stream object around it: a decode step
 # makes two calls per layer, and the object costs as much as a launch.
 _current_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _i32(t, what, device):
@@ -86,16 +87,21 @@ class PagedKV:
         self.ws_bytes = _lib.moe_kv_workspace_bytes(d, Hq, max_rows)
         if self.ws_bytes == 0:
             raise ValueError("unsupported cache: see moe_kv_desc for the limits")
+        self._index = dev.index or 0
+        if dev.type == "cuda":
+            self._stream(None)
         self.ws = torch.empty(self.ws_bytes + 256, dtype=torch.uint8, device=dev)
         self.ws_ptr = self.ws.data_ptr() + (-self.ws.data_ptr()) % 256
         _lib.moe_workspace_init(self.ws_ptr, self.ws_bytes)
         self._desc_ref = ctypes.byref(d)
         self._rows, self._args = moe_kv_rows(), moe_attn_args()
         self._rows_ref, self._args_ref = ctypes.byref(self._rows), ctypes.byref(self._args)
-        self._args.Hq, self._scale, self._index = Hq, 1.0 / math.sqrt(D), dev.index or 0
+        self._args.Hq, self._scale = Hq, 1.0 / math.sqrt(D)
 
     # ---- marshalling
     def _stream(self, stream):
+        if _current_device() != self._index:  # the library launches on the current device
+            raise ValueError(f"the cache is on {self.device}, the current device is cuda:{_current_device()}")
         if stream is None:
             return _current_stream(self._index)
         return stream if isinstance(stream, int) else stream.cuda_stream
