@@ -64,7 +64,9 @@ class MoeLayer:
         """route + expert FFN; returns the output dict (y, ids, w, miss_ids, n_miss)."""
         T = x.shape[0]
         assert T <= self.T_max
-        out = self.alloc_outputs(T) if out is None else out
+        if out is None:
+            with _lib.on_stream(stream):  # whose calls write them
+                out = self.alloc_outputs(T)
         sm = self.inp.slot_map if isinstance(slot_map, str) else slot_map
         _lib.moe_layer_forward(self.desc, logits, x, self.x_dtype, T, sm, out["y"], out["ids"],
                                out["w"], out["miss_ids"], out["n_miss"], self.ws_ptr,
@@ -74,7 +76,9 @@ class MoeLayer:
     def expert_ffn(self, x, ids, w, slot_map="default", out=None, stream=None):
         T = x.shape[0]
         assert T <= self.T_max
-        out = self.alloc_outputs(T) if out is None else out
+        if out is None:
+            with _lib.on_stream(stream):  # whose calls write them
+                out = self.alloc_outputs(T)
         sm = self.inp.slot_map if isinstance(slot_map, str) else slot_map
         _lib.moe_expert_ffn(self.desc, x, self.x_dtype, T, ids, w, sm, out["y"], out["miss_ids"],
                             out["n_miss"], self.ws_ptr, self.ws_bytes, stream)

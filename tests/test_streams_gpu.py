@@ -4,8 +4,9 @@ current stream still has queued for the memory it would hand out."""
 import pytest
 import torch
 
-from routed_expert_ffn_router_gb300 import _lib
+from routed_expert_ffn_router_gb300 import _lib, synth
 from routed_expert_ffn_router_gb300 import build as libbuild
+from routed_expert_ffn_router_gb300.layer import MoeLayer
 from tests._kv_ref import Case
 
 pytestmark = pytest.mark.gpu
@@ -45,3 +46,25 @@ def test_attention_results_on_another_stream(op, raw):
     torch.cuda.synchronize()
     assert kv.status() == (_lib.MOE_OK, 0)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_layer_results_on_another_stream(raw):
+    cfg = synth.MoeConfig("streams", H=512, I=256, E=32, k=4, T=16, zipf_s=1.0, resident_frac=0.5)
+    inp = synth.make_layer(cfg, 5, device="cuda")
+    lay = MoeLayer(inp, T_max=cfg.T)
+    logits, xs = synth.draw_windows(inp, 1, seed=9)
+    want = lay.forward(logits[0], xs[0])
+    assert int(want["n_miss"]) > 0
+    s = torch.cuda.Stream()
+    left_behind(*[(t.shape, t.dtype) for t in want.values()])
+    got = lay.forward(logits[0], xs[0], stream=s.cuda_stream if raw else s)
+    again = lay.expert_ffn(xs[0], want["ids"], want["w"], stream=s.cuda_stream if raw else s)
+    s.synchronize()
+    torch.cuda.synchronize()
+    assert lay.status()[0] == _lib.MOE_OK
+    n = int(want["n_miss"])
+    for k in ("y", "ids", "w", "n_miss"):
+        assert torch.equal(got[k], want[k]), k
+    assert torch.equal(got["miss_ids"][:n], want["miss_ids"][:n])
+    assert torch.equal(again["y"], want["y"]) and torch.equal(again["n_miss"], want["n_miss"])
