@@ -84,16 +84,16 @@ class Mailbox:
     def forward(self, lay, logits, x, slot_map, stream=None):
         """One window: the GPU layer call over the held experts, the missed
         experts on the host threads, their partials added on the GPU."""
-        out = lay.forward(logits, x, slot_map=slot_map, stream=stream)
-        st = torch.cuda.current_stream() if stream is None else stream
-        st.synchronize()
-        ids = out["ids"].cpu().numpy()
-        pairs = self.pairs(ids, slot_map.cpu().numpy())
-        if len(pairs):
-            part = self.compute(x.cpu(), ids, out["w"].cpu().numpy(), pairs)
-            dev = out["y"].device
-            pd = torch.from_numpy(part).to(dev)
-            qd = torch.from_numpy(pairs).to(dev)
-            self.add(pd, qd, x.shape[0], self.cfg.k, out["y"], stream=stream)
+        with _lib.on_stream(stream):  # the copies and the sum go where the layer call does
+            out = lay.forward(logits, x, slot_map=slot_map)
+            torch.cuda.current_stream().synchronize()
+            ids = out["ids"].cpu().numpy()
+            pairs = self.pairs(ids, slot_map.cpu().numpy())
+            if len(pairs):
+                part = self.compute(x.cpu(), ids, out["w"].cpu().numpy(), pairs)
+                dev = out["y"].device
+                pd = torch.from_numpy(part).to(dev)
+                qd = torch.from_numpy(pairs).to(dev)
+                self.add(pd, qd, x.shape[0], self.cfg.k, out["y"])
         out["mailbox_pairs"] = pairs
         return out

@@ -7,6 +7,7 @@ import torch
 from routed_expert_ffn_router_gb300 import _lib, synth
 from routed_expert_ffn_router_gb300 import build as libbuild
 from routed_expert_ffn_router_gb300.layer import MoeLayer
+from routed_expert_ffn_router_gb300.mailbox import Mailbox
 from tests._kv_ref import Case
 
 pytestmark = pytest.mark.gpu
@@ -68,3 +69,28 @@ def test_layer_results_on_another_stream(raw):
         assert torch.equal(got[k], want[k]), k
     assert torch.equal(got["miss_ids"][:n], want["miss_ids"][:n])
     assert torch.equal(again["y"], want["y"]) and torch.equal(again["n_miss"], want["n_miss"])
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_mailbox_window_on_another_stream(raw):
+    cfg = synth.MoeConfig("mbstreams", H=1024, I=512, E=64, k=8, T=16, zipf_s=1.2)
+    store = synth.make_layer(cfg, 5)
+    smt, S = synth.random_slot_map(cfg.E, 0.6, seed=2)
+    pool = synth.make_layer(cfg, 5)
+    keep = (smt >= 0).nonzero().flatten()
+    for name in ("gate_q", "gate_s", "up_q", "up_s", "down_q", "down_s"):
+        setattr(pool, name, getattr(pool, name)[keep].contiguous())
+    pool.S, pool.slot_map = S, smt
+    pool = pool.to(torch.device("cuda", 0))
+    lay = MoeLayer(pool, T_max=cfg.T)
+    mb = Mailbox(store, n_threads=4)
+    want = mb.forward(lay, pool.logits, pool.x, pool.slot_map)
+    n = len(want["mailbox_pairs"])
+    assert n > 0
+    s = torch.cuda.Stream()
+    left_behind(((n, cfg.H), torch.float32), ((n,), torch.int32), (want["y"].shape, torch.float32))
+    got = mb.forward(lay, pool.logits, pool.x, pool.slot_map, stream=s.cuda_stream if raw else s)
+    s.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(got["y"], want["y"])
+    mb.close()
