@@ -220,6 +220,14 @@ def on_stream(stream):
     return torch.cuda.stream(stream)
 
 
+def check_device(device):
+    """The library launches on the current device: refuses another one's buffers."""
+    import torch
+    now = torch._C._cuda_getDevice()
+    if now != device.index:
+        raise ValueError(f"the layer is on {device}, the current device is cuda:{now}")
+
+
 # --------------------------------------------------------------------------- calls
 def moe_router_logits(x, x_dtype, wg, T, H, E, logits, stream=None):
     _check("moe_router_logits", load().moe_router_logits(_ptr(x), x_dtype, _ptr(wg), T, H, E,

@@ -48,6 +48,7 @@ class MoeLayer:
         self.ws = torch.empty(self.ws_bytes + 256, dtype=torch.uint8, device=self.device)
         off = (-self.ws.data_ptr()) % 256
         self.ws_ptr = self.ws.data_ptr() + off
+        _lib.check_device(self.ws.device)
         _lib.moe_workspace_init(self.ws_ptr, self.ws_bytes)
         self.x_dtype = MOE_BF16 if inp.x_is_bf16 else MOE_F32
 
@@ -64,6 +65,7 @@ class MoeLayer:
         """route + expert FFN; returns the output dict (y, ids, w, miss_ids, n_miss)."""
         T = x.shape[0]
         assert T <= self.T_max
+        _lib.check_device(self.ws.device)
         if out is None:
             with _lib.on_stream(stream):  # whose calls write them
                 out = self.alloc_outputs(T)
@@ -76,6 +78,7 @@ class MoeLayer:
     def expert_ffn(self, x, ids, w, slot_map="default", out=None, stream=None):
         T = x.shape[0]
         assert T <= self.T_max
+        _lib.check_device(self.ws.device)
         if out is None:
             with _lib.on_stream(stream):  # whose calls write them
                 out = self.alloc_outputs(T)
@@ -85,9 +88,11 @@ class MoeLayer:
         return out
 
     def status(self, stream=None):
+        _lib.check_device(self.ws.device)
         return _lib.moe_read_status(self.ws_ptr, stream)
 
     def clear_status(self, stream=None):
+        _lib.check_device(self.ws.device)
         _lib.moe_workspace_init(self.ws_ptr, self.ws_bytes, stream)
 
 
@@ -126,6 +131,7 @@ class DecodeStack:
             raise ValueError("invalid layer description")
         self.ws = torch.empty(self.ws_bytes + 256, dtype=torch.uint8, device=self.device)
         self.ws_ptr = self.ws.data_ptr() + (-self.ws.data_ptr()) % 256
+        _lib.check_device(self.ws.device)
         _lib.moe_workspace_init(self.ws_ptr, self.ws_bytes)
         self.outs = []
         for inp in layers:
@@ -157,8 +163,10 @@ class DecodeStack:
                                                  self.plan_bytes, self.ws_ptr, self.ws_bytes)
 
     def forward(self, stream=None):
+        _lib.check_device(self.ws.device)
         _lib.moe_decode_stack(self.plan_ptr, self.L, self.T, self.ws_ptr, self.ws_bytes, stream)
         return self.outs
 
     def status(self, stream=None):
+        _lib.check_device(self.ws.device)
         return _lib.moe_read_status(self.ws_ptr, stream)

@@ -6,6 +6,7 @@ import torch
 
 from routed_expert_ffn_router_gb300 import _lib, paged
 from routed_expert_ffn_router_gb300 import build as libbuild
+from routed_expert_ffn_router_gb300.layer import DecodeStack, MoeLayer
 from routed_expert_ffn_router_gb300.paged import PagedKV
 from tests._kv_ref import Case
 
@@ -45,4 +46,39 @@ def test_cache_calls(name, monkeypatch):
     assert calls == []
     monkeypatch.setattr(paged, "_current_device", lambda: 0)
     CACHE_CALLS[name](kv, c)
+    assert calls == [name]
+
+
+LAYER_CALLS = {
+    "moe_layer_forward": lambda o, x: MoeLayer.forward(o, x, x, out=o.out),
+    "moe_expert_ffn": lambda o, x: MoeLayer.expert_ffn(o, x, x, x, out=o.out),
+    "moe_read_status": lambda o, x: MoeLayer.status(o),
+    "moe_workspace_init": lambda o, x: MoeLayer.clear_status(o),
+    "moe_decode_stack": lambda o, x: DecodeStack.forward(o),
+}
+
+
+class _Buffers:
+    """What the calls above read of a layer or a stack."""
+    desc = x_dtype = ws_ptr = ws_bytes = plan_ptr = L = T = outs = None
+    T_max = 4
+    out = dict.fromkeys(("y", "ids", "w", "miss_ids", "n_miss"))
+
+    class ws:
+        device = torch.device("cuda", 0)
+
+    class inp:
+        slot_map = None
+
+
+@pytest.mark.parametrize("name", list(LAYER_CALLS))
+def test_layer_calls(name, monkeypatch):
+    calls, x = [], torch.zeros(2, 8)
+    monkeypatch.setattr(_lib, name, lambda *a: calls.append(name))
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    with pytest.raises(ValueError, match="cuda:1"):
+        LAYER_CALLS[name](_Buffers(), x)
+    assert calls == []
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    LAYER_CALLS[name](_Buffers(), x)
     assert calls == [name]
