@@ -94,7 +94,9 @@ typedef struct {
 
 /* Workspace bytes of every call on this cache with up to max_rows rows (and
  * sequences) and Hq query heads (256-byte aligned base, moe_workspace_init
- * once). L: HOST. 0 for an invalid description. */
+ * once). Only moe_attn_decode's part grows with max_rows: the bytes for 0 rows
+ * serve chunks and page operations of any size. kv: HOST. 0 for an invalid
+ * description. */
 size_t moe_kv_workspace_bytes(const moe_kv_desc *kv, int32_t Hq, int32_t max_rows);
 
 /* Write the rows' keys and values of one layer into their pages. k, v

@@ -1,5 +1,6 @@
 // C ABI of the paged key-value cache and its attention (include/moe_kv.h):
 // argument validation, workspace layout, choice of kernel.
+#include <algorithm>
 #include <climits>
 
 #include "kv_internal.h"
@@ -59,16 +60,14 @@ Rows rows_of(const moe_kv_rows* r) {
 }
 
 // The workspace: the head that moe_workspace_init zeroes, then one region that
-// every call lays out for itself.
-size_t region_bytes(const moe_kv_desc* d, int32_t Hq, int32_t max_rows) {
-  size_t n = pages_ws_bytes(d->n_pages, d->n_slots);
-  if (d->D == 64 || d->D == 128) {
-    const size_t m = decode_ws_bytes(d->page_size, d->max_pages, d->Hkv, Hq / d->Hkv, d->D, max_rows);
-    n = m > n ? m : n;
-    n = chunk_ws_bytes(d->D) > n ? chunk_ws_bytes(d->D) : n;
-  }
-  return n;
+// every call lays out for itself. The kernel for any head and page size has none.
+bool tiled(const moe_kv_desc* d) {
+  return (d->D == 64 || d->D == 128) && d->page_size >= 8 && !(d->page_size & (d->page_size - 1));
 }
+size_t decode_region(const moe_kv_desc* d, int32_t Hq, int32_t max_rows) {
+  return tiled(d) ? decode_ws_bytes(d->page_size, d->max_pages, d->Hkv, Hq / d->Hkv, d->D, max_rows) : 0;
+}
+size_t chunk_region(const moe_kv_desc* d) { return tiled(d) ? chunk_ws_bytes(d->D) : 0; }
 
 moe_status check_ws(const void* ws, size_t ws_bytes, size_t region) {
   if (!ws || !aligned(ws, 256) || ws_bytes < kWsHeadBytes + region) return MOE_ERR_WORKSPACE;
@@ -95,7 +94,7 @@ moe_status attention(const moe_kv_desc* d, int32_t layer, const moe_kv_rows* r, 
   if (r->n_rows == 0) return MOE_OK;
   if (!a->q || !a->o || !aligned(a->q, 16) || !aligned(a->o, 16) || !aligned(a->lse, 4)) return MOE_ERR_INVALID;
   if (a->q_stride % 8 || a->q_stride < (int64_t)a->Hq * d->D) return MOE_ERR_INVALID;
-  if ((s = check_ws(ws, ws_bytes, region_bytes(d, a->Hq, r->n_rows))) != MOE_OK) return s;
+  if ((s = check_ws(ws, ws_bytes, decode ? decode_region(d, a->Hq, r->n_rows) : chunk_region(d))) != MOE_OK) return s;
   const Cache c = cache_of(d, layer);
   const Rows rw = rows_of(r);
   Attn at;
@@ -134,7 +133,7 @@ extern "C" {
 
 size_t moe_kv_workspace_bytes(const moe_kv_desc* d, int32_t Hq, int32_t max_rows) {
   if (check_kv(d) != MOE_OK || Hq < 1 || Hq % d->Hkv || max_rows < 0) return 0;
-  return kWsHeadBytes + region_bytes(d, Hq, max_rows);
+  return kWsHeadBytes + std::max({pages_ws_bytes(d->n_pages, d->n_slots), decode_region(d, Hq, max_rows), chunk_region(d)});
 }
 
 moe_status moe_kv_append(const moe_kv_desc* d, int32_t layer, const moe_kv_rows* r, const void* k, const void* v,

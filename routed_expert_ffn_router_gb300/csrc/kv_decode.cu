@@ -858,7 +858,8 @@ size_t decode_ws_bytes(int page, int max_pages, int Hkv, int G, int D, int max_r
   size_t most = 0;
   for (int n_q = 1; n_q <= rows; ++n_q) {
     const int RT = (n_q * G + 15) / 16;
-    const long long items = (max_rows / n_q) * (long long)RT * Hkv, keys = items < kMaxCtas ? items : kMaxCtas;
+    const int seqs = max_rows / n_q < kSeqCap ? max_rows / n_q : kSeqCap;  // of one launch; the next one starts over
+    const long long items = seqs * (long long)RT * Hkv, keys = items < kMaxCtas ? items : kMaxCtas;
     const int RG = n_q * G > 8 ? 2 : 1;
     const size_t n = (size_t)keys * RG *
                      max_span_of(page, max_pages, tile_of(D, RG), span_c_of(Hkv, RT), most_spans_of(Hkv, RT));
