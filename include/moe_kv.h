@@ -74,14 +74,15 @@ typedef struct {
  * tokens with the first n_sink tokens always visible.
  *   lse[t][h] = ln sum_j exp(scale q_t,h . k_j)   over the visible tokens j
  *   o[t][h]   = sum_j exp(scale q_t,h . k_j - lse[t][h]) v_j
- * A row that sees nothing gets o = 0 and lse = -inf. q [n_rows][Hq][D] with
- * q_stride elements from row to row (heads contiguous, so q may be a part of a
- * larger projection); o [n_rows][Hq][D] contiguous; both in the cache's type
- * and 16-byte aligned, q_stride a multiple of 8. lse [n_rows][Hq] fp32 or
- * NULL. Products are of the cache's type, sums and softmax in fp32. A token
- * that no row of the call sees (past the length, outside every row's window)
- * is not used and may hold anything, NaN included; pages wholly of such tokens
- * are not read and their table entries may be anything. */
+ * Hq is a multiple of Hkv up to 65,535. A row that sees nothing gets o = 0 and
+ * lse = -inf. q [n_rows][Hq][D] with q_stride elements from row to row (heads
+ * contiguous, so q may be a part of a larger projection); o [n_rows][Hq][D]
+ * contiguous; both in the cache's type and 16-byte aligned, q_stride a multiple
+ * of 8. lse [n_rows][Hq] fp32 or NULL. Products are of the cache's type, sums and
+ * softmax in fp32. A token that no row of the call sees (past the length, outside
+ * every row's window) is not used and may hold anything, NaN included; pages
+ * wholly of such tokens are not read and their table entries may be anything (in
+ * these calls: the page operations below go by every entry of a slot's length). */
 typedef struct {
   int32_t Hq;
   float scale;

@@ -10,6 +10,8 @@ using namespace moe::kv;
 
 namespace {
 
+constexpr int kMostHeads = 65535;
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 moe_status check_kv(const moe_kv_desc* d) {
@@ -90,7 +92,7 @@ moe_status attention(const moe_kv_desc* d, int32_t layer, const moe_kv_rows* r, 
   if (!(a->scale > -3.0e38f && a->scale < 3.0e38f)) return MOE_ERR_INVALID;
   if (decode && r->row_start) return MOE_ERR_INVALID;
   if (decode && r->B > 0 && r->n_rows / r->B > 16) return MOE_ERR_UNSUPPORTED;
-  if ((int64_t)a->Hq * r->n_rows > INT32_MAX || a->Hq > 65535) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)a->Hq * r->n_rows > INT32_MAX || a->Hq > kMostHeads) return MOE_ERR_UNSUPPORTED;
   if (r->n_rows == 0) return MOE_OK;
   if (!a->q || !a->o || !aligned(a->q, 16) || !aligned(a->o, 16) || !aligned(a->lse, 4)) return MOE_ERR_INVALID;
   if (a->q_stride % 8 || a->q_stride < (int64_t)a->Hq * d->D) return MOE_ERR_INVALID;
@@ -132,7 +134,7 @@ moe_status check_pages(const moe_kv_desc* d, int32_t n, void* ws, size_t ws_byte
 extern "C" {
 
 size_t moe_kv_workspace_bytes(const moe_kv_desc* d, int32_t Hq, int32_t max_rows) {
-  if (check_kv(d) != MOE_OK || Hq < 1 || Hq % d->Hkv || max_rows < 0) return 0;
+  if (check_kv(d) != MOE_OK || Hq < 1 || Hq > kMostHeads || Hq % d->Hkv || max_rows < 0) return 0;
   return kWsHeadBytes + std::max({pages_ws_bytes(d->n_pages, d->n_slots), decode_region(d, Hq, max_rows), chunk_region(d)});
 }
 

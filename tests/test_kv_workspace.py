@@ -59,6 +59,17 @@ def test_bytes_grow_with_rows_and_heads(lib):
             assert sizes == sorted(sizes) and sizes[0] > 0
 
 
+def test_no_bytes_for_heads_that_no_call_takes(lib):
+    a = _lib.moe_attn_args(scale=0.1, q=A, q_stride=1 << 40, o=A)
+    for Hkv, Hq in ((1, 65536), (1, 1 << 28), (1, 2 ** 31 - 1), (3, 3 << 29)):
+        d, r = desc(Hkv=Hkv), _lib.moe_kv_rows(B=1, n_rows=1, slots=A)
+        a.Hq = Hq
+        for fn in (lib.moe_attn_decode, lib.moe_attn_chunk):
+            assert fn(ctypes.byref(d), 0, ctypes.byref(r), ctypes.byref(a), A, 1 << 60, None) == _lib.MOE_ERR_UNSUPPORTED
+        assert need(lib, d, Hq, 16) == 0
+    assert need(lib, desc(), 65535, 16) > 0
+
+
 def test_a_call_with_less_is_refused(lib):
     d = desc(Hkv=2, n_slots=256)
     r = _lib.moe_kv_rows(B=128, n_rows=2048, slots=A)
