@@ -67,8 +67,7 @@ template <int RG>
 __host__ __device__ constexpr int dec_ring() { return RG * 96 * 1024; }
 template <int RG>
 __host__ __device__ constexpr int dec_ctas() { return 3 - RG; }  // per SM
-constexpr int kAllBar = 3;              // named barrier of all consumer warps
-constexpr int kPairBar = 4;             // named barriers 4 .. 7: the warps of two groups with the same keys (1, 2: a group's)
+constexpr int kAllBar = 3;              // named barrier of all consumer warps (1, 2: a group's)
 constexpr int kOPitch = 64 + 4;         // floats per row of the buffer in which the warps' O meet
 constexpr uint32_t kTries = 1u << 24;   // of a wait, up to 128 ns long each
 constexpr int kSeqCap = 128;            // sequences per launch
@@ -268,7 +267,7 @@ __global__ void __launch_bounds__(dec_threads<RG>(), dec_ctas<RG>()) decode_kern
   constexpr int kStages = dec_ring<RG>() / kStage;
   constexpr int KK = D / 16, NH = D / 64;
   extern __shared__ __align__(1024) uint8_t smem_dec[];
-  __shared__ __align__(8) uint64_t s_bar[2 * kStages];
+  __shared__ __align__(8) uint64_t s_bar[2 * kStages + 4];
   __shared__ uint32_t s_badbox[kStages];
   __shared__ int s_off[kSeqCap + 1], s_len[kSeqCap], s_slot[kSeqCap];
   __shared__ __align__(16) float s_o[RG][4][8][kOPitch];  // the warps' O: 8 rows, 64 columns at a time
@@ -281,11 +280,13 @@ __global__ void __launch_bounds__(dec_threads<RG>(), dec_ctas<RG>()) decode_kern
   const int B = g.r.B, G = g.a.G, n_q = g.r.n_q, W = g.a.window, S = g.a.n_sink, Hkv = g.c.Hkv;
   const uint32_t ring = smem_u32(smem_dec);  // aligned as declared: a swizzled box starts on 1 KB
   const uint32_t full = smem_u32(s_bar), empty = full + 8 * kStages;
+  const uint32_t pair = empty + 8 * kStages;  // [4]: the warps of two groups with the same keys
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(full + 8 * i, 1);
       mbar_init(empty + 8 * i, 4 * RG);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(pair + 8 * i, 2);
     fence_barrier_init();
     for (int i = 0; i < RG; ++i) s_njoin[i] = 0;
   }
@@ -472,7 +473,7 @@ __global__ void __launch_bounds__(dec_threads<RG>(), dec_ctas<RG>()) decode_kern
   const int ra = 2 * (lane & 3);
   const int mrow = lane >> 2, mcol = wg * 16 + 4 * (lane & 3);  // merged: row mrow, columns 64 h + mcol .. + 3
   const float sc = g.a.scale * 1.4426950408889634f;
-  int st = 0, ph = 0;
+  int st = 0, ph = 0, pph = 0;
 
   uint32_t q[KK][2];
   int pos[2];                    // tokens of this lane's score rows ra, ra + 1 (-1: no row, or before the first token)
@@ -636,9 +637,15 @@ __global__ void __launch_bounds__(dec_threads<RG>(), dec_ctas<RG>()) decode_kern
               if (vb) o[d][2 * e + 1] = fmaf(pb, vv, o[d][2 * e + 1]);
             }
         }
-        // the other group's warp of these keys has added them too (it comes here for the same tiles)
-        if constexpr (RG > 1) named_bar_sync(kPairBar + wg, 64);
-        else __syncwarp();
+        // The other group's warp of these keys has added them too. It comes here for the
+        // same tiles, but after an expired wait the two may read different `bad`: so a
+        // bounded wait, where a named barrier could wait for ever.
+        __syncwarp();
+        if constexpr (RG > 1) {
+          if (lane == 0) mbar_arrive(pair + 8 * wg);
+          wait(pair + 8 * wg, pph);
+          pph ^= 1;
+        }
         for (int i = lane; i < 16 * KB * (D / 8); i += 32) {
           const int k = i / (D / 8);
           if (cut >> k & 1)
