@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         };
         auto queries = [&] {
           wait(q_empty, qph);
-          qph ^= 1;
+          if (!dead) qph ^= 1;
           if (lane == 0 && !dead) {
             mbar_expect_tx(q_full, (uint32_t)(nt * NH * tq * G * 128));
             for (int t = 0; t < nt; ++t)
@@ -559,6 +559,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         }
         opening = false;
       }
+      // No copy is under way when the CTA ends, also where a warp went on without
+      // waiting: a wait, with a limit of its own, for every slot's last fill (a slot
+      // never filled is in the phase before its first).
+      const bool gave_up = dead;
+      dead = false;
+#pragma unroll 1
+      for (int i = 0; i < NST; ++i) wait(kv_full + 8 * i, i < st ? ph ^ 1 : ph);
+      wait(q_full, qph);
+      dead |= gave_up;
     } else if (warp == 10) {
       // ================= values that no row sees become zeros =================
       const int P = 1 << g.logP;

@@ -762,7 +762,14 @@ __global__ void __launch_bounds__(dec_threads<RG>(), dec_ctas<RG>()) decode_kern
       ++span;
     }
   }
-  if (dead) atomicOr(g.status, DEV_TIMEOUT);
+  if (__any_sync(0xffffffffu, dead)) {
+    // No copy is under way when the CTA ends: what this warp did not wait for, with a
+    // limit of its own, is every slot's last fill.
+    atomicOr(g.status, DEV_TIMEOUT);
+    dead = false;
+#pragma unroll 1
+    for (int i = 0; i < kStages; ++i) wait(full + 8 * i, i < st ? ph : ph ^ 1);
+  }
   // ---- joins, after the loop over tiles: they would take registers from it,
   // and the ring is free once every group is here
   named_bar_sync(kAllBar, 128 * RG);
