@@ -42,7 +42,7 @@ class PagedKV:
     """k, v [n_layers][n_pages][Hkv][page_size][D] (bf16 or fp16), table int32
     [n_slots][max_pages], lens int32 [n_slots], refs int32 [n_pages], free int32
     [n_pages] with n_free int32 [1]. Hq: query heads; max_rows: rows of the
-    largest attention call (sizes the workspace). One thread at a time: the
+    largest decode call (sizes the workspace; chunks may have more). One thread at a time: the
     calls share the argument structs and the workspace. A call works on the
     current stream, or on `stream` (a torch stream or a handle), whose the results
     are then; ordering it with other streams, and keeping the arguments alive until
@@ -137,8 +137,6 @@ class PagedKV:
             B, r.row_start = n, row_start.data_ptr()
         if (n_rows > 0 and B < 1) or (slots is None and B > self.n_slots):
             raise ValueError("more sequences than slots, or none")
-        if n_rows > self.max_rows:
-            raise ValueError(f"{n_rows} rows: the workspace is sized for {self.max_rows}")
         r.B, r.n_rows = B, n_rows
 
     # ---- new tokens and attention
@@ -176,7 +174,10 @@ class PagedKV:
     def decode(self, layer, q, slots=None, scale=None, window=0, sinks=0, want_lse=False, out=None, lse=None,
                stream=None):
         """Attention of a decode window: q [rows][Hq][D], the same number of rows
-        (up to 16) for each slot. -> o, or (o, lse) with want_lse."""
+        (up to 16) for each slot (slots None: a row for each of the first slots).
+        -> o, or (o, lse) with want_lse."""
+        if q.dim() == 3 and q.shape[0] > self.max_rows:
+            raise ValueError(f"{q.shape[0]} rows: the workspace is sized for {self.max_rows}")
         return self._attend(_lib.moe_attn_decode, layer, q, slots, None, scale, window, sinks, want_lse, out, lse, stream)
 
     def chunk(self, layer, q, slots=None, row_start=None, scale=None, window=0, sinks=0, want_lse=False, out=None,

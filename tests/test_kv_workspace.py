@@ -5,7 +5,7 @@ import ctypes
 import pytest
 import torch
 
-from routed_expert_ffn_router_gb300 import _lib
+from routed_expert_ffn_router_gb300 import _lib, paged
 from routed_expert_ffn_router_gb300 import build as libbuild
 from tests._kv_ref import Case, check
 
@@ -80,6 +80,23 @@ def test_a_call_with_less_is_refused(lib):
     assert lib.moe_attn_chunk(*ref, need(lib, d, 16, 0) - 256, None) == _lib.MOE_ERR_WORKSPACE
 
 
+def test_max_rows_limits_decode_only(lib, monkeypatch):
+    c = Case([9, 9], [6, 6], 4, 2, 64, 16, dev="cpu")
+    calls = []
+    for name in ("moe_workspace_init", "moe_kv_append", "moe_attn_chunk", "moe_attn_decode"):
+        monkeypatch.setattr(_lib, name, lambda *a, name=name: calls.append(name))
+    monkeypatch.setattr(paged, "_current_stream", lambda i: 0)
+    monkeypatch.setattr(paged, "_current_device", lambda: 0)
+    kv = c.cache(max_rows=4)
+    calls.clear()
+    kv.append(0, c.q[:, :2], c.q[:, :2], slots=c.slots, row_start=c.row_start)
+    assert kv.chunk(0, c.q, slots=c.slots, row_start=c.row_start).shape == c.q.shape
+    with pytest.raises(ValueError):
+        kv.decode(0, c.q, slots=c.slots)
+    kv.decode(0, c.q[:4], slots=c.slots)
+    assert calls == ["moe_kv_append", "moe_attn_chunk", "moe_attn_decode"]
+
+
 @pytest.mark.gpu
 def test_a_chunk_needs_no_rows_of_decode():
     libbuild.build()
@@ -89,7 +106,6 @@ def test_a_chunk_needs_no_rows_of_decode():
     kv = c.cache(max_rows=0)
     bytes0 = need(_lib.load(), kv.desc, 8, 0)
     assert kv.ws_bytes == bytes0 < need(_lib.load(), kv.desc, 8, c.T)
-    kv.max_rows = c.T  # rows of the wrapper's own limit; the workspace stays
     o, lse = kv.chunk(0, c.q, slots=c.slots, row_start=c.row_start, want_lse=True)
     torch.cuda.synchronize()
     assert kv.status() == (_lib.MOE_OK, 0)
