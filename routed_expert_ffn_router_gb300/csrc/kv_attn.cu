@@ -12,7 +12,7 @@
 // up to 4,093 tokens, 16 / 2 heads of 80, 93 us (one warp per row and one key at
 // a time: 1,580); 64 sequences, 32 / 8 heads, 790 us; a 512-token prompt, 16 / 4
 // heads, 294 us.
-#include "kv_internal.h"
+#include "kv_common.cuh"
 
 namespace moe {
 namespace kv {
@@ -24,25 +24,9 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if constexpr (F16) {
-      const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      f[2 * i] = p.x;
-      f[2 * i + 1] = p.y;
-    } else {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
-}
-
-template <bool F16>
-__device__ __forceinline__ uint32_t pack2(float x, float y) {
-  if constexpr (F16) {
-    const __half2 h = __floats2half2_rn(x, y);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-    return *reinterpret_cast<const uint32_t*>(&h);
+    const float2 p = unpack2<F16>(w[i]);
+    f[2 * i] = p.x;
+    f[2 * i + 1] = p.y;
   }
 }
 
@@ -62,19 +46,7 @@ __global__ void __launch_bounds__(SP == 1 ? 128 : 32 * SP) attn_rows_kernel(Cach
   const long long w = SP == 1 ? (long long)blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
   if (w >= (long long)r.n_rows * a.Hq) return;
   const int t = (int)(w / a.Hq), hq = (int)(w - (long long)t * a.Hq), hk = hq / a.G;
-  int b;
-  if (r.row_start) {
-    int lo = 0, hi = r.B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (r.row_start[mid] <= t) lo = mid;
-      else hi = mid - 1;
-    }
-    b = lo;
-  } else {
-    b = t / r.n_q;
-  }
-  const Seq s = load_seq(c, r, b, lane == 0 && part == 0 ? status : nullptr);
+  const Seq s = load_seq(c, r, seq_of_row(r, t), lane == 0 && part == 0 ? status : nullptr);
   const int tok = s.len - s.n + (t - s.row0);
   const bool act = gl * 8 < c.D;
   float q[8], o[8];

@@ -53,7 +53,7 @@
 
 #include <mutex>
 
-#include "kv_internal.h"
+#include "kv_common.cuh"
 #include "kv_tma.h"
 #include "moe_tc.cuh"
 
@@ -312,27 +312,6 @@ __device__ __forceinline__ void schedule(Plan& p, const ChunkArgs& g, Unit* ring
   if (lane == 0 && g.combine) g.split[blockIdx.x] = sp;
 }
 
-__device__ __forceinline__ int add_acq_rel_gpu(int* p, int v) {
-  int old;
-  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
-  return old;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-template <bool F16>
-__device__ __forceinline__ uint32_t pack2(float x, float y) {
-  if constexpr (F16) {
-    const __half2 h = __floats2half2_rn(x, y);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-}
-
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -350,10 +329,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
-
-// log2 of the factor that a probability, and so l and o, carry.
-template <bool F16>
-__host__ __device__ constexpr float lift() { return F16 ? 7.f : 0.f; }
 
 // The n lowest bits (none below 0, all from 32 on).
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }

@@ -48,7 +48,7 @@
 
 #include <mutex>
 
-#include "kv_internal.h"
+#include "kv_common.cuh"
 #include "kv_tma.h"
 
 namespace moe {
@@ -99,16 +99,6 @@ __host__ __device__ inline int span_log(int nvis, int c, int most_spans) {
 
 // (m, l, o) of a span folded into (M, L, O): written with explicit rounding so
 // that the fold in registers and the join give the same bits.
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ int add_acq_rel_gpu(int* p, int v) {
-  int old;
-  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
-  return old;
-}
 __device__ __forceinline__ void fold_ml(float& M, float& L, float m, float l, float& a, float& b) {
   const float n = fmaxf(M, m), z = n == -INFINITY ? 0.f : n;
   a = ex2(M - z);
@@ -132,21 +122,6 @@ struct Item {
 };
 
 template <bool F16>
-__device__ __forceinline__ uint32_t pack2(float x, float y) {
-  if constexpr (F16) {
-    const __half2 h = __floats2half2_rn(x, y);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-}
-template <bool F16>
-__device__ __forceinline__ float2 unpack2(uint32_t v) {
-  if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2*>(&v));
-  else return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
-}
-template <bool F16>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
   if constexpr (F16) mma_f16_16816(d, a0, a1, a2, a3, b0, b1);
@@ -169,10 +144,6 @@ __device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
                : "r"(a)
                : "memory");
 }
-
-// log2 of the factor that a probability, and so l and o, carry.
-template <bool F16>
-__host__ __device__ constexpr float lift() { return F16 ? 7.f : 0.f; }
 
 template <bool F16>
 __device__ __forceinline__ float lse_of(float m, float l) {

@@ -14,7 +14,7 @@
 // them 8.6 us; 64 forks (82 MB of pages of 32 tokens) and their freeing 28 us,
 // 5.8 TB/s read and written (0.86 of a measured copy); compacting 2.6 GB of moves
 // 408 us, 6.4 TB/s (0.94).
-#include "kv_internal.h"
+#include "kv_common.cuh"
 
 namespace moe {
 namespace kv {
@@ -90,19 +90,7 @@ __global__ void __launch_bounds__(128) append_kernel(Cache c, Rows r, const uint
   // the thread's first piece is on its way while the row's page is looked up
   uint4 x = make_uint4(0, 0, 0, 0);
   if (threadIdx.x < 2 * per) x = *src(threadIdx.x);
-  int b;
-  if (r.row_start) {  // the last sequence that starts at or before row t
-    int lo = 0, hi = r.B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (r.row_start[mid] <= t) lo = mid;
-      else hi = mid - 1;
-    }
-    b = lo;
-  } else {
-    b = t / r.n_q;
-  }
-  const Seq s = load_seq(c, r, b, threadIdx.x == 0 ? status : nullptr);
+  const Seq s = load_seq(c, r, seq_of_row(r, t), threadIdx.x == 0 ? status : nullptr);
   if (s.slot < 0 || t < s.row0 || t >= s.row0 + s.n) return;
   const int tok = s.len - s.n + (t - s.row0);
   if (tok < 0) return;
