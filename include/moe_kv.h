@@ -9,7 +9,10 @@
  * shared by all layers' page numbers: token j of slot s is row j % page_size
  * of page table[s][j / page_size] in every layer. lens[s] counts slot s's
  * tokens, those of the call included: moe_kv_grow first, then moe_kv_append
- * and the attention of every layer. refs[p] is the number of slots that hold
+ * and the attention of every layer. The page operations keep lens, table and
+ * refs together: a program that lowers a length itself (a refused proposal) must
+ * stay within the slot's last page, since no later call gives back a page that
+ * lies past the new length. refs[p] is the number of slots that hold
  * page p (0: free); free_pages[0 .. n_free) is a stack, popped from its end.
  * A program that starts empty sets table to -1, lens and refs to 0,
  * free_pages[i] = n_pages - 1 - i and n_free to n_pages.
@@ -26,7 +29,8 @@
  * [0, n_slots) (its rows are treated as a sequence of length 0), a page number
  * outside [0, n_pages) (its tokens are treated as not visible, or not
  * written), or a length beyond max_pages pages (taken as max_pages pages);
- * 4 a bounded wait expired (the call's results are incomplete); 32 not enough
+ * 4 a bounded wait expired (the call's results are incomplete, and the
+ * workspace has to be initialised before its next call); 32 not enough
  * free pages, 64 an argument that a page operation refuses (named at each):
  * after 32 or 64 the operation has changed nothing.
  */
@@ -108,19 +112,25 @@ moe_status moe_kv_append(const moe_kv_desc *kv, int32_t layer, const moe_kv_rows
                          size_t ws_bytes, void *stream);
 
 /* Attention of a decode window: the same number of rows (1 .. 16) for every
- * sequence, row_start NULL. The key-value pairs are read once per 16 query
- * rows of a KV head, the work split over the sequences' lengths and joined. A
- * row's result depends on its own sequence only, bit for bit: not on the other
- * sequences of the call, nor on where the pages lie. A NaN or an infinity in a
- * token reaches only the rows that see the token. */
+ * sequence, row_start NULL. With D 64 or 128 and pages of a power of two of at
+ * least 8 tokens the key-value pairs are read once per 16 query rows of a KV
+ * head, the work split over the sequences' lengths and joined; other shapes read
+ * them once per row and query head, one CTA each. A row's result depends on its
+ * own sequence only, bit for bit: not on the other sequences of the call, nor on
+ * where the pages lie. A NaN or an infinity in a token reaches only the rows that
+ * see the token (an infinite value as an infinity or as NaN). */
 moe_status moe_attn_decode(const moe_kv_desc *kv, int32_t layer, const moe_kv_rows *rows,
                            const moe_attn_args *a, void *ws, size_t ws_bytes, void *stream);
 
-/* Attention of prompt chunks: any number of rows per sequence. How a long
- * sequence is split depends on the call, so a row's last bits may differ in
- * another call. Values that some rows of a sequence see must be finite: as in
- * a plain product of probabilities and values, a NaN or an infinity may reach
- * rows that do not see it. */
+/* Attention of prompt chunks: any number of rows per sequence. On the tensor
+ * cores with the shapes named above, up to 128 query heads per KV head and a
+ * scale above zero; else the keys are read once per row and query head, by a CTA
+ * or a warp each. A probability is rounded to the cache's type for its product
+ * with a value (decode keeps twice as many bits). How a long sequence is split
+ * depends on the call, so a row's last bits may differ in another call. Values
+ * that some rows of a sequence see must be finite: as in a plain product of
+ * probabilities and values, a NaN or an infinity may reach rows that do not see
+ * it. */
 moe_status moe_attn_chunk(const moe_kv_desc *kv, int32_t layer, const moe_kv_rows *rows,
                           const moe_attn_args *a, void *ws, size_t ws_bytes, void *stream);
 
@@ -134,7 +144,9 @@ moe_status moe_kv_grow(const moe_kv_desc *kv, const int32_t *slots, const int32_
 /* Fork slot src[i] into the empty slot dst[i] (i < n; the dst distinct, a src
  * may repeat): the full pages are shared (refs + 1); the rows in use of a
  * partly filled last page are copied, in every layer, into a page popped in
- * order of i. Refused (64): a slot out of range, a dst of non-zero length. */
+ * order of i. Refused (64): a slot out of range, a dst of non-zero length, a
+ * source beyond max_pages pages, a page number out of range among the last pages
+ * or the free ones. */
 moe_status moe_kv_fork(const moe_kv_desc *kv, const int32_t *src, const int32_t *dst, int32_t n,
                        void *ws, size_t ws_bytes, void *stream);
 

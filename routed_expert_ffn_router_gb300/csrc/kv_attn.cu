@@ -9,9 +9,9 @@
 //
 // Every query head reads its keys by itself (from L2), and a key costs a chain of
 // page number, key and value: bound by those latencies. Measured: 8 sequences of
-// up to 4,093 tokens, 16 / 2 heads of 80, 93 us (one warp per row and one key at
+// up to 4,093 tokens, 16 / 2 heads of 80, 86 us (one warp per row and one key at
 // a time: 1,580); 64 sequences, 32 / 8 heads, 790 us; a 512-token prompt, 16 / 4
-// heads, 294 us.
+// heads of 80, 287 us.
 #include "kv_common.cuh"
 
 namespace moe {

@@ -36,7 +36,9 @@
 // below it vanished from the product and stayed in the sum.
 //
 // Measured (head size 128, bf16, append included; of 1,917 TFLOP/s): 2,048 tokens
-// after 30,693, 32 / 8 heads, 667 us, 1,595 TFLOP/s (0.83); a 2,048-token prompt,
+// after 30,693, 32 / 8 heads, 660 to 680 us, 1,590 TFLOP/s (0.83), and 740 to 760
+// called back to back for long, when the power limit lowers the clock (0.74; of the
+// 1,720 TFLOP/s that a long loop of products keeps up, 0.83); a 2,048-token prompt,
 // 16 / 4 heads, 33 us; five chunks of up to 901 tokens with a window of 512 and 4
 // first tokens, 28 / 4 heads, 47 us. A pair of tiles takes about 3,000 cycles per
 // block, 2,048 of them products; a tile's chain is its softmax (1,700), its two
@@ -1084,7 +1086,9 @@ cudaError_t launch_attn_chunk(const Cache& c, const Rows& r, const Attn& a, bool
     // the longest is at most about twice the mean. And not where the table or the
     // window leaves a unit few blocks: a launch less is 2 us of 15 for 40 rows.
     // Joined there, 38 parts of 40 rows over 30,000 tokens are 31 us; 8 parts of
-    // 4,000 tokens 23 us (35 by the last CTA), 256 rows over 16,000 69 (79).
+    // 4,000 tokens 23 us (35 by the last CTA), 256 rows over 16,000 69 (79). The host
+    // knows the table's width and not the lengths: 40 rows of a short sequence take
+    // 9.7 us with a table for 64 tokens and 11.8 with one for 32,768.
     const bool full_gpu = r.B == 1 && 3LL * ((r.n_rows + 2 * g.tq - 1) / (2 * g.tq)) * c.Hkv >= 2LL * grid;
     long long seen = (long long)c.max_pages * c.page;
     const long long win = (long long)a.window + 2 * g.tq - 1;

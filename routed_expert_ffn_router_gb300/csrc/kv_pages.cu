@@ -335,7 +335,8 @@ __global__ void __launch_bounds__(kMoveThreads) free_refs_kernel(Cache c, const 
 
 // Few table entries are released here too, by the one CTA that pushes: a launch
 // less (4 slots of 65 entries, with their forks, 8.6 us against 9.1 and 2 us less
-// for the host; 1,040 entries 12.2 against 11.4).
+// for the host; 1,040 entries 12.2 against 11.4). Counted are the entries of the
+// tables, whatever the slots hold: what n * max_pages is, the host knows.
 constexpr int kFewEntries = 512;
 __global__ void __launch_bounds__(kPlanThreads) free_push_kernel(Cache c, const int32_t* slots, int n, int few,
                                                                  int32_t* status) {
