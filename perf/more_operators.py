@@ -202,6 +202,11 @@ def prepare(case, seed):
         # most tokens of a text are among the likely ones
         pick = torch.where(torch.rand(T, generator=g, device=DEV) < 0.8, best[:, 0], torch.randint(0, V, (T,), generator=g, device=DEV))
         s["tokens"] = pick.to(torch.int32)
+        s["out"] = {n: torch.empty(T, dtype=dt, device=DEV) for n, dt in
+                    (("logprob", torch.float32), ("rank", torch.int32), ("entropy", torch.float32))}
+        if case["top"]:
+            s["out"]["top_ids"] = torch.empty(T, case["top"], dtype=torch.int32, device=DEV)
+            s["out"]["top_logprobs"] = torch.empty(T, case["top"], dtype=torch.float32, device=DEV)
         return s
     n_new = _news(case)
     T, B, D = sum(n_new), case["B"], case["D"]
@@ -400,7 +405,8 @@ def run(s):
         return {"q": q, "k": s["k"], "v": s["v"]}
     if case["op"] == "logprobs":
         from routed_expert_ffn_router_gb300.block import token_logprobs
-        return token_logprobs(s["logits"], s["tokens"], top=case["top"], temperature=case["temperature"])
+        return token_logprobs(s["logits"], s["tokens"], top=case["top"], temperature=case["temperature"],
+                              out=s["out"])
     layer = _states(s)
     if case["what"] == "step":
         layer.step(s["q"], s["k"], s["v"], s["g"], slots=s["slots"], scale=s["scale"], out=s["o"])
