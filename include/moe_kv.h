@@ -111,6 +111,37 @@ moe_status moe_kv_append(const moe_kv_desc *kv, int32_t layer, const moe_kv_rows
                          const void *k, const void *v, int64_t row_stride, void *ws,
                          size_t ws_bytes, void *stream);
 
+/* Rotary positions (a HOST struct). The first rot of a head's D values are
+ * turned in pairs, the rest is left: pair i is (i, i + rot / 2) in the HALF
+ * layout, (2 i, 2 i + 1) INTERLEAVED, and a token at position p turns it by
+ * the angle of p freq[i] turns / 2^64:
+ *   (x, y) -> gain (x cos - y sin, y cos + x sin)
+ * freq [rot / 2] holds turns per token as fractions of 2^64 (radians / 2 pi
+ * times 2^64, modulo 2^64), so that p freq[i] modulo 2^64 is the angle without
+ * an error that grows with p. Contexts are lengthened by other frequencies
+ * (and a gain). rot even, 2 .. D; freq 8-byte aligned. */
+typedef enum { MOE_ROPE_HALF = 0, MOE_ROPE_INTERLEAVED = 1 } moe_rope_layout;
+typedef struct {
+  int32_t rot;
+  moe_rope_layout layout;
+  float gain;
+  const uint64_t *freq;
+} moe_rope_desc;
+
+/* moe_kv_append with rotary positions: the rows' keys are turned on their way
+ * into the pages, their values written as they are, and their queries q
+ * [n_rows][Hq][D] turned into q_out [n_rows][Hq][D] (q_out_stride elements from
+ * row to row; q_out may be q with the same stride; both 16-byte aligned,
+ * strides a multiple of 8). positions [n_rows] int32 (4-byte aligned) or NULL:
+ * each row's token number in its sequence. Angles, products in fp32, one
+ * rounding. A row that is no token has its q copied; rows behind the last
+ * sequence are left as they were. Hq up to 65,535. */
+moe_status moe_kv_append_rope(const moe_kv_desc *kv, int32_t layer, const moe_kv_rows *rows,
+                              const moe_rope_desc *rope, const int32_t *positions, int32_t Hq,
+                              const void *q, int64_t q_stride, void *q_out, int64_t q_out_stride,
+                              const void *k, const void *v, int64_t row_stride, void *ws,
+                              size_t ws_bytes, void *stream);
+
 /* Attention of a decode window: the same number of rows (1 .. 16) for every
  * sequence, row_start NULL. With D 64 or 128 and pages of a power of two of at
  * least 8 tokens the key-value pairs are read once per 16 query rows of a KV

@@ -37,8 +37,13 @@ EXPORTS = ("moe_router_logits", "moe_route", "moe_permute", "moe_expert_ffn", "m
 
 # names of every entry point declared in include/moe_kv.h
 KV_EXPORTS = ("moe_kv_workspace_bytes", "moe_kv_append", "moe_attn_decode", "moe_attn_chunk", "moe_kv_grow",
-              "moe_kv_fork", "moe_kv_free", "moe_kv_compact", "moe_kv_copy_pages")
+              "moe_kv_fork", "moe_kv_free", "moe_kv_compact", "moe_kv_copy_pages", "moe_kv_append_rope")
 MOE_KV_BF16, MOE_KV_F16 = 1, 2
+MOE_ROPE_HALF, MOE_ROPE_INTERLEAVED = 0, 1
+
+# names of every entry point declared in include/moe_block.h
+BLOCK_EXPORTS = ("moe_rms_norm", "moe_token_logprobs", "moe_linear_step", "moe_linear_chunk")
+MOE_T_F32, MOE_T_BF16, MOE_T_F16, MOE_T_E4M3 = range(4)
 
 
 class MoeError(RuntimeError):
@@ -99,6 +104,39 @@ class moe_attn_args(ctypes.Structure):
                 ("o", ctypes.c_void_p), ("lse", ctypes.c_void_p)]
 
 
+class moe_rope_desc(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int32), ("layout", ctypes.c_int32), ("gain", ctypes.c_float),
+                ("freq", ctypes.c_void_p)]
+
+
+class moe_norm_args(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("x_type", ctypes.c_int32), ("res_type", ctypes.c_int32),
+                ("w_type", ctypes.c_int32), ("y_type", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("w_offset", ctypes.c_float), ("x", ctypes.c_void_p),
+                ("x_stride", ctypes.c_int64), ("res", ctypes.c_void_p), ("res_stride", ctypes.c_int64),
+                ("w", ctypes.c_void_p), ("y", ctypes.c_void_p), ("y_stride", ctypes.c_int64),
+                ("scales", ctypes.c_void_p)]
+
+
+class moe_logprobs_args(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("V", ctypes.c_int32), ("top", ctypes.c_int32), ("type", ctypes.c_int32),
+                ("temperature", ctypes.c_float), ("logits", ctypes.c_void_p), ("stride", ctypes.c_int64),
+                ("tokens", ctypes.c_void_p), ("logprob", ctypes.c_void_p), ("rank", ctypes.c_void_p),
+                ("entropy", ctypes.c_void_p), ("top_ids", ctypes.c_void_p), ("top_logprobs", ctypes.c_void_p)]
+
+
+class moe_linear_desc(ctypes.Structure):
+    _fields_ = [("n_slots", ctypes.c_int32), ("Hk", ctypes.c_int32), ("Hv", ctypes.c_int32), ("Dk", ctypes.c_int32),
+                ("Dv", ctypes.c_int32), ("dtype", ctypes.c_int32), ("state", ctypes.c_void_p)]
+
+
+class moe_linear_args(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("g", ctypes.c_void_p),
+                ("g_stride", ctypes.c_int64), ("scale", ctypes.c_float), ("o", ctypes.c_void_p),
+                ("status", ctypes.c_void_p)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -116,6 +154,8 @@ def load(path: str = LIB_PATH):
         P, i32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
         D = ctypes.POINTER(moe_layer_desc)
         KV, KR, KA = (ctypes.POINTER(s) for s in (moe_kv_desc, moe_kv_rows, moe_attn_args))
+        RO, NA, LA, LD, LL = (ctypes.POINTER(s) for s in (moe_rope_desc, moe_norm_args, moe_logprobs_args,
+                                                          moe_linear_desc, moe_linear_args))
         sig = {
             "moe_router_logits": ([P, i32, P, i32, i32, i32, P, P], i32),
             "moe_route": ([P, i32, i32, i32, P, P, P, P], i32),
@@ -168,6 +208,12 @@ def load(path: str = LIB_PATH):
                                 i32),
             "moe_kv_workspace_bytes": ([KV, ctypes.c_int32, ctypes.c_int32], sz),
             "moe_kv_append": ([KV, ctypes.c_int32, KR, P, P, ctypes.c_int64, P, sz, P], i32),
+            "moe_kv_append_rope": ([KV, ctypes.c_int32, KR, RO, P, ctypes.c_int32, P, ctypes.c_int64, P,
+                                    ctypes.c_int64, P, P, ctypes.c_int64, P, sz, P], i32),
+            "moe_rms_norm": ([NA, P], i32),
+            "moe_token_logprobs": ([LA, P], i32),
+            "moe_linear_step": ([LD, KR, LL, P], i32),
+            "moe_linear_chunk": ([LD, KR, LL, P], i32),
             "moe_attn_decode": ([KV, ctypes.c_int32, KR, KA, P, sz, P], i32),
             "moe_attn_chunk": ([KV, ctypes.c_int32, KR, KA, P, sz, P], i32),
             "moe_kv_grow": ([KV, P, P, ctypes.c_int32, P, sz, P], i32),
@@ -334,6 +380,29 @@ def moe_kv_workspace_bytes(desc, Hq, max_rows) -> int:
 # pointers: a decode step makes two of them per layer, so they stay thin.
 def moe_kv_append(desc, layer, rows, k, v, row_stride, ws, ws_bytes, stream=None):
     _check("moe_kv_append", load().moe_kv_append(desc, layer, rows, k, v, row_stride, ws, ws_bytes, _stream(stream)))
+
+
+def moe_kv_append_rope(desc, layer, rows, rope, positions, Hq, q, q_stride, q_out, q_out_stride, k, v, row_stride, ws,
+                       ws_bytes, stream=None):
+    _check("moe_kv_append_rope", load().moe_kv_append_rope(desc, layer, rows, rope, positions, Hq, q, q_stride, q_out,
+                                                           q_out_stride, k, v, row_stride, ws, ws_bytes, _stream(stream)))
+
+
+# The decoder-block calls likewise take references to the structs.
+def moe_rms_norm(args, stream=None):
+    _check("moe_rms_norm", load().moe_rms_norm(args, _stream(stream)))
+
+
+def moe_token_logprobs(args, stream=None):
+    _check("moe_token_logprobs", load().moe_token_logprobs(args, _stream(stream)))
+
+
+def moe_linear_step(desc, rows, args, stream=None):
+    _check("moe_linear_step", load().moe_linear_step(desc, rows, args, _stream(stream)))
+
+
+def moe_linear_chunk(desc, rows, args, stream=None):
+    _check("moe_linear_chunk", load().moe_linear_chunk(desc, rows, args, _stream(stream)))
 
 
 def moe_attn_decode(desc, layer, rows, args, ws, ws_bytes, stream=None):

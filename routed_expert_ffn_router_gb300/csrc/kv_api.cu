@@ -153,6 +153,33 @@ moe_status moe_kv_append(const moe_kv_desc* d, int32_t layer, const moe_kv_rows*
                                    static_cast<cudaStream_t>(stream)));
 }
 
+moe_status moe_kv_append_rope(const moe_kv_desc* d, int32_t layer, const moe_kv_rows* r, const moe_rope_desc* rope,
+                              const int32_t* positions, int32_t Hq, const void* q, int64_t q_stride, void* q_out,
+                              int64_t q_out_stride, const void* k, const void* v, int64_t row_stride, void* ws,
+                              size_t ws_bytes, void* stream) {
+  launch_count_reset();
+  moe_status s = check_kv(d);
+  if (s != MOE_OK) return s;
+  if ((s = check_rows(d, layer, r)) != MOE_OK) return s;
+  if (!rope || rope->rot < 2 || rope->rot % 2 || rope->rot > d->D) return MOE_ERR_INVALID;
+  if (rope->layout != MOE_ROPE_HALF && rope->layout != MOE_ROPE_INTERLEAVED) return MOE_ERR_INVALID;
+  if (!(rope->gain > -3.0e38f && rope->gain < 3.0e38f) || !rope->freq || !aligned(rope->freq, 8)) return MOE_ERR_INVALID;
+  if (Hq < 1 || !aligned(positions, 4)) return MOE_ERR_INVALID;
+  if (Hq > kMostHeads) return MOE_ERR_UNSUPPORTED;
+  if (r->n_rows == 0) return MOE_OK;
+  if (!q || !q_out || !aligned(q, 16) || !aligned(q_out, 16)) return MOE_ERR_INVALID;
+  if (q_stride % 8 || q_stride < (int64_t)Hq * d->D || q_out_stride % 8 || q_out_stride < (int64_t)Hq * d->D)
+    return MOE_ERR_INVALID;
+  if (q == q_out && q_stride != q_out_stride) return MOE_ERR_INVALID;
+  if (!k || !v || !aligned(k, 16) || !aligned(v, 16)) return MOE_ERR_INVALID;
+  if (row_stride % 8 || row_stride < (int64_t)d->Hkv * d->D) return MOE_ERR_INVALID;
+  if ((s = check_ws(ws, ws_bytes, 0)) != MOE_OK) return s;
+  return cuda_status(launch_append_rope(cache_of(d, layer), rows_of(r), *rope, positions, Hq, static_cast<const uint16_t*>(q),
+                                        q_stride, static_cast<uint16_t*>(q_out), q_out_stride,
+                                        static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), row_stride,
+                                        d->dtype == MOE_KV_F16, status_of(ws), static_cast<cudaStream_t>(stream)));
+}
+
 moe_status moe_attn_decode(const moe_kv_desc* d, int32_t layer, const moe_kv_rows* r, const moe_attn_args* a, void* ws,
                            size_t ws_bytes, void* stream) {
   return attention(d, layer, r, a, ws, ws_bytes, stream, true);

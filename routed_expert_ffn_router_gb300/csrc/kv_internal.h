@@ -96,6 +96,9 @@ cudaError_t launch_pdl(int kind, void (*kernel)(P...), dim3 grid, int threads, s
 
 cudaError_t launch_append(const Cache& c, const Rows& r, const uint16_t* k, const uint16_t* v, long long stride,
                           int32_t* status, cudaStream_t st);
+cudaError_t launch_append_rope(const Cache& c, const Rows& r, const moe_rope_desc& d, const int32_t* positions, int Hq,
+                               const uint16_t* q, long long q_stride, uint16_t* q_out, long long q_out_stride, const uint16_t* k,
+                               const uint16_t* v, long long stride, bool f16, int32_t* status, cudaStream_t st);
 cudaError_t launch_attn_rows(const Cache& c, const Rows& r, const Attn& a, bool f16, bool decode, int32_t* status,
                              cudaStream_t st);
 // The one-launch decode kernel (kv_decode.cu): D 64 or 128, pages of a power of

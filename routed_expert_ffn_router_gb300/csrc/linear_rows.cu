@@ -1,0 +1,115 @@
+// Linear attention with a decay, row by row (include/moe_block.h): decode windows
+// of any shape, and the prompt chunks that the matrix kernel does not take.
+//
+// The columns of a state are independent: a CTA owns 32 columns of one head's
+// [Dk][Dv] and keeps them in registers (a thread has 4 columns of every 16th row)
+// from one read to one write, whatever the number of rows, so a decode window
+// costs a read and a write of the state. Rows come through shared memory 16 at a
+// time; a row's products q S are summed over Dk within a warp by shuffles and over
+// the four warps once per 16 rows.
+#include "block_internal.h"
+#include "kv_common.cuh"
+#include "linear_common.cuh"
+
+namespace moe {
+namespace block {
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kCols = 32;   // of Dv per CTA
+constexpr int kRows = 16;   // tokens staged at a time
+
+template <bool F16>
+__device__ __forceinline__ float one(const uint16_t* p) {
+  return kv::unpack2<F16>((uint32_t)*p).x;
+}
+
+// DK: 64, 128 or 256, at least the head size.
+template <bool F16, int DK>
+__global__ void __launch_bounds__(kThreads) linear_rows_kernel(Linear a, kv::Rows r) {
+  constexpr int NI = DK / 16;
+  __shared__ float qs[kRows][DK], ks[kRows][DK], vs[kRows][kCols], po[kRows][4][kCols], decay[kRows];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, col = (tid & 7) * 4, row = tid >> 3;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tiles = (a.Dv + kCols - 1) / kCols;
+  const int tile = blockIdx.x % tiles, h = blockIdx.x / tiles % a.Hv, b = blockIdx.x / tiles / a.Hv;
+  const int c0 = tile * kCols, hk = h / (a.Hv / a.Hk);
+  const Span s = load_span(a, r, b);
+  if (s.n == 0) return;
+  float4* state = reinterpret_cast<float4*>(a.state + ((long long)max(s.slot, 0) * a.Hv + h) * a.Dk * a.Dv + c0 + col);
+  const bool mine = c0 + col < a.Dv && s.slot >= 0;
+  float4 S[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int d = row + 16 * i;
+    S[i] = mine && d < a.Dk ? state[(long long)d * a.Dv / 4] : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  const bool ok = span_allowed(a, r, b, s, tile == 0 && h == 0);
+  for (int t0 = 0; t0 < s.n; t0 += kRows) {
+    const int m = min(kRows, s.n - t0);
+    __syncthreads();  // the last rows have been used
+    for (int i = tid; i < m * a.Dk; i += kThreads) {
+      const int j = i / a.Dk, d = i - j * a.Dk;
+      const long long t = s.row0 + t0 + j;
+      qs[j][d] = one<F16>(a.q + t * a.q_stride + (long long)hk * a.Dk + d) * a.scale;
+      ks[j][d] = one<F16>(a.k + t * a.k_stride + (long long)hk * a.Dk + d);
+    }
+    for (int i = tid; i < m * kCols; i += kThreads) {
+      const int j = i / kCols, c = i % kCols;
+      vs[j][c] = c0 + c < a.Dv ? one<F16>(a.v + (s.row0 + t0 + j) * a.v_stride + (long long)h * a.Dv + c0 + c) : 0.f;
+    }
+    if (tid < m) decay[tid] = expf(bounded_g(a.g[(s.row0 + t0 + tid) * a.g_stride + h]));
+    __syncthreads();
+    for (int j = 0; j < m; ++j) {
+      const float e = decay[j];
+      const float4 v = *reinterpret_cast<const float4*>(&vs[j][col]);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int d = row + 16 * i;
+        if (DK == 256 && d >= a.Dk) break;
+        const float k = d < a.Dk ? ks[j][d] : 0.f, q = d < a.Dk ? qs[j][d] : 0.f;
+        S[i].x = fmaf(k, v.x, S[i].x * e); S[i].y = fmaf(k, v.y, S[i].y * e);
+        S[i].z = fmaf(k, v.z, S[i].z * e); S[i].w = fmaf(k, v.w, S[i].w * e);
+        o.x = fmaf(q, S[i].x, o.x); o.y = fmaf(q, S[i].y, o.y);
+        o.z = fmaf(q, S[i].z, o.z); o.w = fmaf(q, S[i].w, o.w);
+      }
+#pragma unroll
+      for (int x = 8; x < 32; x <<= 1) {
+        o.x += __shfl_xor_sync(0xffffffffu, o.x, x); o.y += __shfl_xor_sync(0xffffffffu, o.y, x);
+        o.z += __shfl_xor_sync(0xffffffffu, o.z, x); o.w += __shfl_xor_sync(0xffffffffu, o.w, x);
+      }
+      if (lane < 8) *reinterpret_cast<float4*>(&po[j][warp][col]) = o;
+    }
+    __syncthreads();
+    for (int i = tid; i < m * kCols / 2; i += kThreads) {
+      const int j = i / (kCols / 2), c = i % (kCols / 2) * 2;
+      if (c0 + c >= a.Dv) continue;
+      const float x = po[j][0][c] + po[j][1][c] + (po[j][2][c] + po[j][3][c]);
+      const float y = po[j][0][c + 1] + po[j][1][c + 1] + (po[j][2][c + 1] + po[j][3][c + 1]);
+      *reinterpret_cast<uint32_t*>(a.o + ((s.row0 + t0 + j) * (long long)a.Hv + h) * a.Dv + c0 + c) = ok ? kv::pack2<F16>(x, y) : 0u;
+    }
+  }
+  if (!ok || !mine) return;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int d = row + 16 * i;
+    if (d < a.Dk) state[(long long)d * a.Dv / 4] = S[i];
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_linear_rows(const Linear& a, const kv::Rows& r, bool f16, bool step, cudaStream_t st) {
+  const unsigned grid = (unsigned)((long long)r.B * a.Hv * ((a.Dv + kCols - 1) / kCols));
+  const auto go = [&](auto kernel) {
+    return launch_pdl(step ? K_LINEAR_STEP : K_LINEAR_CHUNK, kernel, dim3(grid), kThreads, 0, st, a, r);
+  };
+  if (f16) return a.Dk <= 64 ? go(linear_rows_kernel<true, 64>) : a.Dk <= 128 ? go(linear_rows_kernel<true, 128>) : go(linear_rows_kernel<true, 256>);
+  return a.Dk <= 64 ? go(linear_rows_kernel<false, 64>) : a.Dk <= 128 ? go(linear_rows_kernel<false, 128>) : go(linear_rows_kernel<false, 256>);
+}
+
+}  // namespace block
+}  // namespace moe

@@ -262,7 +262,8 @@ const char* moe_profile_kind_name(int32_t kind) {
                                            "gateup", "down", "combine", "fused_decode",
                                            "fused_stack", "kv_append", "kv_pages", "kv_move",
                                            "attn_rows", "attn_decode", "attn_chunk",
-                                           "attn_combine"};
+                                           "attn_combine", "rms_norm", "logprobs", "linear_step",
+                                           "linear_chunk"};
   if (kind < 0 || kind >= K_NUM_KINDS) return "";
   return names[kind];
 }

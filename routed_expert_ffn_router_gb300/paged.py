@@ -150,6 +150,31 @@ class PagedKV:
         _lib.moe_kv_append(self._desc_ref, layer, self._rows_ref, k.data_ptr(), v.data_ptr(), stride, self.ws_ptr,
                            self.ws_bytes, self._stream(stream))
 
+    def append_rotary(self, layer, q, k, v, rotary, slots=None, row_start=None, positions=None, q_out=None, stream=None):
+        """append with rotary positions: the rows' keys are turned on their way into the
+        pages, their queries q [rows][Hq][D] into q_out (a new tensor unless given; may
+        be q). rotary: a `block.Rotary`; positions int32 [rows] (None: each row's token
+        number in its sequence). -> q_out."""
+        Hq = self.Hq
+        q_stride, stride = self._heads(q, Hq, "q"), self._heads(k, self.Hkv, "k")
+        n = q.shape[0]
+        if self._heads(v, self.Hkv, "v") != stride or k.shape[0] != n or v.shape[0] != n:
+            raise ValueError("q, k and v must have the same rows, k and v the same row stride")
+        if rotary.device != self.device:
+            raise ValueError(f"the rotary frequencies are on {rotary.device}, the cache on {self.device}")
+        if positions is not None and _i32(positions, "positions", self.device).numel() != n:
+            raise ValueError("one position per row")
+        self._set_rows(n, slots, row_start)
+        if q_out is None:
+            q_out = self._new((n, Hq, self.D), self.dtype, stream)
+        elif q_out.shape != q.shape:
+            raise ValueError("q_out must be like q")
+        _lib.moe_kv_append_rope(self._desc_ref, layer, self._rows_ref, rotary.desc_ref,
+                                None if positions is None else positions.data_ptr(), Hq, q.data_ptr(), q_stride,
+                                q_out.data_ptr(), self._heads(q_out, Hq, "q_out"), k.data_ptr(), v.data_ptr(), stride,
+                                self.ws_ptr, self.ws_bytes, self._stream(stream))
+        return q_out
+
     def _attend(self, fn, layer, q, slots, row_start, scale, window, sinks, want_lse, out, lse, stream):
         Hq = self.Hq
         stride = self._heads(q, Hq, "q")
