@@ -43,6 +43,8 @@ moe_status linear(const moe_linear_desc* d, const moe_kv_rows* r, const moe_line
   kv::Rows rw;
   rw.B = r->B; rw.n_rows = r->n_rows; rw.n_q = r->row_start ? 0 : r->n_rows / r->B;
   rw.slots = r->slots; rw.row_start = r->row_start;
+  if (!step && linear_chunk_supported(l))
+    return cuda_status(launch_linear_chunk(l, rw, d->dtype == MOE_KV_F16, static_cast<cudaStream_t>(stream)));
   return cuda_status(launch_linear_rows(l, rw, d->dtype == MOE_KV_F16, step, static_cast<cudaStream_t>(stream)));
 }
 

@@ -30,5 +30,9 @@ struct Linear {
 // The recurrence, row by row (any shape).
 cudaError_t launch_linear_rows(const Linear& a, const kv::Rows& r, bool f16, bool step, cudaStream_t st);
 
+// Prompt chunks on the tensor cores: Dk and Dv of 64 or 128.
+bool linear_chunk_supported(const Linear& a);
+cudaError_t launch_linear_chunk(const Linear& a, const kv::Rows& r, bool f16, cudaStream_t st);
+
 }  // namespace block
 }  // namespace moe

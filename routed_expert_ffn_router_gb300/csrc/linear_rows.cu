@@ -29,7 +29,8 @@ __device__ __forceinline__ float one(const uint16_t* p) {
 template <bool F16, int DK>
 __global__ void __launch_bounds__(kThreads) linear_rows_kernel(Linear a, kv::Rows r) {
   constexpr int NI = DK / 16;
-  __shared__ float qs[kRows][DK], ks[kRows][DK], vs[kRows][kCols], po[kRows][4][kCols], decay[kRows];
+  __shared__ float qs[kRows][DK], ks[kRows][DK], vs[kRows][kCols], po[kRows][4][kCols];
+  __shared__ float2 decay[kRows];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, col = (tid & 7) * 4, row = tid >> 3;
   griddep_wait();
   griddep_launch_dependents();
@@ -60,10 +61,10 @@ __global__ void __launch_bounds__(kThreads) linear_rows_kernel(Linear a, kv::Row
       const int j = i / kCols, c = i % kCols;
       vs[j][c] = c0 + c < a.Dv ? one<F16>(a.v + (s.row0 + t0 + j) * a.v_stride + (long long)h * a.Dv + c0 + c) : 0.f;
     }
-    if (tid < m) decay[tid] = expf(bounded_g(a.g[(s.row0 + t0 + tid) * a.g_stride + h]));
+    if (tid < m) decay[tid] = decay_of(bounded_g(a.g[(s.row0 + t0 + tid) * a.g_stride + h]));
     __syncthreads();
     for (int j = 0; j < m; ++j) {
-      const float e = decay[j];
+      const float2 e = decay[j];
       const float4 v = *reinterpret_cast<const float4*>(&vs[j][col]);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -71,8 +72,8 @@ __global__ void __launch_bounds__(kThreads) linear_rows_kernel(Linear a, kv::Row
         const int d = row + 16 * i;
         if (DK == 256 && d >= a.Dk) break;
         const float k = d < a.Dk ? ks[j][d] : 0.f, q = d < a.Dk ? qs[j][d] : 0.f;
-        S[i].x = fmaf(k, v.x, S[i].x * e); S[i].y = fmaf(k, v.y, S[i].y * e);
-        S[i].z = fmaf(k, v.z, S[i].z * e); S[i].w = fmaf(k, v.w, S[i].w * e);
+        S[i].x = fmaf(k, v.x, fmaf(S[i].x, e.x, S[i].x * e.y)); S[i].y = fmaf(k, v.y, fmaf(S[i].y, e.x, S[i].y * e.y));
+        S[i].z = fmaf(k, v.z, fmaf(S[i].z, e.x, S[i].z * e.y)); S[i].w = fmaf(k, v.w, fmaf(S[i].w, e.x, S[i].w * e.y));
         o.x = fmaf(q, S[i].x, o.x); o.y = fmaf(q, S[i].y, o.y);
         o.z = fmaf(q, S[i].z, o.z); o.w = fmaf(q, S[i].w, o.w);
       }
