@@ -52,9 +52,11 @@ constexpr int kRegsScore = 112, kRegsState = 184, kRegsOut = 104, kRegsRest = 11
 constexpr uint32_t kTries = 1u << 22;   // of a wait, each up to a microsecond long
 constexpr int kHalf = kBlk * 128;       // bytes of 128 rows of 64 values
 constexpr int kTile = 2 * kHalf;
-constexpr int kSmem = 1024 + 6 * kTile; // Q, K, V, V' twice, S
+constexpr int kPitch = 144;             // bytes per row of a warp's output buffer (64 values and a pad)
+constexpr int kSmem = 1024 + 6 * kTile + 4 * 32 * kPitch;  // Q, K, V, V' twice, S; outputs
 constexpr int kSortB = 512;             // sequences that are put in order of their length
 constexpr int kMostParts = 8;
+constexpr int kAhead = 2;               // blocks that are fetched into L2 ahead
 
 struct ChunkArgs {
   CUtensorMap tm_q, tm_k, tm_v;
@@ -65,7 +67,7 @@ struct ChunkArgs {
 
 // What the decays of a block come to.
 struct Decays {
-  float2 g[kBlk];     // G_j / ln 2 as two values
+  float gh[kBlk], gl[kBlk];  // -G_j / ln 2 as two values
   float v[kBlk];      // e^(G - G_j); 0 behind the last token
   float q[kBlk];      // scale e^G_i
   float2 all;         // e^G (decay_of)
@@ -78,6 +80,22 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       " mov.b64 {%0, %1}, w;\n}"
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 w, x, y;\n"
+      " mov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return d;
 }
 __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&v)[16]) {
@@ -115,6 +133,10 @@ __device__ __forceinline__ float peer_f32(uint32_t a) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
   return v;
 }
+__device__ __forceinline__ void prefetch_3d(const void* tmap, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(tmap), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
 // 2^e as a float, e in the normal range
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 // The exponent that brings a largest magnitude m (>= 0) to [2^13, 2^14); bounded so
@@ -141,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   const Linear& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sq = (smem_u32(smem_linear) + 1023u) & ~1023u;
-  const uint32_t sk = sq + kTile, sv = sk + kTile, svh = sv + kTile, svl = svh + kTile, ss = svl + kTile;
+  const uint32_t sk = sq + kTile, sv = sk + kTile, svh = sv + kTile, svl = svh + kTile, ss = svl + kTile, so = ss + kTile;
   const uint32_t q_full = smem_u32(s_bar), k_full = q_full + 8, v_full = q_full + 16, q_empty = q_full + 24;
   const uint32_t k_empty = q_full + 32, v_empty = q_full + 40, a_full = q_full + 48, p_full = q_full + 56;
   const uint32_t s_ready = q_full + 64, w_ready = q_full + 72, u_full = q_full + 80, u_free = q_full + 88;
@@ -239,7 +261,21 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         }
         __syncwarp();
       };
+      // the next blocks come into L2 while the tiles are still in use
+      auto ahead = [&](int c) {
+        if (lead && c < n2) {
+          const int row = s.row0 + (first + c) * kBlk;
+          for (int x = 0; x < HK; ++x) {
+            prefetch_3d(&p.tm_k, x * 64, hk, row);
+            prefetch_3d(&p.tm_q, x * 64, hk, row);
+          }
+          for (int x = 0; x < HV; ++x) prefetch_3d(&p.tm_v, x * 64, h, row);
+        }
+        __syncwarp();
+      };
+      for (int c = 1; c < kAhead; ++c) ahead(c);
       auto step = [&](int i, bool full) {
+        ahead(i + kAhead);
         const int row = s.row0 + (first + (i < n1 ? i : i - n1)) * kBlk;
         if (full) {
           wait(q_empty, (i - n1 + 1) & 1);
@@ -348,7 +384,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         for (int j = 0; j < 4; ++j) {
           const double G = (lane ? before : 0.0) + g[j];
           const float hi = (float)G;
-          d.g[lane * 4 + j] = make_float2(hi, (float)(G - hi));
+          d.gh[lane * 4 + j] = -hi;
+          d.gl[lane * 4 + j] = (float)(hi - G);
           d.v[lane * 4 + j] = t0 + j < s.n ? exp2f((float)(total - G)) : 0.f;
           d.q[lane * 4 + j] = a.scale * exp2f(hi);
         }
@@ -379,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       wait(g_full + 8 * (i & 1), (i >> 1) & 1);
       wait(a_full, c & 1);
       tc_fence_after();
-      const float2 g = d.g[tid], gi = g;
+      const float2 gh = make_float2(-d.gh[tid], -d.gh[tid]), gl = make_float2(-d.gl[tid], -d.gl[tid]);
       float up = 1.f;
       if constexpr (F16) {  // the row's largest |q . k| to about 2^13
         float m = 0.f;
@@ -395,32 +432,38 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         up = pow2(e);
         s_row[c & 1][tid] = pow2(-e);
       }
-#pragma unroll
+      // (rolled loops: with all roles' loops unrolled their code did not stay in the
+      // instruction cache, and a block took twice as long)
+#pragma unroll 1
       for (int j = 0; j < 4; ++j) {
-        uint32_t pk[16];
-        if (j > warp) {  // tokens after all of this warp's
-#pragma unroll
-          for (int e = 0; e < 16; ++e) pk[e] = 0u;
-        } else {
-          uint32_t x[32];
+        uint32_t pk[16], x[32];
+        if (j <= warp) {
           tc_ld32(tr + j * 32, x);
           tc_ld_wait();
+          const float4* nh = reinterpret_cast<const float4*>(d.gh + j * 32);
+          const float4* nl = reinterpret_cast<const float4*>(d.gl + j * 32);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float4 gj = *reinterpret_cast<const float4*>(&d.g[j * 32 + 2 * e]);  // G_j, G_{j + 1} as two values each
-            const float2 t = add2(add2(make_float2(gi.x, gi.x), make_float2(-gj.x, -gj.z)),
-                                  add2(make_float2(gi.y, gi.y), make_float2(-gj.y, -gj.w)));
-            float u = __uint_as_float(x[2 * e]) * kv::ex2(t.x), w = __uint_as_float(x[2 * e + 1]) * kv::ex2(t.y);
+          for (int e = 0; e < 8; ++e) {
+            const float4 a4 = nh[e], b4 = nl[e];
+            const float2 t0 = add2(add2(gh, make_float2(a4.x, a4.y)), add2(gl, make_float2(b4.x, b4.y)));
+            const float2 t1 = add2(add2(gh, make_float2(a4.z, a4.w)), add2(gl, make_float2(b4.z, b4.w)));
+            float2 d0 = make_float2(kv::ex2(t0.x), kv::ex2(t0.y)), d1 = make_float2(kv::ex2(t1.x), kv::ex2(t1.y));
             if constexpr (F16) {
-              u *= up;
-              w *= up;
+              d0 = mul2(d0, make_float2(up, up));
+              d1 = mul2(d1, make_float2(up, up));
             }
-            if (j == warp) {  // (a select: what stands there may be NaN)
-              u = 2 * e <= lane ? u : 0.f;
-              w = 2 * e + 1 <= lane ? w : 0.f;
-            }
-            pk[e] = kv::pack2<F16>(u, w);
+            d0 = mul2(d0, make_float2(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1])));
+            d1 = mul2(d1, make_float2(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])));
+            pk[2 * e] = kv::pack2<F16>(d0.x, d0.y);
+            pk[2 * e + 1] = kv::pack2<F16>(d1.x, d1.y);
           }
+          if (j == warp) {  // later tokens (what stands there may be NaN: cleared as bits)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) pk[e] &= (2 * e <= lane ? 0xffffu : 0u) | (2 * e + 1 <= lane ? 0xffff0000u : 0u);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) pk[e] = 0u;
         }
         tc_st16(tr + j * 16, pk);
       }
@@ -435,8 +478,50 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     const int row = tid - 128;
     const bool held = row < DK;  // (head size 64: two of the warps only take part)
     const uint32_t tr = tu + ((uint32_t)((warp & 3) * 32) << 16);
-    float4* state = reinterpret_cast<float4*>(a.state + (((long long)s.slot * a.Hv + h) * DK + row) * DV);
-    float S[DV];
+    float4* state = reinterpret_cast<float4*>(a.state + ((long long)s.slot * a.Hv + h) * DK * DV);
+    float2 S[DV / 2];
+    // The state from or to memory, 64 columns at a time through S's tile, so that
+    // memory is touched along rows (16 pieces of 16 bytes each, in places that
+    // keep a warp's rows in different banks).
+    auto exchange = [&](bool in) {
+#pragma unroll
+      for (int x = 0; x < HV; ++x) {
+        const uint32_t mine = ss + row * 256;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (!in) {
+          if (held)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float2 u = S[x * 32 + 2 * j], w = S[x * 32 + 2 * j + 1];
+              st_s128(mine + ((j ^ (row & 15)) << 4), __float_as_uint(u.x), __float_as_uint(u.y), __float_as_uint(w.x), __float_as_uint(w.y));
+            }
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+        }
+#pragma unroll 8
+        for (int i = 0; i < DK / 8; ++i) {
+          const int r = i * 8 + (row >> 4), j = row & 15;
+          const uint32_t at = ss + r * 256 + ((j ^ (r & 15)) << 4);
+          float4* m = state + r * (DV / 4) + x * 16 + j;
+          if (in) {
+            const float4 f = *m;
+            st_s128(at, __float_as_uint(f.x), __float_as_uint(f.y), __float_as_uint(f.z), __float_as_uint(f.w));
+          } else {
+            const uint4 f = ld_s128(at);
+            *m = make_float4(__uint_as_float(f.x), __uint_as_float(f.y), __uint_as_float(f.z), __uint_as_float(f.w));
+          }
+        }
+        if (in) {
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const uint4 f = held ? ld_s128(mine + ((j ^ (row & 15)) << 4)) : make_uint4(0, 0, 0, 0);
+            S[x * 32 + 2 * j] = make_float2(__uint_as_float(f.x), __uint_as_float(f.y));
+            S[x * 32 + 2 * j + 1] = make_float2(__uint_as_float(f.z), __uint_as_float(f.w));
+          }
+        }
+      }
+      if (in) asm volatile("bar.sync 1, 128;" ::: "memory");  // S's tile is free for S
+    };
     auto step = [&](int i, float* decay) {  // S <- e^G S + U
       wait(g_full + 8 * (i & 1), (i >> 1) & 1);
       const float2 e = s_dec[i & 1].all;
@@ -450,9 +535,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         tc_ld32(tr + j * 32, x);
         tc_ld_wait();
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float u = F16 ? __uint_as_float(x[c]) * up : __uint_as_float(x[c]);
-          S[j * 32 + c] = fmaf(S[j * 32 + c], e.x, fmaf(S[j * 32 + c], e.y, u));
+        for (int c = 0; c < 16; ++c) {
+          float2 u = make_float2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
+          if constexpr (F16) u = mul2(u, make_float2(up, up));
+          S[j * 16 + c] = fma2(S[j * 16 + c], make_float2(e.x, e.x), fma2(S[j * 16 + c], make_float2(e.y, e.y), u));
         }
       }
       tc_fence_before();
@@ -462,24 +548,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     if (parts > 1) {
       float decay = 1.f;
 #pragma unroll
-      for (int j = 0; j < DV; ++j) S[j] = 0.f;
+      for (int j = 0; j < DV / 2; ++j) S[j] = make_float2(0.f, 0.f);
       for (int i = 0; i < n1; ++i) step(i, &decay);
       if (n1 > 0) {  // columns 4 j of all rows side by side, where V' was
         if (held)
 #pragma unroll
           for (int j = 0; j < DV / 4; ++j)
-            st_s128(svh + (j * DK + row) * 16, __float_as_uint(S[4 * j]), __float_as_uint(S[4 * j + 1]),
-                    __float_as_uint(S[4 * j + 2]), __float_as_uint(S[4 * j + 3]));
+            st_s128(svh + (j * DK + row) * 16, __float_as_uint(S[2 * j].x), __float_as_uint(S[2 * j].y),
+                    __float_as_uint(S[2 * j + 1].x), __float_as_uint(S[2 * j + 1].y));
         if (row == 0) s_part = decay;
       }
       meet();
     }
     if (n2 > 0) {
-#pragma unroll
-      for (int j = 0; j < DV / 4; ++j) {
-        const float4 x = held ? state[j] : make_float4(0.f, 0.f, 0.f, 0.f);
-        S[4 * j] = x.x; S[4 * j + 1] = x.y; S[4 * j + 2] = x.z; S[4 * j + 3] = x.w;
-      }
+      exchange(true);
       for (int r = 0; r < part; ++r) {  // the parts before, in their order
         const float e = peer_f32(peer(smem_u32(&s_part), r));
         const uint32_t from = peer(svh, r);
@@ -487,8 +569,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
 #pragma unroll
           for (int j = 0; j < DV / 4; ++j) {
             const float4 x = peer_f128(from + (j * DK + row) * 16);
-            S[4 * j] = fmaf(S[4 * j], e, x.x); S[4 * j + 1] = fmaf(S[4 * j + 1], e, x.y);
-            S[4 * j + 2] = fmaf(S[4 * j + 2], e, x.z); S[4 * j + 3] = fmaf(S[4 * j + 3], e, x.w);
+            S[2 * j] = fma2(S[2 * j], make_float2(e, e), make_float2(x.x, x.y));
+            S[2 * j + 1] = fma2(S[2 * j + 1], make_float2(e, e), make_float2(x.z, x.w));
           }
       }
     }
@@ -498,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       if constexpr (F16) {
         float m = 0.f;
 #pragma unroll
-        for (int j = 0; j < DV; ++j) m = fmaxf(m, held ? fabsf(S[j]) : 0.f);
+        for (int j = 0; j < DV / 2; ++j) m = fmaxf(m, held ? fmaxf(fabsf(S[j].x), fabsf(S[j].y)) : 0.f);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         asm volatile("bar.sync 1, 128;" ::: "memory");  // the last block's have been read
@@ -515,8 +597,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           uint32_t x[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float u = S[8 * j + 2 * e], w = S[8 * j + 2 * e + 1];
-            x[e] = F16 ? kv::pack2<F16>(u * up, w * up) : kv::pack2<F16>(u, w);
+            const float2 u = F16 ? mul2(S[4 * j + e], make_float2(up, up)) : S[4 * j + e];
+            x[e] = kv::pack2<F16>(u.x, u.y);
           }
           st_s128(ss + (j >> 3) * (DK * 128) + row * 128 + (((j & 7) ^ (row & 7)) << 4), x[0], x[1], x[2], x[3]);
         }
@@ -524,9 +606,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       arrive(s_ready);
       step(n1 + c, nullptr);
     }
-    if (last && held)
-#pragma unroll
-      for (int j = 0; j < DV / 4; ++j) state[j] = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
+    if (last) {
+      wait(q_empty, (n2 + 1) & 1);  // the last product with S
+      exchange(false);
+    }
   } else {
     // ================= V' and the output =================
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOut));
@@ -558,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         up = pow2(e);
         if (t == 0) s_v_up[i & 1] = pow2(-e);
       }
-#pragma unroll 4
+#pragma unroll 2
       for (int j = 0; j < 8 * HV; ++j) {
         const int at = (j * 128 + t) * 16, row = (at & (kHalf - 1)) >> 7;
         const uint4 raw = ld_s128(sv + at);
@@ -567,12 +650,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          float2 f = kv::unpack2<F16>(w[x]);
-          f.x *= e;
-          f.y *= e;
+          const float2 f = mul2(kv::unpack2<F16>(w[x]), make_float2(e, e));
           hi[x] = kv::pack2<F16>(f.x, f.y);
-          const float2 r = kv::unpack2<F16>(hi[x]);
-          lo[x] = kv::pack2<F16>(f.x - r.x, f.y - r.y);
+          const float2 r = kv::unpack2<F16>(hi[x]), rest = add2(f, make_float2(-r.x, -r.y));
+          lo[x] = kv::pack2<F16>(rest.x, rest.y);
         }
         const bool in = row < nv;
         if (!in) st_s128(sv + at, 0u, 0u, 0u, 0u);
@@ -595,15 +676,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     meet();
     meet();
     for (int c = 0; c < n2; ++c) {
-      const int i = n1 + c, tok = (first + c) * kBlk + t;
+      const int i = n1 + c;
       scaled(i);
       const float e = s_dec[i & 1].q[t];
       arrive(g_empty + 8 * (i & 1));
       wait(o_full, c & 1);
       tc_fence_after();
       const float ex = F16 ? e * s_state_up[c & 1] : e, ey = F16 ? a.scale * s_row[c & 1][t] : a.scale;
-      uint16_t* out = a.o + ((long long)(s.row0 + tok) * a.Hv + h) * DV;
-#pragma unroll
+#pragma unroll 1
       for (int j = 0; j < DV / 32; ++j) {
         uint32_t x[32], y[32];
         tc_ld32(tx + lanes + j * 32, x);
@@ -615,13 +695,28 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         }
         uint32_t w[16];
 #pragma unroll
-        for (int q = 0; q < 16; ++q)
-          w[q] = kv::pack2<F16>(fmaf(ex, __uint_as_float(x[2 * q]), ey * __uint_as_float(y[2 * q])),
-                                fmaf(ex, __uint_as_float(x[2 * q + 1]), ey * __uint_as_float(y[2 * q + 1])));
-        if (tok < s.n)
+        for (int q = 0; q < 16; ++q) {
+          const float2 o = fma2(make_float2(ex, ex), make_float2(__uint_as_float(x[2 * q]), __uint_as_float(x[2 * q + 1])),
+                                mul2(make_float2(ey, ey), make_float2(__uint_as_float(y[2 * q]), __uint_as_float(y[2 * q + 1]))));
+          w[q] = kv::pack2<F16>(o.x, o.y);
+        }
+        // rows of 64 values go out together, eight lanes a row: a store of one piece
+        // per row and lane takes the load-store unit 32 cycles, and everything waits
+        const uint32_t mine = so + (t >> 5) * (32 * kPitch);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<uint4*>(out + j * 32 + q * 8) = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+        for (int q = 0; q < 4; ++q)
+          st_s128(mine + lane * kPitch + (j & 1) * 64 + q * 16, w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+        if (j & 1) {
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const int r = q * 4 + (lane >> 3), tok = (first + c) * kBlk + (t & ~31) + r;
+            const uint4 v = ld_s128(mine + r * kPitch + (lane & 7) * 16);
+            if (tok < s.n)
+              *reinterpret_cast<uint4*>(a.o + ((long long)(s.row0 + tok) * a.Hv + h) * DV + (j & ~1) * 32 + (lane & 7) * 8) = v;
+          }
+          __syncwarp();
+        }
       }
     }
   }
