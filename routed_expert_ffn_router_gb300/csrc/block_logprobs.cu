@@ -6,21 +6,25 @@
 //   l = sum 2^d_i,  s = sum 2^d_i d_i      a larger maximum m': a = (m - m') c,
 //   s' = 2^a (s + l a),  l' = 2^a l
 // and at the end ln p_i = (z_i - m) / temperature - ln l, entropy = ln l - ln 2 s / l.
-// z - m is taken before the product, so that rows of the type's lowest value are
-// uniform and not NaN; d is bounded by -200, where 2^d is 0 in fp32 already, which
-// makes the terms of -inf zeros.
+// z - m is taken before the product: c m, rounded, would be off by 2^-24 of itself in
+// all terms alike. Two forms of the sums: where m is so far above the lowest values
+// that those vanish, logits below kLow (-inf, the type's lowest value) count as kLow;
+// else d is bounded by -200, where 2^d is 0 in fp32 already (a row of the type's
+// lowest value is uniform, and -inf - -inf no NaN).
 //
-// A row is read by a cluster of 1 to 8 CTAs, each by 16 warps that take chunks of
-// 32 lanes x 64 bytes in turn; rows start anywhere, so the pieces of a row go by
-// 16-byte boundaries of memory and the first and the last by single values. The
-// parts meet through shared memory, then through the cluster's: few rows use many
-// SMs without a workspace or a second launch.
+// A row is read by a cluster of 1 to 8 CTAs, each by 8 warps that take chunks of 32
+// lanes x 64 bytes in turn, the next chunk's loads under way; rows start anywhere,
+// so the pieces of a row go by 16-byte boundaries of memory and the first and the
+// last by single values. The parts meet through shared memory, then through the
+// cluster's: few rows use many SMs without a workspace or a second launch.
 //
 // Top alternatives: each warp keeps its best 32 as sorted keys (order of the logit,
 // then lower id: all distinct), one per lane. A chunk is looked through only if its
-// maximum, which the sum needs anyway, reaches the k-th best of any warp of the CTA
-// so far. The rank likewise counts only in chunks whose maximum reaches the token's
-// logit.
+// maximum, which the sum needs anyway, reaches the k-th best so far of any warp of
+// the CTA; in a warp's first chunk the k-th largest of the lanes' maxima stands in
+// for that. Ruled out tokens (-inf) never enter; a row with fewer than k others is
+// filled up at the end. The rank likewise counts only in chunks whose maximum
+// reaches the token's logit.
 #include "block_internal.h"
 #include "kv_common.cuh"
 
@@ -31,7 +35,7 @@ namespace {
 
 typedef unsigned long long Key;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarpsPerCta = kThreads / 32;
 constexpr int kVecs = 4;  // 16-byte pieces of a lane's chunk
 
@@ -49,6 +53,35 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
+}
+__device__ __forceinline__ float warp_max_nan(float x) {
+  float r;
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 w, x, y;\n"
+      " mov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 w, x, y;\n"
+      " mov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
 }
 // NaN becomes -200
 __device__ __forceinline__ float bounded(float d) { return fmaxf(d, -200.f); }
@@ -117,142 +150,232 @@ __device__ __forceinline__ Key peer_u64(uint32_t a) {
   return v;
 }
 
+// How a type's values lie in the 32-bit words of a piece.
 template <int TYPE>
-__device__ __forceinline__ float value(uint32_t bits) {
-  if constexpr (TYPE == MOE_T_F32) return __uint_as_float(bits);
-  else return kv::unpack2<TYPE == MOE_T_F16>(bits).x;
+struct Words {
+  static constexpr bool kWide = TYPE == MOE_T_F32, kHalf = TYPE == MOE_T_F16;
+  static constexpr int kSize = kWide ? 4 : 2, kPer = 16 / kSize;  // values per piece
+  static constexpr uint32_t kNone = kWide ? 0xff800000u : kHalf ? 0xfc00fc00u : 0xff80ff80u;  // -inf
+  // where the fast sums count everything lower as this much
+  static constexpr uint32_t kLowBits = kHalf ? 0xfbfffbffu : 0xf149f149u;  // 16-bit types
+  static constexpr float kLow = kHalf ? -65504.f : -9.9e29f;  // (that or lower)
+  __device__ static float at(const uint4& v, int e) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (kWide) return __uint_as_float(w[e]);
+    const float2 f = kv::unpack2<kHalf>(w[e >> 1]);
+    return e & 1 ? f.y : f.x;
+  }
+  // the larger, NaN if one is NaN
+  __device__ static uint32_t max_word(uint32_t a, uint32_t b) {
+    if constexpr (kWide) {
+      return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
+    } else if constexpr (kHalf) {
+      const __half2 r = __hmax2_nan(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+      return *reinterpret_cast<const uint32_t*>(&r);
+    } else {
+      const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+      return *reinterpret_cast<const uint32_t*>(&r);
+    }
+  }
+  __device__ static float max_of(uint32_t w) {
+    if constexpr (kWide) return __uint_as_float(w);
+    const float2 f = kv::unpack2<kHalf>(w);
+    return max_nan(f.x, f.y);
+  }
+};
+
+// The row's values as the kernel reads them.
+template <int TYPE>
+struct Row {
+  using W = Words<TYPE>;
+  const char* row;
+  const char* base;  // the 16-byte boundary at or before the row
+  int V, lead, n_vec;
+  __device__ Row(const moe_logprobs_args& a, int t) {
+    row = static_cast<const char*>(a.logits) + (long long)t * a.stride * W::kSize;
+    V = a.V;
+    lead = (int)(reinterpret_cast<uintptr_t>(row) & 15) / W::kSize;
+    base = row - lead * W::kSize;
+    n_vec = (lead + V + W::kPer - 1) / W::kPer;
+  }
+  __device__ uint32_t bits(int id) const {
+    return W::kWide ? *reinterpret_cast<const uint32_t*>(row + (long long)id * 4) : *reinterpret_cast<const uint16_t*>(row + (long long)id * 2);
+  }
+  __device__ float one(int id) const {
+    return W::kWide ? __uint_as_float(bits(id)) : kv::unpack2<W::kHalf>(bits(id)).x;
+  }
+  __device__ int id_of(int j, int e) const { return j * W::kPer + e - lead; }
+  // Piece j: whole ones at once; the first and the last, and what lies behind, with
+  // -inf in the other places.
+  __device__ uint4 piece(int j) const {
+    uint4 v = make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
+    if (j * W::kPer >= lead && (j + 1) * W::kPer <= lead + V) {
+      v = __ldcs(reinterpret_cast<const uint4*>(base + (long long)j * 16));
+    } else if (j < n_vec) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[i] = W::kNone;
+        if constexpr (W::kWide) {
+          if ((unsigned)id_of(j, i) < (unsigned)V) w[i] = bits(id_of(j, i));
+        } else {
+          if ((unsigned)id_of(j, 2 * i) < (unsigned)V) w[i] = (w[i] & 0xffff0000u) | bits(id_of(j, 2 * i));
+          if ((unsigned)id_of(j, 2 * i + 1) < (unsigned)V) w[i] = (w[i] & 0xffffu) | bits(id_of(j, 2 * i + 1)) << 16;
+        }
+      }
+      v = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return v;
+  }
+};
+
+// The k-th largest of the lanes' values (none is NaN).
+__device__ __forceinline__ float kth_of_lanes(float x, int k) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int w = 2; w <= 32; w <<= 1)
+#pragma unroll
+    for (int o = w >> 1; o > 0; o >>= 1) {
+      const float y = __shfl_xor_sync(0xffffffffu, x, o);
+      const bool larger = ((lane & w) == 0) == ((lane & o) == 0);  // descending
+      x = larger ? fmaxf(x, y) : fminf(x, y);
+    }
+  return __shfl_sync(0xffffffffu, x, k - 1);
 }
 
 template <int TYPE>
-__global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const __grid_constant__ moe_logprobs_args a, int parts) {
-  constexpr int S = TYPE == MOE_T_F32 ? 4 : 2, E = 16 / S, N = kVecs * E;
+__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_constant__ moe_logprobs_args a, int parts) {
+  using W = Words<TYPE>;
+  constexpr int E = W::kPer, N = kVecs * E;
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_wait();
   griddep_launch_dependents();
   const int t = blockIdx.x / parts, rank = parts > 1 ? (int)cluster_rank() : 0;
+  const Row<TYPE> row(a, t);
+  const float kNone = -__int_as_float(0x7f800000), kBig = __int_as_float(0x7f800000);
+  const int step = parts * kWarpsPerCta * 32 * kVecs;
+  int v0 = (rank * kWarpsPerCta + warp) * 32 * kVecs;
+  uint4 next[kVecs];
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) next[u] = row.piece(v0 + u * 32 + lane);
   const float c = 1.4426950408889634f / a.temperature;
-  const char* row = static_cast<const char*>(a.logits) + (long long)t * a.stride * S;
-  const int lead = (int)(reinterpret_cast<uintptr_t>(row) & 15) / S;  // values of the first piece before the row
-  const char* base = row - lead * S;
-  const int n_vec = (lead + a.V + E - 1) / E;
   const int token = a.tokens ? a.tokens[t] : -1;
   const bool has = token >= 0 && token < a.V;
-  const auto one = [&](int id) {
-    return TYPE == MOE_T_F32 ? value<TYPE>(*reinterpret_cast<const uint32_t*>(row + (long long)id * S))
-                             : value<TYPE>(*reinterpret_cast<const uint16_t*>(row + (long long)id * S));
-  };
-  const float mine_raw = has ? one(token) : 0.f;
-  // counts are of logits at or above it: with no token, of none
-  const float mine = !has ? __int_as_float(0x7f800000) : mine_raw == mine_raw ? mine_raw : -__int_as_float(0x7f800000);
-  const float kNone = -__int_as_float(0x7f800000);
+  const float mine_raw = has ? row.one(token) : 0.f;
+  // what the rank counts from: with no token, nothing; NaN stands with -inf
+  const float mine = !has ? kBig : mine_raw == mine_raw ? mine_raw : kNone;
+  // a logit above this one is at or above `mine` (for ids before the token's)
+  const float below = mine == 0.f ? -1e-45f : __int_as_float(__float_as_int(mine) + (mine > 0.f ? -1 : 1));
   if (tid == 0) sh.floor = kNone;
   __syncthreads();
 
-  Part p = {kNone, 0.f, 0.f, 0};
+  float m = kNone;                                  // the warp's
+  float2 l2 = make_float2(0.f, 0.f), s2 = l2;       // the lane's
+  int count = 0;
   Key best = 0;
   float floor = kNone;
-  for (int v0 = (rank * kWarpsPerCta + warp) * 32 * kVecs; v0 < n_vec; v0 += parts * kWarpsPerCta * 32 * kVecs) {
+  for (; v0 < row.n_vec; v0 += step) {
     uint4 raw[kVecs];
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-      const int j = v0 + u * 32 + lane;
-      // whole pieces; -inf elsewhere, which the edges below overwrite
-      const bool whole = j * E >= lead && (j + 1) * E <= lead + a.V;
-      const uint32_t none = TYPE == MOE_T_F32 ? 0xff800000u : TYPE == MOE_T_BF16 ? 0xff80ff80u : 0xfc00fc00u;
-      raw[u] = make_uint4(none, none, none, none);
-      if (whole) raw[u] = __ldcs(reinterpret_cast<const uint4*>(base + (long long)j * 16));
-    }
-    float z[N];
+    for (int u = 0; u < kVecs; ++u) raw[u] = next[u];
+    if (v0 + step < row.n_vec)
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-      const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+      for (int u = 0; u < kVecs; ++u) next[u] = row.piece(v0 + step + u * 32 + lane);
+    uint32_t mw = W::kNone;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (TYPE == MOE_T_F32) {
-          z[u * E + i] = __uint_as_float(w[i]);
-        } else {
-          const float2 f = kv::unpack2<TYPE == MOE_T_F16>(w[i]);
-          z[u * E + 2 * i] = f.x;
-          z[u * E + 2 * i + 1] = f.y;
-        }
-      }
+    for (int u = 0; u < kVecs; ++u)
+      mw = W::max_word(W::max_word(W::max_word(mw, raw[u].x), W::max_word(raw[u].y, raw[u].z)), raw[u].w);
+    const float mx = W::max_of(mw), top = warp_max_nan(mx);
+    if (top == kNone && mine != kNone) continue;  // nothing in it
+    if (top > m || top != top) {
+      const float up = max_nan(m, top), d = bounded((m - up) * c), e = kv::ex2(d);
+      s2 = fma2(l2, make_float2(d, d), s2);
+      s2.x *= e; s2.y *= e;
+      l2.x *= e; l2.y *= e;
+      m = up;
     }
-    const auto id_of = [&](int i) { return (v0 + (i / E) * 32 + lane) * E + i % E - lead; };
-    if (v0 == 0 || v0 + 32 * kVecs >= n_vec) {  // the row's first piece and its last
+    if (m < 1e29f && (m - W::kLow) * c > 200.f && c < 1e6f) {  // (the products stay finite)
+      const float2 c2 = make_float2(c, c), m2 = make_float2(-m, -m);
 #pragma unroll
       for (int u = 0; u < kVecs; ++u) {
-        const int j = v0 + u * 32 + lane;
-        if (j < n_vec && !(j * E >= lead && (j + 1) * E <= lead + a.V)) {
+        const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const int id = j * E + e - lead;
-            if (id >= 0 && id < a.V) z[u * E + e] = one(id);
-          }
+        for (int i = 0; i < E / 2; ++i) {
+          float2 f;
+          if constexpr (W::kWide)
+            f = make_float2(fmaxf(__uint_as_float(w[2 * i]), W::kLow), fmaxf(__uint_as_float(w[2 * i + 1]), W::kLow));
+          else
+            f = kv::unpack2<W::kHalf>(W::max_word(w[i], W::kLowBits));
+          const float2 d = mul2(add2(f, m2), c2), e = make_float2(kv::ex2(d.x), kv::ex2(d.y));
+          l2 = add2(l2, e);
+          s2 = fma2(e, d, s2);
         }
       }
-    }
-    float mx = z[0];
+    } else {
 #pragma unroll
-    for (int i = 1; i < N; ++i) mx = max_nan(mx, z[i]);
-    if (mx > p.m || mx != mx) {
-      const float m = max_nan(p.m, mx), d = bounded((p.m - m) * c), e = kv::ex2(d);
-      p.s = e * (p.s + p.l * d);
-      p.l *= e;
-      p.m = m;
-    }
+      for (int u = 0; u < kVecs; ++u)
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float d = bounded((z[i] - p.m) * c), e = kv::ex2(d);
-      p.l += e;
-      p.s = fmaf(e, d, p.s);
+        for (int i = 0; i < E; ++i) {
+          const float d = bounded((W::at(raw[u], i) - m) * c), e = kv::ex2(d);
+          l2.x += e;
+          s2.x = fmaf(e, d, s2.x);
+        }
     }
     if (!(mx < mine)) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float x = z[i] == z[i] ? z[i] : kNone;
-        p.rank += x > mine || (x == mine && (unsigned)id_of(i) < (unsigned)token) ? 1 : 0;
+      for (int u = 0; u < kVecs; ++u) {
+        const int id0 = row.id_of(v0 + u * 32 + lane, 0);
+        if (mine == kNone || (id0 <= token && id0 + E > token)) {
+#pragma unroll
+          for (int i = 0; i < E; ++i) {
+            const float z = W::at(raw[u], i), x = z == z ? z : kNone;
+            count += x > mine || (x == mine && (unsigned)(id0 + i) < (unsigned)token) ? 1 : 0;
+          }
+        } else {
+          const float limit = id0 < token ? below : mine;
+#pragma unroll
+          for (int i = 0; i < E; ++i) count += W::at(raw[u], i) > limit ? 1 : 0;
+        }
       }
     }
     if (a.top) {
       floor = fmaxf(floor, *const_cast<volatile float*>(&sh.floor));
-      if (__any_sync(0xffffffffu, !(mx < floor))) {
+      const float reach = mx == mx ? mx : kBig;  // a lane with a NaN is looked through
+      if (top != top || top >= floor) {
+        if (__shfl_sync(0xffffffffu, best, a.top - 1) == 0)
+          floor = fmaxf(floor, kth_of_lanes(mx == mx ? mx : kNone, a.top));
+        if (__any_sync(0xffffffffu, reach >= floor)) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float x = z[i] == z[i] ? z[i] : kNone;
-          const int id = id_of(i);
-          const Key key = (unsigned)id < (unsigned)a.V ? (Key)order_key(x) << 32 | (uint32_t)~id : 0;
-          unsigned todo = __ballot_sync(0xffffffffu, key != 0 && x >= floor);
-          while (todo) {
-            const Key k = shfl_key(key, __ffs(todo) - 1);
-            todo &= todo - 1;
-            const int at = __popc(__ballot_sync(0xffffffffu, best > k));  // its place in the list
-            if (at < a.top) {
-              const Key up = __shfl_up_sync(0xffffffffu, best, 1);
-              best = lane < at ? best : lane == at ? k : up;
-              const Key last = shfl_key(best, a.top - 1);
-              if (last) floor = fmaxf(floor, key_value((uint32_t)(last >> 32)));
+          for (int i = 0; i < N; ++i) {
+            const float x = W::at(raw[i / E], i % E);
+            unsigned todo = __ballot_sync(0xffffffffu, x >= floor && x > kNone);
+            while (todo) {
+              const int src = __ffs(todo) - 1;
+              todo &= todo - 1;
+              const float xs = __shfl_sync(0xffffffffu, x, src);
+              const Key k = (Key)order_key(xs) << 32 | (uint32_t)~row.id_of(v0 + (i / E) * 32 + src, i % E);
+              const int at = __popc(__ballot_sync(0xffffffffu, best > k));  // its place in the list
+              if (at < a.top) {
+                const Key up = __shfl_up_sync(0xffffffffu, best, 1);
+                best = lane < at ? best : lane == at ? k : up;
+                const Key last = shfl_key(best, a.top - 1);
+                if (last) floor = fmaxf(floor, key_value((uint32_t)(last >> 32)));
+              }
             }
           }
+          if (lane == 0 && floor > *const_cast<volatile float*>(&sh.floor)) *const_cast<volatile float*>(&sh.floor) = floor;
         }
-        if (lane == 0 && floor > *const_cast<volatile float*>(&sh.floor)) *const_cast<volatile float*>(&sh.floor) = floor;
       }
     }
   }
+  Part p = {m, l2.x + l2.y, s2.x + s2.y, count};
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Part q;
-    q.m = __shfl_xor_sync(0xffffffffu, p.m, o);
-    q.l = __shfl_xor_sync(0xffffffffu, p.l, o);
-    q.s = __shfl_xor_sync(0xffffffffu, p.s, o);
-    q.rank = __shfl_xor_sync(0xffffffffu, p.rank, o);
-    if (lane & o) {  // both sides of a pair join in the same order
-      join(q, p, c);
-      p = q;
-    } else {
-      join(p, q, c);
-    }
+  for (int o = 16; o > 0; o >>= 1) {  // (one maximum for the warp)
+    p.l += __shfl_xor_sync(0xffffffffu, p.l, o);
+    p.s += __shfl_xor_sync(0xffffffffu, p.s, o);
   }
+  p.rank = __reduce_add_sync(0xffffffffu, p.rank);
   if (lane == 0) sh.part[warp] = p;
   sh.key[warp][lane] = best;
   join_warps(sh, kWarpsPerCta, a.top > 0, c);
@@ -287,8 +410,24 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const __grid_cons
     if (a.rank) a.rank[t] = has ? p.rank : -1;
     if (a.entropy) a.entropy[t] = broken ? nan : empty ? 0.f : fmaxf(ln_l - 0.6931471805599453f * (p.s / p.l), 0.f);
   }
-  if (lane < a.top && a.top_ids) {
-    const Key k = sh.key[0][lane];
+  if (a.top) {
+    Key k = sh.key[0][lane];
+    const int got = __popc(__ballot_sync(0xffffffffu, k != 0));
+    if (got < a.top) {  // fewer than that are not ruled out: the lowest ids of those that are
+      int place = got;
+      for (int id0 = 0; id0 < a.V && place < a.top; id0 += 32) {
+        const int id = id0 + lane;
+        const float z = id < a.V ? row.one(id) : 0.f;
+        const unsigned out = __ballot_sync(0xffffffffu, z == kNone || z != z);
+        const int n = lane - place;  // this lane's place is the n-th of them
+        if (n >= 0 && n < __popc(out)) {
+          const int src = __fns(out, 0, n + 1);
+          k = (Key)order_key(kNone) << 32 | (uint32_t)~(id0 + src);
+        }
+        place += __popc(out);
+      }
+    }
+    if (lane >= a.top) return;
     a.top_ids[(long long)t * a.top + lane] = (int)~(uint32_t)k;
     a.top_logprobs[(long long)t * a.top + lane] = log_p(key_value((uint32_t)(k >> 32)));
   }
@@ -317,11 +456,11 @@ cudaError_t launch_type(const moe_logprobs_args& a, int parts, cudaStream_t st) 
 }  // namespace
 
 cudaError_t launch_token_logprobs(const moe_logprobs_args& a, cudaStream_t st) {
-  // CTAs per row: while there are fewer than two per SM and each has a chunk or
-  // more for every warp.
+  // CTAs per row: while all fit on the GPU (four per SM) and a part is more than a
+  // chunk for each warp.
   int parts = 1;
   const long long chunk = (long long)kThreads * kVecs * (a.type == MOE_T_F32 ? 4 : 8);
-  while (parts < 8 && (long long)a.T * parts * 2 <= 304 && a.V >= chunk * parts) parts *= 2;
+  while (parts < 8 && (long long)a.T * parts * 2 <= 608 && a.V > chunk * parts) parts *= 2;
   if (a.type == MOE_T_F32) return launch_type<MOE_T_F32>(a, parts, st);
   return a.type == MOE_T_F16 ? launch_type<MOE_T_F16>(a, parts, st) : launch_type<MOE_T_BF16>(a, parts, st);
 }
