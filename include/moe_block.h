@@ -35,7 +35,7 @@ typedef enum { MOE_T_F32 = 0, MOE_T_BF16 = 1, MOE_T_F16 = 2, MOE_T_E4M3 = 3 } mo
  * (a group of zeros has scale 0), saturating, NaN kept. Squares beyond fp32
  * make a row's mean infinite and its y 0 or NaN.
  *
- * H up to 16,384; strides are elements from row to row, at least H. Rows whose
+ * H up to 16,384, T up to 2^30; strides are elements from row to row, at least H. Rows whose
  * pointers and strides keep 8 values on a 16-byte boundary (8 bytes for e4m3)
  * and H a multiple of 8 are read 8 values at a time, others one by one. y may
  * be x where type and stride are the same. x, res: F32, BF16 or F16; w: the

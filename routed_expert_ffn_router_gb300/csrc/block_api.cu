@@ -60,7 +60,7 @@ moe_status moe_rms_norm(const moe_norm_args* a, void* stream) {
   if (!(a->eps >= 0.f && a->eps < 3.0e38f) || !(a->w_offset > -3.0e38f && a->w_offset < 3.0e38f)) return MOE_ERR_INVALID;
   const bool fp8 = a->y_type == MOE_T_E4M3;
   if (a->group && (!fp8 || a->group < 16 || (a->group & (a->group - 1)) || a->H % a->group)) return MOE_ERR_INVALID;
-  if (a->H > kMostNormH) return MOE_ERR_UNSUPPORTED;
+  if (a->H > kMostNormH || a->T > (1 << 30)) return MOE_ERR_UNSUPPORTED;
   if (a->T == 0) return MOE_OK;
   if (!a->x || !a->y || (fp8 && !a->scales) || a->x == a->res || a->y == a->res) return MOE_ERR_INVALID;
   if (a->x_stride < a->H || a->y_stride < a->H || (a->res && a->res_stride < a->H)) return MOE_ERR_INVALID;

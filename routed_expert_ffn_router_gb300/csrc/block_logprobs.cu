@@ -27,6 +27,7 @@
 // reaches the token's logit.
 #include "block_internal.h"
 #include "kv_common.cuh"
+#include "packed.cuh"
 
 namespace moe {
 namespace block {
@@ -58,30 +59,6 @@ __device__ __forceinline__ float warp_max_nan(float x) {
   float r;
   asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
   return r;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 w, x, y;\n"
-      " mov.b64 {%0, %1}, w;\n}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 w, x, y;\n"
-      " mov.b64 {%0, %1}, w;\n}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
-      " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
 }
 // NaN becomes -200
 __device__ __forceinline__ float bounded(float d) { return fmaxf(d, -200.f); }
@@ -157,7 +134,7 @@ struct Words {
   static constexpr int kSize = kWide ? 4 : 2, kPer = 16 / kSize;  // values per piece
   static constexpr uint32_t kNone = kWide ? 0xff800000u : kHalf ? 0xfc00fc00u : 0xff80ff80u;  // -inf
   // where the fast sums count everything lower as this much
-  static constexpr uint32_t kLowBits = kHalf ? 0xfbfffbffu : 0xf149f149u;  // 16-bit types
+  static constexpr uint32_t kLowBits = kHalf ? 0xfbfffbffu : 0xf149f149u;
   static constexpr float kLow = kHalf ? -65504.f : -9.9e29f;  // (that or lower)
   __device__ static float at(const uint4& v, int e) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -246,7 +223,7 @@ __device__ __forceinline__ float kth_of_lanes(float x, int k) {
 template <int TYPE>
 __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_constant__ moe_logprobs_args a, int parts) {
   using W = Words<TYPE>;
-  constexpr int E = W::kPer, N = kVecs * E;
+  constexpr int E = W::kPer;
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_wait();
@@ -256,9 +233,20 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
   const float kNone = -__int_as_float(0x7f800000), kBig = __int_as_float(0x7f800000);
   const int step = parts * kWarpsPerCta * 32 * kVecs;
   int v0 = (rank * kWarpsPerCta + warp) * 32 * kVecs;
-  uint4 next[kVecs];
+  // chunks that hold whole pieces only
+  const int whole0 = row.lead ? 1 : 0, whole1 = (row.lead + a.V) / E;
+  const auto fetch = [&](uint4 (&x)[kVecs], int v) {
+    if (v >= whole0 && v + 32 * kVecs <= whole1) {
+      const uint4* from = reinterpret_cast<const uint4*>(row.base) + v + lane;
 #pragma unroll
-  for (int u = 0; u < kVecs; ++u) next[u] = row.piece(v0 + u * 32 + lane);
+      for (int u = 0; u < kVecs; ++u) x[u] = __ldcs(from + u * 32);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u) x[u] = row.piece(v + u * 32 + lane);
+    }
+  };
+  uint4 even[kVecs], odd[kVecs];
+  fetch(even, v0);
   const float c = 1.4426950408889634f / a.temperature;
   const int token = a.tokens ? a.tokens[t] : -1;
   const bool has = token >= 0 && token < a.V;
@@ -275,19 +263,13 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
   int count = 0;
   Key best = 0;
   float floor = kNone;
-  for (; v0 < row.n_vec; v0 += step) {
-    uint4 raw[kVecs];
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u) raw[u] = next[u];
-    if (v0 + step < row.n_vec)
-#pragma unroll
-      for (int u = 0; u < kVecs; ++u) next[u] = row.piece(v0 + step + u * 32 + lane);
+  const auto chunk = [&](const uint4 (&raw)[kVecs], int v0) {
     uint32_t mw = W::kNone;
 #pragma unroll
     for (int u = 0; u < kVecs; ++u)
       mw = W::max_word(W::max_word(W::max_word(mw, raw[u].x), W::max_word(raw[u].y, raw[u].z)), raw[u].w);
     const float mx = W::max_of(mw), top = warp_max_nan(mx);
-    if (top == kNone && mine != kNone) continue;  // nothing in it
+    if (top == kNone && mine != kNone) return;  // nothing in it
     if (top > m || top != top) {
       const float up = max_nan(m, top), d = bounded((m - up) * c), e = kv::ex2(d);
       s2 = fma2(l2, make_float2(d, d), s2);
@@ -313,29 +295,32 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
         }
       }
     } else {
-#pragma unroll
-      for (int u = 0; u < kVecs; ++u)
+#pragma unroll 1
+      for (int u = 0; u < kVecs; ++u) {  // (read again: the usual path stays short)
+        const uint4 v = row.piece(v0 + u * 32 + lane);
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-          const float d = bounded((W::at(raw[u], i) - m) * c), e = kv::ex2(d);
+          const float d = bounded((W::at(v, i) - m) * c), e = kv::ex2(d);
           l2.x += e;
           s2.x = fmaf(e, d, s2.x);
         }
+      }
     }
     if (!(mx < mine)) {
+      if (mine != kNone) {
 #pragma unroll
-      for (int u = 0; u < kVecs; ++u) {
-        const int id0 = row.id_of(v0 + u * 32 + lane, 0);
-        if (mine == kNone || (id0 <= token && id0 + E > token)) {
-#pragma unroll
-          for (int i = 0; i < E; ++i) {
-            const float z = W::at(raw[u], i), x = z == z ? z : kNone;
-            count += x > mine || (x == mine && (unsigned)(id0 + i) < (unsigned)token) ? 1 : 0;
-          }
-        } else {
-          const float limit = id0 < token ? below : mine;
+        for (int u = 0; u < kVecs; ++u) {  // (those beside the token in its piece: below)
+          const float limit = row.id_of(v0 + u * 32 + lane, E - 1) < token ? below : mine;
 #pragma unroll
           for (int i = 0; i < E; ++i) count += W::at(raw[u], i) > limit ? 1 : 0;
+        }
+      } else {
+#pragma unroll 1
+        for (int u = 0; u < kVecs; ++u) {
+          const uint4 v = row.piece(v0 + u * 32 + lane);
+#pragma unroll
+          for (int i = 0; i < E; ++i)
+            count += W::at(v, i) > kNone || (unsigned)row.id_of(v0 + u * 32 + lane, i) < (unsigned)token ? 1 : 0;
         }
       }
     }
@@ -346,15 +331,21 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
         if (__shfl_sync(0xffffffffu, best, a.top - 1) == 0)
           floor = fmaxf(floor, kth_of_lanes(mx == mx ? mx : kNone, a.top));
         if (__any_sync(0xffffffffu, reach >= floor)) {
+#pragma unroll 1
+          for (int u = 0; u < kVecs; ++u) {
+            const uint4 v = row.piece(v0 + u * 32 + lane);
+            uint32_t mask = 0;  // of this lane's values
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const float x = W::at(raw[i / E], i % E);
-            unsigned todo = __ballot_sync(0xffffffffu, x >= floor && x > kNone);
+            for (int i = 0; i < E; ++i) mask |= W::at(v, i) >= floor && W::at(v, i) > kNone ? 1u << i : 0u;
+            unsigned todo = __ballot_sync(0xffffffffu, mask != 0);
             while (todo) {
-              const int src = __ffs(todo) - 1;
-              todo &= todo - 1;
-              const float xs = __shfl_sync(0xffffffffu, x, src);
-              const Key k = (Key)order_key(xs) << 32 | (uint32_t)~row.id_of(v0 + (i / E) * 32 + src, i % E);
+              const int src = __ffs(todo) - 1, e = __ffs(mask) - 1;
+              const uint32_t w = (e >> (W::kWide ? 0 : 1)) == 0 ? v.x : (e >> (W::kWide ? 0 : 1)) == 1 ? v.y
+                                 : (e >> (W::kWide ? 0 : 1)) == 2 ? v.z : v.w;
+              const float x = W::kWide ? __uint_as_float(w) : (e & 1 ? kv::unpack2<W::kHalf>(w).y : kv::unpack2<W::kHalf>(w).x);
+              const Key k = shfl_key((Key)order_key(x) << 32 | (uint32_t)~row.id_of(v0 + u * 32 + lane, e), src);
+              if (lane == src) mask &= mask - 1;
+              todo = __ballot_sync(0xffffffffu, mask != 0);
               const int at = __popc(__ballot_sync(0xffffffffu, best > k));  // its place in the list
               if (at < a.top) {
                 const Key up = __shfl_up_sync(0xffffffffu, best, 1);
@@ -368,6 +359,18 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
         }
       }
     }
+  };
+  for (; v0 < row.n_vec; v0 += 2 * step) {
+    if (v0 + step < row.n_vec) fetch(odd, v0 + step);
+    chunk(even, v0);
+    if (v0 + step >= row.n_vec) break;
+    if (v0 + 2 * step < row.n_vec) fetch(even, v0 + 2 * step);
+    chunk(odd, v0 + step);
+  }
+  // equal logits before the token in its own piece
+  if (rank == 0 && warp == 0 && has && mine != kNone) {
+    const int id = token - 1 - lane;
+    if (lane < (token + row.lead) % E && id >= 0) count += row.one(id) == mine ? 1 : 0;
   }
   Part p = {m, l2.x + l2.y, s2.x + s2.y, count};
 #pragma unroll

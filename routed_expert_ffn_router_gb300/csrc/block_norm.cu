@@ -1,70 +1,103 @@
 // The residual's addition and the root-mean-square norm of its rows, in 16 or 32
 // bits or in e4m3 with scales (include/moe_block.h).
 //
-// One CTA per row: a thread holds its values of the row in registers from the one
-// read of x and r to the write of y, so the row's sum of squares is the only
-// exchange (a shuffle tree and one barrier). A pass over memory and nothing else:
-// the raw loads of x, r and w are issued together before anything waits for them.
-#include <cuda_fp8.h>
+// A CTA has a row at a time: a thread holds its values in registers from the one read
+// of x and r to the write of y, so the row's sum of squares is the only exchange (a
+// shuffle tree and one barrier). With more rows than CTAs fit on the GPU a CTA goes on
+// to the row a grid further, whose loads are under way meanwhile. A pass over memory
+// and nothing else; what kept it from memory's rate were instructions per value
+// (48 in a first version of the 8-bit form: conversions chosen per value, divisions,
+// addresses in 64 bits).
+#include <atomic>
+
+#include <type_traits>
 
 #include "block_internal.h"
 #include "kv_common.cuh"
+#include "packed.cuh"
 
 namespace moe {
 namespace block {
 
 namespace {
 
-struct Raw {
-  uint4 a, b;  // 8 values: 16 bytes, or 32 in fp32
+// 8 values as they lie in memory; WIDE: fp32 among the types of a call.
+template <bool WIDE>
+struct Raw;
+template <>
+struct Raw<false> {
+  uint4 a;
 };
-__device__ __forceinline__ Raw load_raw(const void* p, int type, long long i) {
-  Raw r;
-  if (type == MOE_T_F32) {
-    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
-    r.a = q[0];
-    r.b = q[1];
-  } else {
-    r.a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+template <>
+struct Raw<true> {
+  uint4 a, b;
+};
+template <bool WIDE>
+__device__ __forceinline__ Raw<WIDE> load_raw(const void* p, int type, int i) {
+  Raw<WIDE> r;
+  if constexpr (WIDE) {
+    if (type == MOE_T_F32) {
+      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
+      r.a = q[0];
+      r.b = q[1];
+      return r;
+    }
     r.b = make_uint4(0, 0, 0, 0);
   }
+  r.a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
   return r;
 }
-__device__ __forceinline__ void widen(const Raw& r, int type, float (&f)[8]) {
-  const uint32_t u[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
-  if (type == MOE_T_F32) {
+// (One branch around all eight values, not a choice per value: with both types'
+// conversions and a select each, the instructions were what bound the kernel.)
+template <bool WIDE>
+__device__ __forceinline__ void widen(const Raw<WIDE>& r, int type, float2 (&f)[4]) {
+  const auto two = [&](auto f16) {
+    const uint32_t u[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(u[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 t = type == MOE_T_F16 ? kv::unpack2<true>(u[i]) : kv::unpack2<false>(u[i]);
-      f[2 * i] = t.x;
-      f[2 * i + 1] = t.y;
-    }
+    for (int i = 0; i < 4; ++i) f[i] = kv::unpack2<decltype(f16)::value>(u[i]);
+  };
+  if (type == MOE_T_BF16) {
+    two(std::false_type());
+  } else if (!WIDE || type == MOE_T_F16) {
+    two(std::true_type());
+  } else if constexpr (WIDE) {
+    f[0] = make_float2(__uint_as_float(r.a.x), __uint_as_float(r.a.y));
+    f[1] = make_float2(__uint_as_float(r.a.z), __uint_as_float(r.a.w));
+    f[2] = make_float2(__uint_as_float(r.b.x), __uint_as_float(r.b.y));
+    f[3] = make_float2(__uint_as_float(r.b.z), __uint_as_float(r.b.w));
   }
 }
-// Rounds f to `type` and writes it; f then holds what was written.
-__device__ __forceinline__ void store8(void* p, int type, long long i, float (&f)[8]) {
-  if (type == MOE_T_F32) {
-    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-    q[0] = make_float4(f[0], f[1], f[2], f[3]);
-    q[1] = make_float4(f[4], f[5], f[6], f[7]);
-  } else if (type == MOE_T_E4M3) {
-    uint32_t u[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) u[j] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * j], f[2 * j + 1]), __NV_SATFINITE, __NV_E4M3);
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p) + i) = make_uint2(u[0] | u[1] << 16, u[2] | u[3] << 16);
-  } else {
+// Two e4m3 values, x in the low byte; to the nearest, saturating, NaN kept.
+__device__ __forceinline__ uint32_t e4m3x2(float x, float y) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(y), "f"(x));
+  return r;
+}
+// Rounds f to `type` and writes it; f then holds what was written (but for e4m3).
+__device__ __forceinline__ void store8(void* p, int type, int i, float2 (&f)[4]) {
+  const auto two = [&](auto f16) {
+    constexpr bool F16 = decltype(f16)::value;
     uint32_t u[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      u[j] = type == MOE_T_F16 ? kv::pack2<true>(f[2 * j], f[2 * j + 1]) : kv::pack2<false>(f[2 * j], f[2 * j + 1]);
-      const float2 t = type == MOE_T_F16 ? kv::unpack2<true>(u[j]) : kv::unpack2<false>(u[j]);
-      f[2 * j] = t.x;
-      f[2 * j + 1] = t.y;
+      u[j] = kv::pack2<F16>(f[j].x, f[j].y);
+      f[j] = kv::unpack2<F16>(u[j]);
     }
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = make_uint4(u[0], u[1], u[2], u[3]);
+  };
+  if (type == MOE_T_BF16) {
+    two(std::false_type());
+  } else if (type == MOE_T_F16) {
+    two(std::true_type());
+  } else if (type == MOE_T_F32) {
+    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+    q[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+    q[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+  } else {
+    uint32_t u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) u[j] = e4m3x2(f[j].x, f[j].y);
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p) + i) = make_uint2(u[0] | u[1] << 16, u[2] | u[3] << 16);
   }
 }
 __device__ __forceinline__ float load1(const void* p, int type, long long i) {
@@ -78,7 +111,7 @@ __device__ __forceinline__ float store1(void* p, int type, long long i, float f)
     return f;
   }
   if (type == MOE_T_E4M3) {
-    static_cast<uint8_t*>(p)[i] = __nv_cvt_float_to_fp8(f, __NV_SATFINITE, __NV_E4M3);
+    static_cast<uint8_t*>(p)[i] = (uint8_t)e4m3x2(f, 0.f);
     return f;
   }
   const uint32_t u = type == MOE_T_F16 ? kv::pack2<true>(f, 0.f) : kv::pack2<false>(f, 0.f);
@@ -86,191 +119,267 @@ __device__ __forceinline__ float store1(void* p, int type, long long i, float f)
   return type == MOE_T_F16 ? kv::unpack2<true>(u).x : kv::unpack2<false>(u).x;
 }
 
-// What a value of a group is multiplied by for its e4m3, in two factors: the
-// reciprocal of a tiny scale would leave fp32.
+// What a value is multiplied by for its e4m3, in two factors: the reciprocal of a tiny
+// scale would leave fp32.
 struct Quant {
   float up, inv;
 };
 __device__ __forceinline__ Quant quant_of(float scale) {
   const float up = scale < 1e-30f ? 0x1p100f : 1.f;
-  return {up, scale == 0.f ? 0.f : 1.f / (scale * up)};
+  return {up, scale == 0.f ? 0.f : __fdividef(1.f, scale * up)};
 }
 
-// NV groups of 8 values per thread. VEC: 8 values that lie together (16-byte
-// loads); else value j of a thread is column j * threads + thread (rows whose
-// alignment allows single values only).
-template <int NV, bool VEC>
-__global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_kernel(const __grid_constant__ moe_norm_args a) {
-  extern __shared__ int group_max[];  // e4m3: largest magnitude of each group, as bits (they are not negative)
-  __shared__ float part[32];
-  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
-  const long long t = blockIdx.x;
+struct Args {
+  moe_norm_args a;
+  float inv_H;
+  int shift, n_groups;  // log2 of a group's columns (of a power of two: not the whole row), groups of a row
+};
+
+// The sum of s over the CTA (all threads); part: a buffer that the row before did not use.
+__device__ __forceinline__ float cta_sum(float s, float* part) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0) part[threadIdx.x >> 5] = s;
+  __syncthreads();
+  s = lane < (blockDim.x >> 5) ? part[lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+
+// Rows on 16-byte boundaries: NV pieces of 8 values per thread.
+template <int NV, bool FP8, bool WIDE, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : (WIDE ? 1280 : 1536) / MAXT) norm_kernel(const __grid_constant__ Args g) {
+  __shared__ float part[2][32];
+  __shared__ int row_max[2];  // e4m3 with one scale a row, or groups wider than a warp: see below
+  extern __shared__ int group_max[];
+  const moe_norm_args& a = g.a;
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
   griddep_wait();
   griddep_launch_dependents();
-  const long long xo = t * a.x_stride, ro = t * a.res_stride, yo = t * a.y_stride;
-  const bool fp8 = a.y_type == MOE_T_E4M3;
-  const int G = a.group ? a.group : a.H, n_groups = a.H / G;
-  if (fp8)
-    for (int i = tid; i < n_groups; i += nt) group_max[i] = 0;
-
-  float r[NV][8];
-  Raw rw[NV];
-  if constexpr (VEC) {
-    Raw rx[NV], rr[NV];
+  Raw<WIDE> rx[NV], rr[NV], rw[NV];
+  const auto fetch = [&](int t) {
+    const char* x = static_cast<const char*>(a.x) + t * a.x_stride * (a.x_type == MOE_T_F32 ? 4 : 2);
+    const char* r = static_cast<const char*>(a.res) + t * a.res_stride * (a.res_type == MOE_T_F32 ? 4 : 2);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * nt + tid) * 8;
       if (c < a.H) {
-        rx[j] = load_raw(a.x, a.x_type, xo + c);
-        if (a.res) rr[j] = load_raw(a.res, a.res_type, ro + c);
-        if (a.w) rw[j] = load_raw(a.w, a.w_type, c);
+        rx[j] = load_raw<WIDE>(x, a.x_type, c);
+        if (a.res) rr[j] = load_raw<WIDE>(r, a.res_type, c);
       }
     }
+  };
+  int t = blockIdx.x;
+  fetch(t);
+  if (a.w)
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * nt + tid) * 8;
+      if (c < a.H) rw[j] = load_raw<WIDE>(a.w, a.w_type, c);
+    }
+  for (int turn = 0;; turn ^= 1) {
+    float2 r[NV][4];
+    float2 sum = make_float2(0.f, 0.f);
+    char* res = static_cast<char*>(a.res) + t * a.res_stride * (a.res_type == MOE_T_F32 ? 4 : 2);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * nt + tid) * 8;
       if (c < a.H) {
         widen(rx[j], a.x_type, r[j]);
         if (a.res) {
-          float f[8];
+          float2 f[4];
           widen(rr[j], a.res_type, f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) r[j][i] += f[i];
-          store8(a.res, a.res_type, ro + c, r[j]);
+          for (int i = 0; i < 4; ++i) r[j][i] = add2(r[j][i], f[i]);
+          store8(res, a.res_type, c, r[j]);
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r[j][i] = 0.f;
+        for (int i = 0; i < 4; ++i) r[j][i] = make_float2(0.f, 0.f);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum = fma2(r[j][i], r[j][i], sum);
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int c = (j * 8 + i) * nt + tid;
-        r[j][i] = 0.f;
-        if (c < a.H) {
-          r[j][i] = load1(a.x, a.x_type, xo + c);
-          if (a.res) r[j][i] = store1(a.res, a.res_type, ro + c, r[j][i] + load1(a.res, a.res_type, ro + c));
-        }
-      }
-  }
-
-  float s = 0.f;
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s = fmaf(r[j][i], r[j][i], s);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (lane == 0) part[warp] = s;
-  __syncthreads();
-  s = lane < (nt >> 5) ? part[lane] : 0.f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  const float root = 1.f / sqrtf(s / (float)a.H + a.eps);
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    float w[8];
-    if constexpr (VEC) {
-      if (a.w) widen(rw[j], a.w_type, w);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int c = (j * 8 + i) * nt + tid;
-        w[i] = a.w && c < a.H ? load1(a.w, a.w_type, c) : 0.f;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[j][i] = a.w ? r[j][i] * root * (w[i] + a.w_offset) : r[j][i] * root;
-  }
-
-  if (!fp8) {
+    const int here = t;
+    t += gridDim.x;
+    if (t < a.T) fetch(t);
+    if (FP8 && g.shift < 0 && tid == 0) row_max[turn] = 0;
+    const float root = rsqrtf(cta_sum(sum.x + sum.y, part[turn]) * g.inv_H + a.eps);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[j][i] = mul2(r[j][i], make_float2(root, root));
+      if (a.w) {
+        float2 w[4];
+        widen(rw[j], a.w_type, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[j][i] = mul2(r[j][i], add2(w[i], make_float2(a.w_offset, a.w_offset)));
+      }
+    }
+    char* y = static_cast<char*>(a.y) + here * a.y_stride * (FP8 ? 1 : a.y_type == MOE_T_F32 ? 4 : 2);
+    if constexpr (!FP8) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
         const int c = (j * nt + tid) * 8;
-        if (c < a.H) store8(a.y, a.y_type, yo + c, r[j]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int c = (j * 8 + i) * nt + tid;
-          if (c < a.H) store1(a.y, a.y_type, yo + c, r[j][i]);
-        }
+        if (c < a.H) store8(y, a.y_type, c, r[j]);
       }
-    }
-    return;
-  }
-
-  // e4m3. A group of up to 256 columns lies within a warp (G / 8 lanes, H a
-  // multiple of G): its maximum by shuffles alone. A wider one, or the whole row,
-  // through shared memory.
-  const bool in_warp = VEC && G <= 256 && a.group;
-  float scale[NV];
-  if constexpr (VEC) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (j * nt + tid) * 8;
-      float m = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(c < a.H ? r[j][i] : 0.f));
-      const int lanes = in_warp ? G >> 3 : 32;
-      for (int o = 1; o < lanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      scale[j] = m / 448.f;
-      // a warp's 256 columns are of one wide group
-      if (!in_warp && lane == 0 && c < a.H) atomicMax(&group_max[c / G], __float_as_int(m));
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int c = (j * 8 + i) * nt + tid;
-        if (c < a.H) atomicMax(&group_max[c / G], __float_as_int(fmaxf(0.f, fabsf(r[j][i]))));
-      }
-  }
-  if (!in_warp) {
-    __syncthreads();
-    for (int i = tid; i < n_groups; i += nt) a.scales[t * n_groups + i] = __int_as_float(group_max[i]) / 448.f;
-  }
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    if constexpr (VEC) {
-      const int c = (j * nt + tid) * 8;
-      if (c >= a.H) continue;
-      const float sc = in_warp ? scale[j] : __int_as_float(group_max[c / G]) / 448.f;
-      if (in_warp && c % G == 0) a.scales[t * n_groups + c / G] = sc;
-      const Quant q = quant_of(sc);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) r[j][i] = r[j][i] * q.up * q.inv;
-      store8(a.y, a.y_type, yo + c, r[j]);
     } else {
+      // The largest magnitude: a group of up to 256 columns lies within a warp; a wider
+      // one takes its warps' together through shared memory, as does a whole row.
+      float m[NV];
+      const int lanes = g.shift >= 0 && g.shift < 8 ? 1 << (g.shift - 3) : 32;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int c = (j * 8 + i) * nt + tid;
+      for (int j = 0; j < NV; ++j) {
+        m[j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m[j] = fmaxf(m[j], fmaxf(fabsf(r[j][i].x), fabsf(r[j][i].y)));
+        if ((j * nt + tid) * 8 >= a.H) m[j] = 0.f;
+        for (int o = 1; o < lanes; o <<= 1) m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], o));
+      }
+      float* scales = a.scales + (long long)here * g.n_groups;
+      if (g.shift < 0) {
+        float top = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) top = fmaxf(top, m[j]);
+        if (lane == 0) atomicMax(&row_max[turn], __float_as_int(top));
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < NV; ++j) m[j] = __int_as_float(row_max[turn]);
+        if (tid == 0) scales[0] = m[0] * (1.f / 448.f);
+      } else if (g.shift > 8) {
+        __syncthreads();  // the row before has been read
+        for (int i = tid; i < g.n_groups; i += nt) group_max[i] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const int c = (j * nt + tid) * 8;
+          if (lane == 0 && c < a.H) atomicMax(&group_max[c >> g.shift], __float_as_int(m[j]));
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const int c = (j * nt + tid) * 8;
+          if (c < a.H) m[j] = __int_as_float(group_max[c >> g.shift]);
+        }
+        for (int i = tid; i < g.n_groups; i += nt) scales[i] = __int_as_float(group_max[i]) * (1.f / 448.f);
+      }
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * nt + tid) * 8;
         if (c >= a.H) continue;
-        const Quant q = quant_of(__int_as_float(group_max[c / G]) / 448.f);
-        store1(a.y, a.y_type, yo + c, r[j][i] * q.up * q.inv);
+        const float scale = m[j] * (1.f / 448.f);
+        if (g.shift >= 0 && g.shift <= 8 && (c & ((1 << g.shift) - 1)) == 0) scales[c >> g.shift] = scale;
+        const Quant q = quant_of(scale);
+        if (q.up != 1.f)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) r[j][i] = mul2(r[j][i], make_float2(q.up, q.up));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[j][i] = mul2(r[j][i], make_float2(q.inv, q.inv));
+        store8(y, MOE_T_E4M3, c, r[j]);
       }
     }
+    if (t >= a.T) break;
   }
 }
 
+// Any alignment and row length, value by value: value j of a thread is column
+// j * threads + thread.
 template <int NV>
-cudaError_t launch_nv(const moe_norm_args& a, bool vec, int threads, size_t smem, cudaStream_t st) {
-  return vec ? launch_pdl(K_NORM, norm_kernel<NV, true>, dim3(a.T), threads, smem, st, a)
-             : launch_pdl(K_NORM, norm_kernel<NV, false>, dim3(a.T), threads, smem, st, a);
+__global__ void __launch_bounds__(NV == 8 ? 1024 : 512) norm_values_kernel(const __grid_constant__ Args g) {
+  __shared__ float part[32];
+  extern __shared__ int group_max[];
+  const moe_norm_args& a = g.a;
+  const int tid = threadIdx.x, nt = blockDim.x;
+  griddep_wait();
+  griddep_launch_dependents();
+  const long long t = blockIdx.x, xo = t * a.x_stride, ro = t * a.res_stride, yo = t * a.y_stride;
+  const bool fp8 = a.y_type == MOE_T_E4M3;
+  const auto group_of = [&](int c) { return g.shift < 0 ? 0 : c >> g.shift; };
+  if (fp8)
+    for (int i = tid; i < g.n_groups; i += nt) group_max[i] = 0;
+  float r[NV], s = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = j * nt + tid;
+    r[j] = 0.f;
+    if (c < a.H) {
+      r[j] = load1(a.x, a.x_type, xo + c);
+      if (a.res) r[j] = store1(a.res, a.res_type, ro + c, r[j] + load1(a.res, a.res_type, ro + c));
+    }
+    s = fmaf(r[j], r[j], s);
+  }
+  const float root = rsqrtf(cta_sum(s, part) * g.inv_H + a.eps);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = j * nt + tid;
+    if (c >= a.H) continue;
+    r[j] *= root;
+    if (a.w) r[j] *= load1(a.w, a.w_type, c) + a.w_offset;
+    if (fp8) atomicMax(&group_max[group_of(c)], __float_as_int(fmaxf(0.f, fabsf(r[j]))));
+    else store1(a.y, a.y_type, yo + c, r[j]);
+  }
+  if (!fp8) return;
+  __syncthreads();
+  for (int i = tid; i < g.n_groups; i += nt) a.scales[t * g.n_groups + i] = __int_as_float(group_max[i]) * (1.f / 448.f);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = j * nt + tid;
+    if (c >= a.H) continue;
+    const Quant q = quant_of(__int_as_float(group_max[group_of(c)]) * (1.f / 448.f));
+    store1(a.y, a.y_type, yo + c, r[j] * q.up * q.inv);
+  }
+}
+
+// A grid of what fits on the GPU at once, or a CTA per row where there are fewer.
+template <int NV, bool FP8, bool WIDE, int MAXT>
+cudaError_t launch_rows(const Args& g, int threads, size_t smem, cudaStream_t st) {
+  static std::atomic<int> fits{0};
+  int n = fits.load(std::memory_order_relaxed);
+  if (n == 0) {
+    int dev = 0, sms = 0, per_sm = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, norm_kernel<NV, FP8, WIDE, MAXT>, MAXT, 0);
+    if (e != cudaSuccess) return e;
+    n = sms * (per_sm > 0 ? per_sm : 1);
+    fits.store(n, std::memory_order_relaxed);
+  }
+  const int grid = g.a.T < n ? g.a.T : n;
+  return launch_pdl(K_NORM, norm_kernel<NV, FP8, WIDE, MAXT>, dim3(grid), threads, smem, st, g);
+}
+template <bool FP8, bool WIDE>
+cudaError_t launch_types(const Args& g, size_t smem, cudaStream_t st) {
+  const int per = g.a.H / 8;  // pieces of a row
+  const int nv = per <= 1024 ? 1 : 2, threads = ((per + nv - 1) / nv + 31) / 32 * 32;
+  if (nv == 2) return launch_rows<2, FP8, WIDE, 1024>(g, threads, smem, st);
+  if (threads <= 256) return launch_rows<1, FP8, WIDE, 256>(g, threads, smem, st);
+  if (threads <= 512) return launch_rows<1, FP8, WIDE, 512>(g, threads, smem, st);
+  return launch_rows<1, FP8, WIDE, 1024>(g, threads, smem, st);
 }
 
 }  // namespace
 
 cudaError_t launch_rms_norm(const moe_norm_args& a, bool vec, cudaStream_t st) {
-  const int per = (a.H + 7) / 8;  // groups of 8 values of a row
-  const int nv = per <= 1024 ? 1 : 4;
-  const int threads = ((per + nv - 1) / nv + 31) / 32 * 32;
-  const size_t smem = a.y_type == MOE_T_E4M3 ? (size_t)(a.H / (a.group ? a.group : a.H)) * 4 : 0;
-  return nv == 1 ? launch_nv<1>(a, vec, threads, smem, st) : launch_nv<4>(a, vec, threads, smem, st);
+  Args g;
+  g.a = a;
+  g.inv_H = 1.f / (float)a.H;
+  g.n_groups = a.group ? a.H / a.group : 1;
+  g.shift = -1;
+  if (a.group)
+    for (g.shift = 0; (1 << g.shift) < a.group;) ++g.shift;
+  const bool fp8 = a.y_type == MOE_T_E4M3;
+  const size_t smem = fp8 ? (size_t)g.n_groups * 4 : 0;
+  if (!vec) {
+    const int nv = a.H <= 8192 ? 8 : 32, threads = ((a.H + nv - 1) / nv + 31) / 32 * 32;
+    return nv == 8 ? launch_pdl(K_NORM, norm_values_kernel<8>, dim3(a.T), threads, smem, st, g)
+                   : launch_pdl(K_NORM, norm_values_kernel<32>, dim3(a.T), threads, smem, st, g);
+  }
+  const bool wide = a.x_type == MOE_T_F32 || (a.res && a.res_type == MOE_T_F32) || (a.w && a.w_type == MOE_T_F32);
+  if (fp8) return wide ? launch_types<true, true>(g, smem, st) : launch_types<true, false>(g, smem, st);
+  return wide ? launch_types<false, true>(g, smem, st) : launch_types<false, false>(g, smem, st);
 }
 
 }  // namespace block

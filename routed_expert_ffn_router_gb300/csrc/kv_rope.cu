@@ -21,6 +21,7 @@ namespace kv {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kAhead = 2;  // items of a thread that are fetched before the row is looked up
 
 struct Rope {
   int rot, interleaved;
@@ -68,6 +69,53 @@ __global__ void __launch_bounds__(kThreads) append_rope_kernel(Cache c, Rows r, 
   // pieces of a turned head and of a copied one
   const int vd = c.D >> 3, pieces = MODE == 0 ? vd - (p.rot >> 4) : MODE == 1 ? vd : c.D - half;
   const int n_q = p.Hq * pieces, n_k = n_q + c.Hkv * pieces, n_all = n_k + c.Hkv * vd;
+  // Item i of the row: a piece of a head of q (kind 0), k (1) or v (2): the values
+  // from d0 on, and their partners from d1 on (-1: there are none).
+  struct Item {
+    int kind, h, d0, d1;
+    const uint16_t* src;
+  };
+  const auto item = [&](int i) {
+    Item x;
+    if (i >= n_k) {
+      x.kind = 2;
+      x.h = (i - n_k) / vd;
+      x.d0 = (i - n_k - x.h * vd) * 8;
+      x.d1 = -1;
+      x.src = v + (long long)t * stride + (long long)x.h * c.D;
+      return x;
+    }
+    x.kind = i >= n_q;
+    const int j = x.kind ? i - n_q : i;
+    x.h = j / pieces;
+    const int e = j - x.h * pieces;
+    x.src = x.kind ? k + (long long)t * stride + (long long)x.h * c.D : p.q + (long long)t * p.q_stride + (long long)x.h * c.D;
+    if (MODE == 0) {
+      const int n8 = p.rot >> 4;
+      x.d0 = e < n8 ? e * 8 : p.rot + (e - n8) * 8;
+      x.d1 = e < n8 ? half + e * 8 : -1;
+    } else if (MODE == 1) {
+      x.d0 = e * 8;
+      x.d1 = -1;
+    } else {
+      x.d0 = e >= half ? p.rot + e - half : p.interleaved ? 2 * e : e;
+      x.d1 = e >= half ? -1 : p.interleaved ? 2 * e + 1 : e + half;
+    }
+    return x;
+  };
+  // the thread's first items: on their way while the row is looked up
+  uint4 first[kAhead][2];
+  if constexpr (MODE != 2) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = tid + u * kThreads;
+      if (i < n_all) {
+        const Item x = item(i);
+        first[u][0] = *reinterpret_cast<const uint4*>(x.src + x.d0);
+        if (MODE == 0 && x.d1 >= 0) first[u][1] = *reinterpret_cast<const uint4*>(x.src + x.d1);
+      }
+    }
+  }
   const Seq s = load_seq(c, r, seq_of_row(r, t), tid == 0 ? status : nullptr);
   const bool inside = t >= s.row0 && t < s.row0 + s.n;
   if (!inside) return;  // behind the last sequence
@@ -90,49 +138,40 @@ __global__ void __launch_bounds__(kThreads) append_rope_kernel(Cache c, Rows r, 
   __syncthreads();
   const long long base = (long long)(pg < 0 ? 0 : pg) * c.Hkv * c.page + (tok < 0 ? 0 : tok % c.page);
   const int last = tok < 0 ? n_q : pg < 0 ? n_q : n_all;  // without a page keys and values go nowhere
-  for (int i = tid; i < last; i += kThreads) {
-    if (i >= n_k) {  // values
-      const int j = i - n_k, h = j / vd, d = (j - h * vd) * 8;
-      *reinterpret_cast<uint4*>(c.v + (base + (long long)h * c.page) * c.D + d) =
-          *reinterpret_cast<const uint4*>(v + (long long)t * stride + h * c.D + d);
-      continue;
-    }
-    const bool is_q = i < n_q;
-    const int j = is_q ? i : i - n_q, h = j / pieces, e = j - h * pieces;
-    const uint16_t* src = is_q ? p.q + (long long)t * p.q_stride + (long long)h * c.D : k + (long long)t * stride + (long long)h * c.D;
-    uint16_t* dst = is_q ? p.q_out + (long long)t * p.q_out_stride + (long long)h * c.D
-                         : c.k + (base + (long long)h * c.page) * c.D;
-    if constexpr (MODE == 0) {
-      const int n8 = p.rot >> 4;
-      if (e < n8) {
-        uint4 x = *reinterpret_cast<const uint4*>(src + e * 8), y = *reinterpret_cast<const uint4*>(src + half + e * 8);
-        if (tok >= 0) turn8<F16>(x, y, cs + e * 8);
-        *reinterpret_cast<uint4*>(dst + e * 8) = x;
-        *reinterpret_cast<uint4*>(dst + half + e * 8) = y;
-      } else {
-        const int d = p.rot + (e - n8) * 8;
-        *reinterpret_cast<uint4*>(dst + d) = *reinterpret_cast<const uint4*>(src + d);
+  const auto work = [&](int i, int u) {  // u: which of `first` holds it, -1 none
+    const Item x = item(i);
+    uint16_t* dst = x.kind == 0 ? p.q_out + (long long)t * p.q_out_stride + (long long)x.h * c.D
+                                : (x.kind == 1 ? c.k : c.v) + (base + (long long)x.h * c.page) * c.D;
+    if constexpr (MODE != 2) {
+      uint4 v0 = u >= 0 ? first[u < 0 ? 0 : u][0] : *reinterpret_cast<const uint4*>(x.src + x.d0), v1;
+      if (MODE == 0 && x.d1 >= 0) {
+        v1 = u >= 0 ? first[u < 0 ? 0 : u][1] : *reinterpret_cast<const uint4*>(x.src + x.d1);
+        if (tok >= 0) turn8<F16>(v0, v1, cs + x.d0);
+        *reinterpret_cast<uint4*>(dst + x.d1) = v1;
       }
-    } else if constexpr (MODE == 1) {
-      uint4 x = *reinterpret_cast<const uint4*>(src + e * 8);
-      if (tok >= 0 && e * 8 < p.rot) turn4<F16>(x, cs + e * 4);
-      *reinterpret_cast<uint4*>(dst + e * 8) = x;
+      if (MODE == 1 && x.kind < 2 && tok >= 0 && x.d0 < p.rot) turn4<F16>(v0, cs + (x.d0 >> 1));
+      *reinterpret_cast<uint4*>(dst + x.d0) = v0;
+    } else if (x.kind == 2) {
+      *reinterpret_cast<uint4*>(dst + x.d0) = *reinterpret_cast<const uint4*>(x.src + x.d0);
+    } else if (x.d1 >= 0) {
+      uint32_t xy = (uint32_t)x.src[x.d0] | (uint32_t)x.src[x.d1] << 16;
+      if (tok >= 0) {
+        const float2 f = unpack2<F16>(xy), w = cs[p.interleaved ? x.d0 >> 1 : x.d0];
+        xy = pack2<F16>(f.x * w.x - f.y * w.y, f.y * w.x + f.x * w.y);
+      }
+      dst[x.d0] = (uint16_t)xy;
+      dst[x.d1] = (uint16_t)(xy >> 16);
     } else {
-      if (e < half) {
-        const int d0 = p.interleaved ? 2 * e : e, d1 = p.interleaved ? 2 * e + 1 : e + half;
-        const uint16_t a = src[d0], b = src[d1];
-        uint32_t xy = (uint32_t)a | (uint32_t)b << 16;
-        if (tok >= 0) {
-          const float2 u = unpack2<F16>(xy), w = cs[e];
-          xy = pack2<F16>(u.x * w.x - u.y * w.y, u.y * w.x + u.x * w.y);
-        }
-        dst[d0] = (uint16_t)xy;
-        dst[d1] = (uint16_t)(xy >> 16);
-      } else {
-        const int d = p.rot + e - half;
-        dst[d] = src[d];
-      }
+      dst[x.d0] = x.src[x.d0];
     }
+  };
+  if constexpr (MODE != 2) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (tid + u * kThreads < last) work(tid + u * kThreads, u);
+    for (int i = tid + kAhead * kThreads; i < last; i += kThreads) work(i, -1);
+  } else {
+    for (int i = tid; i < last; i += kThreads) work(i, -1);
   }
 }
 

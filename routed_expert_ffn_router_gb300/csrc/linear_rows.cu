@@ -27,7 +27,7 @@ __device__ __forceinline__ float one(const uint16_t* p) {
 
 // DK: 64, 128 or 256, at least the head size.
 template <bool F16, int DK>
-__global__ void __launch_bounds__(kThreads) linear_rows_kernel(Linear a, kv::Rows r) {
+__global__ void __launch_bounds__(kThreads, DK <= 128 ? 8 : 4) linear_rows_kernel(Linear a, kv::Rows r) {
   constexpr int NI = DK / 16;
   __shared__ float qs[kRows][DK], ks[kRows][DK], vs[kRows][kCols], po[kRows][4][kCols];
   __shared__ float2 decay[kRows];
