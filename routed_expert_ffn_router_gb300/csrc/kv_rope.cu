@@ -9,10 +9,15 @@
 // off by 2^-24 p: 0.008 radians at 131,072.) A row's rot / 2 sines and cosines
 // are computed once and serve all its heads.
 //
-// One CTA per row. A thread turns 8 pairs of a head (two 16-byte loads, two
-// stores) and reads both halves before it writes them, so q_out may be q. The
-// first loads are under way while the row's sequence, length and page are looked
-// up, which is a chain of loads that a short call's time consists of.
+// One CTA per row. What a short call's time consists of is the chain of loads that
+// finds the row's sequence, length and page: three of them, by a warp whose lanes look
+// at all sequences at once; each thread's first pieces are under way meanwhile. A
+// thread turns 8 pairs of a head at a time (two 16-byte loads, two stores) and reads
+// both halves before it writes them, so q_out may be q. Four rows per CTA, which go
+// through the chain together, were slower (11.4 us for 2,048 rows of 32 / 8 heads
+// against 11.0): their larger CTAs fill the GPU less evenly.
+#include <climits>
+
 #include "kv_common.cuh"
 
 namespace moe {
@@ -20,8 +25,8 @@ namespace kv {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kAhead = 2;  // items of a thread that are fetched before the row is looked up
+constexpr int kThreads = 128;
+constexpr int kBatch = 4;  // pieces of a thread under way together
 
 struct Rope {
   int rot, interleaved;
@@ -34,145 +39,187 @@ struct Rope {
   long long q_stride, q_out_stride;
 };
 
+// Sines and cosines lie in shared memory by pairs of pairs: those of pairs 2 j and
+// 2 j + 1 of all pieces side by side, so that a warp's 16-byte reads meet no bank
+// twice (piece after piece they took four times as long as all the rest).
+// cs: the piece's first two pairs, n: pieces of a head.
 template <bool F16>
-__device__ __forceinline__ void turn8(uint4& x, uint4& y, const float2* cs) {  // pairs (x[i], y[i])
+__device__ __forceinline__ void turn8(uint4& x, uint4& y, const float4* cs, int n) {  // pairs (x[i], y[i])
   uint32_t* a = reinterpret_cast<uint32_t*>(&x);
   uint32_t* b = reinterpret_cast<uint32_t*>(&y);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 u = unpack2<F16>(a[i]), v = unpack2<F16>(b[i]), c0 = cs[2 * i], c1 = cs[2 * i + 1];
-    a[i] = pack2<F16>(u.x * c0.x - v.x * c0.y, u.y * c1.x - v.y * c1.y);
-    b[i] = pack2<F16>(v.x * c0.x + u.x * c0.y, v.y * c1.x + u.y * c1.y);
+    const float2 u = unpack2<F16>(a[i]), v = unpack2<F16>(b[i]);
+    const float4 w = cs[i * n];  // cos, sin, cos, sin
+    a[i] = pack2<F16>(u.x * w.x - v.x * w.y, u.y * w.z - v.y * w.w);
+    b[i] = pack2<F16>(v.x * w.x + u.x * w.y, v.y * w.z + u.y * w.w);
   }
 }
 template <bool F16>
-__device__ __forceinline__ void turn4(uint4& x, const float2* cs) {  // pairs (x[2 i], x[2 i + 1])
+__device__ __forceinline__ void turn4(uint4& x, const float4* cs, int n) {  // pairs (x[2 i], x[2 i + 1])
   uint32_t* a = reinterpret_cast<uint32_t*>(&x);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 u = unpack2<F16>(a[i]), c = cs[i];
-    a[i] = pack2<F16>(u.x * c.x - u.y * c.y, u.y * c.x + u.x * c.y);
+  for (int i = 0; i < 2; ++i) {
+    const float2 u = unpack2<F16>(a[2 * i]), v = unpack2<F16>(a[2 * i + 1]);
+    const float4 w = cs[i * n];
+    a[2 * i] = pack2<F16>(u.x * w.x - u.y * w.y, u.y * w.x + u.x * w.y);
+    a[2 * i + 1] = pack2<F16>(v.x * w.z - v.y * w.w, v.y * w.z + v.x * w.w);
   }
+}
+
+// A thread's way through the pieces of its row's heads: piece e of head h, then the
+// piece `step` further.
+struct Cursor {
+  int h, e, dh, de, per;
+  __device__ Cursor(int at, int step, int per_head) : h(at / per_head), dh(step / per_head), per(per_head) {
+    e = at - h * per_head;
+    de = step - dh * per_head;
+  }
+  __device__ void next() {
+    h += dh;
+    e += de;
+    if (e >= per) {
+      e -= per;
+      ++h;
+    }
+  }
+};
+
+// The sequence of row t, by a whole warp. Up to 32 sequences: every lane looks at one.
+__device__ __forceinline__ Seq find_seq(const Cache& c, const Rows& r, int t, int32_t* status) {
+  const int lane = threadIdx.x & 31;
+  if (!r.row_start || r.B > 32) return load_seq(c, r, seq_of_row(r, t), lane == 0 ? status : nullptr);
+  const Seq mine = load_seq(c, r, min(lane, r.B - 1), nullptr);
+  const int first = lane < r.B ? r.row_start[lane] : INT_MAX;
+  // the last sequence that starts at or before the row
+  const int b = max(0, __popc(__ballot_sync(0xffffffffu, first <= t)) - 1);
+  Seq s;
+  s.slot = __shfl_sync(0xffffffffu, mine.slot, b);
+  s.len = __shfl_sync(0xffffffffu, mine.len, b);
+  s.row0 = __shfl_sync(0xffffffffu, mine.row0, b);
+  s.n = __shfl_sync(0xffffffffu, mine.n, b);
+  if (lane == b && (mine.slot < 0 || c.lens[mine.slot] > (long long)c.max_pages * c.page)) atomicOr(status, DEV_BAD_SLOT);
+  return s;
 }
 
 // MODE 0: halves, 16-byte pieces of 8 pairs (rot a multiple of 16). 1:
 // interleaved, 16-byte pieces of 4 pairs (rot a multiple of 8). 2: single values
 // (any rot, either layout).
 template <bool F16, int MODE>
-__global__ void __launch_bounds__(kThreads) append_rope_kernel(Cache c, Rows r, Rope p, const uint16_t* k, const uint16_t* v,
+__global__ void __launch_bounds__(kThreads, 8) append_rope_kernel(Cache c, Rows r, Rope p, const uint16_t* k, const uint16_t* v,
                                                                long long stride, int32_t* status) {
-  __shared__ __align__(16) float2 cs[128];
-  const int t = blockIdx.x, tid = threadIdx.x;
+  __shared__ __align__(16) float2 cs[kThreads];
+  __shared__ int s_tok, s_page, s_pos;  // token (-1: none, -2: no row), page (-1: none), position
+  const int at = threadIdx.x;
+  const long long t = blockIdx.x;
   griddep_wait();
   griddep_launch_dependents();
-  const int half = p.rot >> 1;
-  // pieces of a turned head and of a copied one
-  const int vd = c.D >> 3, pieces = MODE == 0 ? vd - (p.rot >> 4) : MODE == 1 ? vd : c.D - half;
-  const int n_q = p.Hq * pieces, n_k = n_q + c.Hkv * pieces, n_all = n_k + c.Hkv * vd;
-  // Item i of the row: a piece of a head of q (kind 0), k (1) or v (2): the values
-  // from d0 on, and their partners from d1 on (-1: there are none).
-  struct Item {
-    int kind, h, d0, d1;
-    const uint16_t* src;
-  };
-  const auto item = [&](int i) {
-    Item x;
-    if (i >= n_k) {
-      x.kind = 2;
-      x.h = (i - n_k) / vd;
-      x.d0 = (i - n_k - x.h * vd) * 8;
-      x.d1 = -1;
-      x.src = v + (long long)t * stride + (long long)x.h * c.D;
-      return x;
-    }
-    x.kind = i >= n_q;
-    const int j = x.kind ? i - n_q : i;
-    x.h = j / pieces;
-    const int e = j - x.h * pieces;
-    x.src = x.kind ? k + (long long)t * stride + (long long)x.h * c.D : p.q + (long long)t * p.q_stride + (long long)x.h * c.D;
-    if (MODE == 0) {
-      const int n8 = p.rot >> 4;
-      x.d0 = e < n8 ? e * 8 : p.rot + (e - n8) * 8;
-      x.d1 = e < n8 ? half + e * 8 : -1;
-    } else if (MODE == 1) {
-      x.d0 = e * 8;
-      x.d1 = -1;
-    } else {
-      x.d0 = e >= half ? p.rot + e - half : p.interleaved ? 2 * e : e;
-      x.d1 = e >= half ? -1 : p.interleaved ? 2 * e + 1 : e + half;
-    }
-    return x;
-  };
-  // the thread's first items: on their way while the row is looked up
-  uint4 first[kAhead][2];
-  if constexpr (MODE != 2) {
+  const int half = p.rot >> 1, vd = c.D >> 3;
+  // pieces of a turned head (q's heads, then k's) and of a copied one
+  const int pieces = MODE == 0 ? vd - (p.rot >> 4) : MODE == 1 ? vd : c.D - half;
+  const int n_turn = (p.Hq + c.Hkv) * pieces, n_copy = c.Hkv * vd;
+  const uint16_t* q_row = p.q + t * p.q_stride;
+  const uint16_t* k_row = k + t * stride;
+  const auto source = [&](const Cursor& x) { return x.h < p.Hq ? q_row + x.h * c.D : k_row + (x.h - p.Hq) * c.D; };
+  // where a piece begins, and its partners (-1: it has none and is copied)
+  const auto begin = [&](int e) { return MODE == 0 ? (e < (p.rot >> 4) ? e * 8 : half + e * 8) : e * 8; };
+  const auto partner = [&](int e) { return MODE == 0 && e < (p.rot >> 4) ? half + e * 8 : -1; };
+  uint4 x[kBatch], y[kBatch];
+  const auto fetch = [&](Cursor cur, int i) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int i = tid + u * kThreads;
-      if (i < n_all) {
-        const Item x = item(i);
-        first[u][0] = *reinterpret_cast<const uint4*>(x.src + x.d0);
-        if (MODE == 0 && x.d1 >= 0) first[u][1] = *reinterpret_cast<const uint4*>(x.src + x.d1);
+    for (int u = 0; u < kBatch; ++u) {
+      if (i + u * kThreads < n_turn) {
+        const uint16_t* src = source(cur);
+        x[u] = *reinterpret_cast<const uint4*>(src + begin(cur.e));
+        if (MODE == 0 && partner(cur.e) >= 0) y[u] = *reinterpret_cast<const uint4*>(src + partner(cur.e));
       }
+      cur.next();
     }
-  }
-  const Seq s = load_seq(c, r, seq_of_row(r, t), tid == 0 ? status : nullptr);
-  const bool inside = t >= s.row0 && t < s.row0 + s.n;
-  if (!inside) return;  // behind the last sequence
-  const int tok = s.slot < 0 ? -1 : s.len - s.n + (t - s.row0);
-  int pg = -1;
-  if (tok >= 0) {
-    pg = c.table[(long long)s.slot * c.max_pages + tok / c.page];
-    if (pg < 0 || pg >= c.n_pages) {
-      if (tid == 0) atomicOr(status, DEV_BAD_SLOT);
-      pg = -1;
-    }
-    const long long pos = p.positions ? p.positions[t] : tok;
-    for (int i = tid; i < half; i += kThreads) {
-      const unsigned long long turns = (unsigned long long)pos * p.freq[i];
-      float sn, cn;
-      sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &sn, &cn);
-      cs[i] = make_float2(cn * p.gain, sn * p.gain);
+  };
+  Cursor cur(at, kThreads, pieces);
+  if (MODE != 2) fetch(cur, at);
+  const unsigned long long freq = at < half ? p.freq[at] : 0;
+
+  if (at < 32) {
+    const Seq s = find_seq(c, r, (int)t, status);
+    if (at == 0) {
+      int tok = -2, pg = -1, pos = 0;
+      if (t >= s.row0 && t < s.row0 + s.n) {
+        tok = s.slot < 0 ? -1 : max(-1, s.len - s.n + ((int)t - s.row0));
+        if (tok >= 0) {
+          pg = c.table[(long long)s.slot * c.max_pages + tok / c.page];
+          if (pg < 0 || pg >= c.n_pages) {
+            atomicOr(status, DEV_BAD_SLOT);
+            pg = -1;
+          }
+          pos = p.positions ? p.positions[t] : tok;
+        }
+      }
+      s_tok = tok;
+      s_page = pg;
+      s_pos = pos;
     }
   }
   __syncthreads();
-  const long long base = (long long)(pg < 0 ? 0 : pg) * c.Hkv * c.page + (tok < 0 ? 0 : tok % c.page);
-  const int last = tok < 0 ? n_q : pg < 0 ? n_q : n_all;  // without a page keys and values go nowhere
-  const auto work = [&](int i, int u) {  // u: which of `first` holds it, -1 none
-    const Item x = item(i);
-    uint16_t* dst = x.kind == 0 ? p.q_out + (long long)t * p.q_out_stride + (long long)x.h * c.D
-                                : (x.kind == 1 ? c.k : c.v) + (base + (long long)x.h * c.page) * c.D;
-    if constexpr (MODE != 2) {
-      uint4 v0 = u >= 0 ? first[u < 0 ? 0 : u][0] : *reinterpret_cast<const uint4*>(x.src + x.d0), v1;
-      if (MODE == 0 && x.d1 >= 0) {
-        v1 = u >= 0 ? first[u < 0 ? 0 : u][1] : *reinterpret_cast<const uint4*>(x.src + x.d1);
-        if (tok >= 0) turn8<F16>(v0, v1, cs + x.d0);
-        *reinterpret_cast<uint4*>(dst + x.d1) = v1;
-      }
-      if (MODE == 1 && x.kind < 2 && tok >= 0 && x.d0 < p.rot) turn4<F16>(v0, cs + (x.d0 >> 1));
-      *reinterpret_cast<uint4*>(dst + x.d0) = v0;
-    } else if (x.kind == 2) {
-      *reinterpret_cast<uint4*>(dst + x.d0) = *reinterpret_cast<const uint4*>(x.src + x.d0);
-    } else if (x.d1 >= 0) {
-      uint32_t xy = (uint32_t)x.src[x.d0] | (uint32_t)x.src[x.d1] << 16;
-      if (tok >= 0) {
-        const float2 f = unpack2<F16>(xy), w = cs[p.interleaved ? x.d0 >> 1 : x.d0];
-        xy = pack2<F16>(f.x * w.x - f.y * w.y, f.y * w.x + f.x * w.y);
-      }
-      dst[x.d0] = (uint16_t)xy;
-      dst[x.d1] = (uint16_t)(xy >> 16);
-    } else {
-      dst[x.d0] = x.src[x.d0];
-    }
-  };
-  if constexpr (MODE != 2) {
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-      if (tid + u * kThreads < last) work(tid + u * kThreads, u);
-    for (int i = tid + kAhead * kThreads; i < last; i += kThreads) work(i, -1);
-  } else {
-    for (int i = tid; i < last; i += kThreads) work(i, -1);
+  const int tok = s_tok, pg = s_page;
+  if (tok >= 0 && at < half) {
+    const unsigned long long turns = (unsigned long long)(long long)s_pos * freq;
+    float sn, cn;
+    sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &sn, &cn);
+    const int per = MODE == 0 ? 8 : 4;  // pairs of a piece
+    const int to = MODE == 2 ? at : (((at % per) >> 1) * (half / per) + at / per) * 2 + (at & 1);
+    cs[to] = make_float2(cn * p.gain, sn * p.gain);
   }
+  __syncthreads();
+  if (tok == -2) return;  // behind the last sequence
+  const float4* cs4 = reinterpret_cast<const float4*>(cs);
+  const long long base = (long long)max(pg, 0) * c.Hkv * c.page + (tok < 0 ? 0 : tok % c.page);
+  const auto target = [&](int h) {
+    return h < p.Hq ? p.q_out + t * p.q_out_stride + h * c.D : c.k + (base + (long long)(h - p.Hq) * c.page) * c.D;
+  };
+  const int last = pg < 0 ? p.Hq * pieces : n_turn;  // without a page keys and values go nowhere
+  if constexpr (MODE != 2) {
+    for (int i = at; i < last; i += kBatch * kThreads) {
+      if (i != at) fetch(cur, i);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        if (i + u * kThreads < last) {
+          uint16_t* dst = target(cur.h);
+          const int d0 = begin(cur.e), d1 = partner(cur.e);
+          if (MODE == 0 && d1 >= 0) {
+            if (tok >= 0) turn8<F16>(x[u], y[u], cs4 + cur.e, half >> 3);
+            *reinterpret_cast<uint4*>(dst + d1) = y[u];
+          }
+          if (MODE == 1 && tok >= 0 && d0 < p.rot) turn4<F16>(x[u], cs4 + cur.e, half >> 2);
+          *reinterpret_cast<uint4*>(dst + d0) = x[u];
+        }
+        cur.next();
+      }
+    }
+  } else {
+    for (int i = at; i < last; i += kThreads, cur.next()) {
+      const uint16_t* src = source(cur);
+      uint16_t* dst = target(cur.h);
+      if (cur.e < half) {
+        const int d0 = p.interleaved ? 2 * cur.e : cur.e, d1 = p.interleaved ? 2 * cur.e + 1 : cur.e + half;
+        uint32_t xy = (uint32_t)src[d0] | (uint32_t)src[d1] << 16;
+        if (tok >= 0) {
+          const float2 f = unpack2<F16>(xy), w = cs[cur.e];
+          xy = pack2<F16>(f.x * w.x - f.y * w.y, f.y * w.x + f.x * w.y);
+        }
+        dst[d0] = (uint16_t)xy;
+        dst[d1] = (uint16_t)(xy >> 16);
+      } else {
+        const int d = half + cur.e;
+        dst[d] = src[d];
+      }
+    }
+  }
+  if (pg < 0) return;
+  Cursor copy(at, kThreads, vd);
+  for (int i = at; i < n_copy; i += kThreads, copy.next())
+    *reinterpret_cast<uint4*>(c.v + (base + (long long)copy.h * c.page) * c.D + copy.e * 8) =
+        *reinterpret_cast<const uint4*>(v + t * stride + copy.h * c.D + copy.e * 8);
 }
 
 }  // namespace
