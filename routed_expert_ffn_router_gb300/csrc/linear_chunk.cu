@@ -4,21 +4,24 @@
 // Blocks of 128 tokens. With G_i the sum of the logarithms of the decays of a
 // block's tokens up to i, G the sum of all of them, and S the state before it:
 //   o_i = scale (e^G_i q_i S + sum_{j <= i} e^(G_i - G_j) (q_i . k_j) v_j)
-//   S'  = e^G S + sum_j k_j (e^(G - G_j) v_j)^T
-// Four products, accumulators in tensor memory:
-//   A = Q K^T    X = Q S    U = K^T V'    Y = (A o D) V
-// V' = e^(G - G_j) v_j, D_ij = e^(G_i - G_j) for j <= i, else 0; A o D goes back to
-// tensor memory as the first operand of Y. U does not depend on S, so the blocks of
-// a sequence wait for one another only in S' = e^G S + U, in registers.
+//   S'  = e^G S + sum_j (e^(G - G_j) k_j) v_j^T
+// Three products, accumulators in tensor memory:
+//   A = Q K^T      U = K'^T V      O = [A o D | Q'] [V ; S]
+// K' = e^(G - G_j) k_j, Q' = e^G_i q_i, D_ij = e^(G_i - G_j) for j <= i, else 0. K'^T,
+// A o D and Q' are first operands in tensor memory, which leaves shared memory to the
+// tiles that TMA brings, two of K and of V. U does not depend on S, so the blocks of a
+// sequence wait for one another only in S' = e^G S + U, in registers.
 //
-// Rounding. The state is fp32 throughout: V' enters as two values of the type (its
-// rounding and the rest, 2^-17 of it for bf16), and U is a fresh sum each block. S
-// and A o D, which only o sees, are rounded once to the type (half a step each, as o
-// itself is). In fp16, whose range is narrow and whose step is fixed below 2^-14, V'
-// and S are scaled by a power of two per block and a row of A o D by one of its own,
-// which bring the largest magnitude to 2^13 and are undone in fp32: the smallest
-// values are then off by up to 2^-38 of the largest. Sums of logarithms are taken in fp64 and handed on as two fp32
-// values, so that G_i - G_j is right next to large |G|.
+// Rounding. The state is fp32 throughout: in bf16 K' enters U as three values that
+// add up to its fp32 exactly, in fp16 as two (its rounding and the rest, 2^-22 of
+// it), and U is a fresh sum each block. (Two values of bf16 left the state off by
+// 2.4e-6.) S, Q' and A o D, which only o sees, are rounded once to the type (half a
+// step each, as o itself is). In fp16, whose range is narrow and whose step is fixed
+// below 2^-14, K' and S are scaled by a power of two per block and a row of A o D and
+// Q' by one of its own, which bring the largest magnitude to 2^13 and are undone in
+// fp32: the smallest values are then off by up to 2^-38 of the largest. Sums of
+// logarithms are taken in fp64 and handed on as two fp32 values, so that G_i - G_j is
+// right next to large |G|.
 //
 // Work. An item is a sequence and a v head, by a cluster of 1 to 8 CTAs that have
 // consecutive parts of its blocks. With more than one, each first sums up its own
@@ -27,8 +30,9 @@
 // goes through its part. So a long prompt of few heads fills the GPU in one launch
 // and without a workspace. Items are started longest first.
 //
-// Warps. 0-3: A o D; 4-7: the state (a thread is a row of it); 8-11: V' and the
-// output; 12: issues the products; 13: TMA; 14: decays, two blocks ahead.
+// Warps. 0-3: A o D; 4-7: the state (a thread is a row of it); 8-11: Q' and the
+// output; 12-15: K'; 16: issues the products; 17: TMA; 18: decays, two blocks ahead;
+// 19: zeroes V behind a sequence's end.
 #include <cuda.h>
 
 #include <atomic>
@@ -48,13 +52,13 @@ using namespace tc;
 namespace {
 
 constexpr int kBlk = 128;               // tokens per block
-constexpr int kThreads = 512;
-constexpr int kRegsScore = 112, kRegsState = 184, kRegsOut = 104, kRegsRest = 112;  // at most 4 x 128 together
+constexpr int kThreads = 640;
+constexpr int kRegsScore = 80, kRegsState = 176, kRegsOut = 104, kRegsKey = 64, kRegsRest = 56;  // at most 5 x 96 together
 constexpr uint32_t kTries = 1u << 22;   // of a wait, each up to a microsecond long
 constexpr int kHalf = kBlk * 128;       // bytes of 128 rows of 64 values
 constexpr int kTile = 2 * kHalf;
 constexpr int kPitch = 144;             // bytes per row of a warp's output buffer (64 values and a pad)
-constexpr int kSmem = 1024 + 6 * kTile + 4 * 32 * kPitch;  // Q, K, V, V' twice, S; outputs
+constexpr int kSmem = 1024 + 6 * kTile + 4 * 32 * kPitch;  // Q, two of K and of V, S; outputs
 constexpr int kSortB = 512;             // sequences that are put in order of their length
 constexpr int kMostParts = 8;
 constexpr int kAhead = 2;               // blocks that are fetched into L2 ahead
@@ -69,12 +73,22 @@ struct ChunkArgs {
 // What the decays of a block come to.
 struct Decays {
   float gh[kBlk], gl[kBlk];  // -G_j / ln 2 as two values
-  float v[kBlk];      // e^(G - G_j); 0 behind the last token
-  float q[kBlk];      // scale e^G_i
+  float k[kBlk];      // e^(G - G_j)
+  float q[kBlk];      // e^G_i
   float2 all;         // e^G (decay_of)
   float pad[2];
 };
 
+__device__ __forceinline__ void ldmatrix4_t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+// 16 lanes x 8 columns: r[0] column t % 4 of lane t / 4, r[1] of lane 8 + t / 4,
+// r[2] and r[3] the next four columns.
+__device__ __forceinline__ void tc_st_16x8(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
 __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
@@ -126,39 +140,47 @@ __device__ __forceinline__ int lift_of(float m) {
 template <bool F16, int DK, int DV>
 __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_constant__ ChunkArgs p) {
   constexpr int HK = DK / 64, HV = DV / 64;
+  constexpr int kTerms = F16 ? 2 : 3;  // values that stand for a K'
   extern __shared__ __align__(1024) uint8_t smem_linear[];
   __shared__ __align__(16) Decays s_dec[2];
-  __shared__ __align__(8) uint64_t s_bar[20];
-  __shared__ float s_row[2][kBlk];    // fp16, by block: what a row of A o D was scaled by, undone
-  __shared__ float s_state_up[2], s_v_up[2];  // the same of S, of V'
+  __shared__ __align__(8) uint64_t s_bar[32];
+  __shared__ int s_row[2][F16 ? kBlk : 1];   // fp16, by block: log2 of what a row of A o D and Q' is scaled by
+  __shared__ float s_qmax[F16 ? kBlk : 1];   // largest magnitude of a row of Q'
+  __shared__ int s_state_up[2];              // log2 of what S is scaled by
+  __shared__ float s_key_down[2];            // what undoes the scale of K'
   __shared__ float s_max[4];
-  __shared__ uint32_t s_vmax[4];
-  __shared__ float s_part;            // e^(sum of the part's logarithms)
+  __shared__ uint32_t s_kmax[4];
+  __shared__ float s_part;                   // e^(sum of the part's logarithms)
   __shared__ uint32_t s_tmem;
   __shared__ int s_b;
 
   const Linear& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sq = (smem_u32(smem_linear) + 1023u) & ~1023u;
-  const uint32_t sk = sq + kTile, sv = sk + kTile, svh = sv + kTile, svl = svh + kTile, ss = svl + kTile, so = ss + kTile;
-  const uint32_t q_full = smem_u32(s_bar), k_full = q_full + 8, v_full = q_full + 16, q_empty = q_full + 24;
-  const uint32_t k_empty = q_full + 32, v_empty = q_full + 40, a_full = q_full + 48, p_full = q_full + 56;
-  const uint32_t s_ready = q_full + 64, w_ready = q_full + 72, u_full = q_full + 80, u_free = q_full + 88;
-  const uint32_t o_full = q_full + 96, o_free = q_full + 104, g_full = q_full + 112, g_empty = q_full + 128;
-  const uint32_t drained = q_full + 144;
+  const uint32_t sk = sq + kTile, sv = sk + 2 * kTile, ss = sv + 2 * kTile, so = ss + kTile;
+  const uint32_t meet_at = sk;  // where the parts' sums lie between the passes (K's two tiles)
+  const uint32_t bar = smem_u32(s_bar);
+  // (by block parity where there are two)
+  const uint32_t q_full = bar, q_empty = bar + 8, k_full = bar + 16, k_empty = bar + 32, v_full = bar + 48, v_ready = bar + 64;
+  const uint32_t v_empty = bar + 80, a_full = bar + 96, a_read = bar + 104, p_ready = bar + 112, qp_ready = bar + 120;
+  const uint32_t s_ready = bar + 128, kt_full = bar + 136, kt_empty = bar + 152, u_full = bar + 168, u_free = bar + 176;
+  const uint32_t o_full = bar + 184, o_free = bar + 192, g_full = bar + 200, g_empty = bar + 216, q_known = bar + 232;
+  const uint32_t drained = bar + 240;
   if (tid == 0) {
-    mbar_init(q_full, 1); mbar_init(k_full, 1); mbar_init(v_full, 1);
-    mbar_init(q_empty, 1); mbar_init(k_empty, 1); mbar_init(v_empty, 1);
-    mbar_init(a_full, 1); mbar_init(p_full, 4);
-    mbar_init(s_ready, 4); mbar_init(w_ready, 4);
-    mbar_init(u_full, 1); mbar_init(u_free, 4);
-    mbar_init(o_full, 1); mbar_init(o_free, 4);
-    mbar_init(g_full, 1); mbar_init(g_full + 8, 1);
-    mbar_init(g_empty, 12); mbar_init(g_empty + 8, 12);
+    mbar_init(q_full, 1); mbar_init(q_empty, 5);
+    for (int i = 0; i < 16; i += 8) {
+      mbar_init(k_full + i, 1); mbar_init(k_empty + i, 5);
+      mbar_init(v_full + i, 1); mbar_init(v_ready + i, 1); mbar_init(v_empty + i, 1);
+      mbar_init(kt_full + i, 4); mbar_init(kt_empty + i, 1);
+      mbar_init(g_full + i, 1); mbar_init(g_empty + i, 16);
+    }
+    mbar_init(a_full, 1); mbar_init(a_read, 4); mbar_init(p_ready, 4); mbar_init(qp_ready, 4);
+    mbar_init(s_ready, 4); mbar_init(u_full, 1); mbar_init(u_free, 4);
+    mbar_init(o_full, 1); mbar_init(o_free, 4); mbar_init(q_known, 4);
     mbar_init(drained, 1);
     fence_barrier_init();
   }
-  if (tid == 32 * 13) {
+  if (tid == 32 * 17) {
     prefetch_tensormap(&p.tm_q);
     prefetch_tensormap(&p.tm_k);
     prefetch_tensormap(&p.tm_v);
@@ -198,14 +220,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   const int n1 = parts > 1 && !last ? n2 : 0;                                 // summed up before
   // step i: block first + i of the part's own sum for i < n1, then of the pass proper
 
-  if (warp == 12) {
+  if (warp == 16) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t ta = s_tmem, tx = ta + 128, ty = ta + 256, tu = ta + 384;
+  const uint32_t ta = s_tmem, to = ta + 128, tu = ta + 256, tk = ta + 384;  // A (then A o D and Q'), O, U, K' twice
 
   bool dead = false;  // an expired wait: go on without waiting (the status word says so)
   auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -226,19 +248,22 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     }
   };
 
-  if (warp >= 12) {
+  // the block of step i, and its token rows that are the sequence's
+  const auto block_of = [&](int i) { return first + (i < n1 ? i : i - n1); };
+
+  if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-    if (warp == 13) {
+    if (warp == 17) {
       // ================= TMA =================
       const uint32_t lead = elect_lane();
-      auto load = [&](uint32_t dst, const CUtensorMap* m, int halves, int head, int row, uint32_t bar) {
+      auto load = [&](uint32_t dst, const CUtensorMap* m, int halves, int head, int row, uint32_t full) {
         if (lead) {
-          mbar_expect_tx(bar, (uint32_t)(halves * kHalf));
-          for (int i = 0; i < halves; ++i) tma_load_3d(dst + i * kHalf, m, i * 64, head, row, bar);
+          mbar_expect_tx(full, (uint32_t)(halves * kHalf));
+          for (int i = 0; i < halves; ++i) tma_load_3d(dst + i * kHalf, m, i * 64, head, row, full);
         }
         __syncwarp();
       };
-      // the next blocks come into L2 while the tiles are still in use
+      // the blocks after those come into L2 while the tiles are still in use
       auto ahead = [&](int c) {
         if (lead && c < n2) {
           const int row = s.row0 + (first + c) * kBlk;
@@ -253,94 +278,105 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       for (int c = 1; c < kAhead; ++c) ahead(c);
       auto step = [&](int i, bool full) {
         ahead(i + kAhead);
-        const int row = s.row0 + (first + (i < n1 ? i : i - n1)) * kBlk;
+        const int row = s.row0 + block_of(i) * kBlk, x = i & 1, free = ((i >> 1) + 1) & 1;
+        wait(k_empty + 8 * x, free);
+        load(sk + x * kTile, &p.tm_k, HK, hk, row, k_full + 8 * x);
         if (full) {
           wait(q_empty, (i - n1 + 1) & 1);
           load(sq, &p.tm_q, HK, hk, row, q_full);
         }
-        wait(k_empty, (i + 1) & 1);
-        load(sk, &p.tm_k, HK, hk, row, k_full);
-        wait(v_empty, (i + 1) & 1);
-        load(sv, &p.tm_v, HV, h, row, v_full);
+        wait(v_empty + 8 * x, free);
+        load(sv + x * kTile, &p.tm_v, HV, h, row, v_full + 8 * x);
       };
       for (int i = 0; i < n1; ++i) step(i, false);
-      if (n2 > 0) step(n1, true);
+      meet();  // (K's tiles hold the parts' sums until the second one)
       meet();
-      meet();
-      for (int i = 1; i < n2; ++i) step(n1 + i, true);
-      // no copy is under way when the CTA ends, also where a warp went on without waiting
+      fence_proxy_async_shared();
+      for (int i = 0; i < n2; ++i) step(n1 + i, true);
+      // no copy is under way when the CTA ends, also where a warp went on without
+      // waiting: the last fill of every tile
       const bool gave_up = dead;
       dead = false;
       const int n = n1 + n2;
       if (n2 > 0) wait(q_full, (n2 + 1) & 1);
-      if (n > 0) {
-        wait(k_full, (n + 1) & 1);
-        wait(v_full, (n + 1) & 1);
-      }
+      for (int x = 0; x < 2; ++x)
+        if (n > x) {
+          const int fills = (n - x + 1) >> 1;
+          wait(k_full + 8 * x, (fills + 1) & 1);
+          wait(v_full + 8 * x, (fills + 1) & 1);
+        }
       dead |= gave_up;
-    } else if (warp == 12) {
+    } else if (warp == 16) {
       // ================= products =================
       const uint32_t lead = elect_lane();
       const uint32_t id_a = idesc_16(F16, 128, kBlk, false), id_o = idesc_16(F16, 128, DV, true);
-      const uint32_t id_u = id_o | 1u << 15;  // the first operand, too, lies along its rows' dimension
-      const uint64_t qd = sdesc_sw128(sq), kd = sdesc_sw128(sk), kt = sdesc_sw128_n(sk, kHalf), vd = sdesc_sw128_n(sv, kHalf);
-      const uint64_t vh = sdesc_sw128_n(svh, kHalf), vl = sdesc_sw128_n(svl, kHalf), sd = sdesc_sw128_n(ss, DK * 128);
+      uint64_t qd = sdesc_sw128(sq), kd = sdesc_sw128(sk), vd = sdesc_sw128_n(sv, kHalf), sd = sdesc_sw128_n(ss, DK * 128);
+      int term = 0;  // K' values so far
       auto update = [&](int i) {  // U of step i
-        wait(w_ready, i & 1);
+        const int x = i & 1;
+        wait(v_ready + 8 * x, (i >> 1) & 1);
         wait(u_free, (i + 1) & 1);
-        tc_fence_after();
+#pragma unroll 1
+        for (int j = 0; j < kTerms; ++j, ++term) {
+          const int y = term & 1;
+          wait(kt_full + 8 * y, (term >> 1) & 1);
+          tc_fence_after();
+          asm volatile("" : "+l"(vd));  // (its sums are made anew: few registers)
+          const uint64_t v = vd + (uint32_t)(x * kTile >> 4);
 #pragma unroll
-        for (int kk = 0; kk < kBlk / 16; ++kk) tc_mma_el(tu, kt + kk * 128, vh + kk * 128, id_u, kk > 0, lead);
-#pragma unroll
-        for (int kk = 0; kk < kBlk / 16; ++kk) tc_mma_el(tu, kt + kk * 128, vl + kk * 128, id_u, 1, lead);
+          for (int kk = 0; kk < kBlk / 16; ++kk) tc_mma_ts_el(tu, tk + y * 64 + kk * 8, v + kk * 128, id_o, j > 0 || kk > 0, lead);
+          tc_commit_el(kt_empty + 8 * y, lead);
+        }
         tc_commit_el(u_full, lead);
-        tc_commit_el(k_empty, lead);
       };
       for (int i = 0; i < n1; ++i) {
-        wait(k_full, i & 1);
         update(i);
-        tc_commit_el(v_empty, lead);
+        tc_commit_el(k_empty + 8 * (i & 1), lead);
+        tc_commit_el(v_empty + 8 * (i & 1), lead);
       }
       meet();
       meet();
       for (int c = 0; c < n2; ++c) {
-        const int i = n1 + c;
-        wait(k_full, i & 1);
+        const int i = n1 + c, x = i & 1;
+        wait(k_full + 8 * x, (i >> 1) & 1);
         wait(q_full, c & 1);
         tc_fence_after();
+        asm volatile("" : "+l"(qd), "+l"(kd), "+l"(sd));
+        const uint64_t k = kd + (uint32_t)(x * kTile >> 4);
 #pragma unroll
         for (int kk = 0; kk < DK / 16; ++kk) {
           const uint32_t o = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-          tc_mma_el(ta, qd + o, kd + o, id_a, kk > 0, lead);
+          tc_mma_el(ta, qd + o, k + o, id_a, kk > 0, lead);
         }
         tc_commit_el(a_full, lead);
+        tc_commit_el(q_empty, lead);
+        tc_commit_el(k_empty + 8 * x, lead);
+        update(i);
         wait(s_ready, c & 1);
         wait(o_free, (c + 1) & 1);
+        wait(qp_ready, c & 1);
         tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < DK / 16; ++kk) {
-          const uint32_t o = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-          tc_mma_el(tx, qd + o, sd + kk * 128, id_o, kk > 0, lead);
-        }
-        tc_commit_el(q_empty, lead);
-        update(i);
-        wait(p_full, c & 1);
+        for (int kk = 0; kk < DK / 16; ++kk) tc_mma_ts_el(to, ta + 64 + kk * 8, sd + kk * 128, id_o, kk > 0, lead);
+        wait(p_ready, c & 1);
         tc_fence_after();
+        asm volatile("" : "+l"(vd));
+        const uint64_t v = vd + (uint32_t)(x * kTile >> 4);
 #pragma unroll
-        for (int kk = 0; kk < kBlk / 16; ++kk) tc_mma_ts_el(ty, ta + kk * 8, vd + kk * 128, id_o, kk > 0, lead);
+        for (int kk = 0; kk < kBlk / 16; ++kk) tc_mma_ts_el(to, ta + kk * 8, v + kk * 128, id_o, 1, lead);
         tc_commit_el(o_full, lead);
-        tc_commit_el(v_empty, lead);
+        tc_commit_el(v_empty + 8 * x, lead);
       }
       tc_commit_el(drained, lead);  // every product has ended before tensor memory is given back
       wait(drained, 0);
-    } else if (warp == 14) {
+    } else if (warp == 18) {
       // ================= decays =================
       for (int i = 0; i < n1 + n2; ++i) {
         if (i == n1) {
           meet();
           meet();
         }
-        const int t0 = (first + (i < n1 ? i : i - n1)) * kBlk + lane * 4, slot = i & 1;
+        const int t0 = block_of(i) * kBlk + lane * 4, slot = i & 1;
         double g[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -363,8 +399,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           const float hi = (float)G;
           d.gh[lane * 4 + j] = -hi;
           d.gl[lane * 4 + j] = (float)(hi - G);
-          d.v[lane * 4 + j] = t0 + j < s.n ? exp2f((float)(total - G)) : 0.f;
-          d.q[lane * 4 + j] = a.scale * exp2f(hi);
+          d.k[lane * 4 + j] = exp2f((float)(total - G));
+          d.q[lane * 4 + j] = exp2f(hi);
         }
         if (lane == 0) d.all = decay_of((float)(total * 0.6931471805599453));
         arrive(g_full + 8 * slot);
@@ -374,8 +410,26 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         meet();
       }
     } else {
-      meet();
-      meet();
+      // ================= V behind the sequence's end =================
+      for (int i = 0; i < n1 + n2; ++i) {
+        if (i == n1) {
+          meet();
+          meet();
+        }
+        const int x = i & 1, rows = s.n - block_of(i) * kBlk;
+        wait(v_full + 8 * x, (i >> 1) & 1);
+        if (rows < kBlk) {
+          for (int at = rows * 128 + lane * 16; at < kHalf; at += 512)
+#pragma unroll
+            for (int y = 0; y < HV; ++y) st_s128(sv + x * kTile + y * kHalf + at, 0u, 0u, 0u, 0u);
+          fence_proxy_async_shared();
+        }
+        arrive(v_ready + 8 * x);
+      }
+      if (n2 == 0) {
+        meet();
+        meet();
+      }
     }
   } else if (warp < 4) {
     // ================= A o D: a thread is a token's row =================
@@ -395,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       tc_fence_after();
       const float2 gh = make_float2(-d.gh[tid], -d.gh[tid]), gl = make_float2(-d.gl[tid], -d.gl[tid]);
       float up = 1.f;
-      if constexpr (F16) {  // the row's largest |q . k| to about 2^13
+      if constexpr (F16) {  // the largest of the row's |q . k| and of its Q' (times S's scale) to about 2^13
         float m = 0.f;
         for (int j = 0; j <= warp; ++j) {
           uint32_t x[32];
@@ -405,9 +459,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           for (int e = 0; e < 32; ++e)
             if (j < warp || e <= lane) m = fmaxf(m, fabsf(__uint_as_float(x[e])));
         }
-        const int e = lift_of(m);
+        wait(q_known, c & 1);
+        wait(s_ready, c & 1);
+        const int e = max(-100, min(lift_of(m), lift_of(s_qmax[tid]) + s_state_up[c & 1]));
         up = pow2(e);
-        s_row[c & 1][tid] = pow2(-e);
+        s_row[c & 1][tid] = e;
       }
       // (rolled loops: with all roles' loops unrolled their code did not stay in the
       // instruction cache, and a block took twice as long)
@@ -417,6 +473,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         if (j <= warp) {
           tc_ld32(tr + j * 32, x);
           tc_ld_wait();
+          if (j == warp) {  // the row has been read: Q' may take its place from column 64 on
+            tc_fence_before();
+            arrive(a_read);
+          }
           const float4* nh = reinterpret_cast<const float4*>(d.gh + j * 32);
           const float4* nl = reinterpret_cast<const float4*>(d.gl + j * 32);
 #pragma unroll
@@ -446,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       }
       tc_st_wait();
       tc_fence_before();
-      arrive(p_full);
+      arrive(p_ready);
       arrive(g_empty + 8 * (i & 1));
     }
   } else if (warp < 8) {
@@ -505,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       if (decay) *decay = fmaf(*decay, e.x, *decay * e.y);
       wait(u_full, i & 1);
       tc_fence_after();
-      const float up = F16 ? s_v_up[i & 1] : 1.f;
+      const float up = F16 ? s_key_down[i & 1] : 1.f;
 #pragma unroll
       for (int j = 0; j < DV / 32; ++j) {
         uint32_t x[32];
@@ -527,11 +587,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
 #pragma unroll
       for (int j = 0; j < DV / 2; ++j) S[j] = make_float2(0.f, 0.f);
       for (int i = 0; i < n1; ++i) step(i, &decay);
-      if (n1 > 0) {  // columns 4 j of all rows side by side, where V' was
+      if (n1 > 0) {  // columns 4 j of all rows side by side, where K was
         if (held)
 #pragma unroll
           for (int j = 0; j < DV / 4; ++j)
-            st_s128(svh + (j * DK + row) * 16, __float_as_uint(S[2 * j].x), __float_as_uint(S[2 * j].y),
+            st_s128(meet_at + (j * DK + row) * 16, __float_as_uint(S[2 * j].x), __float_as_uint(S[2 * j].y),
                     __float_as_uint(S[2 * j + 1].x), __float_as_uint(S[2 * j + 1].y));
         if (row == 0) s_part = decay;
       }
@@ -541,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       exchange(true);
       for (int r = 0; r < part; ++r) {  // the parts before, in their order
         const float e = peer_f32(peer(smem_u32(&s_part), r));
-        const uint32_t from = peer(svh, r);
+        const uint32_t from = peer(meet_at, r);
         if (held)
 #pragma unroll
           for (int j = 0; j < DV / 4; ++j) {
@@ -565,9 +625,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         asm volatile("bar.sync 1, 128;" ::: "memory");
         const int e = lift_of(fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3])));
         up = pow2(e);
-        if (row == 0) s_state_up[c & 1] = pow2(-e);
+        if (row == 0) s_state_up[c & 1] = e;
       }
-      if (c > 0) wait(q_empty, (c + 1) & 1);  // the product with the S before
+      if (c > 0) wait(o_full, (c + 1) & 1);  // the product with the S before
       if (held)
 #pragma unroll
         for (int j = 0; j < DV / 8; ++j) {
@@ -584,110 +644,90 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       step(n1 + c, nullptr);
     }
     if (last) {
-      wait(q_empty, (n2 + 1) & 1);  // the last product with S
+      wait(o_full, (n2 + 1) & 1);  // the last product with S
       exchange(false);
     }
-  } else {
-    // ================= V' and the output =================
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOut));
+  } else if (warp < 12) {
+    // ================= Q' and the output: a thread is a token's row =================
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsOut));
     const int t = tid - 256;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    auto scaled = [&](int i) {  // V' of step i; rows behind the last token become zeros, in K and V too
-      const int nv = s.n - (first + (i < n1 ? i : i - n1)) * kBlk;
-      const Decays& d = s_dec[i & 1];
-      wait(g_full + 8 * (i & 1), (i >> 1) & 1);
-      wait(v_full, i & 1);
-      if (i > 0) wait(u_full, (i + 1) & 1);  // the product with the V' before
-      float up = 1.f;
-      if constexpr (F16) {  // the block's largest |v| (infinities and NaN apart) to about 2^13
-        uint32_t m = 0;
-#pragma unroll 4
-        for (int j = 0; j < 8 * HV; ++j) {
-          const int at = (j * 128 + t) * 16;
-          const uint4 raw = ld_s128(sv + at);
-          if ((at & (kHalf - 1)) >> 7 < nv)
-            m = __vmaxu2(__vmaxu2(m, __vmaxu2(raw.x & 0x7fff7fffu, raw.y & 0x7fff7fffu)),
-                         __vmaxu2(raw.z & 0x7fff7fffu, raw.w & 0x7fff7fffu));
-        }
-        m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
-        asm volatile("bar.sync 2, 128;" ::: "memory");  // the last block's have been read
-        if (lane == 0) s_vmax[warp & 3] = m;
-        asm volatile("bar.sync 2, 128;" ::: "memory");
-        m = min(max(max(s_vmax[0], s_vmax[1]), max(s_vmax[2], s_vmax[3])), 0x7bffu);
-        const int e = lift_of(kv::unpack2<true>(m).x);
-        up = pow2(e);
-        if (t == 0) s_v_up[i & 1] = pow2(-e);
-      }
-#pragma unroll 2
-      for (int j = 0; j < 8 * HV; ++j) {
-        const int at = (j * 128 + t) * 16, row = (at & (kHalf - 1)) >> 7;
-        const uint4 raw = ld_s128(sv + at);
-        const float e = F16 ? d.v[row] * up : d.v[row];
-        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float2 f = mul2(kv::unpack2<F16>(w[x]), make_float2(e, e));
-          hi[x] = kv::pack2<F16>(f.x, f.y);
-          const float2 r = kv::unpack2<F16>(hi[x]), rest = add2(f, make_float2(-r.x, -r.y));
-          lo[x] = kv::pack2<F16>(rest.x, rest.y);
-        }
-        const bool in = row < nv;
-        if (!in) st_s128(sv + at, 0u, 0u, 0u, 0u);
-        st_s128(svh + at, in ? hi[0] : 0u, in ? hi[1] : 0u, in ? hi[2] : 0u, in ? hi[3] : 0u);
-        st_s128(svl + at, in ? lo[0] : 0u, in ? lo[1] : 0u, in ? lo[2] : 0u, in ? lo[3] : 0u);
-      }
-      if (nv < kBlk) {
-        wait(k_full, i & 1);
-        for (int at = nv * 128 + t * 16; at < kHalf; at += 128 * 16)
-#pragma unroll
-          for (int x = 0; x < HK; ++x) st_s128(sk + x * kHalf + at, 0u, 0u, 0u, 0u);
-      }
-      fence_proxy_async_shared();
-      arrive(w_ready);
-    };
     for (int i = 0; i < n1; ++i) {
-      scaled(i);
+      wait(g_full + 8 * (i & 1), (i >> 1) & 1);
       arrive(g_empty + 8 * (i & 1));
     }
     meet();
     meet();
     for (int c = 0; c < n2; ++c) {
       const int i = n1 + c;
-      scaled(i);
+      wait(g_full + 8 * (i & 1), (i >> 1) & 1);
       const float e = s_dec[i & 1].q[t];
       arrive(g_empty + 8 * (i & 1));
+      uint32_t q[DK / 2];
+      wait(q_full, c & 1);
+#pragma unroll
+      for (int j = 0; j < DK / 8; ++j) {
+        const uint4 v = ld_s128(sq + (j >> 3) * kHalf + t * 128 + (((j & 7) ^ (t & 7)) << 4));
+        q[4 * j] = v.x; q[4 * j + 1] = v.y; q[4 * j + 2] = v.z; q[4 * j + 3] = v.w;
+      }
+      arrive(q_empty);
+      float f = e;
+      if constexpr (F16) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < DK / 2; ++j) m = __vmaxu2(m, q[j] & 0x7fff7fffu);
+        m = min(max(m & 0xffffu, m >> 16), 0x7bffu);
+        s_qmax[t] = kv::unpack2<true>(m).x * e;
+        arrive(q_known);
+        wait(a_read, c & 1);
+        const int x = s_row[c & 1][t] - s_state_up[c & 1];
+        f = x < -126 ? 0.f : e * pow2(min(x, 127));
+      }
+#pragma unroll
+      for (int j = 0; j < DK / 2; ++j) {
+        const float2 x = mul2(kv::unpack2<F16>(q[j]), make_float2(f, f));
+        q[j] = kv::pack2<F16>(x.x, x.y);
+      }
+      if constexpr (!F16) wait(a_read, c & 1);
+      tc_fence_after();
+#pragma unroll
+      for (int j = 0; j < DK / 32; ++j) {
+        uint32_t w[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x) w[x] = q[j * 16 + x];
+        tc_st16(ta + lanes + 64 + j * 16, w);
+      }
+      tc_st_wait();
+      tc_fence_before();
+      arrive(qp_ready);
       wait(o_full, c & 1);
       tc_fence_after();
-      const float ex = F16 ? e * s_state_up[c & 1] : e, ey = F16 ? a.scale * s_row[c & 1][t] : a.scale;
+      const float scale = F16 ? a.scale * pow2(-s_row[c & 1][t]) : a.scale;
 #pragma unroll 1
       for (int j = 0; j < DV / 32; ++j) {
-        uint32_t x[32], y[32];
-        tc_ld32(tx + lanes + j * 32, x);
-        tc_ld32(ty + lanes + j * 32, y);
+        uint32_t x[32], w[16];
+        tc_ld32(to + lanes + j * 32, x);
         tc_ld_wait();
         if (j == DV / 32 - 1) {
           tc_fence_before();
           arrive(o_free);
         }
-        uint32_t w[16];
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          const float2 o = fma2(make_float2(ex, ex), make_float2(__uint_as_float(x[2 * q]), __uint_as_float(x[2 * q + 1])),
-                                mul2(make_float2(ey, ey), make_float2(__uint_as_float(y[2 * q]), __uint_as_float(y[2 * q + 1]))));
-          w[q] = kv::pack2<F16>(o.x, o.y);
+        for (int y = 0; y < 16; ++y) {
+          const float2 o = mul2(make_float2(__uint_as_float(x[2 * y]), __uint_as_float(x[2 * y + 1])), make_float2(scale, scale));
+          w[y] = kv::pack2<F16>(o.x, o.y);
         }
         // rows of 64 values go out together, eight lanes a row: a store of one piece
         // per row and lane takes the load-store unit 32 cycles, and everything waits
         const uint32_t mine = so + (t >> 5) * (32 * kPitch);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          st_s128(mine + lane * kPitch + (j & 1) * 64 + q * 16, w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+        for (int y = 0; y < 4; ++y)
+          st_s128(mine + lane * kPitch + (j & 1) * 64 + y * 16, w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
         if (j & 1) {
           __syncwarp();
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const int r = q * 4 + (lane >> 3), tok = (first + c) * kBlk + (t & ~31) + r;
+          for (int y = 0; y < 8; ++y) {
+            const int r = y * 4 + (lane >> 3), tok = (first + c) * kBlk + (t & ~31) + r;
             const uint4 v = ld_s128(mine + r * kPitch + (lane & 7) * 16);
             if (tok < s.n)
               *reinterpret_cast<uint4*>(a.o + ((long long)(s.row0 + tok) * a.Hv + h) * DV + (j & ~1) * 32 + (lane & 7) * 8) = v;
@@ -696,12 +736,115 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         }
       }
     }
+  } else {
+    // ================= K'^T: a warp has 32 of its rows (values of a key) =================
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsKey));
+    const int w = warp - 12;
+    const bool held = w * 32 < DK;
+    int term = 0;
+    for (int i = 0; i < n1 + n2; ++i) {
+      if (i == n1) {
+        meet();
+        meet();
+      }
+      const int x = i & 1, rows = s.n - block_of(i) * kBlk;
+      const Decays& d = s_dec[x];
+      wait(g_full + 8 * x, (i >> 1) & 1);
+      wait(k_full + 8 * x, (i >> 1) & 1);
+      // this lane's row of the matrices: tokens (lane & 7) + 8 (lane >> 4), the warp's first or
+      // second 8 values of 16 by (lane >> 3) & 1
+      const uint32_t tile = sk + x * kTile + (w >> 1) * kHalf;
+      const auto fetch = [&](int g, int half, uint32_t (&m)[4]) {
+        const int tok = g * 16 + (lane & 7) + ((lane >> 4) << 3), piece = (w & 1) * 4 + half * 2 + ((lane >> 3) & 1);
+        ldmatrix4_t(tile + tok * 128 + ((piece ^ (tok & 7)) << 4), m);
+        if (g * 16 + 16 > rows) {  // tokens behind the end (which may be NaN) become zeros
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int t0 = g * 16 + (y >> 1) * 8 + (lane & 3) * 2;
+            m[y] &= (t0 < rows ? 0xffffu : 0u) | (t0 + 1 < rows ? 0xffff0000u : 0u);
+          }
+        }
+      };
+      float up = 1.f;
+      if constexpr (F16) {  // the block's largest |k| (infinities and NaN apart) to about 2^13
+        uint32_t m = 0;
+        if (held)
+#pragma unroll 2
+          for (int y = 0; y < 16; ++y) {
+            uint32_t v[4];
+            fetch(y >> 1, y & 1, v);
+            m = __vmaxu2(__vmaxu2(m, __vmaxu2(v[0] & 0x7fff7fffu, v[1] & 0x7fff7fffu)),
+                         __vmaxu2(v[2] & 0x7fff7fffu, v[3] & 0x7fff7fffu));
+          }
+        m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+        asm volatile("bar.sync 2, 128;" ::: "memory");  // the last block's have been read
+        if (lane == 0) s_kmax[w] = m;
+        asm volatile("bar.sync 2, 128;" ::: "memory");
+        m = min(max(max(s_kmax[0], s_kmax[1]), max(s_kmax[2], s_kmax[3])), 0x7bffu);
+        const int e = lift_of(kv::unpack2<true>(m).x);
+        up = pow2(e);
+        if (tid == 32 * 12) s_key_down[x] = pow2(-e);
+      }
+      const uint32_t lanes = (uint32_t)(w * 32) << 16;
+      // One value of all K', written to tensor memory where the value two before it was.
+      const auto write = [&](int which) {
+        const int y = term & 1;
+        wait(kt_empty + 8 * y, ((term >> 1) + 1) & 1);
+        tc_fence_after();
+        if (held) {
+#pragma unroll 1
+          for (int g = 0; g < kBlk / 16; ++g) {
+            const float2 e0 = *reinterpret_cast<const float2*>(&d.k[g * 16 + (lane & 3) * 2]);
+            const float2 e1 = *reinterpret_cast<const float2*>(&d.k[g * 16 + 8 + (lane & 3) * 2]);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint32_t m[4];
+              fetch(g, half, m);
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                float2 f = mul2(kv::unpack2<F16>(m[z]), z < 2 ? e0 : e1);
+                if constexpr (F16) {
+                  f = mul2(f, make_float2(up, up));
+                  m[z] = kv::pack2<true>(f.x, f.y);
+                  if (which == 1) {
+                    const float2 r = kv::unpack2<true>(m[z]);
+                    m[z] = kv::pack2<true>(f.x - r.x, f.y - r.y);
+                  }
+                } else {
+                  // cut off after 8 bits: three such values are all of an fp32
+                  const auto rest = [](float2 u) {
+                    return add2(u, make_float2(-__uint_as_float(__float_as_uint(u.x) & 0xffff0000u),
+                                               -__uint_as_float(__float_as_uint(u.y) & 0xffff0000u)));
+                  };
+                  if (which > 0) f = rest(f);
+                  if (which > 1) f = rest(f);
+                  m[z] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
+                }
+              }
+              tc_st_16x8(tk + lanes + ((uint32_t)(half * 16) << 16) + y * 64 + g * 8, m);
+            }
+          }
+          tc_st_wait();
+        }
+        tc_fence_before();
+        arrive(kt_full + 8 * y);
+        ++term;
+      };
+#pragma unroll 1
+      for (int which = 0; which < kTerms; ++which) write(which);
+      arrive(k_empty + 8 * x);
+      arrive(g_empty + 8 * x);
+    }
+    if (n2 == 0) {
+      meet();
+      meet();
+    }
   }
 
   if (dead && a.status && lane == 0) atomicOr(a.status, DEV_TIMEOUT);
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 16) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(ta));
   }

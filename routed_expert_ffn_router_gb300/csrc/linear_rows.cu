@@ -4,7 +4,7 @@
 // The columns of a state are independent: a CTA owns 32 columns of one head's
 // [Dk][Dv] and keeps them in registers (a thread has 4 columns of every 16th row)
 // from one read to one write, whatever the number of rows, so a decode window
-// costs a read and a write of the state. Rows come through shared memory 16 at a
+// costs a read and a write of the state. Rows come through shared memory up to 16 at a
 // time; a row's products q S are summed over Dk within a warp by shuffles and over
 // the four warps once per 16 rows.
 #include "block_internal.h"
@@ -16,22 +16,26 @@ namespace block {
 
 namespace {
 
-constexpr int kThreads = 128;
 constexpr int kCols = 32;   // of Dv per CTA
-constexpr int kRows = 16;   // tokens staged at a time
+constexpr int kThreads = 4 * kCols, kWarps = kThreads / 32;
+constexpr int kRows = 16;   // tokens staged at a time, at most
 
 template <bool F16>
 __device__ __forceinline__ float one(const uint16_t* p) {
   return kv::unpack2<F16>((uint32_t)*p).x;
 }
 
-// DK: 64, 128 or 256, at least the head size.
+// DK: 64, 128 or 256, at least the head size. staged: tokens at a time.
 template <bool F16, int DK>
-__global__ void __launch_bounds__(kThreads, DK <= 128 ? 8 : 4) linear_rows_kernel(Linear a, kv::Rows r) {
-  constexpr int NI = DK / 16;
-  __shared__ float qs[kRows][DK], ks[kRows][DK], vs[kRows][kCols], po[kRows][4][kCols];
+__global__ void __launch_bounds__(kThreads, DK <= 128 ? 8 : 4) linear_rows_kernel(Linear a, kv::Rows r, int staged) {
+  constexpr int NI = DK / 16, kLanes = kCols / 4;  // lanes of a row
+  extern __shared__ __align__(16) float smem_rows[];
+  float (*qs)[DK] = reinterpret_cast<float (*)[DK]>(smem_rows);
+  float (*ks)[DK] = qs + staged;
+  float (*vs)[kCols] = reinterpret_cast<float (*)[kCols]>(ks + staged);
+  float (*po)[kWarps][kCols] = reinterpret_cast<float (*)[kWarps][kCols]>(vs + staged);
   __shared__ float2 decay[kRows];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, col = (tid & 7) * 4, row = tid >> 3;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, col = (tid % kLanes) * 4, row = tid / kLanes;
   griddep_wait();
   griddep_launch_dependents();
   const int tiles = (a.Dv + kCols - 1) / kCols;
@@ -48,8 +52,8 @@ __global__ void __launch_bounds__(kThreads, DK <= 128 ? 8 : 4) linear_rows_kerne
     S[i] = mine && d < a.Dk ? state[(long long)d * a.Dv / 4] : make_float4(0.f, 0.f, 0.f, 0.f);
   }
   const bool ok = span_allowed(a, r, b, s, tile == 0 && h == 0);
-  for (int t0 = 0; t0 < s.n; t0 += kRows) {
-    const int m = min(kRows, s.n - t0);
+  for (int t0 = 0; t0 < s.n; t0 += staged) {
+    const int m = min(staged, s.n - t0);
     __syncthreads();  // the last rows have been used
     for (int i = tid; i < m * a.Dk; i += kThreads) {
       const int j = i / a.Dk, d = i - j * a.Dk;
@@ -78,18 +82,23 @@ __global__ void __launch_bounds__(kThreads, DK <= 128 ? 8 : 4) linear_rows_kerne
         o.z = fmaf(q, S[i].z, o.z); o.w = fmaf(q, S[i].w, o.w);
       }
 #pragma unroll
-      for (int x = 8; x < 32; x <<= 1) {
+      for (int x = kLanes; x < 32; x <<= 1) {
         o.x += __shfl_xor_sync(0xffffffffu, o.x, x); o.y += __shfl_xor_sync(0xffffffffu, o.y, x);
         o.z += __shfl_xor_sync(0xffffffffu, o.z, x); o.w += __shfl_xor_sync(0xffffffffu, o.w, x);
       }
-      if (lane < 8) *reinterpret_cast<float4*>(&po[j][warp][col]) = o;
+      if (lane < kLanes) *reinterpret_cast<float4*>(&po[j][warp][col]) = o;
     }
     __syncthreads();
     for (int i = tid; i < m * kCols / 2; i += kThreads) {
       const int j = i / (kCols / 2), c = i % (kCols / 2) * 2;
       if (c0 + c >= a.Dv) continue;
-      const float x = po[j][0][c] + po[j][1][c] + (po[j][2][c] + po[j][3][c]);
-      const float y = po[j][0][c + 1] + po[j][1][c + 1] + (po[j][2][c + 1] + po[j][3][c + 1]);
+      float x = 0.f, y = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 f = *reinterpret_cast<const float2*>(&po[j][w][c]);
+        x += f.x;
+        y += f.y;
+      }
       *reinterpret_cast<uint32_t*>(a.o + ((s.row0 + t0 + j) * (long long)a.Hv + h) * a.Dv + c0 + c) = ok ? kv::pack2<F16>(x, y) : 0u;
     }
   }
@@ -101,15 +110,21 @@ __global__ void __launch_bounds__(kThreads, DK <= 128 ? 8 : 4) linear_rows_kerne
   }
 }
 
+template <bool F16, int DK>
+cudaError_t launch_rows(const Linear& a, const kv::Rows& r, bool step, cudaStream_t st) {
+  // no more shared memory than a window's rows need: 16 rows' of it (27 KB) left six
+  // CTAs on an SM and a window of one row at 52 us instead of 47
+  const int staged = step && r.n_q < kRows ? r.n_q : kRows;
+  const size_t smem = (size_t)staged * (2 * DK + kCols + kWarps * kCols) * 4;
+  const unsigned grid = (unsigned)((long long)r.B * a.Hv * ((a.Dv + kCols - 1) / kCols));
+  return launch_pdl(step ? K_LINEAR_STEP : K_LINEAR_CHUNK, linear_rows_kernel<F16, DK>, dim3(grid), kThreads, smem, st, a, r, staged);
+}
+
 }  // namespace
 
 cudaError_t launch_linear_rows(const Linear& a, const kv::Rows& r, bool f16, bool step, cudaStream_t st) {
-  const unsigned grid = (unsigned)((long long)r.B * a.Hv * ((a.Dv + kCols - 1) / kCols));
-  const auto go = [&](auto kernel) {
-    return launch_pdl(step ? K_LINEAR_STEP : K_LINEAR_CHUNK, kernel, dim3(grid), kThreads, 0, st, a, r);
-  };
-  if (f16) return a.Dk <= 64 ? go(linear_rows_kernel<true, 64>) : a.Dk <= 128 ? go(linear_rows_kernel<true, 128>) : go(linear_rows_kernel<true, 256>);
-  return a.Dk <= 64 ? go(linear_rows_kernel<false, 64>) : a.Dk <= 128 ? go(linear_rows_kernel<false, 128>) : go(linear_rows_kernel<false, 256>);
+  if (f16) return a.Dk <= 64 ? launch_rows<true, 64>(a, r, step, st) : a.Dk <= 128 ? launch_rows<true, 128>(a, r, step, st) : launch_rows<true, 256>(a, r, step, st);
+  return a.Dk <= 64 ? launch_rows<false, 64>(a, r, step, st) : a.Dk <= 128 ? launch_rows<false, 128>(a, r, step, st) : launch_rows<false, 256>(a, r, step, st);
 }
 
 }  // namespace block
