@@ -83,11 +83,13 @@ __device__ __forceinline__ void ldmatrix4_t(uint32_t a, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
 }
-// 16 lanes x 8 columns: r[0] column t % 4 of lane t / 4, r[1] of lane 8 + t / 4,
-// r[2] and r[3] the next four columns.
-__device__ __forceinline__ void tc_st_16x8(uint32_t taddr, const uint32_t (&r)[4]) {
-  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
-               : "memory");
+// 16 lanes x 32 columns: r[2 i] column 4 i + t % 4 of lane t / 4, r[2 i + 1] of lane 8 + t / 4.
+__device__ __forceinline__ void tc_st_16x32(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
@@ -786,52 +788,80 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         if (tid == 32 * 12) s_key_down[x] = pow2(-e);
       }
       const uint32_t lanes = (uint32_t)(w * 32) << 16;
-      // One value of all K', written to tensor memory where the value two before it was.
-      const auto write = [&](int which) {
-        const int y = term & 1;
-        wait(kt_empty + 8 * y, ((term >> 1) + 1) & 1);
+      // 16 values of the head by 64 tokens at a time, which takes 16 registers.
+      // The first two values that stand for K', then (bf16) the third.
+      const auto scaled = [&](int g, uint32_t m, bool second) {  // a pair of tokens
+        const float2 e = *reinterpret_cast<const float2*>(&d.k[g * 16 + (second ? 8 : 0) + (lane & 3) * 2]);
+        float2 f = mul2(kv::unpack2<F16>(m), e);
+        if constexpr (F16) f = mul2(f, make_float2(up, up));
+        return f;
+      };
+      // what is left of f without its upper 8 bits: three such values are all of an fp32
+      const auto rest = [](float2 f) {
+        return add2(f, make_float2(-__uint_as_float(__float_as_uint(f.x) & 0xffff0000u), -__uint_as_float(__float_as_uint(f.y) & 0xffff0000u)));
+      };
+      const auto upper = [](float2 f) { return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632); };
+      const auto free_slot = [&](int n) { wait(kt_empty + 8 * (n & 1), ((n >> 1) + 1) & 1); };
+      free_slot(term);
+      free_slot(term + 1);
+      tc_fence_after();
+      if (held) {
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            uint32_t m[4];
+            fetch((j & 1) * 4 + g, j >> 1, m);
+#pragma unroll
+            for (int z = 0; z < 4; ++z) hi[4 * g + z] = m[z];
+          }
+#pragma unroll
+          for (int z = 0; z < 16; ++z) {
+            const float2 f = scaled((j & 1) * 4 + (z >> 2), hi[z], z & 2);
+            if constexpr (F16) {
+              hi[z] = kv::pack2<true>(f.x, f.y);
+              const float2 r = kv::unpack2<true>(hi[z]);
+              lo[z] = kv::pack2<true>(f.x - r.x, f.y - r.y);
+            } else {
+              hi[z] = upper(f);
+              lo[z] = upper(rest(f));
+            }
+          }
+          const uint32_t to = tk + lanes + ((uint32_t)((j >> 1) * 16) << 16) + (j & 1) * 32;
+          tc_st_16x32(to + (term & 1) * 64, hi);
+          tc_st_16x32(to + ((term + 1) & 1) * 64, lo);
+        }
+        tc_st_wait();
+      }
+      tc_fence_before();
+      arrive(kt_full + 8 * (term & 1));
+      arrive(kt_full + 8 * ((term + 1) & 1));
+      term += 2;
+      if constexpr (!F16) {
+        free_slot(term);
         tc_fence_after();
         if (held) {
 #pragma unroll 1
-          for (int g = 0; g < kBlk / 16; ++g) {
-            const float2 e0 = *reinterpret_cast<const float2*>(&d.k[g * 16 + (lane & 3) * 2]);
-            const float2 e1 = *reinterpret_cast<const float2*>(&d.k[g * 16 + 8 + (lane & 3) * 2]);
+          for (int j = 0; j < 4; ++j) {
+            uint32_t v[16];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
+            for (int g = 0; g < 4; ++g) {
               uint32_t m[4];
-              fetch(g, half, m);
+              fetch((j & 1) * 4 + g, j >> 1, m);
 #pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                float2 f = mul2(kv::unpack2<F16>(m[z]), z < 2 ? e0 : e1);
-                if constexpr (F16) {
-                  f = mul2(f, make_float2(up, up));
-                  m[z] = kv::pack2<true>(f.x, f.y);
-                  if (which == 1) {
-                    const float2 r = kv::unpack2<true>(m[z]);
-                    m[z] = kv::pack2<true>(f.x - r.x, f.y - r.y);
-                  }
-                } else {
-                  // cut off after 8 bits: three such values are all of an fp32
-                  const auto rest = [](float2 u) {
-                    return add2(u, make_float2(-__uint_as_float(__float_as_uint(u.x) & 0xffff0000u),
-                                               -__uint_as_float(__float_as_uint(u.y) & 0xffff0000u)));
-                  };
-                  if (which > 0) f = rest(f);
-                  if (which > 1) f = rest(f);
-                  m[z] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
-                }
-              }
-              tc_st_16x8(tk + lanes + ((uint32_t)(half * 16) << 16) + y * 64 + g * 8, m);
+              for (int z = 0; z < 4; ++z) v[4 * g + z] = m[z];
             }
+#pragma unroll
+            for (int z = 0; z < 16; ++z) v[z] = upper(rest(rest(scaled((j & 1) * 4 + (z >> 2), v[z], z & 2))));
+            tc_st_16x32(tk + lanes + ((uint32_t)((j >> 1) * 16) << 16) + (j & 1) * 32 + (term & 1) * 64, v);
           }
           tc_st_wait();
         }
         tc_fence_before();
-        arrive(kt_full + 8 * y);
+        arrive(kt_full + 8 * (term & 1));
         ++term;
-      };
-#pragma unroll 1
-      for (int which = 0; which < kTerms; ++which) write(which);
+      }
       arrive(k_empty + 8 * x);
       arrive(g_empty + 8 * x);
     }
