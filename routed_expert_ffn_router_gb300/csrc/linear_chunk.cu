@@ -20,8 +20,8 @@
 // below 2^-14, K' and S are scaled by a power of two per block and a row of A o D and
 // Q' by one of its own, which bring the largest magnitude to 2^13 and are undone in
 // fp32: the smallest values are then off by up to 2^-38 of the largest. Sums of
-// logarithms are taken in fp64 and handed on as two fp32 values, so that G_i - G_j is
-// right next to large |G|.
+// logarithms are pairs of fp32 values, so that G_i - G_j is right next to large |G|
+// (in fp64 a block's sums took 5,000 cycles).
 //
 // Work. An item is a sequence and a v head, by a cluster of 1 to 8 CTAs that have
 // consecutive parts of its blocks. With more than one, each first sums up its own
@@ -30,9 +30,10 @@
 // goes through its part. So a long prompt of few heads fills the GPU in one launch
 // and without a workspace. Items are started longest first.
 //
-// Warps. 0-3: A o D; 4-7: the state (a thread is a row of it); 8-11: Q' and the
-// output; 12-15: K'; 16: issues the products; 17: TMA; 18: decays, two blocks ahead;
-// 19: zeroes V behind a sequence's end.
+// Warps. 0-3: A o D and Q' (a thread is a token); 4-7: the state (a thread is a row of
+// it); 8-11: the output; 12-15 and 16-19: K' of a block's first and last 64 tokens;
+// 20: issues the products; 21: TMA; 22 and 23: decays of every other block each (one
+// warp for all of them was what the others waited for: 8,000 cycles a block).
 #include <cuda.h>
 
 #include <atomic>
@@ -52,14 +53,15 @@ using namespace tc;
 namespace {
 
 constexpr int kBlk = 128;               // tokens per block
-constexpr int kThreads = 640;
-constexpr int kRegsScore = 80, kRegsState = 176, kRegsOut = 104, kRegsKey = 64, kRegsRest = 56;  // at most 5 x 96 together
+constexpr int kThreads = 768;
+constexpr int kRegsScore = 72, kRegsState = 168, kRegsOut = 64, kRegsKey = 64, kRegsRest = 48;  // (KEY twice) at most 6 x 80 together
 constexpr uint32_t kTries = 1u << 22;   // of a wait, each up to a microsecond long
 constexpr int kHalf = kBlk * 128;       // bytes of 128 rows of 64 values
 constexpr int kTile = 2 * kHalf;
 constexpr int kPitch = 144;             // bytes per row of a warp's output buffer (64 values and a pad)
 constexpr int kSmem = 1024 + 6 * kTile + 4 * 32 * kPitch;  // Q, two of K and of V, S; outputs
 constexpr int kSortB = 512;             // sequences that are put in order of their length
+constexpr int kKeySlots = 4;            // of K', 32 columns (64 tokens) each
 constexpr int kMostParts = 8;
 constexpr int kAhead = 2;               // blocks that are fetched into L2 ahead
 
@@ -75,6 +77,7 @@ struct Decays {
   float gh[kBlk], gl[kBlk];  // -G_j / ln 2 as two values
   float k[kBlk];      // e^(G - G_j)
   float q[kBlk];      // e^G_i
+  float piece[kBlk];  // e^(G_p - G_j), p the last of j's 32 tokens
   float2 all;         // e^G (decay_of)
   float pad[2];
 };
@@ -83,13 +86,11 @@ __device__ __forceinline__ void ldmatrix4_t(uint32_t a, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
 }
-// 16 lanes x 32 columns: r[2 i] column 4 i + t % 4 of lane t / 4, r[2 i + 1] of lane 8 + t / 4.
-__device__ __forceinline__ void tc_st_16x32(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+// 16 lanes x 16 columns: r[2 i] column 4 i + t % 4 of lane t / 4, r[2 i + 1] of lane 8 + t / 4.
+__device__ __forceinline__ void tc_st_16x16(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
@@ -145,13 +146,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   constexpr int kTerms = F16 ? 2 : 3;  // values that stand for a K'
   extern __shared__ __align__(1024) uint8_t smem_linear[];
   __shared__ __align__(16) Decays s_dec[2];
-  __shared__ __align__(8) uint64_t s_bar[32];
+  __shared__ __align__(8) uint64_t s_bar[40];
   __shared__ int s_row[2][F16 ? kBlk : 1];   // fp16, by block: log2 of what a row of A o D and Q' is scaled by
-  __shared__ float s_qmax[F16 ? kBlk : 1];   // largest magnitude of a row of Q'
   __shared__ int s_state_up[2];              // log2 of what S is scaled by
   __shared__ float s_key_down[2];            // what undoes the scale of K'
   __shared__ float s_max[4];
-  __shared__ uint32_t s_kmax[4];
+  __shared__ uint32_t s_kmax[8];
   __shared__ float s_part;                   // e^(sum of the part's logarithms)
   __shared__ uint32_t s_tmem;
   __shared__ int s_b;
@@ -164,25 +164,30 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   const uint32_t bar = smem_u32(s_bar);
   // (by block parity where there are two)
   const uint32_t q_full = bar, q_empty = bar + 8, k_full = bar + 16, k_empty = bar + 32, v_full = bar + 48, v_ready = bar + 64;
-  const uint32_t v_empty = bar + 80, a_full = bar + 96, a_read = bar + 104, p_ready = bar + 112, qp_ready = bar + 120;
-  const uint32_t s_ready = bar + 128, kt_full = bar + 136, kt_empty = bar + 152, u_full = bar + 168, u_free = bar + 176;
-  const uint32_t o_full = bar + 184, o_free = bar + 192, g_full = bar + 200, g_empty = bar + 216, q_known = bar + 232;
+  const uint32_t v_empty = bar + 80, a_full = bar + 96, p_ready = bar + 112;
+  const uint32_t s_ready = bar + 128, kt_full = bar + 256, kt_empty = bar + 288, u_full = bar + 168, u_free = bar + 176;
+  const uint32_t o_full = bar + 184, o_free = bar + 192, g_full = bar + 200, g_empty = bar + 216;
   const uint32_t drained = bar + 240;
   if (tid == 0) {
     mbar_init(q_full, 1); mbar_init(q_empty, 5);
+#pragma unroll 1
     for (int i = 0; i < 16; i += 8) {
-      mbar_init(k_full + i, 1); mbar_init(k_empty + i, 5);
-      mbar_init(v_full + i, 1); mbar_init(v_ready + i, 1); mbar_init(v_empty + i, 1);
-      mbar_init(kt_full + i, 4); mbar_init(kt_empty + i, 1);
+      mbar_init(k_full + i, 1); mbar_init(k_empty + i, 9);
+      mbar_init(v_full + i, 1); mbar_init(v_empty + i, 1);
       mbar_init(g_full + i, 1); mbar_init(g_empty + i, 16);
     }
-    mbar_init(a_full, 1); mbar_init(a_read, 4); mbar_init(p_ready, 4); mbar_init(qp_ready, 4);
+#pragma unroll 1
+    for (int i = 0; i < 8 * kKeySlots; i += 8) {
+      mbar_init(kt_full + i, 4);
+      mbar_init(kt_empty + i, 1);
+    }
+    mbar_init(v_ready, 4); mbar_init(a_full, 1); mbar_init(p_ready, 4);
     mbar_init(s_ready, 4); mbar_init(u_full, 1); mbar_init(u_free, 4);
-    mbar_init(o_full, 1); mbar_init(o_free, 4); mbar_init(q_known, 4);
+    mbar_init(o_full, 1); mbar_init(o_free, 4);
     mbar_init(drained, 1);
     fence_barrier_init();
   }
-  if (tid == 32 * 17) {
+  if (tid == 32 * 21) {
     prefetch_tensormap(&p.tm_q);
     prefetch_tensormap(&p.tm_k);
     prefetch_tensormap(&p.tm_v);
@@ -200,6 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     __syncthreads();
     if (tid < p.r.B) {
       int place = 0;
+#pragma unroll 1
       for (int i = 0; i < p.r.B; ++i) place += len[i] > n || (len[i] == n && i < tid) ? 1 : 0;
       if (place == item / a.Hv) s_b = tid;
     }
@@ -211,6 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   const Span s = load_span(a, p.r, b);
   if (s.n == 0) return;  // (as the other CTAs of the cluster)
   if (!span_allowed(a, p.r, b, s, h == 0 && part == 0)) {
+#pragma unroll 1
     for (int i = part * kThreads + tid; i < s.n * (DV / 8); i += parts * kThreads)
       *reinterpret_cast<uint4*>(a.o + ((long long)(s.row0 + i / (DV / 8)) * a.Hv + h) * DV + i % (DV / 8) * 8) =
           make_uint4(0, 0, 0, 0);
@@ -222,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   const int n1 = parts > 1 && !last ? n2 : 0;                                 // summed up before
   // step i: block first + i of the part's own sum for i < n1, then of the pass proper
 
-  if (warp == 16) {
+  if (warp == 20) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
@@ -253,14 +260,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   // the block of step i, and its token rows that are the sequence's
   const auto block_of = [&](int i) { return first + (i < n1 ? i : i - n1); };
 
-  if (warp >= 16) {
+  if (warp >= 20) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-    if (warp == 17) {
+    if (warp == 21) {
       // ================= TMA =================
       const uint32_t lead = elect_lane();
       auto load = [&](uint32_t dst, const CUtensorMap* m, int halves, int head, int row, uint32_t full) {
         if (lead) {
           mbar_expect_tx(full, (uint32_t)(halves * kHalf));
+#pragma unroll 1
           for (int i = 0; i < halves; ++i) tma_load_3d(dst + i * kHalf, m, i * 64, head, row, full);
         }
         __syncwarp();
@@ -269,14 +277,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       auto ahead = [&](int c) {
         if (lead && c < n2) {
           const int row = s.row0 + (first + c) * kBlk;
+#pragma unroll 1
           for (int x = 0; x < HK; ++x) {
             prefetch_3d(&p.tm_k, x * 64, hk, row);
             prefetch_3d(&p.tm_q, x * 64, hk, row);
           }
+#pragma unroll 1
           for (int x = 0; x < HV; ++x) prefetch_3d(&p.tm_v, x * 64, h, row);
         }
         __syncwarp();
       };
+#pragma unroll 1
       for (int c = 1; c < kAhead; ++c) ahead(c);
       auto step = [&](int i, bool full) {
         ahead(i + kAhead);
@@ -290,10 +301,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         wait(v_empty + 8 * x, free);
         load(sv + x * kTile, &p.tm_v, HV, h, row, v_full + 8 * x);
       };
+#pragma unroll 1
       for (int i = 0; i < n1; ++i) step(i, false);
       meet();  // (K's tiles hold the parts' sums until the second one)
       meet();
       fence_proxy_async_shared();
+#pragma unroll 1
       for (int i = 0; i < n2; ++i) step(n1 + i, true);
       // no copy is under way when the CTA ends, also where a warp went on without
       // waiting: the last fill of every tile
@@ -301,6 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       dead = false;
       const int n = n1 + n2;
       if (n2 > 0) wait(q_full, (n2 + 1) & 1);
+#pragma unroll 1
       for (int x = 0; x < 2; ++x)
         if (n > x) {
           const int fills = (n - x + 1) >> 1;
@@ -308,29 +322,30 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           wait(v_full + 8 * x, (fills + 1) & 1);
         }
       dead |= gave_up;
-    } else if (warp == 16) {
+    } else if (warp == 20) {
       // ================= products =================
       const uint32_t lead = elect_lane();
       const uint32_t id_a = idesc_16(F16, 128, kBlk, false), id_o = idesc_16(F16, 128, DV, true);
-      uint64_t qd = sdesc_sw128(sq), kd = sdesc_sw128(sk), vd = sdesc_sw128_n(sv, kHalf), sd = sdesc_sw128_n(ss, DK * 128);
-      int term = 0;  // K' values so far
+      const uint64_t qd = sdesc_sw128(sq), kd = sdesc_sw128(sk), vd = sdesc_sw128_n(sv, kHalf), sd = sdesc_sw128_n(ss, DK * 128);
+      int piece = 0;  // of K' so far
       auto update = [&](int i) {  // U of step i
         const int x = i & 1;
-        wait(v_ready + 8 * x, (i >> 1) & 1);
+        wait(v_full + 8 * x, (i >> 1) & 1);
+        if (s.n - block_of(i) * kBlk < kBlk) wait(v_ready, 0);  // (the sequence's last block)
         wait(u_free, (i + 1) & 1);
 #pragma unroll 1
-        for (int j = 0; j < kTerms; ++j, ++term) {
-          const int y = term & 1;
-          wait(kt_full + 8 * y, (term >> 1) & 1);
+        for (int j = 0; j < 2 * kTerms; ++j, ++piece) {
+          const int y = piece % kKeySlots;
+          wait(kt_full + 8 * y, (piece / kKeySlots) & 1);
           tc_fence_after();
-          asm volatile("" : "+l"(vd));  // (its sums are made anew: few registers)
-          const uint64_t v = vd + (uint32_t)(x * kTile >> 4);
+          const uint64_t v = vd + (uint32_t)((x * kTile + (j >= kTerms ? kHalf / 2 : 0)) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < kBlk / 16; ++kk) tc_mma_ts_el(tu, tk + y * 64 + kk * 8, v + kk * 128, id_o, j > 0 || kk > 0, lead);
+          for (int kk = 0; kk < 4; ++kk) tc_mma_ts_el(tu, tk + y * 32 + kk * 8, v + kk * 128, id_o, j > 0 || kk > 0, lead);
           tc_commit_el(kt_empty + 8 * y, lead);
         }
         tc_commit_el(u_full, lead);
       };
+#pragma unroll 1
       for (int i = 0; i < n1; ++i) {
         update(i);
         tc_commit_el(k_empty + 8 * (i & 1), lead);
@@ -338,12 +353,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       }
       meet();
       meet();
+#pragma unroll 1
       for (int c = 0; c < n2; ++c) {
         const int i = n1 + c, x = i & 1;
         wait(k_full + 8 * x, (i >> 1) & 1);
         wait(q_full, c & 1);
         tc_fence_after();
-        asm volatile("" : "+l"(qd), "+l"(kd), "+l"(sd));
         const uint64_t k = kd + (uint32_t)(x * kTile >> 4);
 #pragma unroll
         for (int kk = 0; kk < DK / 16; ++kk) {
@@ -356,13 +371,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         update(i);
         wait(s_ready, c & 1);
         wait(o_free, (c + 1) & 1);
-        wait(qp_ready, c & 1);
+        wait(p_ready, c & 1);
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < DK / 16; ++kk) tc_mma_ts_el(to, ta + 64 + kk * 8, sd + kk * 128, id_o, kk > 0, lead);
-        wait(p_ready, c & 1);
-        tc_fence_after();
-        asm volatile("" : "+l"(vd));
         const uint64_t v = vd + (uint32_t)(x * kTile >> 4);
 #pragma unroll
         for (int kk = 0; kk < kBlk / 16; ++kk) tc_mma_ts_el(to, ta + kk * 8, v + kk * 128, id_o, 1, lead);
@@ -371,64 +383,60 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       }
       tc_commit_el(drained, lead);  // every product has ended before tensor memory is given back
       wait(drained, 0);
-    } else if (warp == 18) {
+    } else {
       // ================= decays =================
-      for (int i = 0; i < n1 + n2; ++i) {
-        if (i == n1) {
+      const int slot = warp - 22;
+      bool met = false;
+      float next[4];
+      const auto fetch = [&](int i) {
+        const int t0 = block_of(i) * kBlk + lane * 4;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) next[j] = t0 + j < s.n ? a.g[(s.row0 + t0 + j) * a.g_stride + h] : 0.f;
+      };
+      if (slot < n1 + n2) fetch(slot);
+#pragma unroll 1
+      for (int i = slot; i < n1 + n2; i += 2) {
+        if (!met && i >= n1) {
           meet();
           meet();
+          met = true;
         }
-        const int t0 = block_of(i) * kBlk + lane * 4, slot = i & 1;
-        double g[4];
+        // sums of logarithms to base 2 as pairs of fp32 values
+        FF g[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          g[j] = t0 + j < s.n ? (double)bounded_g(a.g[(s.row0 + t0 + j) * a.g_stride + h]) * 1.4426950408889634 : 0.0;
-#pragma unroll
-        for (int j = 1; j < 4; ++j) g[j] += g[j - 1];
-        double x = g[3];
+        for (int j = 0; j < 4; ++j) {
+          const float x = bounded_g(next[j]), hi = x * 0x1.715476p+0f;
+          g[j] = ff_fast_two_sum(hi, fmaf(x, 0x1.4ae0cp-26f, fmaf(x, 0x1.715476p+0f, -hi)));
+          if (j) g[j] = ff_add(g[j - 1], g[j]);
+        }
+        if (i + 2 < n1 + n2) fetch(i + 2);
+        FF x = g[3];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const double y = __shfl_up_sync(0xffffffffu, x, o);
-          if (lane >= o) x += y;
+          const FF y = {__shfl_up_sync(0xffffffffu, x.h, o), __shfl_up_sync(0xffffffffu, x.l, o)};
+          if (lane >= o) x = ff_add(y, x);
         }
-        const double total = __shfl_sync(0xffffffffu, x, 31);
-        const double before = __shfl_up_sync(0xffffffffu, x, 1);
+        const FF total = {__shfl_sync(0xffffffffu, x.h, 31), __shfl_sync(0xffffffffu, x.l, 31)};
+        FF before = {__shfl_up_sync(0xffffffffu, x.h, 1), __shfl_up_sync(0xffffffffu, x.l, 1)};
+        if (lane == 0) before = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) g[j] = ff_add(before, g[j]);
+        const FF end = {__shfl_sync(0xffffffffu, g[3].h, lane | 7), __shfl_sync(0xffffffffu, g[3].l, lane | 7)};
+        const float2 all = decay_of(total.h * 0x1.62e43p-1f + fmaf(total.l, 0x1.62e43p-1f, total.h * -0x1.05c61p-29f));
         wait(g_empty + 8 * slot, ((i >> 1) + 1) & 1);
         Decays& d = s_dec[slot];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const double G = (lane ? before : 0.0) + g[j];
-          const float hi = (float)G;
-          d.gh[lane * 4 + j] = -hi;
-          d.gl[lane * 4 + j] = (float)(hi - G);
-          d.k[lane * 4 + j] = exp2f((float)(total - G));
-          d.q[lane * 4 + j] = exp2f(hi);
+          d.gh[lane * 4 + j] = -g[j].h;
+          d.gl[lane * 4 + j] = -g[j].l;
+          d.k[lane * 4 + j] = kv::ex2((total.h - g[j].h) + (total.l - g[j].l));
+          d.q[lane * 4 + j] = kv::ex2(g[j].h + g[j].l);
+          d.piece[lane * 4 + j] = kv::ex2((end.h - g[j].h) + (end.l - g[j].l));
         }
-        if (lane == 0) d.all = decay_of((float)(total * 0.6931471805599453));
+        if (lane == 0) d.all = all;
         arrive(g_full + 8 * slot);
       }
-      if (n2 == 0) {
-        meet();
-        meet();
-      }
-    } else {
-      // ================= V behind the sequence's end =================
-      for (int i = 0; i < n1 + n2; ++i) {
-        if (i == n1) {
-          meet();
-          meet();
-        }
-        const int x = i & 1, rows = s.n - block_of(i) * kBlk;
-        wait(v_full + 8 * x, (i >> 1) & 1);
-        if (rows < kBlk) {
-          for (int at = rows * 128 + lane * 16; at < kHalf; at += 512)
-#pragma unroll
-            for (int y = 0; y < HV; ++y) st_s128(sv + x * kTile + y * kHalf + at, 0u, 0u, 0u, 0u);
-          fence_proxy_async_shared();
-        }
-        arrive(v_ready + 8 * x);
-      }
-      if (n2 == 0) {
+      if (!met) {
         meet();
         meet();
       }
@@ -436,6 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   } else if (warp < 4) {
     // ================= A o D: a thread is a token's row =================
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsScore));
+#pragma unroll 1
     for (int i = 0; i < n1; ++i) {
       wait(g_full + 8 * (i & 1), (i >> 1) & 1);
       arrive(g_empty + 8 * (i & 1));
@@ -443,16 +452,27 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     meet();
     meet();
     const uint32_t tr = ta + ((uint32_t)(warp * 32) << 16);
+#pragma unroll 1
     for (int c = 0; c < n2; ++c) {
       const int i = n1 + c;
       const Decays& d = s_dec[i & 1];
+      const auto query = [&](int j) { return ld_s128(sq + (j >> 3) * kHalf + tid * 128 + (((j & 7) ^ (tid & 7)) << 4)); };
       wait(g_full + 8 * (i & 1), (i >> 1) & 1);
+      wait(q_full, c & 1);
+      const float gh = -d.gh[tid], gl = -d.gl[tid];
+      float up = F16 ? 1.f : a.scale, fq = d.q[tid];  // of A o D, of Q'
+      uint32_t mq = 0;
+      if constexpr (F16)
+#pragma unroll 4
+        for (int j = 0; j < DK / 8; ++j) {
+          const uint4 v = query(j);
+          mq = __vmaxu2(__vmaxu2(mq, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu)), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+        }
       wait(a_full, c & 1);
       tc_fence_after();
-      const float2 gh = make_float2(-d.gh[tid], -d.gh[tid]), gl = make_float2(-d.gl[tid], -d.gl[tid]);
-      float up = 1.f;
       if constexpr (F16) {  // the largest of the row's |q . k| and of its Q' (times S's scale) to about 2^13
         float m = 0.f;
+#pragma unroll 1
         for (int j = 0; j <= warp; ++j) {
           uint32_t x[32];
           tc_ld32(tr + j * 32, x);
@@ -461,55 +481,81 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           for (int e = 0; e < 32; ++e)
             if (j < warp || e <= lane) m = fmaxf(m, fabsf(__uint_as_float(x[e])));
         }
-        wait(q_known, c & 1);
         wait(s_ready, c & 1);
-        const int e = max(-100, min(lift_of(m), lift_of(s_qmax[tid]) + s_state_up[c & 1]));
+        mq = min(max(mq & 0xffffu, mq >> 16), 0x7bffu);
+        const int up_s = s_state_up[c & 1], e = max(-100, min(lift_of(m), lift_of(kv::unpack2<true>(mq).x * fq) + up_s));
         up = pow2(e);
+        fq = e - up_s < -126 ? 0.f : fq * pow2(min(e - up_s, 127));
         s_row[c & 1][tid] = e;
+      } else {
+        fq *= a.scale;
       }
       // (rolled loops: with all roles' loops unrolled their code did not stay in the
       // instruction cache, and a block took twice as long)
 #pragma unroll 1
       for (int j = 0; j < 4; ++j) {
         uint32_t pk[16], x[32];
-        if (j <= warp) {
-          tc_ld32(tr + j * 32, x);
-          tc_ld_wait();
-          if (j == warp) {  // the row has been read: Q' may take its place from column 64 on
-            tc_fence_before();
-            arrive(a_read);
-          }
-          const float4* nh = reinterpret_cast<const float4*>(d.gh + j * 32);
-          const float4* nl = reinterpret_cast<const float4*>(d.gl + j * 32);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 a4 = nh[e], b4 = nl[e];
-            const float2 t0 = add2(add2(gh, make_float2(a4.x, a4.y)), add2(gl, make_float2(b4.x, b4.y)));
-            const float2 t1 = add2(add2(gh, make_float2(a4.z, a4.w)), add2(gl, make_float2(b4.z, b4.w)));
-            float2 d0 = make_float2(kv::ex2(t0.x), kv::ex2(t0.y)), d1 = make_float2(kv::ex2(t1.x), kv::ex2(t1.y));
-            if constexpr (F16) {
-              d0 = mul2(d0, make_float2(up, up));
-              d1 = mul2(d1, make_float2(up, up));
-            }
-            d0 = mul2(d0, make_float2(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1])));
-            d1 = mul2(d1, make_float2(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])));
-            pk[2 * e] = kv::pack2<F16>(d0.x, d0.y);
-            pk[2 * e + 1] = kv::pack2<F16>(d1.x, d1.y);
-          }
-          if (j == warp) {  // later tokens (what stands there may be NaN: cleared as bits)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) pk[e] &= (2 * e <= lane ? 0xffffu : 0u) | (2 * e + 1 <= lane ? 0xffff0000u : 0u);
-          }
-        } else {
+        if (j > warp) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) pk[e] = 0u;
+        } else {
+          tc_ld32(tr + j * 32, x);
+          tc_ld_wait();
+          if (j < warp) {
+            // 32 tokens before all of the warp's, p the last of them: D_ij = e^(G_i - G_p)
+            // e^(G_p - G_j), neither above 1
+            const float f = kv::ex2((gh + d.gh[j * 32 + 31]) + (gl + d.gl[j * 32 + 31])) * up;
+            const float4* ep = reinterpret_cast<const float4*>(d.piece + j * 32);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 w = ep[e];
+              const float2 d0 = mul2(make_float2(w.x, w.y), make_float2(f, f)), d1 = mul2(make_float2(w.z, w.w), make_float2(f, f));
+              const float2 p0 = mul2(d0, make_float2(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1])));
+              const float2 p1 = mul2(d1, make_float2(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])));
+              pk[2 * e] = kv::pack2<F16>(p0.x, p0.y);
+              pk[2 * e + 1] = kv::pack2<F16>(p1.x, p1.y);
+            }
+          } else {
+            const float4* nh = reinterpret_cast<const float4*>(d.gh + j * 32);
+            const float4* nl = reinterpret_cast<const float4*>(d.gl + j * 32);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 a4 = nh[e], b4 = nl[e];
+              const float2 t0 = add2(add2(make_float2(gh, gh), make_float2(a4.x, a4.y)), add2(make_float2(gl, gl), make_float2(b4.x, b4.y)));
+              const float2 t1 = add2(add2(make_float2(gh, gh), make_float2(a4.z, a4.w)), add2(make_float2(gl, gl), make_float2(b4.z, b4.w)));
+              const float2 d0 = mul2(make_float2(kv::ex2(t0.x), kv::ex2(t0.y)), make_float2(up, up));
+              const float2 d1 = mul2(make_float2(kv::ex2(t1.x), kv::ex2(t1.y)), make_float2(up, up));
+              const float2 p0 = mul2(d0, make_float2(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1])));
+              const float2 p1 = mul2(d1, make_float2(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])));
+              // later tokens (what stands there may be NaN) are cleared as bits
+              pk[2 * e] = kv::pack2<F16>(p0.x, p0.y) & ((4 * e <= lane ? 0xffffu : 0u) | (4 * e + 1 <= lane ? 0xffff0000u : 0u));
+              pk[2 * e + 1] = kv::pack2<F16>(p1.x, p1.y) & ((4 * e + 2 <= lane ? 0xffffu : 0u) | (4 * e + 3 <= lane ? 0xffff0000u : 0u));
+            }
+          }
         }
         tc_st16(tr + j * 16, pk);
       }
+      arrive(g_empty + 8 * (i & 1));
+      // Q' in the columns from 64 on, which the row has read
+#pragma unroll 1
+      for (int j = 0; j < DK / 32; ++j) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint4 v = query(j * 4 + e);
+          w[4 * e] = v.x; w[4 * e + 1] = v.y; w[4 * e + 2] = v.z; w[4 * e + 3] = v.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float2 x = mul2(kv::unpack2<F16>(w[e]), make_float2(fq, fq));
+          w[e] = kv::pack2<F16>(x.x, x.y);
+        }
+        tc_st16(tr + 64 + j * 16, w);
+      }
+      arrive(q_empty);
       tc_st_wait();
       tc_fence_before();
       arrive(p_ready);
-      arrive(g_empty + 8 * (i & 1));
     }
   } else if (warp < 8) {
     // ================= the state: a thread is a row =================
@@ -588,6 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       float decay = 1.f;
 #pragma unroll
       for (int j = 0; j < DV / 2; ++j) S[j] = make_float2(0.f, 0.f);
+#pragma unroll 1
       for (int i = 0; i < n1; ++i) step(i, &decay);
       if (n1 > 0) {  // columns 4 j of all rows side by side, where K was
         if (held)
@@ -601,6 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     }
     if (n2 > 0) {
       exchange(true);
+#pragma unroll 1
       for (int r = 0; r < part; ++r) {  // the parts before, in their order
         const float e = peer_f32(peer(smem_u32(&s_part), r));
         const uint32_t from = peer(meet_at, r);
@@ -614,6 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       }
     }
     meet();
+#pragma unroll 1
     for (int c = 0; c < n2; ++c) {
       float up = 1.f;
       if constexpr (F16) {
@@ -650,61 +699,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       exchange(false);
     }
   } else if (warp < 12) {
-    // ================= Q' and the output: a thread is a token's row =================
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsOut));
+    // ================= the output: a thread is a token's row =================
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOut));
     const int t = tid - 256;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    for (int i = 0; i < n1; ++i) {
-      wait(g_full + 8 * (i & 1), (i >> 1) & 1);
-      arrive(g_empty + 8 * (i & 1));
-    }
     meet();
     meet();
+#pragma unroll 1
     for (int c = 0; c < n2; ++c) {
-      const int i = n1 + c;
-      wait(g_full + 8 * (i & 1), (i >> 1) & 1);
-      const float e = s_dec[i & 1].q[t];
-      arrive(g_empty + 8 * (i & 1));
-      uint32_t q[DK / 2];
-      wait(q_full, c & 1);
-#pragma unroll
-      for (int j = 0; j < DK / 8; ++j) {
-        const uint4 v = ld_s128(sq + (j >> 3) * kHalf + t * 128 + (((j & 7) ^ (t & 7)) << 4));
-        q[4 * j] = v.x; q[4 * j + 1] = v.y; q[4 * j + 2] = v.z; q[4 * j + 3] = v.w;
-      }
-      arrive(q_empty);
-      float f = e;
-      if constexpr (F16) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < DK / 2; ++j) m = __vmaxu2(m, q[j] & 0x7fff7fffu);
-        m = min(max(m & 0xffffu, m >> 16), 0x7bffu);
-        s_qmax[t] = kv::unpack2<true>(m).x * e;
-        arrive(q_known);
-        wait(a_read, c & 1);
-        const int x = s_row[c & 1][t] - s_state_up[c & 1];
-        f = x < -126 ? 0.f : e * pow2(min(x, 127));
-      }
-#pragma unroll
-      for (int j = 0; j < DK / 2; ++j) {
-        const float2 x = mul2(kv::unpack2<F16>(q[j]), make_float2(f, f));
-        q[j] = kv::pack2<F16>(x.x, x.y);
-      }
-      if constexpr (!F16) wait(a_read, c & 1);
-      tc_fence_after();
-#pragma unroll
-      for (int j = 0; j < DK / 32; ++j) {
-        uint32_t w[16];
-#pragma unroll
-        for (int x = 0; x < 16; ++x) w[x] = q[j * 16 + x];
-        tc_st16(ta + lanes + 64 + j * 16, w);
-      }
-      tc_st_wait();
-      tc_fence_before();
-      arrive(qp_ready);
       wait(o_full, c & 1);
       tc_fence_after();
-      const float scale = F16 ? a.scale * pow2(-s_row[c & 1][t]) : a.scale;
+      const float scale = F16 ? a.scale * pow2(-s_row[c & 1][t]) : 1.f;
 #pragma unroll 1
       for (int j = 0; j < DV / 32; ++j) {
         uint32_t x[32], w[16];
@@ -716,7 +721,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         }
 #pragma unroll
         for (int y = 0; y < 16; ++y) {
-          const float2 o = mul2(make_float2(__uint_as_float(x[2 * y]), __uint_as_float(x[2 * y + 1])), make_float2(scale, scale));
+          float2 o = make_float2(__uint_as_float(x[2 * y]), __uint_as_float(x[2 * y + 1]));
+          if constexpr (F16) o = mul2(o, make_float2(scale, scale));
           w[y] = kv::pack2<F16>(o.x, o.y);
         }
         // rows of 64 values go out together, eight lanes a row: a store of one piece
@@ -739,11 +745,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       }
     }
   } else {
-    // ================= K'^T: a warp has 32 of its rows (values of a key) =================
+    // ================= K'^T of 64 tokens: a warp has 32 of its rows (values of a key) =================
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsKey));
-    const int w = warp - 12;
+    const int w = warp & 3, part = (warp - 12) >> 2;  // (its place in shared memory: warp - 12)
     const bool held = w * 32 < DK;
-    int term = 0;
+    int piece = part * kTerms;
+#pragma unroll 1
     for (int i = 0; i < n1 + n2; ++i) {
       if (i == n1) {
         meet();
@@ -752,18 +759,28 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       const int x = i & 1, rows = s.n - block_of(i) * kBlk;
       const Decays& d = s_dec[x];
       wait(g_full + 8 * x, (i >> 1) & 1);
+      if (rows < kBlk && part == 0) {  // the sequence's last block: V behind its end becomes zeros
+        wait(v_full + 8 * x, (i >> 1) & 1);
+#pragma unroll 1
+        for (int at = rows * 128 + (tid & 127) * 16; at < kHalf; at += 128 * 16)
+#pragma unroll
+          for (int y = 0; y < HV; ++y) st_s128(sv + x * kTile + y * kHalf + at, 0u, 0u, 0u, 0u);
+        fence_proxy_async_shared();
+        arrive(v_ready);
+      }
       wait(k_full + 8 * x, (i >> 1) & 1);
       // this lane's row of the matrices: tokens (lane & 7) + 8 (lane >> 4), the warp's first or
       // second 8 values of 16 by (lane >> 3) & 1
-      const uint32_t tile = sk + x * kTile + (w >> 1) * kHalf;
-      const auto fetch = [&](int g, int half, uint32_t (&m)[4]) {
-        const int tok = g * 16 + (lane & 7) + ((lane >> 4) << 3), piece = (w & 1) * 4 + half * 2 + ((lane >> 3) & 1);
-        ldmatrix4_t(tile + tok * 128 + ((piece ^ (tok & 7)) << 4), m);
-        if (g * 16 + 16 > rows) {  // tokens behind the end (which may be NaN) become zeros
+      const uint32_t tile = sk + x * kTile + (w >> 1) * kHalf + (part * 64 + (lane & 7) + ((lane >> 4) << 3)) * 128;
+      const int left = rows - part * 64;
+      const auto fetch = [&](int g, int half, uint32_t (&m)[4]) {  // 16 tokens, 16 values
+        const int at = (w & 1) * 4 + half * 2 + ((lane >> 3) & 1);
+        ldmatrix4_t(tile + g * 2048 + ((at ^ (lane & 7)) << 4), m);
+        if (g * 16 + 16 > left) {  // tokens behind the end (which may be NaN) become zeros
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             const int t0 = g * 16 + (y >> 1) * 8 + (lane & 3) * 2;
-            m[y] &= (t0 < rows ? 0xffffu : 0u) | (t0 + 1 < rows ? 0xffff0000u : 0u);
+            m[y] &= (t0 < left ? 0xffffu : 0u) | (t0 + 1 < left ? 0xffff0000u : 0u);
           }
         }
       };
@@ -772,96 +789,73 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         uint32_t m = 0;
         if (held)
 #pragma unroll 2
-          for (int y = 0; y < 16; ++y) {
+          for (int y = 0; y < 8; ++y) {
             uint32_t v[4];
             fetch(y >> 1, y & 1, v);
             m = __vmaxu2(__vmaxu2(m, __vmaxu2(v[0] & 0x7fff7fffu, v[1] & 0x7fff7fffu)),
                          __vmaxu2(v[2] & 0x7fff7fffu, v[3] & 0x7fff7fffu));
           }
         m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
-        asm volatile("bar.sync 2, 128;" ::: "memory");  // the last block's have been read
-        if (lane == 0) s_kmax[w] = m;
-        asm volatile("bar.sync 2, 128;" ::: "memory");
-        m = min(max(max(s_kmax[0], s_kmax[1]), max(s_kmax[2], s_kmax[3])), 0x7bffu);
-        const int e = lift_of(kv::unpack2<true>(m).x);
+        asm volatile("bar.sync 2, 256;" ::: "memory");  // the last block's have been read
+        if (lane == 0) s_kmax[warp - 12] = m;
+        asm volatile("bar.sync 2, 256;" ::: "memory");
+#pragma unroll
+        for (int y = 0; y < 8; ++y) m = max(m, s_kmax[y]);
+        const int e = lift_of(kv::unpack2<true>(min(m, 0x7bffu)).x);
         up = pow2(e);
         if (tid == 32 * 12) s_key_down[x] = pow2(-e);
       }
       const uint32_t lanes = (uint32_t)(w * 32) << 16;
-      // 16 values of the head by 64 tokens at a time, which takes 16 registers.
-      // The first two values that stand for K', then (bf16) the third.
-      const auto scaled = [&](int g, uint32_t m, bool second) {  // a pair of tokens
-        const float2 e = *reinterpret_cast<const float2*>(&d.k[g * 16 + (second ? 8 : 0) + (lane & 3) * 2]);
-        float2 f = mul2(kv::unpack2<F16>(m), e);
-        if constexpr (F16) f = mul2(f, make_float2(up, up));
-        return f;
-      };
       // what is left of f without its upper 8 bits: three such values are all of an fp32
       const auto rest = [](float2 f) {
         return add2(f, make_float2(-__uint_as_float(__float_as_uint(f.x) & 0xffff0000u), -__uint_as_float(__float_as_uint(f.y) & 0xffff0000u)));
       };
       const auto upper = [](float2 f) { return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632); };
-      const auto free_slot = [&](int n) { wait(kt_empty + 8 * (n & 1), ((n >> 1) + 1) & 1); };
-      free_slot(term);
-      free_slot(term + 1);
-      tc_fence_after();
-      if (held) {
+      // 32 tokens by 16 values of the head at a time, in 8 registers each of the values
+      // that stand for K'
 #pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
-          uint32_t hi[16], lo[16];
+      for (int j = 0; j < 4; ++j) {
+        uint32_t v[kTerms][8];
+        if (held) {
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
+          for (int g = 0; g < 2; ++g) {
             uint32_t m[4];
-            fetch((j & 1) * 4 + g, j >> 1, m);
+            fetch((j >> 1) * 2 + g, j & 1, m);
 #pragma unroll
-            for (int z = 0; z < 4; ++z) hi[4 * g + z] = m[z];
+            for (int z = 0; z < 4; ++z) v[0][4 * g + z] = m[z];
           }
+          const float* e0 = d.k + part * 64 + (j >> 1) * 32 + (lane & 3) * 2;
 #pragma unroll
-          for (int z = 0; z < 16; ++z) {
-            const float2 f = scaled((j & 1) * 4 + (z >> 2), hi[z], z & 2);
+          for (int z = 0; z < 8; ++z) {  // a pair of tokens
+            float2 f = mul2(kv::unpack2<F16>(v[0][z]), *reinterpret_cast<const float2*>(e0 + (z >> 1) * 8));
             if constexpr (F16) {
-              hi[z] = kv::pack2<true>(f.x, f.y);
-              const float2 r = kv::unpack2<true>(hi[z]);
-              lo[z] = kv::pack2<true>(f.x - r.x, f.y - r.y);
+              f = mul2(f, make_float2(up, up));
+              v[0][z] = kv::pack2<true>(f.x, f.y);
+              const float2 r = kv::unpack2<true>(v[0][z]);
+              v[1][z] = kv::pack2<true>(f.x - r.x, f.y - r.y);
             } else {
-              hi[z] = upper(f);
-              lo[z] = upper(rest(f));
+              v[0][z] = upper(f);
+              f = rest(f);
+              v[1][z] = upper(f);
+              v[kTerms - 1][z] = upper(rest(f));
             }
           }
-          const uint32_t to = tk + lanes + ((uint32_t)((j >> 1) * 16) << 16) + (j & 1) * 32;
-          tc_st_16x32(to + (term & 1) * 64, hi);
-          tc_st_16x32(to + ((term + 1) & 1) * 64, lo);
         }
-        tc_st_wait();
-      }
-      tc_fence_before();
-      arrive(kt_full + 8 * (term & 1));
-      arrive(kt_full + 8 * ((term + 1) & 1));
-      term += 2;
-      if constexpr (!F16) {
-        free_slot(term);
+        if (j == 0)
+#pragma unroll
+          for (int y = 0; y < kTerms; ++y) wait(kt_empty + 8 * ((piece + y) % kKeySlots), ((piece + y) / kKeySlots + 1) & 1);
         tc_fence_after();
         if (held) {
-#pragma unroll 1
-          for (int j = 0; j < 4; ++j) {
-            uint32_t v[16];
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              uint32_t m[4];
-              fetch((j & 1) * 4 + g, j >> 1, m);
-#pragma unroll
-              for (int z = 0; z < 4; ++z) v[4 * g + z] = m[z];
-            }
-#pragma unroll
-            for (int z = 0; z < 16; ++z) v[z] = upper(rest(rest(scaled((j & 1) * 4 + (z >> 2), v[z], z & 2))));
-            tc_st_16x32(tk + lanes + ((uint32_t)((j >> 1) * 16) << 16) + (j & 1) * 32 + (term & 1) * 64, v);
-          }
-          tc_st_wait();
+          for (int y = 0; y < kTerms; ++y)
+            tc_st_16x16(tk + lanes + ((uint32_t)((j & 1) * 16) << 16) + (piece + y) % kKeySlots * 32 + (j >> 1) * 16, v[y]);
         }
-        tc_fence_before();
-        arrive(kt_full + 8 * (term & 1));
-        ++term;
       }
+      tc_st_wait();
+      tc_fence_before();
+#pragma unroll
+      for (int y = 0; y < kTerms; ++y) arrive(kt_full + 8 * ((piece + y) % kKeySlots));
+      piece += 2 * kTerms;
       arrive(k_empty + 8 * x);
       arrive(g_empty + 8 * x);
     }
@@ -874,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   if (dead && a.status && lane == 0) atomicOr(a.status, DEV_TIMEOUT);
   tc_fence_before();
   __syncthreads();
-  if (warp == 16) {
+  if (warp == 20) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(ta));
   }
