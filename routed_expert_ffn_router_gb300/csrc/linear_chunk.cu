@@ -31,7 +31,7 @@
 // and without a workspace. Items are started longest first.
 //
 // Warps. 0-3: A o D and Q' (a thread is a token); 4-7: the state (a thread is a row of
-// it); 8-11: the output; 12-15 and 16-19: K' of a block's first and last 64 tokens;
+// it); 8-11: the output; 12-15 and 16-19: K', each group 32 tokens of every 64;
 // 20: issues the products; 21: TMA; 22 and 23: decays of every other block each (one
 // warp for all of them was what the others waited for: 8,000 cycles a block).
 #include <cuda.h>
@@ -61,7 +61,7 @@ constexpr int kTile = 2 * kHalf;
 constexpr int kPitch = 144;             // bytes per row of a warp's output buffer (64 values and a pad)
 constexpr int kSmem = 1024 + 6 * kTile + 4 * 32 * kPitch;  // Q, two of K and of V, S; outputs
 constexpr int kSortB = 512;             // sequences that are put in order of their length
-constexpr int kKeySlots = 4;            // of K', 32 columns (64 tokens) each
+constexpr int kKeyCols = 48;            // tensor memory of a group of K's warps: three values of 32 tokens
 constexpr int kMostParts = 8;
 constexpr int kAhead = 2;               // blocks that are fetched into L2 ahead
 
@@ -174,13 +174,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     for (int i = 0; i < 16; i += 8) {
       mbar_init(k_full + i, 1); mbar_init(k_empty + i, 9);
       mbar_init(v_full + i, 1); mbar_init(v_empty + i, 1);
+      mbar_init(kt_full + i, 4); mbar_init(kt_empty + i, 1);
       mbar_init(g_full + i, 1); mbar_init(g_empty + i, 16);
     }
 #pragma unroll 1
-    for (int i = 0; i < 8 * kKeySlots; i += 8) {
-      mbar_init(kt_full + i, 4);
-      mbar_init(kt_empty + i, 1);
-    }
     mbar_init(v_ready, 4); mbar_init(a_full, 1); mbar_init(p_ready, 4);
     mbar_init(s_ready, 4); mbar_init(u_full, 1); mbar_init(u_free, 4);
     mbar_init(o_full, 1); mbar_init(o_free, 4);
@@ -327,20 +324,22 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       const uint32_t lead = elect_lane();
       const uint32_t id_a = idesc_16(F16, 128, kBlk, false), id_o = idesc_16(F16, 128, DV, true);
       const uint64_t qd = sdesc_sw128(sq), kd = sdesc_sw128(sk), vd = sdesc_sw128_n(sv, kHalf), sd = sdesc_sw128_n(ss, DK * 128);
-      int piece = 0;  // of K' so far
       auto update = [&](int i) {  // U of step i
         const int x = i & 1;
         wait(v_full + 8 * x, (i >> 1) & 1);
         if (s.n - block_of(i) * kBlk < kBlk) wait(v_ready, 0);  // (the sequence's last block)
         wait(u_free, (i + 1) & 1);
+        const uint64_t v = vd + (uint32_t)(x * kTile >> 4);
 #pragma unroll 1
-        for (int j = 0; j < 2 * kTerms; ++j, ++piece) {
-          const int y = piece % kKeySlots;
-          wait(kt_full + 8 * y, (piece / kKeySlots) & 1);
+        for (int j = 0; j < 4; ++j) {  // 32 tokens, by the groups of warps in turn
+          const int y = j & 1;
+          wait(kt_full + 8 * y, j >> 1);  // (two uses a step)
           tc_fence_after();
-          const uint64_t v = vd + (uint32_t)((x * kTile + (j >= kTerms ? kHalf / 2 : 0)) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) tc_mma_ts_el(tu, tk + y * 32 + kk * 8, v + kk * 128, id_o, j > 0 || kk > 0, lead);
+          for (int z = 0; z < kTerms; ++z)
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+              tc_mma_ts_el(tu, tk + y * kKeyCols + z * 16 + kk * 8, v + (uint32_t)(j * 256) + kk * 128, id_o, j > 0 || z > 0 || kk > 0, lead);
           tc_commit_el(kt_empty + 8 * y, lead);
         }
         tc_commit_el(u_full, lead);
@@ -745,11 +744,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       }
     }
   } else {
-    // ================= K'^T of 64 tokens: a warp has 32 of its rows (values of a key) =================
+    // ================= K'^T: a warp has 32 of its rows (values of a key) =================
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsKey));
     const int w = warp & 3, part = (warp - 12) >> 2;  // (its place in shared memory: warp - 12)
     const bool held = w * 32 < DK;
-    int piece = part * kTerms;
 #pragma unroll 1
     for (int i = 0; i < n1 + n2; ++i) {
       if (i == n1) {
@@ -771,16 +769,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       wait(k_full + 8 * x, (i >> 1) & 1);
       // this lane's row of the matrices: tokens (lane & 7) + 8 (lane >> 4), the warp's first or
       // second 8 values of 16 by (lane >> 3) & 1
-      const uint32_t tile = sk + x * kTile + (w >> 1) * kHalf + (part * 64 + (lane & 7) + ((lane >> 4) << 3)) * 128;
-      const int left = rows - part * 64;
-      const auto fetch = [&](int g, int half, uint32_t (&m)[4]) {  // 16 tokens, 16 values
+      const uint32_t tile = sk + x * kTile + (w >> 1) * kHalf + ((lane & 7) + ((lane >> 4) << 3)) * 128;
+      const auto fetch = [&](int t0, int half, uint32_t (&m)[4]) {  // 16 tokens from t0 on, 16 values
         const int at = (w & 1) * 4 + half * 2 + ((lane >> 3) & 1);
-        ldmatrix4_t(tile + g * 2048 + ((at ^ (lane & 7)) << 4), m);
-        if (g * 16 + 16 > left) {  // tokens behind the end (which may be NaN) become zeros
+        ldmatrix4_t(tile + t0 * 128 + ((at ^ (lane & 7)) << 4), m);
+        if (t0 + 16 > rows) {  // tokens behind the end (which may be NaN) become zeros
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            const int t0 = g * 16 + (y >> 1) * 8 + (lane & 3) * 2;
-            m[y] &= (t0 < left ? 0xffffu : 0u) | (t0 + 1 < left ? 0xffff0000u : 0u);
+            const int t = t0 + (y >> 1) * 8 + (lane & 3) * 2;
+            m[y] &= (t < rows ? 0xffffu : 0u) | (t + 1 < rows ? 0xffff0000u : 0u);
           }
         }
       };
@@ -791,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
 #pragma unroll 2
           for (int y = 0; y < 8; ++y) {
             uint32_t v[4];
-            fetch(y >> 1, y & 1, v);
+            fetch(part * 64 + (y >> 1) * 16, y & 1, v);
             m = __vmaxu2(__vmaxu2(m, __vmaxu2(v[0] & 0x7fff7fffu, v[1] & 0x7fff7fffu)),
                          __vmaxu2(v[2] & 0x7fff7fffu, v[3] & 0x7fff7fffu));
           }
@@ -815,16 +812,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       // that stand for K'
 #pragma unroll 1
       for (int j = 0; j < 4; ++j) {
+        const int t0 = (j >> 1) * 64 + part * 32;
         uint32_t v[kTerms][8];
         if (held) {
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             uint32_t m[4];
-            fetch((j >> 1) * 2 + g, j & 1, m);
+            fetch(t0 + g * 16, j & 1, m);
 #pragma unroll
             for (int z = 0; z < 4; ++z) v[0][4 * g + z] = m[z];
           }
-          const float* e0 = d.k + part * 64 + (j >> 1) * 32 + (lane & 3) * 2;
+          const float* e0 = d.k + t0 + (lane & 3) * 2;
 #pragma unroll
           for (int z = 0; z < 8; ++z) {  // a pair of tokens
             float2 f = mul2(kv::unpack2<F16>(v[0][z]), *reinterpret_cast<const float2*>(e0 + (z >> 1) * 8));
@@ -841,21 +839,21 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
             }
           }
         }
-        if (j == 0)
-#pragma unroll
-          for (int y = 0; y < kTerms; ++y) wait(kt_empty + 8 * ((piece + y) % kKeySlots), ((piece + y) / kKeySlots + 1) & 1);
-        tc_fence_after();
+        if (!(j & 1)) {
+          wait(kt_empty + 8 * part, (j >> 1) ^ 1);
+          tc_fence_after();
+        }
         if (held) {
 #pragma unroll
           for (int y = 0; y < kTerms; ++y)
-            tc_st_16x16(tk + lanes + ((uint32_t)((j & 1) * 16) << 16) + (piece + y) % kKeySlots * 32 + (j >> 1) * 16, v[y]);
+            tc_st_16x16(tk + lanes + ((uint32_t)((j & 1) * 16) << 16) + part * kKeyCols + y * 16, v[y]);
+        }
+        if (j & 1) {
+          tc_st_wait();
+          tc_fence_before();
+          arrive(kt_full + 8 * part);
         }
       }
-      tc_st_wait();
-      tc_fence_before();
-#pragma unroll
-      for (int y = 0; y < kTerms; ++y) arrive(kt_full + 8 * ((piece + y) % kKeySlots));
-      piece += 2 * kTerms;
       arrive(k_empty + 8 * x);
       arrive(g_empty + 8 * x);
     }
