@@ -235,12 +235,21 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   tc_fence_after();
   const uint32_t ta = s_tmem, to = ta + 128, tu = ta + 256, tk = ta + 384;  // A (then A o D and Q'), O, U, K' twice
 
-  bool dead = false;  // an expired wait: go on without waiting (the status word says so)
+  // A wait of kTries of up to a microsecond each; after an expired one a warp goes on
+  // without waiting (the status word says so). Few instructions: there are many, and
+  // the roles' code competes for the instruction caches.
+  uint32_t tries = kTries;
   auto wait = [&](uint32_t bar, uint32_t parity) {
-    uint32_t n = dead ? 1u : kTries;
-    while (!mbar_try_wait_ns(bar, parity, 1000) && --n) {
-    }
-    dead |= n == 0;
+    uint32_t left;
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .u32 n;\n mov.u32 n, %3;\n"
+        "W:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n @p bra D;\n"
+        " sub.u32 n, n, 1;\n setp.ne.u32 p, n, 0;\n @p bra W;\n"
+        "D:\n mov.u32 %0, n;\n}"
+        : "=r"(left)
+        : "r"(bar), "r"(parity), "r"(tries)
+        : "memory");
+    tries = left ? tries : 1u;
     __syncwarp();
   };
   auto arrive = [&](uint32_t bar) {
@@ -307,8 +316,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       for (int i = 0; i < n2; ++i) step(n1 + i, true);
       // no copy is under way when the CTA ends, also where a warp went on without
       // waiting: the last fill of every tile
-      const bool gave_up = dead;
-      dead = false;
+      const bool gave_up = tries == 1;
+      tries = kTries;
       const int n = n1 + n2;
       if (n2 > 0) wait(q_full, (n2 + 1) & 1);
 #pragma unroll 1
@@ -318,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           wait(k_full + 8 * x, (fills + 1) & 1);
           wait(v_full + 8 * x, (fills + 1) & 1);
         }
-      dead |= gave_up;
+      if (gave_up) tries = 1;
     } else if (warp == 20) {
       // ================= products =================
       const uint32_t lead = elect_lane();
@@ -863,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     }
   }
 
-  if (dead && a.status && lane == 0) atomicOr(a.status, DEV_TIMEOUT);
+  if (tries == 1 && a.status && lane == 0) atomicOr(a.status, DEV_TIMEOUT);
   tc_fence_before();
   __syncthreads();
   if (warp == 20) {
