@@ -32,8 +32,9 @@
 //
 // Warps. 0-3: A o D and Q' (a thread is a token); 4-7: the state (a thread is a row of
 // it); 8-11: the output; 12-15 and 16-19: K', each group 32 tokens of every 64;
-// 20: issues the products; 21: TMA; 22 and 23: decays of every other block each (one
-// warp for all of them was what the others waited for: 8,000 cycles a block).
+// 20 and 23: issue the products, those of A and O and those of U (a product takes a
+// warp 20 instructions, more time than the tensor cores need for it); 21: TMA; 22:
+// decays, two blocks ahead.
 #include <cuda.h>
 
 #include <atomic>
@@ -167,13 +168,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   const uint32_t v_empty = bar + 80, a_full = bar + 96, p_ready = bar + 112;
   const uint32_t s_ready = bar + 128, kt_full = bar + 256, kt_empty = bar + 288, u_full = bar + 168, u_free = bar + 176;
   const uint32_t o_full = bar + 184, o_free = bar + 192, g_full = bar + 200, g_empty = bar + 216;
-  const uint32_t drained = bar + 240;
+  const uint32_t drained = bar + 240, u_drained = bar + 248;
   if (tid == 0) {
     mbar_init(q_full, 1); mbar_init(q_empty, 5);
 #pragma unroll 1
     for (int i = 0; i < 16; i += 8) {
       mbar_init(k_full + i, 1); mbar_init(k_empty + i, 9);
-      mbar_init(v_full + i, 1); mbar_init(v_empty + i, 1);
+      mbar_init(v_full + i, 1); mbar_init(v_empty + i, 2);
       mbar_init(kt_full + i, 4); mbar_init(kt_empty + i, 1);
       mbar_init(g_full + i, 1); mbar_init(g_empty + i, 16);
     }
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     mbar_init(v_ready, 4); mbar_init(a_full, 1); mbar_init(p_ready, 4);
     mbar_init(s_ready, 4); mbar_init(u_full, 1); mbar_init(u_free, 4);
     mbar_init(o_full, 1); mbar_init(o_free, 4);
-    mbar_init(drained, 1);
+    mbar_init(drained, 1); mbar_init(u_drained, 1);
     fence_barrier_init();
   }
   if (tid == 32 * 21) {
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t ta = s_tmem, to = ta + 128, tu = ta + 256, tk = ta + 384;  // A (then A o D and Q'), O, U, K' twice
+  constexpr uint32_t ta = 0, to = ta + 128, tu = ta + 256, tk = ta + 384;  // (all 512 columns are allocated) A, then A o D and Q'; O; U; K'
 
   // A wait of kTries of up to a microsecond each; after an expired one a warp goes on
   // without waiting (the status word says so). Few instructions: there are many, and
@@ -329,35 +330,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         }
       if (gave_up) tries = 1;
     } else if (warp == 20) {
-      // ================= products =================
+      // ================= products: A and O =================
       const uint32_t lead = elect_lane();
       const uint32_t id_a = idesc_16(F16, 128, kBlk, false), id_o = idesc_16(F16, 128, DV, true);
       const uint64_t qd = sdesc_sw128(sq), kd = sdesc_sw128(sk), vd = sdesc_sw128_n(sv, kHalf), sd = sdesc_sw128_n(ss, DK * 128);
-      auto update = [&](int i) {  // U of step i
+#pragma unroll 1
+      for (int i = 0; i < n1; ++i) {  // (K and V of the first pass are not this warp's)
         const int x = i & 1;
+        wait(k_full + 8 * x, (i >> 1) & 1);
+        arrive(k_empty + 8 * x);
         wait(v_full + 8 * x, (i >> 1) & 1);
-        if (s.n - block_of(i) * kBlk < kBlk) wait(v_ready, 0);  // (the sequence's last block)
-        wait(u_free, (i + 1) & 1);
-        const uint64_t v = vd + (uint32_t)(x * kTile >> 4);
-#pragma unroll 1
-        for (int j = 0; j < 4; ++j) {  // 32 tokens, by the groups of warps in turn
-          const int y = j & 1;
-          wait(kt_full + 8 * y, j >> 1);  // (two uses a step)
-          tc_fence_after();
-#pragma unroll
-          for (int z = 0; z < kTerms; ++z)
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-              tc_mma_ts_el(tu, tk + y * kKeyCols + z * 16 + kk * 8, v + (uint32_t)(j * 256) + kk * 128, id_o, j > 0 || z > 0 || kk > 0, lead);
-          tc_commit_el(kt_empty + 8 * y, lead);
-        }
-        tc_commit_el(u_full, lead);
-      };
-#pragma unroll 1
-      for (int i = 0; i < n1; ++i) {
-        update(i);
-        tc_commit_el(k_empty + 8 * (i & 1), lead);
-        tc_commit_el(v_empty + 8 * (i & 1), lead);
+        arrive(v_empty + 8 * x);
       }
       meet();
       meet();
@@ -376,7 +359,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         tc_commit_el(a_full, lead);
         tc_commit_el(q_empty, lead);
         tc_commit_el(k_empty + 8 * x, lead);
-        update(i);
+        wait(v_full + 8 * x, (i >> 1) & 1);
+        if (s.n - block_of(i) * kBlk < kBlk) wait(v_ready, 0);  // (the sequence's last block)
         wait(s_ready, c & 1);
         wait(o_free, (c + 1) & 1);
         wait(p_ready, c & 1);
@@ -391,24 +375,58 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       }
       tc_commit_el(drained, lead);  // every product has ended before tensor memory is given back
       wait(drained, 0);
+    } else if (warp == 23) {
+      // ================= products: U =================
+      const uint32_t lead = elect_lane(), id_o = idesc_16(F16, 128, DV, true);
+      const uint64_t vd = sdesc_sw128_n(sv, kHalf);
+#pragma unroll 1
+      for (int i = 0; i < n1 + n2; ++i) {
+        if (i == n1) {
+          meet();
+          meet();
+        }
+        const int x = i & 1;
+        wait(v_full + 8 * x, (i >> 1) & 1);
+        if (s.n - block_of(i) * kBlk < kBlk) wait(v_ready, 0);
+        wait(u_free, (i + 1) & 1);
+        const uint64_t v = vd + (uint32_t)(x * kTile >> 4);
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {  // 32 tokens, by the groups of warps in turn
+          const int y = j & 1;
+          wait(kt_full + 8 * y, j >> 1);  // (two uses a step)
+          tc_fence_after();
+#pragma unroll
+          for (int z = 0; z < kTerms; ++z)
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+              tc_mma_ts_el(tu, tk + y * kKeyCols + z * 16 + kk * 8, v + (uint32_t)(j * 256) + kk * 128, id_o, j > 0 || z > 0 || kk > 0, lead);
+          tc_commit_el(kt_empty + 8 * y, lead);
+        }
+        tc_commit_el(u_full, lead);
+        tc_commit_el(v_empty + 8 * x, lead);
+      }
+      if (n2 == 0) {
+        meet();
+        meet();
+      }
+      tc_commit_el(u_drained, lead);
+      wait(u_drained, 0);
     } else {
       // ================= decays =================
-      const int slot = warp - 22;
-      bool met = false;
       float next[4];
       const auto fetch = [&](int i) {
         const int t0 = block_of(i) * kBlk + lane * 4;
 #pragma unroll
         for (int j = 0; j < 4; ++j) next[j] = t0 + j < s.n ? a.g[(s.row0 + t0 + j) * a.g_stride + h] : 0.f;
       };
-      if (slot < n1 + n2) fetch(slot);
+      if (n1 + n2 > 0) fetch(0);
 #pragma unroll 1
-      for (int i = slot; i < n1 + n2; i += 2) {
-        if (!met && i >= n1) {
+      for (int i = 0; i < n1 + n2; ++i) {
+        if (i == n1) {
           meet();
           meet();
-          met = true;
         }
+        const int slot = i & 1;
         // sums of logarithms to base 2 as pairs of fp32 values
         FF g[4];
 #pragma unroll
@@ -417,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           g[j] = ff_fast_two_sum(hi, fmaf(x, 0x1.4ae0cp-26f, fmaf(x, 0x1.715476p+0f, -hi)));
           if (j) g[j] = ff_add(g[j - 1], g[j]);
         }
-        if (i + 2 < n1 + n2) fetch(i + 2);
+        if (i + 1 < n1 + n2) fetch(i + 1);
         FF x = g[3];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -444,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         if (lane == 0) d.all = all;
         arrive(g_full + 8 * slot);
       }
-      if (!met) {
+      if (n2 == 0) {
         meet();
         meet();
       }
