@@ -592,46 +592,55 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     float4* state = reinterpret_cast<float4*>(a.state + ((long long)s.slot * a.Hv + h) * DK * DV);
     float2 S[DV / 2];
     // The state from or to memory, 64 columns at a time through S's tile, so that
-    // memory is touched along rows (16 pieces of 16 bytes each, in places that
-    // keep a warp's rows in different banks).
-    auto exchange = [&](bool in) {
+    // memory is touched along rows (16 pieces of 16 bytes each, in places that keep a
+    // warp's rows in different banks). Coming in, all of a thread's pieces are under
+    // way together.
+    const int piece_row = row >> 4, piece = row & 15;
+    const auto place = [&](int r, int j) { return ss + r * 256 + ((j ^ (r & 15)) << 4); };
+    auto put = [&](int i, uint32_t at) {  // S[2 i], S[2 i + 1]
+      st_s128(at, __float_as_uint(S[2 * i].x), __float_as_uint(S[2 * i].y), __float_as_uint(S[2 * i + 1].x), __float_as_uint(S[2 * i + 1].y));
+    };
+    auto get = [&](int i, uint32_t at) {
+      const uint4 f = ld_s128(at);
+      S[2 * i] = make_float2(__uint_as_float(f.x), __uint_as_float(f.y));
+      S[2 * i + 1] = make_float2(__uint_as_float(f.z), __uint_as_float(f.w));
+    };
+    auto meet_state = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+    auto bring = [&] {
+#pragma unroll
+      for (int i = 0; i < HV * DK / 8; ++i) {  // (DK / 8 <= 16: a thread's part of 64 columns)
+        const int x = i / (DK / 8), r = i % (DK / 8) * 8 + piece_row, at = x * 16 + i % (DK / 8);
+        const float4 f = state[r * (DV / 4) + x * 16 + piece];
+        S[2 * at] = make_float2(f.x, f.y);
+        S[2 * at + 1] = make_float2(f.z, f.w);
+      }
 #pragma unroll
       for (int x = 0; x < HV; ++x) {
-        const uint32_t mine = ss + row * 256;
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (!in) {
-          if (held)
+        meet_state();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float2 u = S[x * 32 + 2 * j], w = S[x * 32 + 2 * j + 1];
-              st_s128(mine + ((j ^ (row & 15)) << 4), __float_as_uint(u.x), __float_as_uint(u.y), __float_as_uint(w.x), __float_as_uint(w.y));
-            }
-          asm volatile("bar.sync 1, 128;" ::: "memory");
-        }
-#pragma unroll 8
+        for (int i = 0; i < DK / 8; ++i) put(x * 16 + i, place(i * 8 + piece_row, piece));
+        meet_state();
+        if (held)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) get(x * 16 + j, place(row, j));
+      }
+      meet_state();  // S's tile is free for S
+    };
+    auto leave = [&] {
+#pragma unroll
+      for (int x = 0; x < HV; ++x) {
+        meet_state();
+        if (held)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) put(x * 16 + j, place(row, j));
+        meet_state();
+#pragma unroll
         for (int i = 0; i < DK / 8; ++i) {
-          const int r = i * 8 + (row >> 4), j = row & 15;
-          const uint32_t at = ss + r * 256 + ((j ^ (r & 15)) << 4);
-          float4* m = state + r * (DV / 4) + x * 16 + j;
-          if (in) {
-            const float4 f = *m;
-            st_s128(at, __float_as_uint(f.x), __float_as_uint(f.y), __float_as_uint(f.z), __float_as_uint(f.w));
-          } else {
-            const uint4 f = ld_s128(at);
-            *m = make_float4(__uint_as_float(f.x), __uint_as_float(f.y), __uint_as_float(f.z), __uint_as_float(f.w));
-          }
-        }
-        if (in) {
-          asm volatile("bar.sync 1, 128;" ::: "memory");
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const uint4 f = held ? ld_s128(mine + ((j ^ (row & 15)) << 4)) : make_uint4(0, 0, 0, 0);
-            S[x * 32 + 2 * j] = make_float2(__uint_as_float(f.x), __uint_as_float(f.y));
-            S[x * 32 + 2 * j + 1] = make_float2(__uint_as_float(f.z), __uint_as_float(f.w));
-          }
+          const int r = i * 8 + piece_row;
+          const uint4 f = ld_s128(place(r, piece));
+          state[r * (DV / 4) + x * 16 + piece] = make_float4(__uint_as_float(f.x), __uint_as_float(f.y), __uint_as_float(f.z), __uint_as_float(f.w));
         }
       }
-      if (in) asm volatile("bar.sync 1, 128;" ::: "memory");  // S's tile is free for S
     };
     auto step = [&](int i, float* decay) {  // S <- e^G S + U
       wait(g_full + 8 * (i & 1), (i >> 1) & 1);
@@ -673,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       meet();
     }
     if (n2 > 0) {
-      exchange(true);
+      bring();
 #pragma unroll 1
       for (int r = 0; r < part; ++r) {  // the parts before, in their order
         const float e = peer_f32(peer(smem_u32(&s_part), r));
@@ -722,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     }
     if (last) {
       wait(o_full, (n2 + 1) & 1);  // the last product with S
-      exchange(false);
+      leave();
     }
   } else if (warp < 12) {
     // ================= the output: a thread is a token's row =================
