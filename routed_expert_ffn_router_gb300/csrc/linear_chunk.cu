@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sq = (smem_u32(smem_linear) + 1023u) & ~1023u;
   const uint32_t sk = sq + kTile, sv = sk + 2 * kTile, ss = sv + 2 * kTile, so = ss + kTile;
-  const uint32_t meet_at = sk;  // where the parts' sums lie between the passes (K's two tiles)
+  const uint32_t sums = sk, start = sv;  // between the passes: this part's sum, the state at its start (K's tiles, V's)
   const uint32_t bar = smem_u32(s_bar);
   // (by block parity where there are two)
   const uint32_t q_full = bar, q_empty = bar + 8, k_full = bar + 16, k_empty = bar + 32, v_full = bar + 48, v_ready = bar + 64;
@@ -257,13 +257,31 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
   };
-  auto meet = [&] {  // between the two passes: the parts' sums are there; they have been read
-    if (parts > 1) {
-      __syncwarp();
-      cluster_sync();
-    }
+  // Between the two passes: the parts' sums are there; the state at this part's start is
+  // put together from those before it by all warps (a quarter of them took four times
+  // as long: the cluster's shared memory answers late); `take` reads it; all have read.
+  auto between = [&](auto take) {
+    if (parts == 1) return;
+    __syncwarp();
+    cluster_sync();
+    if (part > 0 && n2 > 0)
+#pragma unroll 2
+      for (int i = tid; i < DK * DV / 4; i += kThreads) {
+        float4 x = peer_f128(peer(sums, 0) + i * 16);
+#pragma unroll 1
+        for (int r = 1; r < part; ++r) {
+          const float4 y = peer_f128(peer(sums, r) + i * 16);
+          const float e = peer_f32(peer(smem_u32(&s_part), r));
+          x = make_float4(fmaf(x.x, e, y.x), fmaf(x.y, e, y.y), fmaf(x.z, e, y.z), fmaf(x.w, e, y.w));
+        }
+        st_s128(start + i * 16, __float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(x.z), __float_as_uint(x.w));
+      }
+    __syncthreads();
+    take();
+    __syncwarp();
+    cluster_sync();
   };
-
+  auto meet = [&] { between([] {}); };
   // the block of step i, and its token rows that are the sequence's
   const auto block_of = [&](int i) { return first + (i < n1 ? i : i - n1); };
 
@@ -310,7 +328,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       };
 #pragma unroll 1
       for (int i = 0; i < n1; ++i) step(i, false);
-      meet();  // (K's tiles hold the parts' sums until the second one)
       meet();
       fence_proxy_async_shared();
 #pragma unroll 1
@@ -342,7 +359,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         wait(v_full + 8 * x, (i >> 1) & 1);
         arrive(v_empty + 8 * x);
       }
-      meet();
       meet();
 #pragma unroll 1
       for (int c = 0; c < n2; ++c) {
@@ -383,7 +399,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       for (int i = 0; i < n1 + n2; ++i) {
         if (i == n1) {
           meet();
-          meet();
         }
         const int x = i & 1;
         wait(v_full + 8 * x, (i >> 1) & 1);
@@ -407,7 +422,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       }
       if (n2 == 0) {
         meet();
-        meet();
       }
       tc_commit_el(u_drained, lead);
       wait(u_drained, 0);
@@ -423,7 +437,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
 #pragma unroll 1
       for (int i = 0; i < n1 + n2; ++i) {
         if (i == n1) {
-          meet();
           meet();
         }
         const int slot = i & 1;
@@ -464,7 +477,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       }
       if (n2 == 0) {
         meet();
-        meet();
       }
     }
   } else if (warp < 4) {
@@ -475,7 +487,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       wait(g_full + 8 * (i & 1), (i >> 1) & 1);
       arrive(g_empty + 8 * (i & 1));
     }
-    meet();
     meet();
     const uint32_t tr = ta + ((uint32_t)(warp * 32) << 16);
 #pragma unroll 1
@@ -667,36 +678,27 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     };
     if (parts > 1) {
       float decay = 1.f;
+      if (n1 > 0 && part == 0) {
+        bring();
+      } else {
 #pragma unroll
-      for (int j = 0; j < DV / 2; ++j) S[j] = make_float2(0.f, 0.f);
+        for (int j = 0; j < DV / 2; ++j) S[j] = make_float2(0.f, 0.f);
+      }
 #pragma unroll 1
       for (int i = 0; i < n1; ++i) step(i, &decay);
-      if (n1 > 0) {  // columns 4 j of all rows side by side, where K was
+      if (n1 > 0) {  // columns 4 j of all rows side by side
         if (held)
 #pragma unroll
-          for (int j = 0; j < DV / 4; ++j)
-            st_s128(meet_at + (j * DK + row) * 16, __float_as_uint(S[2 * j].x), __float_as_uint(S[2 * j].y),
-                    __float_as_uint(S[2 * j + 1].x), __float_as_uint(S[2 * j + 1].y));
+          for (int j = 0; j < DV / 4; ++j) put(j, sums + (j * DK + row) * 16);
         if (row == 0) s_part = decay;
       }
-      meet();
-    }
-    if (n2 > 0) {
-      bring();
-#pragma unroll 1
-      for (int r = 0; r < part; ++r) {  // the parts before, in their order
-        const float e = peer_f32(peer(smem_u32(&s_part), r));
-        const uint32_t from = peer(meet_at, r);
-        if (held)
+      between([&] {
+        if (part > 0 && n2 > 0 && held)
 #pragma unroll
-          for (int j = 0; j < DV / 4; ++j) {
-            const float4 x = peer_f128(from + (j * DK + row) * 16);
-            S[2 * j] = fma2(S[2 * j], make_float2(e, e), make_float2(x.x, x.y));
-            S[2 * j + 1] = fma2(S[2 * j + 1], make_float2(e, e), make_float2(x.z, x.w));
-          }
-      }
+          for (int j = 0; j < DV / 4; ++j) get(j, start + (j * DK + row) * 16);
+      });
     }
-    meet();
+    if (part == 0 && n2 > 0) bring();
 #pragma unroll 1
     for (int c = 0; c < n2; ++c) {
       float up = 1.f;
@@ -738,7 +740,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOut));
     const int t = tid - 256;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    meet();
     meet();
 #pragma unroll 1
     for (int c = 0; c < n2; ++c) {
@@ -787,7 +788,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
 #pragma unroll 1
     for (int i = 0; i < n1 + n2; ++i) {
       if (i == n1) {
-        meet();
         meet();
       }
       const int x = i & 1, rows = s.n - block_of(i) * kBlk;
@@ -894,7 +894,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       arrive(g_empty + 8 * x);
     }
     if (n2 == 0) {
-      meet();
       meet();
     }
   }
