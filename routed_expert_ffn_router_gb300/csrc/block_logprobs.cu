@@ -21,8 +21,8 @@
 // Top alternatives: each warp keeps its best 32 as sorted keys (order of the logit,
 // then lower id: all distinct), one per lane. A chunk is looked through only if its
 // maximum, which the sum needs anyway, reaches the k-th best so far of any warp of
-// the CTA; in a warp's first chunk the k-th largest of the lanes' maxima stands in
-// for that. Ruled out tokens (-inf) never enter; a row with fewer than k others is
+// the CTA; at first a bound from the lanes' maxima of the first chunks stands in for
+// that. Ruled out tokens (-inf) never enter; a row with fewer than k others is
 // filled up at the end. The rank likewise counts only in chunks whose maximum
 // reaches the token's logit.
 #include "block_internal.h"
@@ -47,6 +47,7 @@ struct Part {
 struct Shared {
   Part part[kWarpsPerCta];
   Key key[kWarpsPerCta][32];
+  float mth[kWarpsPerCta];
   float floor;  // some warp's k-th best logit: no smaller one is among the k best
 };
 
@@ -206,18 +207,18 @@ struct Row {
   }
 };
 
-// The k-th largest of the lanes' values (none is NaN).
-__device__ __forceinline__ float kth_of_lanes(float x, int k) {
+// The lanes' values (none is NaN) in descending order.
+__device__ __forceinline__ float sorted_lanes(float x) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int w = 2; w <= 32; w <<= 1)
 #pragma unroll
     for (int o = w >> 1; o > 0; o >>= 1) {
       const float y = __shfl_xor_sync(0xffffffffu, x, o);
-      const bool larger = ((lane & w) == 0) == ((lane & o) == 0);  // descending
+      const bool larger = ((lane & w) == 0) == ((lane & o) == 0);
       x = larger ? fmaxf(x, y) : fminf(x, y);
     }
-  return __shfl_sync(0xffffffffu, x, k - 1);
+  return x;
 }
 
 template <int TYPE>
@@ -255,20 +256,38 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
   const float mine = !has ? kBig : mine_raw == mine_raw ? mine_raw : kNone;
   // a logit above this one is at or above `mine` (for ids before the token's)
   const float below = mine == 0.f ? -1e-45f : __int_as_float(__float_as_int(mine) + (mine > 0.f ? -1 : 1));
-  if (tid == 0) sh.floor = kNone;
-  __syncthreads();
+  const auto largest = [&](const uint4 (&raw)[kVecs]) {
+    uint32_t mw = W::kNone;
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u)
+      mw = W::max_word(W::max_word(W::max_word(mw, raw[u].x), W::max_word(raw[u].y, raw[u].z)), raw[u].w);
+    return W::max_of(mw);
+  };
+  // What the k best are not below, from the first chunks: the k-th largest of the
+  // warp's lane maxima; and with m = k / warps (rounded up) the smallest of the warps'
+  // m-th largest, since m of each are not below it.
+  float floor = kNone;
+  if (a.top) {
+    const int warps = min(max((row.n_vec - rank * kWarpsPerCta * 32 * kVecs + 32 * kVecs - 1) / (32 * kVecs), 0), kWarpsPerCta);
+    if (warp < warps) {
+      const float mx = largest(even), x = sorted_lanes(mx == mx ? mx : kNone);
+      floor = __shfl_sync(0xffffffffu, x, a.top - 1);
+      if (lane == (a.top + warps - 1) / warps - 1) sh.mth[warp] = x;
+    }
+    __syncthreads();
+    float low = kBig;
+    for (int w = 0; w < warps; ++w) low = fminf(low, sh.mth[w]);
+    if (warps) floor = fmaxf(floor, low);
+    if (tid == 0) sh.floor = floor;
+    __syncthreads();
+  }
 
   float m = kNone;                                  // the warp's
   float2 l2 = make_float2(0.f, 0.f), s2 = l2;       // the lane's
   int count = 0;
   Key best = 0;
-  float floor = kNone;
   const auto chunk = [&](const uint4 (&raw)[kVecs], int v0) {
-    uint32_t mw = W::kNone;
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u)
-      mw = W::max_word(W::max_word(W::max_word(mw, raw[u].x), W::max_word(raw[u].y, raw[u].z)), raw[u].w);
-    const float mx = W::max_of(mw), top = warp_max_nan(mx);
+    const float mx = largest(raw), top = warp_max_nan(mx);
     if (top == kNone && mine != kNone) return;  // nothing in it
     if (top > m || top != top) {
       const float up = max_nan(m, top), d = bounded((m - up) * c), e = kv::ex2(d);
@@ -328,12 +347,10 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
       floor = fmaxf(floor, *const_cast<volatile float*>(&sh.floor));
       const float reach = mx == mx ? mx : kBig;  // a lane with a NaN is looked through
       if (top != top || top >= floor) {
-        if (__shfl_sync(0xffffffffu, best, a.top - 1) == 0)
-          floor = fmaxf(floor, kth_of_lanes(mx == mx ? mx : kNone, a.top));
         if (__any_sync(0xffffffffu, reach >= floor)) {
-#pragma unroll 1
+#pragma unroll
           for (int u = 0; u < kVecs; ++u) {
-            const uint4 v = row.piece(v0 + u * 32 + lane);
+            const uint4 v = raw[u];
             uint32_t mask = 0;  // of this lane's values
 #pragma unroll
             for (int i = 0; i < E; ++i) mask |= W::at(v, i) >= floor && W::at(v, i) > kNone ? 1u << i : 0u;
