@@ -331,3 +331,13 @@ def test_on_another_stream_and_in_graphs():
     torch.cuda.synchronize()
     for out in outs:
         assert all(torch.equal(out[n], want[n]) for n in want)
+
+
+def test_logprobs_of_rows_beyond_what_fits_at_once():
+    """Rows for several turns of the CTAs that fit on the GPU."""
+    T, V = 700, 33001
+    z = torch.randn(T, V, generator=torch.Generator(device="cuda").manual_seed(8), device="cuda").bfloat16()
+    tok = torch.arange(T, dtype=torch.int32, device="cuda")
+    check_logprobs(z, tok, 3)
+    first = token_logprobs(z[:50], tok[:50], top=3)
+    assert torch.equal(first["top_ids"], token_logprobs(z, tok, top=3)["top_ids"][:50])
