@@ -3,7 +3,7 @@ decoder whose layers are attention over a `PagedKV` and a routed-expert FFN
 (`MoeLayer`). Random weights; the projections around them are plain matrix
 products.
 
-    python examples/serve.py [--steps N] [--branches N]
+    python examples/serve.py [--steps N] [--branches N] [--hybrid]
 
 Three prompts of different lengths go through the layers as one chunk. Each is
 forked into branches, which share the prompt's full pages and differ from their
@@ -11,6 +11,10 @@ first token on; the prompts' own slots are freed. The branches then decode
 token by token, with a compaction of the pool half way. Nothing between the
 prompts and the end waits for the GPU: the pages that a step needs are found
 there.
+
+--hybrid serves a decoder whose layers alternate between linear attention, which
+keeps a state per sequence, and attention over the cache with rotary positions;
+norms add the residual, and each token's log probability is reported.
 """
 import argparse
 import os
@@ -21,7 +25,9 @@ import torch
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 from routed_expert_ffn_router_gb300 import build, synth  # noqa: E402
+from routed_expert_ffn_router_gb300.block import Rotary, rms_norm, token_logprobs  # noqa: E402
 from routed_expert_ffn_router_gb300.layer import MoeLayer  # noqa: E402
+from routed_expert_ffn_router_gb300.linear import LinearAttention  # noqa: E402
 from routed_expert_ffn_router_gb300.paged import PagedKV  # noqa: E402
 
 BF16 = torch.bfloat16
@@ -80,6 +86,45 @@ class Decoder:
         return [f.status() for f in self.ffn]
 
 
+class HybridDecoder(Decoder):
+    """Layers in turn of linear attention (Hkv heads of queries and keys shared by Hq of
+    values) and of attention with rotary positions, each followed by the experts."""
+
+    def __init__(self, n_slots, seed=0, **kw):
+        super().__init__(seed=seed, **kw)
+        H, Hq, Hkv, D, dev = self.embed.shape[1], self.Hq, self.Hkv, self.D, self.device
+        g = torch.Generator().manual_seed(seed + 1)
+        self.rotary = Rotary(D, scaling=dict(kind="yarn", factor=4, original=256), device=dev)
+        self.norms = [(1 + 0.1 * torch.randn(H, generator=g)).to(BF16).to(dev) for _ in range(2 * self.n_layers + 1)]
+        self.linear = {l: LinearAttention(n_slots, Hkv, Hq, D, D, device=dev) for l in range(0, self.n_layers, 2)}
+        # queries, keys, values and a gate per head
+        self.win = {l: (torch.randn(H, (2 * Hkv + Hq) * D + Hq, generator=g) * H ** -0.5).to(BF16).to(dev) for l in self.linear}
+        self.rate = torch.logspace(-3, 0, Hq).to(dev)  # heads that forget slowly and fast
+
+    def states(self):
+        return [s.state for s in self.linear.values()]
+
+    def __call__(self, kv, tokens, slots, row_start=None):
+        Hq, Hkv, D = self.Hq, self.Hkv, self.D
+        rows = {} if row_start is None else dict(row_start=row_start)
+        r, x = self.embed[tokens], None  # the residual, what joins it in the next norm
+        for l in range(self.n_layers):
+            h = rms_norm(r, self.norms[2 * l]) if x is None else rms_norm(x, self.norms[2 * l], residual=r)
+            if l in self.linear:
+                p = h @ self.win[l]
+                heads, gate = p[:, :-Hq].unflatten(1, (2 * Hkv + Hq, D)), p[:, -Hq:].float()
+                call = self.linear[l].step if row_start is None else self.linear[l].chunk
+                o = call(heads[:, :Hkv], heads[:, Hkv:2 * Hkv], heads[:, 2 * Hkv:], -self.rate * torch.nn.functional.softplus(gate),
+                         slots=slots, **rows)
+            else:
+                qkv = (h @ self.wqkv[l]).unflatten(1, (Hq + 2 * Hkv, D))
+                q = kv.append_rotary(l, qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:], self.rotary, slots=slots, **rows)
+                o = (kv.decode if row_start is None else kv.chunk)(l, q, slots=slots, window=self.window, sinks=self.sinks, **rows)
+            h = rms_norm(o.flatten(1) @ self.wo[l], self.norms[2 * l + 1], residual=r)
+            x = self.ffn[l].forward((h @ self.router[l]).float(), h)["y"]  # fp32
+        return rms_norm(x, self.norms[-1], residual=r) @ self.head
+
+
 class Session:
     """Sequences of one decoder in the slots of one cache."""
 
@@ -112,9 +157,24 @@ class Session:
         return self.model(self.kv, tokens, slots)
 
 
-def serve(model, kv, prompts, branches, steps, compact=True):
-    """-> (tokens [steps + 1][branches of all prompts], last logits)."""
-    s = Session(model, kv)
+class HybridSession(Session):
+    """The states follow the slots."""
+
+    def fork(self, src, dst):
+        super().fork(src, dst)
+        for state in self.model.states():
+            state[self.ints(dst).long()] = state[self.ints(src).long()]
+
+    def free(self, slots):
+        super().free(slots)
+        for state in self.model.states():
+            state[self.ints(slots).long()] = 0
+
+
+def serve(model, kv, prompts, branches, steps, compact=True, session=Session, scores=None):
+    """-> (tokens [steps + 1][branches of all prompts], last logits). scores: a list that
+    receives each step's log probabilities (`token_logprobs`) of the tokens taken."""
+    s = session(model, kv)
     n = len(prompts)
     logits = s.prompts(list(range(n)), prompts)
     slots = list(range(n, n + n * branches))
@@ -122,12 +182,16 @@ def serve(model, kv, prompts, branches, steps, compact=True):
     s.free(list(range(n)))
     # branch j of a prompt starts with its j-th best token
     tokens = logits.topk(branches, dim=1).indices.flatten().to(torch.int32)
+    if scores is not None:
+        scores.append(token_logprobs(logits.repeat_interleave(branches, 0), tokens, top=2))
     slots, ones, out = s.ints(slots), s.ints([1] * (n * branches)), [tokens]
     for i in range(steps):
         if compact and i == steps // 2:
             kv.compact()
         logits = s.step(slots, tokens, ones)
         tokens = logits.argmax(1).to(torch.int32)
+        if scores is not None:
+            scores.append(token_logprobs(logits, tokens, top=2))
         out.append(tokens)
     return torch.stack(out), logits
 
@@ -136,24 +200,33 @@ def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--steps", type=int, default=32)
     ap.add_argument("--branches", type=int, default=4)
+    ap.add_argument("--hybrid", action="store_true")
     a = ap.parse_args()
     build.build()
     g = torch.Generator().manual_seed(1)
     prompts = [torch.randint(0, 512, (n,), generator=g).tolist() for n in (200, 41, 97)]
-    model = Decoder()
+    n_slots = 3 + 3 * a.branches
+    model = HybridDecoder(n_slots) if a.hybrid else Decoder()
     for run in range(2):  # the second is the timed one
-        kv = model.cache(n_pages=512, page_size=16, n_slots=3 + 3 * a.branches, max_tokens=256 + a.steps)
+        if a.hybrid:
+            for state in model.states():
+                state.zero_()
+        scores = [] if a.hybrid else None
+        kv = model.cache(n_pages=512, page_size=16, n_slots=n_slots, max_tokens=256 + a.steps)
         t0, t1 = (torch.cuda.Event(enable_timing=True) for _ in range(2))
         t0.record()
-        tokens, _ = serve(model, kv, prompts, a.branches, a.steps)
+        tokens, _ = serve(model, kv, prompts, a.branches, a.steps, session=HybridSession if a.hybrid else Session, scores=scores)
         t1.record()
         torch.cuda.synchronize()
         if kv.status()[0] != 0 or any(c != 0 for c, _ in model.status()):
             raise SystemExit(f"device status: {kv.status()} {model.status()}")
+        if a.hybrid and any(l.status() for l in model.linear.values()):
+            raise SystemExit("device status of the linear attention")
     print(f"{len(prompts)} prompts, {tokens.shape[1]} branches, {a.steps} steps: {t0.elapsed_time(t1):.1f} ms, "
           f"{kv.table.shape[1]} pages per slot, {512 - int(kv.n_free)} pages in use")
     for j in range(tokens.shape[1]):
-        print(f"prompt {j // a.branches} branch {j % a.branches}:", " ".join(map(str, tokens[:12, j].tolist())), "...")
+        print(f"prompt {j // a.branches} branch {j % a.branches}:", " ".join(map(str, tokens[:12, j].tolist())), "...",
+              f"log probability {sum(float(x['logprob'][j]) for x in scores):.1f}" if scores else "")
 
 
 if __name__ == "__main__":
