@@ -44,20 +44,26 @@ def _on(device, stream):
 
 
 def _new(shape, dtype, device, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
     with _lib.on_stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _rows(t, T, H, types, what, device):
+def _rows(t, shape, types, what, device):
     """-> (type, row stride) of a [T][H] tensor with contiguous rows."""
-    if t.dim() != 2 or t.shape[0] != T or t.shape[1] != H or t.dtype not in types or t.device != device:
-        raise ValueError(f"{what} must be [{T}][{H}] on {device}, of {', '.join(str(x)[6:] for x in types)}")
-    if t.stride(1) != 1 and H > 1:
+    kind = types.get(t.dtype)
+    if kind is None or t.shape != shape or t.device != device:
+        raise ValueError(f"{what} must be {list(shape)} on {device}, of {', '.join(str(x)[6:] for x in types)}")
+    T, H = shape
+    s0, s1 = t.stride()
+    if s1 != 1 and H > 1:
         raise ValueError(f"{what}: the values of a row must be contiguous")
-    s = t.stride(0)
-    if T > 1 and s < H:
+    if T <= 1:
+        return kind, max(s0, H)
+    if s0 < H:
         raise ValueError(f"{what}: rows must not overlap")
-    return types[t.dtype], s if T > 1 else max(s, H)
+    return kind, s0
 
 
 def rms_norm(x, weight=None, residual=None, eps=1e-6, weight_offset=0.0, out_dtype=None, group=0, out=None, scales=None,
@@ -68,43 +74,42 @@ def rms_norm(x, weight=None, residual=None, eps=1e-6, weight_offset=0.0, out_dty
     (the residual's type unless given) or out; with float8_e4m3fn (y, scales), y times
     scales [rows][H / group] being the norm (group 0: one scale per row; else a power
     of two from 16). out may be x."""
-    if x.dim() != 2:
+    shape, dev = x.shape, x.device
+    if len(shape) != 2:
         raise ValueError("x must be [rows][H]")
-    T, H = x.shape
-    dev = x.device
-    a = moe_norm_args()
-    a.T, a.H, a.eps, a.w_offset, a.group = T, H, eps, weight_offset, group
-    a.x_type, a.x_stride = _rows(x, T, H, _TYPES, "x", dev)
-    a.x = x.data_ptr()
+    T, H = shape
+    x_type, x_stride = _rows(x, shape, _TYPES, "x", dev)
+    res_type = res_stride = w_type = 0
+    res = w = s = None
     if residual is not None:
-        a.res_type, a.res_stride = _rows(residual, T, H, _TYPES, "residual", dev)
-        a.res = residual.data_ptr()
+        res_type, res_stride = _rows(residual, shape, _TYPES, "residual", dev)
+        res = residual.data_ptr()
     if weight is not None:
-        if weight.shape != (H,) or weight.dtype not in _TYPES or weight.device != dev or (H > 1 and weight.stride(0) != 1):
-            raise ValueError(f"weight must be a contiguous [{H}] on {dev}")
-        a.w_type, a.w = _TYPES[weight.dtype], weight.data_ptr()
+        w_type = _TYPES.get(weight.dtype)
+        if w_type is None or weight.shape != (H,) or weight.device != dev or not weight.is_contiguous():
+            raise ValueError(f"weight must be a contiguous [{H}] on {dev}, of fp32, bf16 or fp16")
+        w = weight.data_ptr()
     handle = _on(dev, stream)
     if out is None:
-        out = _new((T, H), (x if residual is None else residual).dtype if out_dtype is None else out_dtype, dev, stream)
+        out = _new(shape, (x if residual is None else residual).dtype if out_dtype is None else out_dtype, dev, stream)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise ValueError("out is not of out_dtype")
-    a.y_type, a.y_stride = _rows(out, T, H, _OUT_TYPES, "out", dev)
-    a.y = out.data_ptr()
-    if out.dtype != _E4M3:
+    y_type, y_stride = _rows(out, shape, _OUT_TYPES, "out", dev)
+    if y_type != _lib.MOE_T_E4M3:
         if scales is not None or group:
             raise ValueError("scales and group are for float8_e4m3fn")
-        _lib.moe_rms_norm(ctypes.byref(a), handle)
-        return out
-    if group < 0 or (group and H % group):
-        raise ValueError("group must divide the row")
-    n = H // group if group else 1
-    if scales is None:
-        scales = _new((T, n), _F32, dev, stream)
-    elif scales.shape != (T, n) or scales.dtype != _F32 or not scales.is_contiguous() or scales.device != dev:
-        raise ValueError(f"scales must be a contiguous fp32 [{T}][{n}] on {dev}")
-    a.scales = scales.data_ptr()
-    _lib.moe_rms_norm(ctypes.byref(a), handle)
-    return out, scales
+    else:
+        if group < 0 or (group and H % group):
+            raise ValueError("group must divide the row")
+        n = H // group if group else 1
+        if scales is None:
+            scales = _new((T, n), _F32, dev, stream)
+        elif scales.shape != (T, n) or scales.dtype != _F32 or not scales.is_contiguous() or scales.device != dev:
+            raise ValueError(f"scales must be a contiguous fp32 [{T}][{n}] on {dev}")
+        s = scales.data_ptr()
+    _lib.moe_rms_norm(ctypes.byref(moe_norm_args(T, H, x_type, res_type, w_type, y_type, group, eps, weight_offset, x.data_ptr(),
+                                                 x_stride, res, res_stride, w, out.data_ptr(), y_stride, s)), handle)
+    return out if s is None else (out, scales)
 
 
 _LOGPROB_OUT = (("logprob", _F32), ("rank", _I32), ("entropy", _F32), ("top_ids", _I32), ("top_logprobs", _F32))
@@ -116,35 +121,33 @@ def token_logprobs(logits, tokens=None, top=0, temperature=1.0, out=None, stream
     (0: the most likely one; a token outside [0, V): 0 and -1); with top (up to 32)
     top_ids and top_logprobs [rows][top], the most likely tokens in order, ties to the
     lower id. out: a dict of such tensors to write to."""
-    if logits.dim() != 2:
+    shape, dev = logits.shape, logits.device
+    if len(shape) != 2:
         raise ValueError("logits must be [rows][V]")
-    T, V = logits.shape
-    dev = logits.device
-    a = moe_logprobs_args()
-    a.T, a.V, a.top, a.temperature = T, V, top, temperature
-    a.type, a.stride = _rows(logits, T, V, _TYPES, "logits", dev)
-    a.logits = logits.data_ptr()
-    if tokens is not None:
-        if tokens.shape != (T,) or tokens.dtype != _I32 or not tokens.is_contiguous() or tokens.device != dev:
-            raise ValueError(f"tokens must be a contiguous int32 [{T}] on {dev}")
-        a.tokens = tokens.data_ptr()
+    T, V = shape
+    kind, stride = _rows(logits, shape, _TYPES, "logits", dev)
+    if tokens is not None and (tokens.shape != (T,) or tokens.dtype != _I32 or not tokens.is_contiguous() or tokens.device != dev):
+        raise ValueError(f"tokens must be a contiguous int32 [{T}] on {dev}")
     if top < 0:
         raise ValueError("top must not be negative")
     handle = _on(dev, stream)
-    r = {}
+    r, at = {}, []
     for name, dtype in _LOGPROB_OUT:
-        if tokens is None and name in ("logprob", "rank") or not top and name.startswith("top"):
+        wide = name[0] == "t"
+        if (not top) if wide else (tokens is None and name != "entropy"):
+            at.append(None)
             continue
-        shape = (T, top) if name.startswith("top") else (T,)
+        want = (T, top) if wide else (T,)
         if out is None:
-            t = _new(shape, dtype, dev, stream)
+            t = _new(want, dtype, dev, stream)
         else:
             t = out.get(name)
-            if t is None or t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.device != dev:
-                raise ValueError(f"out[{name!r}] must be a contiguous {str(dtype)[6:]} {list(shape)} on {dev}")
+            if t is None or t.shape != want or t.dtype != dtype or not t.is_contiguous() or t.device != dev:
+                raise ValueError(f"out[{name!r}] must be a contiguous {str(dtype)[6:]} {list(want)} on {dev}")
         r[name] = t
-        setattr(a, name, t.data_ptr())
-    _lib.moe_token_logprobs(ctypes.byref(a), handle)
+        at.append(t.data_ptr())
+    _lib.moe_token_logprobs(ctypes.byref(moe_logprobs_args(T, V, top, kind, temperature, logits.data_ptr(), stride,
+                                                           None if tokens is None else tokens.data_ptr(), *at)), handle)
     return r
 
 

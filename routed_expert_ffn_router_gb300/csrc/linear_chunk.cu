@@ -7,15 +7,17 @@
 //   S'  = e^G S + sum_j (e^(G - G_j) k_j) v_j^T
 // Three products, accumulators in tensor memory:
 //   A = Q K^T      U = K'^T V      O = [A o D | Q'] [V ; S]
-// K' = e^(G - G_j) k_j, Q' = e^G_i q_i, D_ij = e^(G_i - G_j) for j <= i, else 0. K'^T,
-// A o D and Q' are first operands in tensor memory, which leaves shared memory to the
+// K' = e^(G - G_j) k_j, Q' = e^G_i q_i, D_ij = e^(G_i - G_j) for j <= i, else 0. Where
+// e^-G is no more than 2^64 (2^8 in fp16), Q' is q itself, D_ij is e^-G_j and the
+// factor e^G_i is left to the output: Q' is then exact where the state matters most.
+// K'^T, A o D and Q' are first operands in tensor memory, which leaves shared memory to the
 // tiles that TMA brings, two of K and of V. U does not depend on S, so the blocks of a
 // sequence wait for one another only in S' = e^G S + U, in registers.
 //
 // Rounding. The state is fp32 throughout: in bf16 K' enters U as three values that
 // add up to its fp32 exactly, in fp16 as two (its rounding and the rest, 2^-22 of
 // it), and U is a fresh sum each block. (Two values of bf16 left the state off by
-// 2.4e-6.) S, Q' and A o D, which only o sees, are rounded once to the type (half a
+// 2.4e-6.) S, A o D and a scaled Q', which only o sees, are rounded once to the type (half a
 // step each, as o itself is). In fp16, whose range is narrow and whose step is fixed
 // below 2^-14, K' and S are scaled by a power of two per block and a row of A o D and
 // Q' by one of its own, which bring the largest magnitude to 2^13 and are undone in
@@ -74,13 +76,13 @@ struct ChunkArgs {
 };
 
 // What the decays of a block come to.
-struct Decays {
+struct alignas(16) Decays {
   float gh[kBlk], gl[kBlk];  // -G_j / ln 2 as two values
   float k[kBlk];      // e^(G - G_j)
   float q[kBlk];      // e^G_i
-  float piece[kBlk];  // e^(G_p - G_j), p the last of j's 32 tokens
+  float col[kBlk];    // weak: e^-G_j; else e^(G_p - G_j), p the last of j's 32 tokens
+  bool weak;          // whether e^-G is within reach (kWeak)
   float2 all;         // e^G (decay_of)
-  float pad[2];
 };
 
 __device__ __forceinline__ void ldmatrix4_t(uint32_t a, uint32_t (&r)[4]) {
@@ -132,6 +134,10 @@ __device__ __forceinline__ void prefetch_3d(const void* tmap, int c0, int c1, in
   asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(tmap), "r"(c0), "r"(c1), "r"(c2)
                : "memory");
 }
+// Up to which sum of a block's decays (in powers of two) its tokens are weighted by
+// e^-G_j alone.
+template <bool F16>
+__device__ constexpr float kWeak() { return F16 ? 8.f : 64.f; }
 // 2^e as a float, e in the normal range
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 // The exponent that brings a largest magnitude m (>= 0) to [2^13, 2^14); bounded so
@@ -148,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   extern __shared__ __align__(1024) uint8_t smem_linear[];
   __shared__ __align__(16) Decays s_dec[2];
   __shared__ __align__(8) uint64_t s_bar[40];
-  __shared__ int s_row[2][F16 ? kBlk : 1];   // fp16, by block: log2 of what a row of A o D and Q' is scaled by
+  __shared__ float s_row[2][kBlk];           // by block: what makes a row of O the output
   __shared__ int s_state_up[2];              // log2 of what S is scaled by
   __shared__ float s_key_down[2];            // what undoes the scale of K'
   __shared__ float s_max[4];
@@ -462,6 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         for (int j = 0; j < 4; ++j) g[j] = ff_add(before, g[j]);
         const FF end = {__shfl_sync(0xffffffffu, g[3].h, lane | 7), __shfl_sync(0xffffffffu, g[3].l, lane | 7)};
         const float2 all = decay_of(total.h * 0x1.62e43p-1f + fmaf(total.l, 0x1.62e43p-1f, total.h * -0x1.05c61p-29f));
+        const bool weak = total.h > -kWeak<F16>();
         wait(g_empty + 8 * slot, ((i >> 1) + 1) & 1);
         Decays& d = s_dec[slot];
 #pragma unroll
@@ -470,9 +477,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           d.gl[lane * 4 + j] = -g[j].l;
           d.k[lane * 4 + j] = kv::ex2((total.h - g[j].h) + (total.l - g[j].l));
           d.q[lane * 4 + j] = kv::ex2(g[j].h + g[j].l);
-          d.piece[lane * 4 + j] = kv::ex2((end.h - g[j].h) + (end.l - g[j].l));
+          d.col[lane * 4 + j] = weak ? kv::ex2(-g[j].h - g[j].l) : kv::ex2((end.h - g[j].h) + (end.l - g[j].l));
         }
-        if (lane == 0) d.all = all;
+        if (lane == 0) {
+          d.all = all;
+          d.weak = weak;
+        }
         arrive(g_full + 8 * slot);
       }
       if (n2 == 0) {
@@ -497,7 +507,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       wait(g_full + 8 * (i & 1), (i >> 1) & 1);
       wait(q_full, c & 1);
       const float gh = -d.gh[tid], gl = -d.gl[tid];
-      float up = F16 ? 1.f : a.scale, fq = d.q[tid];  // of A o D, of Q'
+      const bool weak = d.weak;
+      // of A o D; of Q' (weak: it is exact); of the output
+      float up = 1.f, fq = weak ? 1.f : d.q[tid], out = weak ? d.q[tid] * a.scale : a.scale;
       uint32_t mq = 0;
       if constexpr (F16)
 #pragma unroll 4
@@ -507,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         }
       wait(a_full, c & 1);
       tc_fence_after();
-      if constexpr (F16) {  // the largest of the row's |q . k| and of its Q' (times S's scale) to about 2^13
+      if constexpr (F16) {  // the largest of the row's weighted |q . k| and of its Q' (times S's scale) to about 2^13
         float m = 0.f;
 #pragma unroll 1
         for (int j = 0; j <= warp; ++j) {
@@ -518,15 +530,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           for (int e = 0; e < 32; ++e)
             if (j < warp || e <= lane) m = fmaxf(m, fabsf(__uint_as_float(x[e])));
         }
+        if (weak) m *= d.col[tid];
         wait(s_ready, c & 1);
         mq = min(max(mq & 0xffffu, mq >> 16), 0x7bffu);
         const int up_s = s_state_up[c & 1], e = max(-100, min(lift_of(m), lift_of(kv::unpack2<true>(mq).x * fq) + up_s));
         up = pow2(e);
         fq = e - up_s < -126 ? 0.f : fq * pow2(min(e - up_s, 127));
-        s_row[c & 1][tid] = e;
-      } else {
-        fq *= a.scale;
+        out *= pow2(-e);
       }
+      s_row[c & 1][tid] = out;
       // (rolled loops: with all roles' loops unrolled their code did not stay in the
       // instruction cache, and a block took twice as long)
 #pragma unroll 1
@@ -538,14 +550,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         } else {
           tc_ld32(tr + j * 32, x);
           tc_ld_wait();
-          if (j < warp) {
-            // 32 tokens before all of the warp's, p the last of them: D_ij = e^(G_i - G_p)
-            // e^(G_p - G_j), neither above 1
-            const float f = kv::ex2((gh + d.gh[j * 32 + 31]) + (gl + d.gl[j * 32 + 31])) * up;
-            const float4* ep = reinterpret_cast<const float4*>(d.piece + j * 32);
+          if (weak || j < warp) {
+            // weak: e^G_i is left to the output. Else 32 tokens before all of the warp's,
+            // p the last of them: D_ij = e^(G_i - G_p) e^(G_p - G_j), neither above 1
+            const float f = weak ? up : kv::ex2((gh + d.gh[j * 32 + 31]) + (gl + d.gl[j * 32 + 31])) * up;
+            const float4* col = reinterpret_cast<const float4*>(d.col + j * 32);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float4 w = ep[e];
+              const float4 w = col[e];
               const float2 d0 = mul2(make_float2(w.x, w.y), make_float2(f, f)), d1 = mul2(make_float2(w.z, w.w), make_float2(f, f));
               const float2 p0 = mul2(d0, make_float2(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1])));
               const float2 p1 = mul2(d1, make_float2(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])));
@@ -564,11 +576,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
               const float2 d1 = mul2(make_float2(kv::ex2(t1.x), kv::ex2(t1.y)), make_float2(up, up));
               const float2 p0 = mul2(d0, make_float2(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1])));
               const float2 p1 = mul2(d1, make_float2(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])));
-              // later tokens (what stands there may be NaN) are cleared as bits
-              pk[2 * e] = kv::pack2<F16>(p0.x, p0.y) & ((4 * e <= lane ? 0xffffu : 0u) | (4 * e + 1 <= lane ? 0xffff0000u : 0u));
-              pk[2 * e + 1] = kv::pack2<F16>(p1.x, p1.y) & ((4 * e + 2 <= lane ? 0xffffu : 0u) | (4 * e + 3 <= lane ? 0xffff0000u : 0u));
+              pk[2 * e] = kv::pack2<F16>(p0.x, p0.y);
+              pk[2 * e + 1] = kv::pack2<F16>(p1.x, p1.y);
             }
           }
+          if (j == warp)  // later tokens (what stands there may be NaN) are cleared as bits
+#pragma unroll
+            for (int e = 0; e < 16; ++e) pk[e] &= (2 * e <= lane ? 0xffffu : 0u) | (2 * e + 1 <= lane ? 0xffff0000u : 0u);
         }
         tc_st16(tr + j * 16, pk);
       }
@@ -745,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     for (int c = 0; c < n2; ++c) {
       wait(o_full, c & 1);
       tc_fence_after();
-      const float scale = F16 ? a.scale * pow2(-s_row[c & 1][t]) : 1.f;
+      const float scale = s_row[c & 1][t];
 #pragma unroll 1
       for (int j = 0; j < DV / 32; ++j) {
         uint32_t x[32], w[16];
@@ -757,8 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         }
 #pragma unroll
         for (int y = 0; y < 16; ++y) {
-          float2 o = make_float2(__uint_as_float(x[2 * y]), __uint_as_float(x[2 * y + 1]));
-          if constexpr (F16) o = mul2(o, make_float2(scale, scale));
+          const float2 o = mul2(make_float2(__uint_as_float(x[2 * y]), __uint_as_float(x[2 * y + 1])), make_float2(scale, scale));
           w[y] = kv::pack2<F16>(o.x, o.y);
         }
         // rows of 64 values go out together, eight lanes a row: a store of one piece

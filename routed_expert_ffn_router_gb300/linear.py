@@ -54,6 +54,7 @@ class LinearAttention:
         d.dtype, d.state = _DTYPES[dtype], state.data_ptr()
         self._desc_ref = ctypes.byref(d)
         self._status = torch.zeros(1, dtype=_I32, device=self.device)
+        self._status_ptr = self._status.data_ptr()
 
     def _heads(self, t, heads, D, what):
         """-> row stride of [rows][heads][D] with contiguous heads."""
@@ -71,35 +72,32 @@ class LinearAttention:
         return t
 
     def _call(self, fn, q, k, v, g, slots, row_start, scale, out, stream):
-        a, r = moe_linear_args(), moe_kv_rows()
-        a.q_stride, a.k_stride = self._heads(q, self.Hk, self.Dk, "q"), self._heads(k, self.Hk, self.Dk, "k")
-        a.v_stride = self._heads(v, self.Hv, self.Dv, "v")
+        q_stride, k_stride = self._heads(q, self.Hk, self.Dk, "q"), self._heads(k, self.Hk, self.Dk, "k")
+        v_stride = self._heads(v, self.Hv, self.Dv, "v")
         n = q.shape[0]
         if k.shape[0] != n or v.shape[0] != n:
             raise ValueError("q, k and v must have the same rows")
-        if g.dtype != _F32 or g.device != self.device or g.shape not in ((n, self.Hv), (self.Hv,)) or \
-                (g.stride(-1) != 1 and self.Hv > 1):
+        shape, strides = g.shape, g.stride()
+        if g.dtype != _F32 or g.device != self.device or shape not in ((n, self.Hv), (self.Hv,)) or \
+                (strides[-1] != 1 and self.Hv > 1):
             raise ValueError(f"g must be fp32 [{n}][{self.Hv}] or [{self.Hv}] on {self.device}, heads contiguous")
-        a.g_stride = 0 if g.dim() == 1 else g.stride(0) if n > 1 else self.Hv
+        g_stride = 0 if len(shape) == 1 else strides[0] if n > 1 else self.Hv
         B = n if slots is None else self._ints(slots, "slots").numel()
         if row_start is not None:
             m = self._ints(row_start, "row_start").numel() - 1
             if m < 0 or (slots is not None and B != m):
                 raise ValueError("row_start has one entry more than there are sequences")
             B = m
-            r.row_start = row_start.data_ptr()
         if (n > 0 and B < 1) or (slots is None and B > self.n_slots):
             raise ValueError("more sequences than slots, or none")
-        r.B, r.n_rows = B, n
-        if slots is not None:
-            r.slots = slots.data_ptr()
         handle = _on(self.device, stream)
         if out is None:
             out = _new((n, self.Hv, self.Dv), self.dtype, self.device, stream)
         elif out.shape != v.shape or out.dtype != self.dtype or not out.is_contiguous() or out.device != self.device:
             raise ValueError("out must be a contiguous tensor like v")
-        a.q, a.k, a.v, a.g, a.o = q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), out.data_ptr()
-        a.scale, a.status = self.Dk ** -0.5 if scale is None else scale, self._status.data_ptr()
+        r = moe_kv_rows(B, n, None if slots is None else slots.data_ptr(), None if row_start is None else row_start.data_ptr())
+        a = moe_linear_args(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride, g.data_ptr(), g_stride,
+                            self.Dk ** -0.5 if scale is None else scale, out.data_ptr(), self._status_ptr)
         fn(self._desc_ref, ctypes.byref(r), ctypes.byref(a), handle)
         return out
 
