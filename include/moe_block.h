@@ -97,7 +97,8 @@ moe_status moe_token_logprobs(const moe_logprobs_args *a, void *stream);
  * those of moe_kv_rows: sequence b is slot slots[b] (NULL: slot b), the slots
  * of a call distinct; a sequence without rows leaves its state as it was. A
  * slot out of range (2) or one that an earlier sequence of the call has (64)
- * ORs that bit into *status (nullable): its rows' o is 0 and no state changes.
+ * ORs that bit into *status (nullable): its rows' o is 0 and no state changes. 4: a
+ * bounded wait expired, the call's results are incomplete.
  * Rows behind the last sequence are left as they were.
  *
  * q, k [n_rows][Hk][Dk] and v [n_rows][Hv][Dv] in `dtype`, 16-byte aligned, the
@@ -125,7 +126,13 @@ typedef struct {
  * row_start NULL. The state is read and written once; products in fp32. */
 moe_status moe_linear_step(const moe_linear_desc *d, const moe_kv_rows *rows, const moe_linear_args *a, void *stream);
 
-/* Prompt chunks: any number of rows per sequence. */
+/* Prompt chunks: any number of rows per sequence. With Dk and Dv of 64 or 128, and
+ * more than a few rows, on the tensor cores: a state and a score enter their products
+ * rounded once to `dtype` (the state itself stays within fp32's roundings), and how a
+ * long sequence is split depends on the call, so a row's last bits may differ in
+ * another call. There values that a sequence's rows see must be finite: a NaN or an
+ * infinity may reach rows before it. Other sequences' rows and heads, and rows behind
+ * the last sequence, reach nothing. */
 moe_status moe_linear_chunk(const moe_linear_desc *d, const moe_kv_rows *rows, const moe_linear_args *a, void *stream);
 
 #ifdef __cplusplus

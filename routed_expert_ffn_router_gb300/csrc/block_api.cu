@@ -43,7 +43,12 @@ moe_status linear(const moe_linear_desc* d, const moe_kv_rows* r, const moe_line
   kv::Rows rw;
   rw.B = r->B; rw.n_rows = r->n_rows; rw.n_q = r->row_start ? 0 : r->n_rows / r->B;
   rw.slots = r->slots; rw.row_start = r->row_start;
-  if (!step && linear_chunk_supported(l))
+  // A chunk of few rows goes row by row, as a decode window: 32 heads of 128, 8
+  // sequences of 8 rows 15 us row by row and 22 on the tensor cores, of 16 rows 26 and
+  // 22; heads of 64, 16 rows 10 and 17. With rows given by row_start a sequence may
+  // have all of them.
+  const int rows_each = r->row_start ? r->n_rows : rw.n_q;
+  if (!step && rows_each > (d->Dk > 64 || d->Dv > 64 ? 12 : 24) && linear_chunk_supported(l))
     return cuda_status(launch_linear_chunk(l, rw, d->dtype == MOE_KV_F16, static_cast<cudaStream_t>(stream)));
   return cuda_status(launch_linear_rows(l, rw, d->dtype == MOE_KV_F16, step, static_cast<cudaStream_t>(stream)));
 }

@@ -8,7 +8,7 @@
 // Three products, accumulators in tensor memory:
 //   A = Q K^T      U = K'^T V      O = [A o D | Q'] [V ; S]
 // K' = e^(G - G_j) k_j, Q' = e^G_i q_i, D_ij = e^(G_i - G_j) for j <= i, else 0. Where
-// e^-G is no more than 2^64 (2^8 in fp16), Q' is q itself, D_ij is e^-G_j and the
+// e^-G is no more than 2^32 (2^8 in fp16), Q' is q itself, D_ij is e^-G_j and the
 // factor e^G_i is left to the output: Q' is then exact where the state matters most.
 // K'^T, A o D and Q' are first operands in tensor memory, which leaves shared memory to the
 // tiles that TMA brings, two of K and of V. U does not depend on S, so the blocks of a
@@ -137,7 +137,7 @@ __device__ __forceinline__ void prefetch_3d(const void* tmap, int c0, int c1, in
 // Up to which sum of a block's decays (in powers of two) its tokens are weighted by
 // e^-G_j alone.
 template <bool F16>
-__device__ constexpr float kWeak() { return F16 ? 8.f : 64.f; }
+__device__ constexpr float kWeak() { return F16 ? 8.f : 32.f; }
 // 2^e as a float, e in the normal range
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 // The exponent that brings a largest magnitude m (>= 0) to [2^13, 2^14); bounded so

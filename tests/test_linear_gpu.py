@@ -241,3 +241,30 @@ def test_streams_graphs_and_repeats(op):
     torch.cuda.synchronize()
     for l, o in zip(two, got):
         assert torch.equal(o, want) and torch.equal(l.state, a.state)
+
+
+def test_short_sequences_beside_a_long_one_of_few_heads():
+    """The long one is split over a cluster, most of whose CTAs have nothing of the others."""
+    i = Inputs([9000, 1, 0, 300, 1200], 1, 1, 64, 64, BF, seed=13)
+    layer = i.layer()
+    check(i, layer, layer.chunk(i.q, i.k, i.v, i.g, slots=i.slots, row_start=i.start), 64 ** -0.5, True)
+
+
+def test_many_sequences():
+    news = [(7 * j) % 5 for j in range(700)]
+    i = Inputs(news, 1, 2, 64, 64, HF, seed=14)
+    layer = i.layer()
+    check(i, layer, layer.chunk(i.q, i.k, i.v, i.g, slots=i.slots, row_start=i.start), 64 ** -0.5, True)
+
+
+@pytest.mark.parametrize("value", [math.nan, INF])
+def test_padding_may_hold_anything(value):
+    """Rows behind the last sequence, and a neighbour's in the same block, reach nothing."""
+    i = Inputs([70, 33], 2, 2, 128, 128, BF, seed=15, tail=60)
+    for t in (i.q, i.k, i.v):
+        t[i.T:] = value
+    i.g[i.T:] = value
+    layer = i.layer()
+    out = torch.zeros(i.T + 60, 2, 128, dtype=BF, device="cuda")
+    layer.chunk(i.q, i.k, i.v, i.g, slots=i.slots, row_start=i.start, out=out)
+    check(i, layer, out, 128 ** -0.5, True)
