@@ -1,6 +1,7 @@
 // Internal declarations of the decoder-block operators (include/moe_block.h).
 #pragma once
 
+#include "kinds.h"
 #include "kv_internal.h"
 #include "moe_block.h"
 

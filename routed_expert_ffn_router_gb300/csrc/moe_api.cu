@@ -5,7 +5,7 @@
 #include <mutex>
 #include <vector>
 
-#include "moe_internal.h"
+#include "kinds.h"
 
 namespace moe {
 
@@ -24,8 +24,8 @@ struct Profiler {
   std::vector<ProfPair> pairs;  // recorded since the last collect
   std::vector<cudaEvent_t> pool;
   size_t used = 0;
-  double total_ms[K_NUM_KINDS] = {};
-  int64_t count[K_NUM_KINDS] = {};
+  double total_ms[K_ALL_KINDS] = {};
+  int64_t count[K_ALL_KINDS] = {};
   int pending_kind = -1;
   cudaEvent_t pending = nullptr;
 };
@@ -212,7 +212,7 @@ moe_status moe_profile_enable(int32_t max_launches) {
   g_prof.pairs.clear();
   g_prof.used = 0;
   g_prof.pending = nullptr;
-  for (int i = 0; i < K_NUM_KINDS; ++i) {
+  for (int i = 0; i < K_ALL_KINDS; ++i) {
     g_prof.total_ms[i] = 0;
     g_prof.count[i] = 0;
   }
@@ -250,7 +250,7 @@ moe_status moe_profile_forget(void) {
 }
 
 moe_status moe_profile_totals(int32_t kind, double* total_ms, int64_t* count) {
-  if (kind < 0 || kind >= K_NUM_KINDS || !total_ms || !count) return MOE_ERR_INVALID;
+  if (kind < 0 || kind >= K_ALL_KINDS || !total_ms || !count) return MOE_ERR_INVALID;
   std::lock_guard<std::mutex> lk(g_prof_mu);
   *total_ms = g_prof.total_ms[kind];
   *count = g_prof.count[kind];
@@ -258,13 +258,13 @@ moe_status moe_profile_totals(int32_t kind, double* total_ms, int64_t* count) {
 }
 
 const char* moe_profile_kind_name(int32_t kind) {
-  static const char* names[K_NUM_KINDS] = {"router_logits", "route", "permute", "x_prep",
+  static const char* names[K_ALL_KINDS] = {"router_logits", "route", "permute", "x_prep",
                                            "gateup", "down", "combine", "fused_decode",
                                            "fused_stack", "kv_append", "kv_pages", "kv_move",
                                            "attn_rows", "attn_decode", "attn_chunk",
                                            "attn_combine", "rms_norm", "logprobs", "linear_step",
                                            "linear_chunk"};
-  if (kind < 0 || kind >= K_NUM_KINDS) return "";
+  if (kind < 0 || kind >= K_ALL_KINDS) return "";
   return names[kind];
 }
 
