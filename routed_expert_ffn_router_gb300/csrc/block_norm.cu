@@ -4,10 +4,16 @@
 // A CTA has a row at a time: a thread holds its values in registers from the one read
 // of x and r to the write of y, so the row's sum of squares is the only exchange (a
 // shuffle tree and one barrier). With more rows than CTAs fit on the GPU a CTA goes on
-// to the row a grid further, whose loads are under way meanwhile. A pass over memory
-// and nothing else; what kept it from memory's rate were instructions per value
-// (48 in a first version of the 8-bit form: conversions chosen per value, divisions,
-// addresses in 64 bits).
+// to the row a grid further, whose loads are under way meanwhile; its weights stay in
+// registers, widened, and its addresses go forward by a step. A pass over memory and
+// nothing else; what kept it from memory's rate were instructions per value (the
+// 8-bit form: 82 us with conversions chosen per value, divisions and a CTA per row, 47
+// without, 44 with rows fetched ahead, 39.5 with the weights widened once).
+//
+// Measured, back to back in a graph: 8 rows of 2,048 (fp32 to a bf16 residual and
+// result) 1.8 us, a launch's latency; 2,048 such rows 5.9 us for 42 MB (7.1 TB/s, part
+// of it from the L2); 8,192 x 4,096 with residual to e4m3 39.5 us for 235 MB (6.0 TB/s,
+// 0.88 of a copy's rate: what remains are the issue slots and the ends of rows).
 #include <atomic>
 
 #include <type_traits>
@@ -158,10 +164,16 @@ __global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : (WIDE ? 1280 : 1536) 
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
   griddep_wait();
   griddep_launch_dependents();
-  Raw<WIDE> rx[NV], rr[NV], rw[NV];
-  const auto fetch = [&](int t) {
-    const char* x = static_cast<const char*>(a.x) + t * a.x_stride * (a.x_type == MOE_T_F32 ? 4 : 2);
-    const char* r = static_cast<const char*>(a.res) + t * a.res_stride * (a.res_type == MOE_T_F32 ? 4 : 2);
+  Raw<WIDE> rx[NV], rr[NV];
+  // the row that is fetched next, and the one that is written
+  const int xs = a.x_type == MOE_T_F32 ? 4 : 2, rs = a.res_type == MOE_T_F32 ? 4 : 2, ys = FP8 ? 1 : a.y_type == MOE_T_F32 ? 4 : 2;
+  int t = blockIdx.x;
+  const char* x = static_cast<const char*>(a.x) + t * a.x_stride * xs;
+  char* res = static_cast<char*>(a.res) + t * a.res_stride * rs;
+  char* y = static_cast<char*>(a.y) + t * a.y_stride * ys;
+  float* scales = FP8 ? a.scales + (long long)t * g.n_groups : nullptr;
+  const long long x_step = gridDim.x * a.x_stride * xs, r_step = gridDim.x * a.res_stride * rs, y_step = gridDim.x * a.y_stride * ys;
+  const auto fetch = [&](const char* r) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * nt + tid) * 8;
@@ -171,18 +183,23 @@ __global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : (WIDE ? 1280 : 1536) 
       }
     }
   };
-  int t = blockIdx.x;
-  fetch(t);
-  if (a.w)
+  fetch(res);
+  float2 w[NV][4];  // the weights, their offset added
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (j * nt + tid) * 8;
-      if (c < a.H) rw[j] = load_raw<WIDE>(a.w, a.w_type, c);
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * nt + tid) * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[j][i] = make_float2(1.f, 1.f);
+    if (a.w && c < a.H) {
+      const Raw<WIDE> rw = load_raw<WIDE>(a.w, a.w_type, c);
+      widen(rw, a.w_type, w[j]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[j][i] = add2(w[j][i], make_float2(a.w_offset, a.w_offset));
     }
+  }
   for (int turn = 0;; turn ^= 1) {
     float2 r[NV][4];
     float2 sum = make_float2(0.f, 0.f);
-    char* res = static_cast<char*>(a.res) + t * a.res_stride * (a.res_type == MOE_T_F32 ? 4 : 2);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * nt + tid) * 8;
@@ -202,23 +219,17 @@ __global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : (WIDE ? 1280 : 1536) 
 #pragma unroll
       for (int i = 0; i < 4; ++i) sum = fma2(r[j][i], r[j][i], sum);
     }
-    const int here = t;
     t += gridDim.x;
-    if (t < a.T) fetch(t);
+    x += x_step;
+    res += r_step;
+    if (t < a.T) fetch(res);
     if (FP8 && g.shift < 0 && tid == 0) row_max[turn] = 0;
     const float root = rsqrtf(cta_sum(sum.x + sum.y, part[turn]) * g.inv_H + a.eps);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r[j][i] = mul2(r[j][i], make_float2(root, root));
-      if (a.w) {
-        float2 w[4];
-        widen(rw[j], a.w_type, w);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r[j][i] = mul2(r[j][i], add2(w[i], make_float2(a.w_offset, a.w_offset)));
-      }
+      for (int i = 0; i < 4; ++i) r[j][i] = mul2(mul2(r[j][i], make_float2(root, root)), w[j][i]);
     }
-    char* y = static_cast<char*>(a.y) + here * a.y_stride * (FP8 ? 1 : a.y_type == MOE_T_F32 ? 4 : 2);
     if constexpr (!FP8) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
@@ -238,7 +249,6 @@ __global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : (WIDE ? 1280 : 1536) 
         if ((j * nt + tid) * 8 >= a.H) m[j] = 0.f;
         for (int o = 1; o < lanes; o <<= 1) m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], o));
       }
-      float* scales = a.scales + (long long)here * g.n_groups;
       if (g.shift < 0) {
         float top = 0.f;
 #pragma unroll
@@ -281,6 +291,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : (WIDE ? 1280 : 1536) 
       }
     }
     if (t >= a.T) break;
+    y += y_step;
+    if (FP8) scales += (long long)gridDim.x * g.n_groups;
   }
 }
 
