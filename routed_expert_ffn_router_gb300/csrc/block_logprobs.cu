@@ -12,11 +12,15 @@
 // else d is bounded by -200, where 2^d is 0 in fp32 already (a row of the type's
 // lowest value is uniform, and -inf - -inf no NaN).
 //
+// One value of the maximum is left out of l, which ln(1 + l) puts back: where one token
+// has nearly all of the probability, its logarithm and the entropy are as exact
+// relative to themselves as elsewhere.
+//
 // A row is read by a cluster of 1 to 8 CTAs, each by 8 warps that take chunks of 32
-// lanes x 64 bytes in turn, the next chunk's loads under way; rows start anywhere,
-// so the pieces of a row go by 16-byte boundaries of memory and the first and the
-// last by single values. The parts meet through shared memory, then through the
-// cluster's: few rows use many SMs without a workspace or a second launch.
+// lanes x 64 bytes in turn, through shared memory, the next chunk's copies under way; rows
+// start anywhere, so the pieces of a row go by 16-byte boundaries of memory and the
+// first and the last by single values. The parts meet through shared memory, then
+// through the cluster's: few rows use many SMs without a workspace or a second launch.
 //
 // Top alternatives: each warp keeps its best 32 as sorted keys (order of the logit,
 // then lower id: all distinct), one per lane. A chunk is looked through only if its
@@ -25,6 +29,17 @@
 // that. Ruled out tokens (-inf) never enter; a row with fewer than k others is
 // filled up at the end. The rank likewise counts only in chunks whose maximum
 // reaches the token's logit.
+//
+// Measured, back to back in a graph: a row of 32,000 fp32 logits 7.2 us (latency: first
+// loads, joins); 64 rows of 50,257, nine tenths ruled out, 20 alternatives, 17.1 us; 2,048
+// rows of 131,072 bf16, one alternative, 109 us for 537 MB (4.9 TB/s, 0.73 of a copy's
+// rate). What binds there is the way through a chunk (maximum, vote, sums) and the
+// ends of rows, not the copies: three or four chunks under way take as long, chunks of 16,
+// 32, 48, 80 and 96 bytes a lane 157, 123, 115, 108 and 109 us (the larger ones cost the
+// short calls), five and six CTAs per SM 112 and 117. Chunks in registers, which
+// spilled, took 126; two CTAs a row then 146, CTAs of 512 threads 137.
+#include <atomic>
+
 #include "block_internal.h"
 #include "kv_common.cuh"
 #include "packed.cuh"
@@ -39,9 +54,13 @@ typedef unsigned long long Key;
 constexpr int kThreads = 256;
 constexpr int kWarpsPerCta = kThreads / 32;
 constexpr int kVecs = 4;  // 16-byte pieces of a lane's chunk
+constexpr int kStages = 2;  // chunks of a warp: one is worked on, the others under way
+constexpr int kRing = kStages * kThreads * kVecs * 16;  // bytes
 constexpr int kMostParts = 8;  // CTAs of a row
 static_assert(kWarpsPerCta >= kMostParts, "a warp fetches each part's result, and they meet in the warps' places");
 
+// Over some values with the maximum m: one value of m is left out of l (and its share of
+// s is 0), so that ln(1 + l) is right where the maximum is nearly all.
 struct Part {
   float m, l, s;
   int rank;
@@ -70,8 +89,10 @@ __device__ __forceinline__ void join(Part& a, const Part& b, float c) {
   const float m = max_nan(a.m, b.m);
   const float da = bounded((a.m - m) * c), db = bounded((b.m - m) * c);
   const float ea = kv::ex2(da), eb = kv::ex2(db);
-  a.s = ea * (a.s + a.l * da) + eb * (b.s + b.l * db);
-  a.l = ea * a.l + eb * b.l;
+  const bool first = a.m >= b.m;  // whose value is left out; the other's joins
+  const float e = first ? eb : ea, d = first ? db : da;
+  a.s = ea * (a.s + a.l * da) + eb * (b.s + b.l * db) + e * d;
+  a.l = ea * a.l + eb * b.l + e;
   a.m = m;
   a.rank += b.rank;
 }
@@ -130,6 +151,14 @@ __device__ __forceinline__ Key peer_u64(uint32_t a) {
   return v;
 }
 
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_but() {  // all but the last N groups are there
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // How a type's values lie in the 32-bit words of a piece.
 template <int TYPE>
 struct Words {
@@ -137,7 +166,7 @@ struct Words {
   static constexpr int kSize = kWide ? 4 : 2, kPer = 16 / kSize;  // values per piece
   static constexpr uint32_t kNone = kWide ? 0xff800000u : kHalf ? 0xfc00fc00u : 0xff80ff80u;  // -inf
   // where the fast sums count everything lower as this much
-  static constexpr uint32_t kLowBits = kHalf ? 0xfbfffbffu : 0xf149f149u;
+  static constexpr uint32_t kLowBits = kWide ? 0xf147edcdu : kHalf ? 0xfbfffbffu : 0xf149f149u;
   static constexpr float kLow = kHalf ? -65504.f : -9.9e29f;  // (that or lower)
   __device__ static float at(const uint4& v, int e) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -145,17 +174,34 @@ struct Words {
     const float2 f = kv::unpack2<kHalf>(w[e >> 1]);
     return e & 1 ? f.y : f.x;
   }
+  __device__ static __half2 half2_of(uint32_t a) { return *reinterpret_cast<__half2*>(&a); }
+  __device__ static __nv_bfloat162 bf162_of(uint32_t a) { return *reinterpret_cast<__nv_bfloat162*>(&a); }
+  template <typename T2>
+  __device__ static uint32_t word(T2 a) { return *reinterpret_cast<const uint32_t*>(&a); }
   // the larger, NaN if one is NaN
   __device__ static uint32_t max_word(uint32_t a, uint32_t b) {
-    if constexpr (kWide) {
-      return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
-    } else if constexpr (kHalf) {
-      const __half2 r = __hmax2_nan(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
-      return *reinterpret_cast<const uint32_t*>(&r);
-    } else {
-      const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
-      return *reinterpret_cast<const uint32_t*>(&r);
-    }
+    if constexpr (kWide) return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
+    if constexpr (kHalf) return word(__hmax2_nan(half2_of(a), half2_of(b)));
+    return word(__hmax2_nan(bf162_of(a), bf162_of(b)));
+  }
+  // the bits of a value of w that is m; 0: none
+  __device__ static uint32_t half_at(uint32_t w, float m) {
+    if constexpr (kWide) return __uint_as_float(w) == m ? ~0u : 0u;
+    const float2 f = kv::unpack2<kHalf>(w);
+    return f.x == m ? 0xffffu : f.y == m ? 0xffff0000u : 0u;
+  }
+  // per 16-bit value: the sum; 1 where a >= b or a > b, else 0 (and with a NaN)
+  __device__ static uint32_t add_word(uint32_t a, uint32_t b) {
+    if constexpr (kHalf) return word(__hadd2(half2_of(a), half2_of(b)));
+    return word(__hadd2(bf162_of(a), bf162_of(b)));
+  }
+  __device__ static uint32_t ge_word(uint32_t a, uint32_t b) {
+    if constexpr (kHalf) return word(__hge2(half2_of(a), half2_of(b)));
+    return word(__hge2(bf162_of(a), bf162_of(b)));
+  }
+  __device__ static uint32_t gt_word(uint32_t a, uint32_t b) {
+    if constexpr (kHalf) return word(__hgt2(half2_of(a), half2_of(b)));
+    return word(__hgt2(bf162_of(a), bf162_of(b)));
   }
   __device__ static float max_of(uint32_t w) {
     if constexpr (kWide) return __uint_as_float(w);
@@ -228,6 +274,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
   using W = Words<TYPE>;
   constexpr int E = W::kPer;
   __shared__ Shared sh;
+  extern __shared__ uint4 ring[];  // [kStages][kWarpsPerCta][kVecs][32]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_wait();
   griddep_launch_dependents();
@@ -238,18 +285,23 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
   int v0 = (rank * kWarpsPerCta + warp) * 32 * kVecs;
   // chunks that hold whole pieces only
   const int whole0 = row.lead ? 1 : 0, whole1 = (row.lead + a.V) / E;
-  const auto fetch = [&](uint4 (&x)[kVecs], int v) {
+  // Chunk v on its way into a stage, where a lane finds the pieces that it has fetched
+  // itself (no other reads them, so its own waits are all there is).
+  const auto place = [&](int stage) { return ring + (stage * kWarpsPerCta + warp) * kVecs * 32 + lane; };
+  const auto fetch = [&](int stage, int v) {
+    uint4* to = place(stage);
     if (v >= whole0 && v + 32 * kVecs <= whole1) {
       const uint4* from = reinterpret_cast<const uint4*>(row.base) + v + lane;
 #pragma unroll
-      for (int u = 0; u < kVecs; ++u) x[u] = __ldcs(from + u * 32);
-    } else {
+      for (int u = 0; u < kVecs; ++u) copy16(to + u * 32, from + u * 32);
+    } else if (v < row.n_vec) {
 #pragma unroll
-      for (int u = 0; u < kVecs; ++u) x[u] = row.piece(v + u * 32 + lane);
+      for (int u = 0; u < kVecs; ++u) to[u * 32] = row.piece(v + u * 32 + lane);
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  uint4 even[kVecs], odd[kVecs];
-  fetch(even, v0);
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(i, v0 + i * step);
   const float c = 1.4426950408889634f / a.temperature;
   const int token = a.tokens ? a.tokens[t] : -1;
   const bool has = token >= 0 && token < a.V;
@@ -258,11 +310,13 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
   const float mine = !has ? kBig : mine_raw == mine_raw ? mine_raw : kNone;
   // a logit above this one is at or above `mine` (for ids before the token's)
   const float below = mine == 0.f ? -1e-45f : __int_as_float(__float_as_int(mine) + (mine > 0.f ? -1 : 1));
-  const auto largest = [&](const uint4 (&raw)[kVecs]) {
+  const auto largest = [&](const uint4* at) {
     uint32_t mw = W::kNone;
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u)
-      mw = W::max_word(W::max_word(W::max_word(mw, raw[u].x), W::max_word(raw[u].y, raw[u].z)), raw[u].w);
+    for (int u = 0; u < kVecs; ++u) {
+      const uint4 v = at[u * 32];
+      mw = W::max_word(W::max_word(mw, W::max_word(v.x, v.y)), W::max_word(v.z, v.w));
+    }
     return W::max_of(mw);
   };
   // What the k best are not below, from the first chunks: the k-th largest of the
@@ -272,7 +326,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
   if (a.top) {
     const int warps = min(max((row.n_vec - rank * kWarpsPerCta * 32 * kVecs + 32 * kVecs - 1) / (32 * kVecs), 0), kWarpsPerCta);
     if (warp < warps) {
-      const float mx = largest(even), x = sorted_lanes(mx == mx ? mx : kNone);
+      copies_but<kStages - 2>();
+      const float mx = largest(place(0)), x = sorted_lanes(mx == mx ? mx : kNone);
       floor = __shfl_sync(0xffffffffu, x, a.top - 1);
       if (lane == (a.top + warps - 1) / warps - 1) sh.mth[warp] = x;
     }
@@ -284,25 +339,56 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
     __syncthreads();
   }
 
-  float m = kNone;                                  // the warp's
-  float2 l2 = make_float2(0.f, 0.f), s2 = l2;       // the lane's
+  float m = kNone;  // the warp's
+  float2 l2 = make_float2(0.f, 0.f), s2 = l2;  // the lane's, but for one value of m
   int count = 0;
   Key best = 0;
-  const auto chunk = [&](const uint4 (&raw)[kVecs], int v0) {
-    const float mx = largest(raw), top = warp_max_nan(mx);
+  const uint32_t mine_word = has && !W::kWide ? row.bits(token) * 0x10001u : 0;
+  // (Each pass over a chunk reads it from shared memory again: held in registers, it could
+  // not be as large.)
+  const auto chunk = [&](uint4* at, int v0) {
+    const float mx = largest(at), top = warp_max_nan(mx);
     if (top == kNone && mine != kNone) return;  // nothing in it
-    if (top > m || top != top) {
+    const bool rose = top > m || top != top;
+    bool out = false;  // whether the lane leaves one of its values out
+    if (rose) {
       const float up = max_nan(m, top), d = bounded((m - up) * c), e = kv::ex2(d);
       s2 = fma2(l2, make_float2(d, d), s2);
       s2.x *= e; s2.y *= e;
       l2.x *= e; l2.y *= e;
+      if (lane == 0) {  // the value that had been left out
+        l2.x += e;
+        s2.x = fmaf(e, d, s2.x);
+      }
       m = up;
+      out = lane == __ffs(__ballot_sync(0xffffffffu, mx == top)) - 1;
     }
+    asm volatile("" ::: "memory");
     if (m < 1e29f && (m - W::kLow) * c > 200.f && c < 1e6f) {  // (the products stay finite)
+      // The value that is left out gives way to one that adds nothing, for the time of the sums.
+      uint32_t *gone = nullptr, was = 0;
+      if (out) {
+#pragma unroll 1
+        for (int u = 0; u < kVecs && !gone; ++u) {
+          const uint4 v = at[u * 32];
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t half = W::half_at(w[i], m);
+            if (!gone && half) {
+              gone = reinterpret_cast<uint32_t*>(at + u * 32) + i;
+              was = w[i];
+              *gone = (was & ~half) | (W::kLowBits & half);
+            }
+          }
+        }
+      }
       const float2 c2 = make_float2(c, c), m2 = make_float2(-m, -m);
+      float2 l = make_float2(0.f, 0.f), s = l;
 #pragma unroll
       for (int u = 0; u < kVecs; ++u) {
-        const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+        const uint4 v = at[u * 32];
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) {
           float2 f;
@@ -311,34 +397,55 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
           else
             f = kv::unpack2<W::kHalf>(W::max_word(w[i], W::kLowBits));
           const float2 d = mul2(add2(f, m2), c2), e = make_float2(kv::ex2(d.x), kv::ex2(d.y));
-          l2 = add2(l2, e);
-          s2 = fma2(e, d, s2);
+          l = add2(l, e);
+          s = fma2(e, d, s);
         }
       }
+      l2 = add2(l2, l);
+      s2 = add2(s2, s);
+      if (gone) *gone = was;
     } else {
 #pragma unroll 1
-      for (int u = 0; u < kVecs; ++u) {  // (read again: the usual path stays short)
-        const uint4 v = row.piece(v0 + u * 32 + lane);
+      for (int u = 0; u < kVecs; ++u) {
+        const uint4 v = at[u * 32];
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-          const float d = bounded((W::at(v, i) - m) * c), e = kv::ex2(d);
-          l2.x += e;
-          s2.x = fmaf(e, d, s2.x);
+          const float x = W::at(v, i), d = bounded((x - m) * c), e = kv::ex2(d);
+          if (out && x == m) {
+            out = false;
+          } else {
+            l2.x += e;
+            s2.x = fmaf(e, d, s2.x);
+          }
         }
       }
     }
     if (!(mx < mine)) {
-      if (mine != kNone) {
+      const bool before = row.id_of(v0 + 32 * kVecs, 0) <= token, after = row.id_of(v0, 0) > token;
+      if (!W::kWide && mine != kNone && (before || after)) {
+        // two at a time: ones, summed up in the type (16 at most)
+        uint32_t n = 0;
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u) {
+          const uint4 v = at[u * 32];
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) n = W::add_word(n, before ? W::ge_word(w[i], mine_word) : W::gt_word(w[i], mine_word));
+        }
+        const float2 two = kv::unpack2<W::kHalf>(n);
+        count += (int)(two.x + two.y);
+      } else if (mine != kNone) {
 #pragma unroll
         for (int u = 0; u < kVecs; ++u) {  // (those beside the token in its piece: below)
+          const uint4 v = at[u * 32];
           const float limit = row.id_of(v0 + u * 32 + lane, E - 1) < token ? below : mine;
 #pragma unroll
-          for (int i = 0; i < E; ++i) count += W::at(raw[u], i) > limit ? 1 : 0;
+          for (int i = 0; i < E; ++i) count += W::at(v, i) > limit ? 1 : 0;
         }
       } else {
 #pragma unroll 1
         for (int u = 0; u < kVecs; ++u) {
-          const uint4 v = row.piece(v0 + u * 32 + lane);
+          const uint4 v = at[u * 32];
 #pragma unroll
           for (int i = 0; i < E; ++i)
             count += W::at(v, i) > kNone || (unsigned)row.id_of(v0 + u * 32 + lane, i) < (unsigned)token ? 1 : 0;
@@ -352,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
         if (__any_sync(0xffffffffu, reach >= floor)) {
 #pragma unroll
           for (int u = 0; u < kVecs; ++u) {
-            const uint4 v = raw[u];
+            const uint4 v = at[u * 32];
             uint32_t mask = 0;  // of this lane's values
 #pragma unroll
             for (int i = 0; i < E; ++i) mask |= W::at(v, i) >= floor && W::at(v, i) > kNone ? 1u << i : 0u;
@@ -379,12 +486,12 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
       }
     }
   };
-  for (; v0 < row.n_vec; v0 += 2 * step) {
-    if (v0 + step < row.n_vec) fetch(odd, v0 + step);
-    chunk(even, v0);
-    if (v0 + step >= row.n_vec) break;
-    if (v0 + 2 * step < row.n_vec) fetch(even, v0 + 2 * step);
-    chunk(odd, v0 + step);
+  for (int stage = 0; v0 < row.n_vec; v0 += step) {
+    copies_but<kStages - 2>();
+    // into the stage that was worked on last
+    fetch(stage == 0 ? kStages - 1 : stage - 1, v0 + (kStages - 1) * step);
+    chunk(place(stage), v0);
+    stage = stage == kStages - 1 ? 0 : stage + 1;
   }
   // equal logits before the token in its own piece
   if (rank == 0 && warp == 0 && has && mine != kNone) {
@@ -425,12 +532,12 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
   p = sh.part[0];
   const float nan = __int_as_float(0x7fffffff);
   const bool broken = !(p.m < __int_as_float(0x7f800000)), empty = p.m == kNone;
-  const float ln_l = logf(p.l);
+  const float ln_l = log1pf(p.l);
   const auto log_p = [&](float z) { return broken ? nan : empty ? kNone : (z - p.m) / a.temperature - ln_l; };
   if (lane == 0) {
     if (a.logprob) a.logprob[t] = has ? log_p(mine_raw) : 0.f;
     if (a.rank) a.rank[t] = has ? p.rank : -1;
-    if (a.entropy) a.entropy[t] = broken ? nan : empty ? 0.f : fmaxf(ln_l - 0.6931471805599453f * (p.s / p.l), 0.f);
+    if (a.entropy) a.entropy[t] = broken ? nan : empty ? 0.f : fmaxf(ln_l - 0.6931471805599453f * (p.s / (1.f + p.l)), 0.f);
   }
   if (a.top) {
     Key k = sh.key[0][lane];
@@ -457,9 +564,21 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
 
 template <int TYPE>
 cudaError_t launch_type(const moe_logprobs_args& a, int parts, cudaStream_t st) {
+  if (kRing + sizeof(Shared) > 48 << 10) {
+    static std::atomic<unsigned long long> ready{0};  // by device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !(ready.load() >> dev & 1)) {
+      e = cudaFuncSetAttribute(logprobs_kernel<TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
+      if (e != cudaSuccess) return e;
+      if (dev < 64) ready.fetch_or(1ull << dev);
+    }
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.T * parts);
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kRing;
   cfg.stream = st;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -479,7 +598,7 @@ cudaError_t launch_type(const moe_logprobs_args& a, int parts, cudaStream_t st) 
 
 cudaError_t launch_token_logprobs(const moe_logprobs_args& a, cudaStream_t st) {
   // CTAs per row: while all fit on the GPU (four per SM) and a part is more than a
-  // chunk for each warp. (2,048 rows of 131,072 by two CTAs each: 146 us instead of 126;
+  // chunk for each warp. (2,048 rows of 131,072 by two CTAs each, when one took 126 us: 146;
   // the last third of them by two, in a launch of its own: no change.)
   int parts = 1;
   const long long chunk = (long long)kThreads * kVecs * (a.type == MOE_T_F32 ? 4 : 8);

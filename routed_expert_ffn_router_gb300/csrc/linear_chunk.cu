@@ -37,6 +37,13 @@
 // 20 and 23: issue the products, those of A and O and those of U (a product takes a
 // warp 20 instructions, more time than the tensor cores need for it); 21: TMA; 22:
 // decays, two blocks ahead.
+//
+// Measured, back to back in a graph, 16 k heads and 32 v heads of [128][128], bf16: a
+// prompt of 2,048 tokens 40.5 us (19 GFLOP; floor 8.1 us of bytes: the time is latency,
+// start, two passes over a part's two blocks, the exchange); eight ragged prompts of
+// up to 4,001 tokens 155 us (floor 78.6 us of bytes; 512 MB, tensor pipe 34 % busy, a
+// block of 128 tokens 7,500 cycles of products, conversions and the waits that tie
+// them). An item's fixed cost is about 11 us, which is why few rows go row by row.
 #include <cuda.h>
 
 #include <atomic>

@@ -7,6 +7,11 @@
 // costs a read and a write of the state. Rows come through shared memory up to 16 at a
 // time; a row's products q S are summed over Dk within a warp by shuffles and over
 // the four warps once per 16 rows.
+//
+// What bounds it: the state, read and written once; a token's arithmetic is 6 Dk Dv
+// flops per head and small beside it. Measured, back to back in a graph: 64 sequences
+// of one token, 32 heads of [128][128], 47 to 49 us for 270 MB (5.6 TB/s, 0.83 of a copy's
+// rate). CTAs of 64 columns took 48.6; rows staged one at a time 52.
 #include "block_internal.h"
 #include "kv_common.cuh"
 #include "linear_common.cuh"

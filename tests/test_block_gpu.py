@@ -341,3 +341,29 @@ def test_logprobs_of_rows_beyond_what_fits_at_once():
     check_logprobs(z, tok, 3)
     first = token_logprobs(z[:50], tok[:50], top=3)
     assert torch.equal(first["top_ids"], token_logprobs(z, tok, top=3)["top_ids"][:50])
+
+
+@pytest.mark.parametrize("T,V,dtype", [(1, 32000, torch.float32), (6, 50257, torch.bfloat16), (700, 9001, torch.float16)])
+def test_logprobs_of_a_token_with_nearly_all(T, V, dtype):
+    """Logarithm and entropy of a row in which one token (rarely two equal ones) has all but
+    e^-6 to e^-20: right relative to themselves. The rest, sum e^d: each term's argument is
+    off by 3 F |d| (difference, factor, product), its exponential by 4 F, and it goes
+    through at most V / 256 + 60 additions of a relative F; ln(1 + rest), the entropy's
+    quotient, products and sum: 16 F."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    z = torch.randn(T, V, generator=g, device="cuda")
+    at = torch.randint(0, V, (T,), generator=g, device="cuda")
+    z.scatter_(1, at[:, None], (math.log(V) + 6 + 14 * torch.rand(T, 1, generator=g, device="cuda")))
+    z = z.to(dtype)
+    tok = z.argmax(1).int()
+    got = token_logprobs(z, tok, top=2)
+    d = z.double() - z.double().amax(1, keepdim=True)
+    d.scatter_(1, tok.long()[:, None], -INF)
+    e = torch.exp(d)
+    rest, far = e.sum(1), torch.where(e > 0, -d, torch.zeros_like(d)).amax(1)
+    want = -torch.log1p(rest)
+    ent = -want - torch.where(e > 0, e * d, torch.zeros_like(d)).sum(1) / (1 + rest)
+    part = (V / 256 + 60 + 3 * far + 4 + 16) * ref.F
+    within(got["logprob"], want, part * want.abs(), "logprob")
+    within(got["top_logprobs"][:, 0], want, part * want.abs(), "top")
+    within(got["entropy"], ent, (part + 3 * ref.F) * ent, "entropy")
