@@ -56,6 +56,8 @@ def _rows(t, shape, types, what, device):
     if kind is None or t.shape != shape or t.device != device:
         raise ValueError(f"{what} must be {list(shape)} on {device}, of {', '.join(str(x)[6:] for x in types)}")
     T, H = shape
+    if T >= 1 << 31 or H >= 1 << 31:
+        raise ValueError(f"{what}: more than 2^31 - 1 rows or columns")
     s0, s1 = t.stride()
     if s1 != 1 and H > 1:
         raise ValueError(f"{what}: the values of a row must be contiguous")

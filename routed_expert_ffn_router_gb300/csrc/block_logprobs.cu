@@ -38,8 +38,6 @@
 // 32, 48, 80 and 96 bytes a lane 157, 123, 115, 108 and 109 us (the larger ones cost the
 // short calls), five and six CTAs per SM 112 and 117. Chunks in registers, which
 // spilled, took 126; two CTAs a row then 146, CTAs of 512 threads 137.
-#include <atomic>
-
 #include "block_internal.h"
 #include "kv_common.cuh"
 #include "packed.cuh"
@@ -55,7 +53,6 @@ constexpr int kThreads = 256;
 constexpr int kWarpsPerCta = kThreads / 32;
 constexpr int kVecs = 4;  // 16-byte pieces of a lane's chunk
 constexpr int kStages = 2;  // chunks of a warp: one is worked on, the others under way
-constexpr int kRing = kStages * kThreads * kVecs * 16;  // bytes
 constexpr int kMostParts = 8;  // CTAs of a row
 static_assert(kWarpsPerCta >= kMostParts, "a warp fetches each part's result, and they meet in the warps' places");
 
@@ -274,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
   using W = Words<TYPE>;
   constexpr int E = W::kPer;
   __shared__ Shared sh;
-  extern __shared__ uint4 ring[];  // [kStages][kWarpsPerCta][kVecs][32]
+  __shared__ uint4 ring[kStages * kWarpsPerCta * kVecs * 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_wait();
   griddep_launch_dependents();
@@ -564,21 +561,9 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
 
 template <int TYPE>
 cudaError_t launch_type(const moe_logprobs_args& a, int parts, cudaStream_t st) {
-  if (kRing + sizeof(Shared) > 48 << 10) {
-    static std::atomic<unsigned long long> ready{0};  // by device
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev >= 64 || !(ready.load() >> dev & 1)) {
-      e = cudaFuncSetAttribute(logprobs_kernel<TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
-      if (e != cudaSuccess) return e;
-      if (dev < 64) ready.fetch_or(1ull << dev);
-    }
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.T * parts);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kRing;
   cfg.stream = st;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -75,8 +75,8 @@ class LinearAttention:
         q_stride, k_stride = self._heads(q, self.Hk, self.Dk, "q"), self._heads(k, self.Hk, self.Dk, "k")
         v_stride = self._heads(v, self.Hv, self.Dv, "v")
         n = q.shape[0]
-        if k.shape[0] != n or v.shape[0] != n:
-            raise ValueError("q, k and v must have the same rows")
+        if k.shape[0] != n or v.shape[0] != n or n >= 1 << 31:
+            raise ValueError("q, k and v must have the same rows, fewer than 2^31")
         shape, strides = g.shape, g.stride()
         if g.dtype != _F32 or g.device != self.device or shape not in ((n, self.Hv), (self.Hv,)) or \
                 (strides[-1] != 1 and self.Hv > 1):

@@ -255,3 +255,17 @@ def test_calls_refuse_another_device(monkeypatch):
         with pytest.raises(ValueError, match="cuda:1"):
             block._on(device, None)
     assert block._on(torch.device("cuda", 1), 77) == 77
+
+
+def test_sizes_beyond_int32_are_refused():
+    """They would come out modulo 2^32 in the C structs."""
+    for shape in ((1 << 31, 1), (1, 1 << 31), (1 << 32, 1)):
+        x = torch.zeros(1, dtype=torch.bfloat16).expand(shape)
+        with pytest.raises(ValueError, match="more than"):
+            rms_norm(x)
+        with pytest.raises(ValueError, match="more than"):
+            token_logprobs(x)
+    layer = LinearAttention(1, 1, 1, 8, 8, device="cpu")
+    q = torch.zeros(8, dtype=torch.bfloat16).as_strided((1 << 31, 1, 8), (0, 8, 1))
+    with pytest.raises(ValueError, match="fewer than"):
+        layer.step(q, q, q, torch.zeros(1))
