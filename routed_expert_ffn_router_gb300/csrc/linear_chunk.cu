@@ -43,7 +43,12 @@
 // start, two passes over a part's two blocks, the exchange); eight ragged prompts of
 // up to 4,001 tokens 155 us (floor 78.6 us of bytes; 512 MB, tensor pipe 34 % busy, a
 // block of 128 tokens 7,500 cycles of products, conversions and the waits that tie
-// them). An item's fixed cost is about 11 us, which is why few rows go row by row.
+// them). An item's fixed cost is about 11 us, which is why few rows go row by row. The
+// chain of a block: A, its conversion by the warp with the last 32 tokens (which has
+// four pieces of A, the first warp one), O, the next A in O's place behind it. Tried on
+// the eight prompts (159 us that time): the output's warps converting half of A 189 (they
+// come late from the output), Q' taken from shared memory where it is q itself 174 (Q's tile
+// is free later), V before Q 162.
 #include <cuda.h>
 
 #include <atomic>
@@ -191,7 +196,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       mbar_init(kt_full + i, 4); mbar_init(kt_empty + i, 1);
       mbar_init(g_full + i, 1); mbar_init(g_empty + i, 16);
     }
-#pragma unroll 1
     mbar_init(v_ready, 4); mbar_init(a_full, 1); mbar_init(p_ready, 4);
     mbar_init(s_ready, 4); mbar_init(u_full, 1); mbar_init(u_free, 4);
     mbar_init(o_full, 1); mbar_init(o_free, 4);
