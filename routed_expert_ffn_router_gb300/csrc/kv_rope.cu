@@ -17,12 +17,16 @@
 // through the chain together, were slower (11.4 us for 2,048 rows of 32 / 8 heads
 // against 11.0): their larger CTAs fill the GPU less evenly.
 //
-// Measured, back to back in a graph (append with rotary positions): 8 rows of 16 / 2
-// heads 3.4 us, the chain and a launch; 2,048 rows of 32 / 8 heads, pages of 64, 10.9
-// us for 50 MB (4.6 TB/s, 0.68 of a copy's rate); five ragged chunks of up to 901 rows,
-// 28 / 4 heads, 64 of 128 values turned in interleaved pairs, fp16, 14.3 us (0.61). A
-// CTA's life is the chain (three latencies of memory) and then few bytes, so that
-// waves of CTAs and not bandwidth bound the long calls.
+// Measured, back to back in a graph: 8 rows of 16 / 2 heads 2.9 us, the chain and a
+// launch; 2,048 rows of 32 / 8 heads, pages of 64, 9.3 us for 50 MB (5.4 TB/s, 0.79 of a
+// copy's rate); five ragged chunks of up to 901 rows, 28 / 4 heads, 64 of 128 values
+// turned in interleaved pairs, fp16, 13.6 us (0.64). A CTA's life is the chain (three
+// latencies of memory) and then few bytes, so that waves of CTAs and not bandwidth
+// bound the long calls. With the values' first pieces fetched behind the chain: 10.8 and
+// 14.3. In halves three pieces at a time and seven CTAs per SM were the best for 16 to 64
+// query heads (32 / 8: four and eight 10.4, four and seven 10.0, two and eight 10.2);
+// interleaved pairs gain and lose with the shape (32 / 8 11.3 with four and eight, 11.7
+// with two and eleven; the ragged case 13.6 and 12.9).
 #include <climits>
 
 #include "kv_common.cuh"
@@ -33,7 +37,6 @@ namespace kv {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kBatch = 4;  // pieces of a thread under way together
 
 struct Rope {
   int rot, interleaved;
@@ -113,10 +116,11 @@ __device__ __forceinline__ Seq find_seq(const Cache& c, const Rows& r, int t, in
 // interleaved, 16-byte pieces of 4 pairs (rot a multiple of 8). 2: single values
 // (any rot, either layout).
 template <bool F16, int MODE>
-__global__ void __launch_bounds__(kThreads, 8) append_rope_kernel(Cache c, Rows r, Rope p, const uint16_t* k, const uint16_t* v,
+__global__ void __launch_bounds__(kThreads, MODE == 0 ? 7 : 8) append_rope_kernel(Cache c, Rows r, Rope p, const uint16_t* k, const uint16_t* v,
                                                                long long stride, int32_t* status) {
   __shared__ __align__(16) float2 cs[kThreads];
   __shared__ int s_tok, s_page, s_pos;  // token (-1: none, -2: no row), page (-1: none), position
+  constexpr int kBatch = MODE == 0 ? 3 : 4;  // pieces of a thread under way together
   const int at = threadIdx.x;
   const long long t = blockIdx.x;
   griddep_wait();
@@ -145,6 +149,10 @@ __global__ void __launch_bounds__(kThreads, 8) append_rope_kernel(Cache c, Rows 
   };
   Cursor cur(at, kThreads, pieces);
   if (MODE != 2) fetch(cur, at);
+  const uint16_t* v_row = v + t * stride;
+  Cursor copy(at, kThreads, vd);
+  uint4 first_v;
+  if (at < n_copy) first_v = *reinterpret_cast<const uint4*>(v_row + copy.h * c.D + copy.e * 8);
   const unsigned long long freq = at < half ? p.freq[at] : 0;
 
   if (at < 32) {
@@ -223,10 +231,9 @@ __global__ void __launch_bounds__(kThreads, 8) append_rope_kernel(Cache c, Rows 
     }
   }
   if (pg < 0) return;
-  Cursor copy(at, kThreads, vd);
   for (int i = at; i < n_copy; i += kThreads, copy.next())
     *reinterpret_cast<uint4*>(c.v + (base + (long long)copy.h * c.page) * c.D + copy.e * 8) =
-        *reinterpret_cast<const uint4*>(v + t * stride + copy.h * c.D + copy.e * 8);
+        i == at ? first_v : *reinterpret_cast<const uint4*>(v_row + copy.h * c.D + copy.e * 8);
 }
 
 }  // namespace

@@ -39,13 +39,13 @@
 // decays, two blocks ahead.
 //
 // Measured, back to back in a graph, 16 k heads and 32 v heads of [128][128], bf16: a
-// prompt of 2,048 tokens 40.5 us (19 GFLOP; floor 8.1 us of bytes: the time is latency,
-// start, two passes over a part's two blocks, the exchange); eight ragged prompts of
-// up to 4,001 tokens 155 us (floor 78.6 us of bytes; 512 MB, tensor pipe 34 % busy, a
+// prompt of 2,048 tokens 40.5 us (floor 8.1 us of bytes: the time is latency, start,
+// two passes over a part's two blocks, the exchange); eight ragged prompts of
+// up to 4,001 tokens 155 us (532 MB, floor 78.3 us; tensor pipe 34 % busy, a
 // block of 128 tokens 7,500 cycles of products, conversions and the waits that tie
 // them). An item's fixed cost is about 11 us, which is why few rows go row by row. The
 // chain of a block: A, its conversion by the warp with the last 32 tokens (which has
-// four pieces of A, the first warp one), O, the next A in O's place behind it. Tried on
+// four pieces of A, the first warp one), O, the next A, which takes the place that O reads. Tried on
 // the eight prompts (159 us that time): the output's warps converting half of A 189 (they
 // come late from the output), Q' taken from shared memory where it is q itself 174 (Q's tile
 // is free later), V before Q 162.
