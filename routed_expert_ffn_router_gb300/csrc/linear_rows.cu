@@ -10,8 +10,9 @@
 //
 // What bounds it: the state, read and written once; a token's arithmetic is 6 Dk Dv
 // flops per head and small beside it. Measured, back to back in a graph: 64 sequences
-// of one token, 32 heads of [128][128], 47 to 49 us for 270 MB (5.6 TB/s, 0.83 of a copy's
-// rate). CTAs of 64 columns took 48.6; rows staged one at a time 52.
+// of one token, 32 heads of [128][128], 43 us for 270 MB (6.2 TB/s, 0.92 of a copy's
+// rate). CTAs of 64 columns were no faster. A one-row window's q, k and v fetched beside the
+// state took 42 to 44 us, and longer windows a fifth more.
 #include "block_internal.h"
 #include "kv_common.cuh"
 #include "linear_common.cuh"
@@ -54,7 +55,9 @@ __global__ void __launch_bounds__(kThreads, DK <= 128 ? 8 : 4) linear_rows_kerne
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int d = row + 16 * i;
-    S[i] = mine && d < a.Dk ? state[(long long)d * a.Dv / 4] : make_float4(0.f, 0.f, 0.f, 0.f);
+    // (evict first, here and below: 64 sequences 48.4 -> 43.3 us, of three rows 69 -> 57; states
+    // that stay in the L2, as those of a model of many layers do not, 12.6 -> 13.9)
+    S[i] = mine && d < a.Dk ? __ldcs(&state[(long long)d * a.Dv / 4]) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
   const bool ok = span_allowed(a, r, b, s, tile == 0 && h == 0);
   for (int t0 = 0; t0 < s.n; t0 += staged) {
@@ -111,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, DK <= 128 ? 8 : 4) linear_rows_kerne
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int d = row + 16 * i;
-    if (d < a.Dk) state[(long long)d * a.Dv / 4] = S[i];
+    if (d < a.Dk) __stcs(&state[(long long)d * a.Dv / 4], S[i]);
   }
 }
 
