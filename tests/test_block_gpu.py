@@ -367,3 +367,18 @@ def test_logprobs_of_a_token_with_nearly_all(T, V, dtype):
     within(got["logprob"], want, part * want.abs(), "logprob")
     within(got["top_logprobs"][:, 0], want, part * want.abs(), "top")
     within(got["entropy"], ent, (part + 3 * ref.F) * ent, "entropy")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_logprobs_order_of_subnormal_logits(dtype):
+    """Logits below the type's normal range are in their order too, and either zero ties."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    T, V = 12, 20011
+    step = torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps
+    z = (torch.randint(-60, 61, (T, V), generator=g, device="cuda").double() * step).to(dtype)
+    z[:, ::7] = -0.0
+    tok = torch.randint(0, V, (T,), generator=g, device="cuda").int()
+    got = token_logprobs(z, tok, top=8)
+    order = torch.sort(z.double(), dim=1, descending=True, stable=True)[1]
+    assert torch.equal(got["rank"], (order == tok[:, None]).int().argmax(1).int())
+    assert torch.equal(got["top_ids"], order[:, :8].int())
