@@ -277,23 +277,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   // Between the two passes: the parts' sums are there; the state at this part's start is
   // put together from those before it by all warps (a quarter of them took four times
   // as long: the cluster's shared memory answers late); `take` reads it; all have read.
-  // The first part's is the initial state, read from memory once more here: behind the
-  // second barrier the part with the sequence's end may write the final one in its place.
   auto between = [&](auto take) {
     if (parts == 1) return;
     __syncwarp();
     cluster_sync();
-    if (part == 0) {
-      // 4 rows x 8 pieces of 16 bytes per warp: whole sectors of memory, banks at most twice
-      const float4* state = reinterpret_cast<const float4*>(a.state + ((long long)s.slot * a.Hv + h) * DK * DV);
-      constexpr int kWide = DV / 32;
-#pragma unroll 2
-      for (int i = tid; i < DK * DV / 4; i += kThreads) {
-        const int r = (i >> 5) / kWide * 4 + (i & 3), j = (i >> 5) % kWide * 8 + (i >> 2 & 7);
-        const float4 x = state[r * (DV / 4) + j];
-        st_s128(start + (j * DK + r) * 16, __float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(x.z), __float_as_uint(x.w));
-      }
-    } else if (n2 > 0)
+    if (part > 0 && n2 > 0)
 #pragma unroll 2
       for (int i = tid; i < DK * DV / 4; i += kThreads) {
         float4 x = peer_f128(peer(sums, 0) + i * 16);
@@ -729,10 +717,21 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           for (int j = 0; j < DV / 4; ++j) put(j, sums + (j * DK + row) * 16);
         if (row == 0) s_part = decay;
       }
+      // The first part reads the initial state again here, before the cluster's second
+      // barrier: behind it the part with the sequence's end may write the final one in
+      // its place at any time. (A pointer that is either memory's or shared memory's: the
+      // state by way of `start` as well was a loop more in every role's code, and the eight
+      // prompts took 2 % longer.)
       between([&] {
+        const float4* from = part == 0 ? state + row * (DV / 4) : reinterpret_cast<const float4*>(smem_linear + (start - smem_u32(smem_linear))) + row;
+        const int pitch = part == 0 ? 1 : DK;
         if (n2 > 0 && held)
 #pragma unroll
-          for (int j = 0; j < DV / 4; ++j) get(j, start + (j * DK + row) * 16);
+          for (int j = 0; j < DV / 4; ++j) {
+            const float4 f = from[j * pitch];
+            S[2 * j] = make_float2(f.x, f.y);
+            S[2 * j + 1] = make_float2(f.z, f.w);
+          }
       });
     }
     if (parts == 1) bring();
