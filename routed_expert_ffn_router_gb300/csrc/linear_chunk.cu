@@ -274,6 +274,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
   };
+  // Every product of this warp has ended before tensor memory is given back and the CTA
+  // ends, also where the warp went on without waiting: with a wait's full time.
+  auto drain = [&](uint32_t bar, uint32_t lead) {
+    const bool gave_up = tries == 1;
+    tries = kTries;
+    tc_commit_el(bar, lead);
+    wait(bar, 0);
+    if (gave_up) tries = 1;
+  };
   // Between the two passes: the parts' sums are there; the state at this part's start is
   // put together from those before it by all warps (a quarter of them took four times
   // as long: the cluster's shared memory answers late); `take` reads it; all have read.
@@ -406,8 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         tc_commit_el(o_full, lead);
         tc_commit_el(v_empty + 8 * x, lead);
       }
-      tc_commit_el(drained, lead);  // every product has ended before tensor memory is given back
-      wait(drained, 0);
+      drain(drained, lead);
     } else if (warp == 23) {
       // ================= products: U =================
       const uint32_t lead = elect_lane(), id_o = idesc_16(F16, 128, DV, true);
@@ -440,8 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       if (n2 == 0) {
         meet();
       }
-      tc_commit_el(u_drained, lead);
-      wait(u_drained, 0);
+      drain(u_drained, lead);
     } else {
       // ================= decays =================
       float next[4];
