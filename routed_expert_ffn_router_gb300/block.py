@@ -61,8 +61,8 @@ def _rows(t, shape, types, what, device):
     s0, s1 = t.stride()
     if s1 != 1 and H > 1:
         raise ValueError(f"{what}: the values of a row must be contiguous")
-    if T <= 1:
-        return kind, max(s0, H)
+    if T <= 1:  # (the distance to a next row says nothing of one)
+        return kind, H
     if s0 < H:
         raise ValueError(f"{what}: rows must not overlap")
     return kind, s0

@@ -64,7 +64,7 @@ class LinearAttention:
         s0, s1, s2 = t.stride()
         if (s2 != 1 and D > 1) or (s1 != D and heads > 1):
             raise ValueError(f"{what}: the heads of a row must be contiguous")
-        return s0 if shape[0] > 1 or s0 > heads * D else heads * D
+        return s0 if shape[0] > 1 else heads * D  # (the distance to a next row says nothing of one)
 
     def _ints(self, t, what):
         if t.dtype != _I32 or t.device != self.device or not t.is_contiguous():

@@ -120,7 +120,7 @@ class PagedKV:
         s0, s1, s2 = t.stride()
         if s2 != 1 or (s1 != D and heads > 1):
             raise ValueError(f"{what}: the heads of a row must be contiguous")
-        return s0 if shape[0] > 1 or s0 > heads * D else heads * D
+        return s0 if shape[0] > 1 else heads * D  # (the distance to a next row says nothing of one)
 
     def _set_rows(self, n_rows, slots, row_start):
         r = self._rows
