@@ -92,8 +92,9 @@ moe_status moe_token_logprobs(const moe_logprobs_args *a, void *stream);
  * fp32; for the rows of a sequence in their order, v head h reading q and k
  * head h / (Hv / Hk),
  *   S   <- exp(g[t][h]) S + k_t^T v_t        o[t][h] = scale q_t S
- * g is the logarithm of the decay: above 0 counts as 0, -inf forgets all that
- * was before the token; g_stride 0: one row of g for all tokens. The rows are
+ * g is the logarithm of the decay: above 0 counts as 0, -inf forgets all finite values
+ * before the token (0 times an infinity or a NaN is NaN: a state that holds one is emptied by
+ * writing zeros); g_stride 0: one row of g for all tokens. The rows are
  * those of moe_kv_rows: sequence b is slot slots[b] (NULL: slot b), the slots
  * of a call distinct; a sequence without rows leaves its state as it was. A
  * slot out of range (2) or one that an earlier sequence of the call has (64)
@@ -128,9 +129,11 @@ moe_status moe_linear_step(const moe_linear_desc *d, const moe_kv_rows *rows, co
 
 /* Prompt chunks: any number of rows per sequence. With Dk and Dv of 64 or 128, and
  * more than a few rows, on the tensor cores: a state and a score enter their products
- * rounded once to `dtype` (the state itself stays within fp32's roundings), and how a
+ * rounded once to `dtype`. The state itself stays within fp32's roundings in bf16; in
+ * fp16 each decayed key is besides off by up to 2^-38 of the largest |k| of its head among
+ * the 128 tokens around it, which shows where larger keys have all but decayed. How a
  * long sequence is split depends on the call, so a row's last bits may differ in
- * another call. There values that a sequence's rows see must be finite: a NaN or an
+ * another call. There a state and values that a sequence's rows see must be finite: a NaN or an
  * infinity may reach rows before it. Other sequences' rows and heads, and rows behind
  * the last sequence, reach nothing. */
 moe_status moe_linear_chunk(const moe_linear_desc *d, const moe_kv_rows *rows, const moe_linear_args *a, void *stream);

@@ -21,7 +21,9 @@
 // step each, as o itself is). In fp16, whose range is narrow and whose step is fixed
 // below 2^-14, K' and S are scaled by a power of two per block and a row of A o D and
 // Q' by one of its own, which bring the largest magnitude to 2^13 and are undone in
-// fp32: the smallest values are then off by up to 2^-38 of the largest. Sums of
+// fp32: the smallest values are then off by up to 2^-38 of the largest. (Of the largest
+// |k|, not the largest decayed one: a head that forgets within a few tokens keeps fewer bits
+// of a key that has decayed to 2^-14 or less when the block ends.) Sums of
 // logarithms are pairs of fp32 values, so that G_i - G_j is right next to large |G|
 // (in fp64 a block's sums took 5,000 cycles).
 //
