@@ -3,7 +3,8 @@
 //
 // A CTA has a row at a time: a thread holds its values in registers from the one read
 // of x and r to the write of y, so the row's sum of squares is the only exchange (a
-// shuffle tree and one barrier). With more rows than CTAs fit on the GPU a CTA goes on
+// shuffle tree and one barrier). With more rows than the grid has CTAs (at most six, three
+// or one per SM: see launch_rows) a CTA goes on
 // to the row a grid further, whose loads are under way meanwhile; its weights stay in
 // registers, widened, and its addresses go forward by a step. A pass over memory and
 // nothing else; what kept it from memory's rate were instructions per value (the
@@ -13,7 +14,12 @@
 // Measured, back to back in a graph: 8 rows of 2,048 (fp32 to a bf16 residual and
 // result) 1.8 us, a launch's latency; 2,048 such rows 5.9 us for 42 MB (7.1 TB/s, part
 // of it from the L2); 8,192 x 4,096 with residual to e4m3 39.5 us for 235 MB (6.0 TB/s,
-// 0.88 of a copy's rate: what remains are the issue slots and the ends of rows).
+// 0.88 of a copy's rate: what remains are the issue slots and the ends of rows). The grid
+// suits 2,048 and 4,096 columns. Others, with 16-bit x, residual and result, the same
+// buffers each call: 4,096 x 8,192 44 us (floor 40), 4,096 x 5,120 33 (25), 16,384 x 512 11
+// (10, with help of the L2), but 65,536 x 128 36 us (floor 10), where an SM has six warps.
+// Value by value, 4,096 x 5,121 takes 261 us (floor 25). The kernel for more than 8,192
+// columns with fp32 among its types spills 112 bytes by stores and 56 by loads.
 #include <atomic>
 
 #include <type_traits>
@@ -344,7 +350,9 @@ __global__ void __launch_bounds__(NV == 8 ? 1024 : 512) norm_values_kernel(const
   }
 }
 
-// A grid of what fits on the GPU at once, or a CTA per row where there are fewer.
+// A grid of what fits on the GPU at once with the most threads that this kernel is launched
+// with, or a CTA per row where there are fewer: for less wide rows more CTAs would fit (the
+// figures at the top), and no more than this are launched.
 template <int NV, bool FP8, bool WIDE, int MAXT>
 cudaError_t launch_rows(const Args& g, int threads, size_t smem, cudaStream_t st) {
   static std::atomic<int> fits{0};

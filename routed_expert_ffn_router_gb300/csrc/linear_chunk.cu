@@ -41,11 +41,15 @@
 // decays, two blocks ahead.
 //
 // Measured, back to back in a graph, 16 k heads and 32 v heads of [128][128], bf16: a
-// prompt of 2,048 tokens 40.5 us (floor 8.1 us of bytes: the time is latency, start,
-// two passes over a part's two blocks, the exchange); eight ragged prompts of
-// up to 4,001 tokens 155 us (532 MB, floor 78.3 us; tensor pipe 34 % busy, a
+// prompt of 2,048 tokens 40 us (floor 8.1 us of bytes: the time is latency, start,
+// two passes over a part's four blocks, the exchange); eight ragged prompts of
+// up to 4,001 tokens 161 us (532 MB, floor 78.3 us; tensor pipe 34 % busy, a
 // block of 128 tokens 7,500 cycles of products, conversions and the waits that tie
-// them). An item's fixed cost is about 11 us, which is why few rows go row by row. The
+// them). An item's fixed cost is about 11 us, which is why few rows go row by row; a
+// short sequence of a call that comes here beside long ones pays it too (64 sequences of
+// one row 194 us, where a decode window of them takes 44). The roles share 80 registers a
+// thread: 112 bytes are spilled by stores and 336 by loads of the code of 128 x 128 in bf16
+// (up to 156 / 468 in the others), by which role is not known. The
 // chain of a block: A, its conversion by the warp with the last 32 tokens (which has
 // four pieces of A, the first warp one), O, the next A, which takes the place that O reads. Tried on
 // the eight prompts (159 us that time): the output's warps converting half of A 189 (they
@@ -1010,7 +1014,7 @@ cudaError_t launch_linear_chunk(const Linear& a, const kv::Rows& r, bool f16, cu
   if (!encode(&g.tm_q, a.q, a.Dk, a.Hk, r.n_rows, a.q_stride) || !encode(&g.tm_k, a.k, a.Dk, a.Hk, r.n_rows, a.k_stride) ||
       !encode(&g.tm_v, a.v, a.Dv, a.Hv, r.n_rows, a.v_stride))
     return cudaErrorInvalidValue;
-  // CTAs per item: while the items leave half of the GPU's SMs or more without one
+  // CTAs per item: while the items leave half of the GPU's 152 SMs or more without one
   // and the mean sequence has two blocks or more for each.
   const long long items = (long long)r.B * a.Hv, mean = ((long long)r.n_rows / r.B + kBlk - 1) / kBlk;
   g.parts = 1;

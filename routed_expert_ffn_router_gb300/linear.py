@@ -110,11 +110,13 @@ class LinearAttention:
 
     def chunk(self, q, k, v, g, slots=None, row_start=None, scale=None, out=None, stream=None):
         """Prompt chunks: rows row_start[b] .. row_start[b + 1) belong to slot slots[b]
-        (row_start None: the same number each)."""
+        (row_start None: the same number each). Sequences of one row or a few are better
+        off in a call of step."""
         return self._call(_lib.moe_linear_chunk, q, k, v, g, slots, row_start, scale, out, stream)
 
     def status(self, stream=None):
-        """-> device status bits: 2 a slot out of range, 64 a slot twice in a call; waits."""
+        """-> device status bits: 2 a slot out of range, 64 a slot twice in a call, 4 a bounded
+        wait of a chunk expired (its results are incomplete); waits."""
         handle = _on(self.device, stream)
         torch.cuda.ExternalStream(handle).synchronize() if handle else torch.cuda.default_stream().synchronize()
         return int(self._status)
